@@ -475,6 +475,131 @@ pgd_status pgd_varlen_plan(int num_seqs, int total_q, int max_q_len, int num_q_h
                            int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
                            int kv_partition, int *chosen_kv_partition, size_t *workspace_bytes);
 
+/*
+ * paged_gqa_tree — attention of trees of drafted tokens over the paged cache:
+ * the verification step of speculative decoding with more than one
+ * continuation per sequence.  Arguments, layouts, scratch and checks are those
+ * of paged_gqa_varlen (one row of q per drafted token, K and V of all of them
+ * already in the cache as the sequence's newest n_s tokens, in row order); what
+ * a row sees is not every earlier token but the tokens before the tree, its
+ * ancestors and itself:
+ *     out[r][h][:] = softmax( q[r][h] . K^T * scale over t < seq_lens[s] - n_s,
+ *                             the ancestors of r, and r ) . V
+ *
+ * parents    [total_q] int32: the node of the same sequence's tree (0 .. n_s-1)
+ *            that row r continues, an earlier one; any negative value: none (a
+ *            continuation of the sequence itself).  A value that is not an
+ *            earlier node counts as none and sets PGD_DEVERR_TREE.
+ * out        [total_q][num_q_heads][head_dim], 16-byte aligned
+ * out_type   PGD_OUT_F32 or PGD_OUT_F16 (the fp32 result rounded to nearest).
+ *            In both, the weights are rounded to fp16 (relative 2^-11) before
+ *            they multiply V, as in paged_gqa_varlen; sums are fp32.
+ * max_q_len  bound on every n_s, at most PGD_TREE_MAX_NODES.
+ *
+ * parents[i] = i - 1 is paged_gqa_varlen's causal form.  A sequence whose query
+ * rows are inconsistent (PGD_DEVERR_QUERY_LEN, also where they do not lie
+ * inside total_q) is skipped; rows behind the last sequence (total_q above
+ * cu_seqlens_q[num_seqs], a padded batch) are left as they were.  K and V rows
+ * of one sequence's tree must be finite: a weight of 0 does not hide an
+ * infinity or NaN in a sibling's V.  Library scratch, where there is any, is
+ * per call (also in a captured graph), and there is no state between calls:
+ * calls on different streams and replays of different graphs may overlap.
+ */
+#define PGD_OUT_F32 0
+#define PGD_OUT_F16 1
+#define PGD_TREE_MAX_NODES 256
+#define PGD_DEVERR_TREE 32u
+
+pgd_status paged_gqa_tree(void *out, int out_type, const uint16_t *q, const int32_t *cu_seqlens_q,
+                          const int32_t *parents, const uint16_t *k_cache, const uint16_t *v_cache,
+                          const int32_t *block_tables, const int32_t *seq_lens, float scale,
+                          int num_seqs, int total_q, int max_q_len, int num_q_heads,
+                          int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                          int num_blocks, int64_t page_stride, int64_t head_stride,
+                          int64_t token_stride, int kv_partition, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* pgd_varlen_plan for paged_gqa_tree. */
+pgd_status pgd_tree_plan(int num_seqs, int total_q, int max_q_len, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                         int kv_partition, int *chosen_kv_partition, size_t *workspace_bytes);
+
+/*
+ * paged_kv_slots — a step's page tables, slots, positions and lengths from the
+ * requests' token counts, on the GPU: what paged_kv_write / paged_kv_quantize
+ * (slots) and paged_gqa_varlen / paged_gqa_tree (cu_seqlens_q, seq_lens,
+ * block_tables) of the same step take.  ("vllm-metal", introduction: the paged
+ * block manager above the attention path.)
+ *
+ * Request s has context_lens[s] cached tokens on the first owned_s =
+ * ceil(context_lens[s] / block_size) pages of its row of block_tables, and gets
+ * query_lens[s] more.  The pages it lacks are taken from the list of free
+ * pages, request by request from entry *free_start on, and entered in its row:
+ *     cu_seqlens_q[s]  = sum of query_lens[0 .. s-1]        (num_seqs + 1 values)
+ *     seq_lens[s]      = context_lens[s] + query_lens[s]
+ *     *free_end        = *free_start + the pages taken
+ * and for row r = cu_seqlens_q[s] + i, which is token t = context_lens[s] + i:
+ *     positions[r]     = t
+ *     slots[r]         = block_tables[s][t / block_size] * block_size + t % block_size
+ * Rows behind the last request, up to num_rows (a launch padded to a fixed row
+ * count), get slot and position -1, which the writing calls skip.
+ *
+ * slots, positions  [num_rows] int32, written (positions may be NULL)
+ * cu_seqlens_q      [num_seqs + 1], seq_lens [num_seqs], free_end [1]: written
+ * block_tables      [num_seqs][max_blocks_per_seq]: entries below owned_s are
+ *                   read (those of the rows' pages), the new ones written, no
+ *                   other touched
+ * context_lens, query_lens  [num_seqs]; free_pages [num_free]; free_start [1] or
+ *                   NULL (0): read.  free_end must not be free_start, nor
+ *                   seq_lens one of the counts.
+ * The result depends on the arguments alone (the same pages every time), so a
+ * call may be repeated or replayed before its counts are advanced.
+ *
+ * num_seqs up to PGD_SLOTS_MAX_SEQS, num_blocks * block_size up to 2^31.
+ * Device-side checks, each with what the call does instead: a negative count
+ * counts as 0 (PGD_DEVERR_SEQ_LEN / PGD_DEVERR_QUERY_LEN); tokens past the
+ * table's max_blocks_per_seq * block_size get slot -1 and seq_lens is clamped
+ * (PGD_DEVERR_SEQ_LEN); rows that do not fit in num_rows are left out, of
+ * cu_seqlens_q and seq_lens too (PGD_DEVERR_QUERY_LEN); where the list runs out
+ * the entries and slots are -1 and *free_end counts what was needed
+ * (PGD_DEVERR_NO_PAGE); a page id outside [0, num_blocks) gives slot -1
+ * (PGD_DEVERR_PAGE_RANGE).
+ */
+#define PGD_DEVERR_NO_PAGE 16u
+#define PGD_SLOTS_MAX_SEQS 16384
+
+pgd_status paged_kv_slots(int32_t *slots, int32_t *positions, int32_t *cu_seqlens_q,
+                          int32_t *seq_lens, int32_t *free_end, int32_t *block_tables,
+                          const int32_t *context_lens, const int32_t *query_lens,
+                          const int32_t *free_pages, const int32_t *free_start, int num_seqs,
+                          int num_rows, int num_free, int block_size, int max_blocks_per_seq,
+                          int num_blocks, void *stream);
+
+/*
+ * paged_kv_write — writes fp16 K and V rows into their pages, the fp16
+ * counterpart of paged_kv_quantize (K and V in one call): prompt chunks,
+ * drafted tokens, or the accepted ones of a verified tree at their final
+ * places.
+ *
+ * k_new, v_new  the rows: head h of row n at element n * src_token_stride +
+ *               h * src_head_stride (head_dim contiguous halves; strides in
+ *               halves, positive multiples of 8: slices of a fused projection's
+ *               output need no copy), 16-byte aligned, read
+ * slots         [num_rows] int32 as paged_kv_slots gives them: page *
+ *               block_size + row; negative: the row is skipped
+ * k_cache, v_cache  written at the strides of paged_gqa_decode_strided; no other
+ *               row of the cache is touched
+ * Slots must differ from one another (of two rows with one slot, which one
+ * stays, or pieces of both, is not defined), and the source must not overlap
+ * the rows written.  A slot whose page is at or past num_blocks is skipped and
+ * sets PGD_DEVERR_PAGE_RANGE.  Asynchronous on `stream`, no scratch.
+ */
+pgd_status paged_kv_write(uint16_t *k_cache, uint16_t *v_cache, const uint16_t *k_new,
+                          const uint16_t *v_new, const int32_t *slots, int num_rows,
+                          int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                          int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                          int64_t src_token_stride, int64_t src_head_stride, void *stream);
+
 /* Partition size used by this thread's last successful call (0 if none);
  * the diagnostic of the pages' "Hands-on" section. */
 int pgd_last_partition_size(void);

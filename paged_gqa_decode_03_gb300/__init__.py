@@ -31,7 +31,8 @@ __all__ = ["paged_gqa_decode", "paged_gqa_decode_ex", "paged_gqa_decode_noalloc"
            "paged_gqa_decode_append", "paged_gqa_decode_strided", "kv_strides",
            "paged_gqa_varlen", "pgd_varlen_plan", "paged_gqa_decode_q8",
            "paged_gqa_decode_q8_append", "paged_gqa_decode_q8_strided", "q8_strides",
-           "paged_kv_quantize", "pgd_plan", "pgd_workspace_size", "pgd_release",
+           "paged_kv_quantize", "paged_gqa_tree", "pgd_tree_plan", "paged_kv_slots",
+           "paged_kv_write", "pgd_plan", "pgd_workspace_size", "pgd_release",
            "pgd_last_partition_size",
            "pgd_last_error", "pgd_check_device_error", "pgd_set_timing_events",
            "pgd_test_stall_next_decode", "pgd_test_fail_next_reduce",
@@ -45,6 +46,10 @@ _lib = None
 STATUS_NAMES = {0: "PGD_OK", 1: "PGD_ERR_INVALID_ARG", 2: "PGD_ERR_UNSUPPORTED",
                 3: "PGD_ERR_WORKSPACE", 4: "PGD_ERR_CUDA", 5: "PGD_ERR_DEVICE"}
 DEVERR_PAGE_RANGE, DEVERR_SEQ_LEN, DEVERR_TIMEOUT, DEVERR_QUERY_LEN = 1, 2, 4, 8
+DEVERR_NO_PAGE, DEVERR_TREE = 16, 32
+OUT_F32, OUT_F16 = 0, 1
+TREE_MAX_NODES = 256        # PGD_TREE_MAX_NODES of include/pgd.h
+SLOTS_MAX_SEQS = 16384      # PGD_SLOTS_MAX_SEQS
 
 # Every exported symbol of include/pgd.h with its ctypes signature.
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -63,6 +68,10 @@ SIGNATURES = {
     "paged_gqa_decode_q8_append": (_I, [_P] * 10 + [_F] + [_I] * 8 + [_P]),
     "paged_kv_quantize": (_I, [_P] * 4 + [_I] * 5 + [_P]),
     "paged_gqa_decode_q8_strided": (_I, [_P] * 10 + [_F] + [_I] * 8 + [_L] * 6 + [_P, _Z, _P]),
+    "paged_gqa_tree": (_I, [_P, _I] + [_P] * 7 + [_F] + [_I] * 9 + [_L] * 3 + [_I, _P, _Z, _P]),
+    "pgd_tree_plan": (_I, [_I] * 9 + [ctypes.POINTER(_I), ctypes.POINTER(_Z)]),
+    "paged_kv_slots": (_I, [_P] * 10 + [_I] * 6 + [_P]),
+    "paged_kv_write": (_I, [_P] * 5 + [_I] * 5 + [_L] * 5 + [_P]),
     "pgd_plan": (_I, [_I] * 7 + [ctypes.POINTER(_I), ctypes.POINTER(_Z)]),
     "pgd_workspace_size": (_Z, [_I] * 6),
     "pgd_release": (_I, []),
@@ -486,6 +495,170 @@ def paged_kv_quantize(codes, meta, src, slots, stream=None) -> None:
     st = lib.paged_kv_quantize(_ptr(codes), _ptr(meta), _ptr(src), _ptr(slots), N, Hkv, D, BS,
                                NB, _stream_handle(stream, src.device))
     _raise(st)
+
+
+def _one_device(*tensors):
+    """The device all of a call's tensors are on (the launch goes there)."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return dev
+
+
+def _on(dev, fn, *args, stream=None):
+    """Calls the library with ``dev`` as the current device."""
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, _stream_handle(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream_handle(stream, dev))
+    if st:
+        _raise(st)
+
+
+def _out_type(out):
+    if not isinstance(out, torch.Tensor) or out.dtype not in (torch.float32, torch.float16):
+        raise TypeError("out must be a float32 or float16 tensor")
+    return OUT_F16 if out.dtype == torch.float16 else OUT_F32
+
+
+def paged_gqa_tree(out, q, cu_seqlens_q, parents, k_cache, v_cache, block_tables, seq_lens, scale,
+                   max_q_len: int, kv_partition: int = 0, layout=None, workspace=None,
+                   stream=None) -> None:
+    """Attention of trees of drafted tokens over the paged cache.  As
+    ``paged_gqa_varlen`` (q: [total_q, Hq, D]; sequence s owns rows
+    cu_seqlens_q[s]..cu_seqlens_q[s+1]-1, its newest tokens, at most
+    TREE_MAX_NODES), but row i sees the tokens before the tree, its ancestors
+    by ``parents`` (int32 [total_q]: an earlier node of the same tree, or
+    negative for none) and itself.  ``out`` is float32 or float16."""
+    lib = load_library()
+    kind = _out_type(out)
+    _check(q, "q", torch.float16, 3)
+    _check(out, "out", out.dtype, 3)
+    _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    _check(parents, "parents", torch.int32, 1)
+    _check(block_tables, "block_tables", torch.int32, 2)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    T, Hq, D = q.shape
+    S = seq_lens.shape[0]
+    if (out.shape != q.shape or cu_seqlens_q.shape[0] != S + 1 or block_tables.shape[0] != S
+            or parents.shape[0] != T):
+        raise ValueError("inconsistent shapes of q, out, cu_seqlens_q, parents, block_tables, "
+                         "seq_lens")
+    if layout is None:
+        _check(k_cache, "k_cache", torch.float16, 4)
+        _check(v_cache, "v_cache", torch.float16, 4)
+        NB, Hkv, BS, D2 = k_cache.shape
+        if v_cache.shape != k_cache.shape or D2 != D:
+            raise ValueError("k_cache / v_cache shapes")
+        sp, sh, st = Hkv * BS * D, BS * D, D
+    else:
+        Hkv, BS, NB, strides = layout
+        _check_rows_inside(k_cache, "k_cache", NB, Hkv, BS, D, strides)
+        _check_rows_inside(v_cache, "v_cache", NB, Hkv, BS, D, strides)
+        sp, sh, st = (int(x) for x in strides)
+    ws_bytes = 0
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    dev = _one_device(q, out, cu_seqlens_q, parents, k_cache, v_cache, block_tables, seq_lens,
+                      workspace)
+    _on(dev, lib.paged_gqa_tree, out.data_ptr(), kind, q.data_ptr(), cu_seqlens_q.data_ptr(),
+        parents.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), float(scale), S, T, int(max_q_len), Hq, int(Hkv), D, int(BS),
+        block_tables.shape[1], int(NB), sp, sh, st, int(kv_partition),
+        workspace.data_ptr() if workspace is not None else None, ws_bytes, stream=stream)
+
+
+def pgd_tree_plan(num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                  max_blocks_per_seq, kv_partition=0):
+    """(KV partition used, scratch bytes needed) of a paged_gqa_tree call."""
+    lib = load_library()
+    pk = ctypes.c_int(0)
+    b = ctypes.c_size_t(0)
+    _raise(lib.pgd_tree_plan(num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim,
+                             block_size, max_blocks_per_seq, kv_partition, ctypes.byref(pk),
+                             ctypes.byref(b)))
+    return pk.value, b.value
+
+
+def paged_kv_slots(slots, cu_seqlens_q, seq_lens, free_end, block_tables, context_lens,
+                   query_lens, free_pages, block_size: int, num_blocks: int, free_start=None,
+                   positions=None, stream=None) -> None:
+    """A step's page tables, slots, positions and lengths from the requests'
+    cached (``context_lens``) and new (``query_lens``) token counts, int32 on
+    the device throughout.  Pages a request lacks are taken from
+    ``free_pages``, from entry ``free_start`` (int32 [1]; None: 0) on, and
+    entered in ``block_tables``; ``cu_seqlens_q``, ``seq_lens``, ``free_end``
+    (int32 [1]), ``slots`` and ``positions`` (int32 [rows], or None) are
+    written, with -1 in the rows behind the last request."""
+    lib = load_library()
+    for t, name in ((slots, "slots"), (cu_seqlens_q, "cu_seqlens_q"), (seq_lens, "seq_lens"),
+                    (free_end, "free_end"), (context_lens, "context_lens"),
+                    (query_lens, "query_lens"), (free_pages, "free_pages"),
+                    (free_start, "free_start"), (positions, "positions")):
+        if t is not None or name not in ("free_start", "positions"):
+            _check(t, name, torch.int32, 1)
+    _check(block_tables, "block_tables", torch.int32, 2)
+    S, N = context_lens.shape[0], slots.shape[0]
+    if (query_lens.shape[0] != S or seq_lens.shape[0] != S or block_tables.shape[0] != S
+            or cu_seqlens_q.shape[0] != S + 1):
+        raise ValueError("inconsistent shapes of context_lens, query_lens, seq_lens, "
+                         "cu_seqlens_q, block_tables")
+    if positions is not None and positions.shape[0] != N:
+        raise ValueError("positions must have a value per slot")
+    if free_end.shape[0] != 1 or (free_start is not None and free_start.shape[0] != 1):
+        raise ValueError("free_start and free_end hold one value")
+    dev = _one_device(slots, cu_seqlens_q, seq_lens, free_end, block_tables, context_lens,
+                      query_lens, free_pages, free_start, positions)
+    _on(dev, lib.paged_kv_slots, slots.data_ptr(),
+        positions.data_ptr() if positions is not None else None, cu_seqlens_q.data_ptr(),
+        seq_lens.data_ptr(), free_end.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), query_lens.data_ptr(), free_pages.data_ptr(),
+        free_start.data_ptr() if free_start is not None else None, S, N, free_pages.shape[0],
+        int(block_size), block_tables.shape[1], int(num_blocks), stream=stream)
+
+
+def paged_kv_write(k_cache, v_cache, k_new, v_new, slots, layout=None, stream=None) -> None:
+    """Writes the fp16 rows k_new, v_new [N, num_kv_heads, head_dim] (contiguous
+    rows of head_dim; any token and head strides, so slices of a fused
+    projection need no copy) into the cache at rows slots[n] = page *
+    block_size + row (int32 [N], distinct; negative: skipped).  Caches
+    head-major [NB, Hkv, BS, D], or any tensors with ``layout =
+    (num_kv_heads, block_size, num_blocks, strides)``."""
+    lib = load_library()
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float16 or not t.is_cuda:
+            raise TypeError(f"{name} must be a float16 CUDA tensor")
+        if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+            raise ValueError(f"{name} must be [N, num_kv_heads, head_dim] with contiguous rows")
+    _check(slots, "slots", torch.int32, 1)
+    N, Hkv, D = k_new.shape
+    if v_new.shape != k_new.shape or v_new.stride() != k_new.stride() or slots.shape[0] != N:
+        raise ValueError("k_new and v_new must have the same shape and strides, and a slot per row")
+    if layout is None:
+        _check(k_cache, "k_cache", torch.float16, 4)
+        _check(v_cache, "v_cache", torch.float16, 4)
+        NB, H2, BS, D2 = k_cache.shape
+        if v_cache.shape != k_cache.shape or D2 != D or H2 != Hkv:
+            raise ValueError("inconsistent shapes of k_cache, v_cache, k_new")
+        sp, sh, st = Hkv * BS * D, BS * D, D
+    else:
+        H2, BS, NB, strides = layout
+        if H2 != Hkv:
+            raise ValueError(f"layout of {H2} KV heads for rows of {Hkv}")
+        _check_rows_inside(k_cache, "k_cache", NB, Hkv, BS, D, strides)
+        _check_rows_inside(v_cache, "v_cache", NB, Hkv, BS, D, strides)
+        sp, sh, st = (int(x) for x in strides)
+    dev = _one_device(k_new, v_new, slots, k_cache, v_cache)
+    # (the stride of a dimension of one element says nothing)
+    from_token = k_new.stride(0) if N > 1 else Hkv * D
+    from_head = k_new.stride(1) if Hkv > 1 else D
+    _on(dev, lib.paged_kv_write, k_cache.data_ptr(), v_cache.data_ptr(), k_new.data_ptr(),
+        v_new.data_ptr(), slots.data_ptr(), N, Hkv, D, int(BS), int(NB), sp, sh, st, from_token,
+        from_head, stream=stream)
 
 
 NOALLOC_SCRATCH_BYTES = 64 << 20  # PGD_NOALLOC_SCRATCH_BYTES of include/pgd.h

@@ -1063,8 +1063,10 @@ int varlen_tokens_per_stage(int D) { return D == 64 ? VShape<64>::NT : D == 128 
 // per (sequence, KV head); the KV range is cut into partitions of PK tokens
 // only when the tiles alone (counted at max_q_len) would not give every SM
 // two units.  Scratch (partials) only when some row spans two partitions.
+// tree: trees of drafted tokens (paged_gqa_tree), on the tensor-core kernels
+// at every size.
 pgd_status make_varlen_plan(int S, int total_q, int max_q, int Hq, int Hkv, int D, int BS,
-                            int MB, int kv_partition, VarlenPlan *vp)
+                            int MB, int kv_partition, VarlenPlan *vp, bool tree = false)
 {
     pgd_status st;
     if (S < 0)
@@ -1083,6 +1085,9 @@ pgd_status make_varlen_plan(int S, int total_q, int max_q, int Hq, int Hkv, int 
         return fail(PGD_ERR_UNSUPPORTED, "length bound %lld above 2^30", (long long)MB * BS);
     if (total_q < 0 || max_q < 0 || (total_q > 0 && max_q < 1))
         return fail(PGD_ERR_INVALID_ARG, "total_q %d / max_q_len %d", total_q, max_q);
+    if (tree && max_q > kTreeMaxNodes)
+        return fail(PGD_ERR_UNSUPPORTED, "max_q_len %d: trees of up to %d nodes", max_q,
+                    kTreeMaxNodes);
     vp->NT = varlen_tokens_per_stage(D);
     if (kv_partition < 0 || (kv_partition > 0 && kv_partition % vp->NT != 0))
         return fail(PGD_ERR_INVALID_ARG, "kv_partition %d: 0 or a positive multiple of %d",
@@ -1096,7 +1101,7 @@ pgd_status make_varlen_plan(int S, int total_q, int max_q, int Hq, int Hkv, int 
     // read each K/V byte for only a few rows: an HBM-bound scan, which the
     // decode kernel's MQ form does (one n8 column tile of mma.sync, partitions of
     // 256 / 512 tokens chosen as for the decode, partials per query row).
-    vp->mq = D <= 128 && vp->G <= kMaxGroup && max_q >= 1 &&
+    vp->mq = !tree && D <= 128 && vp->G <= kMaxGroup && max_q >= 1 &&
              (long long)max_q * vp->G <= kMaxCols &&
              (kv_partition == 0 || kv_partition == kPartitionSmall ||
               kv_partition == kPartitionLarge);
@@ -1169,29 +1174,43 @@ pgd_status make_varlen_plan(int S, int total_q, int max_q, int Hq, int Hkv, int 
     return PGD_OK;
 }
 
+// What a call over trees of drafted tokens has beside the plain form's
+// arguments (then `out` is null): the parents and either output.
+struct TreeArgs {
+    const int32_t *parents;
+    float *out;
+    uint16_t *out_half;
+};
+
 pgd_status run_varlen(float *out, const uint16_t *q, const int32_t *cu_q, const uint16_t *k_cache,
                       const uint16_t *v_cache, const int32_t *block_tables,
                       const int32_t *seq_lens, float scale, int S, int total_q, int max_q, int Hq,
                       int Hkv, int D, int BS, int MB, int NB, const Strides &kv_strides,
-                      int kv_partition, void *workspace, size_t ws_bytes, void *stream_v)
+                      int kv_partition, void *workspace, size_t ws_bytes, void *stream_v,
+                      const TreeArgs *tree = nullptr)
 {
     VarlenPlan vp;
-    pgd_status st = make_varlen_plan(S, total_q, max_q, Hq, Hkv, D, BS, MB, kv_partition, &vp);
+    pgd_status st = make_varlen_plan(S, total_q, max_q, Hq, Hkv, D, BS, MB, kv_partition, &vp,
+                                     tree != nullptr);
     if (st)
         return st;
     if (S == 0 || total_q == 0) {
         t_last_error.clear();
         return PGD_OK;
     }
-    if (!out || !q || !cu_q || !k_cache || !v_cache || !block_tables || !seq_lens)
+    const void *dst = tree && tree->out_half ? static_cast<const void *>(tree->out_half)
+                      : tree                 ? tree->out
+                                             : out;
+    if (!dst || (tree && !tree->parents) || !q || !cu_q || !k_cache || !v_cache || !block_tables || !seq_lens)
         return fail(PGD_ERR_INVALID_ARG, "null array argument");
     if (!std::isfinite(scale))
         return fail(PGD_ERR_INVALID_ARG, "scale is not finite");
     if (NB <= 0)
         return fail(PGD_ERR_INVALID_ARG, "num_blocks %d <= 0", NB);
-    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(dst, 16))
         return fail(PGD_ERR_INVALID_ARG, "q, k_cache, v_cache and out must be 16-byte aligned");
-    if (!aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4))
+    if (!aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+        (tree && !aligned(tree->parents, 4)))
         return fail(PGD_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
     if ((st = check_strides(kv_strides, D)))
         return st;
@@ -1234,7 +1253,10 @@ pgd_status run_varlen(float *out, const uint16_t *q, const int32_t *cu_q, const 
         return st;
     }
     VarlenParams p = {};
-    p.out = out;
+    p.out = tree ? tree->out : out;
+    p.out_half = tree ? reinterpret_cast<__half *>(tree->out_half) : nullptr;
+    p.parents = tree ? tree->parents : nullptr;
+    p.total_q = total_q;
     p.cu_q = cu_q;
     p.block_tables = block_tables;
     p.seq_lens = seq_lens;
@@ -1261,8 +1283,8 @@ pgd_status run_varlen(float *out, const uint16_t *q, const int32_t *cu_q, const 
     p.blk_head = (int)(kv_strides.head / blk_u);
     p.max_q = max_q;
     p.wait_budget_ns = kWaitBudgetNs;
-    e = launch_varlen(D, vp.pairs, tq, *tk, *tv, p, (int)vp.grid, vp.NP > 1 ? total_q * Hq : 0,
-                      stream);
+    e = (tree ? launch_tree : launch_varlen)(D, vp.pairs, tq, *tk, *tv, p, (int)vp.grid,
+                                             vp.NP > 1 ? total_q * Hq : 0, stream);
     if (own && ws) {
         cudaError_t e2 = cudaFreeAsync(ws, stream);
         if (e == cudaSuccess)
@@ -1325,6 +1347,143 @@ HostStaging host_staging(int S, int Hq, int D, int MB)
     h.out = h.sl + align256((size_t)S * 4);
     h.bytes = h.out + align256((size_t)S * Hq * D * 4);
     return h;
+}
+
+// ------------------------------------------------------------------ the step around the cache
+pgd_status run_slots(int32_t *slots, int32_t *positions, int32_t *cu_seqlens_q, int32_t *seq_lens,
+                     int32_t *free_end, int32_t *block_tables, const int32_t *context_lens,
+                     const int32_t *query_lens, const int32_t *free_pages,
+                     const int32_t *free_start, int S, int N, int num_free, int BS, int MB, int NB,
+                     void *stream)
+{
+    if (S < 0 || N < 0 || num_free < 0)
+        return fail(PGD_ERR_INVALID_ARG, "num_seqs %d, num_rows %d, num_free %d", S, N, num_free);
+    if (!supported_block_size(BS))
+        return fail(PGD_ERR_UNSUPPORTED, "block_size %d not in {8, 16, 32, 64, 128}", BS);
+    if (MB <= 0 || NB <= 0)
+        return fail(PGD_ERR_INVALID_ARG, "max_blocks_per_seq %d / num_blocks %d", MB, NB);
+    if ((long long)MB * BS > (1ll << 30))
+        return fail(PGD_ERR_UNSUPPORTED, "length bound %lld above 2^30", (long long)MB * BS);
+    if ((long long)NB * BS > (1ll << 31))
+        return fail(PGD_ERR_UNSUPPORTED, "%d pages of %d rows: slots above 2^31", NB, BS);
+    if (S > kSlotMaxSeqs)
+        return fail(PGD_ERR_UNSUPPORTED, "num_seqs %d above %d", S, kSlotMaxSeqs);
+    if (N >= kSlotCountCap || num_free >= kSlotCountCap)
+        return fail(PGD_ERR_UNSUPPORTED, "num_rows %d / num_free %d: below 2^30", N, num_free);
+    if (!cu_seqlens_q || !free_end || (N > 0 && !slots) || (num_free > 0 && !free_pages) ||
+        (S > 0 && (!seq_lens || !block_tables || !context_lens || !query_lens)))
+        return fail(PGD_ERR_INVALID_ARG, "null array argument");
+    for (const void *a : {(const void *)slots, (const void *)positions, (const void *)cu_seqlens_q,
+                          (const void *)seq_lens, (const void *)free_end,
+                          (const void *)block_tables, (const void *)context_lens,
+                          (const void *)query_lens, (const void *)free_pages,
+                          (const void *)free_start})
+        if (!aligned(a, 4))
+            return fail(PGD_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+    // every thread block reads the counts while one writes the results
+    if (free_end == free_start || (S > 0 && (seq_lens == context_lens || seq_lens == query_lens)))
+        return fail(PGD_ERR_INVALID_ARG, "free_end and seq_lens are written while free_start and "
+                                         "the counts are read: give other arrays");
+    DeviceState *ds;
+    pgd_status st;
+    if ((st = device_state(&ds)))
+        return st;
+    SlotParams p = {};
+    p.slots = slots;
+    p.positions = positions;
+    p.cu_seqlens_q = cu_seqlens_q;
+    p.seq_lens = seq_lens;
+    p.free_end = free_end;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_lens = query_lens;
+    p.free_pages = free_pages;
+    p.free_start = free_start;
+    p.err = ds->err_word;
+    p.S = S;
+    p.N = N;
+    p.num_free = num_free;
+    p.log2BS = 3 + bs_index(BS);
+    p.MB = MB;
+    p.NB = NB;
+    p.vector_slots = aligned(slots, 16);
+    p.vector_positions = aligned(positions, 16);
+    const cudaError_t e = launch_kv_slots(p, ds->num_sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "kernel launch");
+    t_last_error.clear();
+    return PGD_OK;
+}
+
+pgd_status run_write(uint16_t *k_cache, uint16_t *v_cache, const uint16_t *k_new,
+                     const uint16_t *v_new, const int32_t *slots, int rows, int Hkv, int D, int BS,
+                     int NB, const Strides &kv, long long src_token, long long src_head,
+                     void *stream)
+{
+    if (rows < 0 || Hkv <= 0 || NB <= 0)
+        return fail(PGD_ERR_INVALID_ARG, "num_rows %d, num_kv_heads %d, num_blocks %d", rows, Hkv,
+                    NB);
+    if (!supported_head_dim(D))
+        return fail(PGD_ERR_UNSUPPORTED, "head_dim %d not in {64, 128, 256}", D);
+    if (!supported_block_size(BS))
+        return fail(PGD_ERR_UNSUPPORTED, "block_size %d not in {8, 16, 32, 64, 128}", BS);
+    if (Hkv > 65536)
+        return fail(PGD_ERR_UNSUPPORTED, "num_kv_heads %d above 65536", Hkv);
+    pgd_status st;
+    if ((st = check_strides(kv, D)))
+        return st;
+    for (long long x : {src_token, src_head})
+        if (x <= 0 || x % 8 != 0 || x >= (1ll << 39))
+            return fail(PGD_ERR_INVALID_ARG,
+                        "source strides (%lld, %lld) must be positive multiples of 8 halves "
+                        "below 2^39",
+                        src_token, src_head);
+    if (rows == 0) {
+        t_last_error.clear();
+        return PGD_OK;
+    }
+    if (!k_cache || !v_cache || !k_new || !v_new || !slots)
+        return fail(PGD_ERR_INVALID_ARG, "null array argument");
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_new, 16) ||
+        !aligned(v_new, 16) || !aligned(slots, 4))
+        return fail(PGD_ERR_INVALID_ARG, "k_cache, v_cache, k_new and v_new must be 16-byte "
+                                         "aligned, slots 4");
+    DeviceState *ds;
+    if ((st = device_state(&ds)))
+        return st;
+    WriteParams p = {};
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.slots = slots;
+    p.err = ds->err_word;
+    p.rows = rows;
+    p.Hkv = Hkv;
+    p.vec = D / 8;
+    p.log2BS = 3 + bs_index(BS);
+    p.NB = NB;
+    p.page_stride = kv.page;
+    p.head_stride = kv.head;
+    p.token_stride = kv.token;
+    p.src_token_stride = src_token;
+    p.src_head_stride = src_head;
+    const cudaError_t e = launch_kv_write(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "kernel launch");
+    t_last_error.clear();
+    return PGD_OK;
+}
+
+// Runs a C entry's body: nothing it throws (an allocation of the host's that
+// failed) leaves the library.
+template <class F> pgd_status guarded(F &&body) noexcept
+{
+    try {
+        return body();
+    } catch (...) {
+        return PGD_ERR_CUDA;
+    }
 }
 
 }  // namespace
@@ -1614,6 +1773,75 @@ pgd_status pgd_varlen_plan(int num_seqs, int total_q, int max_q_len, int num_q_h
     if (workspace_bytes)
         *workspace_bytes = vp.ws_bytes;
     return PGD_OK;
+}
+
+pgd_status paged_gqa_tree(void *out, int out_type, const uint16_t *q, const int32_t *cu_seqlens_q,
+                          const int32_t *parents, const uint16_t *k_cache, const uint16_t *v_cache,
+                          const int32_t *block_tables, const int32_t *seq_lens, float scale,
+                          int num_seqs, int total_q, int max_q_len, int num_q_heads,
+                          int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                          int num_blocks, int64_t page_stride, int64_t head_stride,
+                          int64_t token_stride, int kv_partition, void *workspace,
+                          size_t workspace_bytes, void *stream)
+{
+    return guarded([&]() -> pgd_status {
+        if (out_type != PGD_OUT_F32 && out_type != PGD_OUT_F16)
+            return fail(PGD_ERR_INVALID_ARG, "out_type %d: PGD_OUT_F32 or PGD_OUT_F16", out_type);
+        const bool half = out_type == PGD_OUT_F16;
+        const TreeArgs tree = {parents, half ? nullptr : static_cast<float *>(out),
+                               half ? static_cast<uint16_t *>(out) : nullptr};
+        return run_varlen(nullptr, q, cu_seqlens_q, k_cache, v_cache, block_tables, seq_lens, scale,
+                          num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim,
+                          block_size, max_blocks_per_seq, num_blocks,
+                          Strides{page_stride, head_stride, token_stride}, kv_partition, workspace,
+                          workspace_bytes, stream, &tree);
+    });
+}
+
+pgd_status pgd_tree_plan(int num_seqs, int total_q, int max_q_len, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                         int kv_partition, int *chosen_kv_partition, size_t *workspace_bytes)
+{
+    return guarded([&]() -> pgd_status {
+        VarlenPlan vp;
+        pgd_status st = make_varlen_plan(num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads,
+                                         head_dim, block_size, max_blocks_per_seq, kv_partition,
+                                         &vp, true);
+        if (st)
+            return st;
+        if (chosen_kv_partition)
+            *chosen_kv_partition = vp.PK;
+        if (workspace_bytes)
+            *workspace_bytes = vp.ws_bytes;
+        return PGD_OK;
+    });
+}
+
+pgd_status paged_kv_slots(int32_t *slots, int32_t *positions, int32_t *cu_seqlens_q,
+                          int32_t *seq_lens, int32_t *free_end, int32_t *block_tables,
+                          const int32_t *context_lens, const int32_t *query_lens,
+                          const int32_t *free_pages, const int32_t *free_start, int num_seqs,
+                          int num_rows, int num_free, int block_size, int max_blocks_per_seq,
+                          int num_blocks, void *stream)
+{
+    return guarded([&]() -> pgd_status {
+        return run_slots(slots, positions, cu_seqlens_q, seq_lens, free_end, block_tables,
+                         context_lens, query_lens, free_pages, free_start, num_seqs, num_rows,
+                         num_free, block_size, max_blocks_per_seq, num_blocks, stream);
+    });
+}
+
+pgd_status paged_kv_write(uint16_t *k_cache, uint16_t *v_cache, const uint16_t *k_new,
+                          const uint16_t *v_new, const int32_t *slots, int num_rows,
+                          int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                          int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                          int64_t src_token_stride, int64_t src_head_stride, void *stream)
+{
+    return guarded([&]() -> pgd_status {
+        return run_write(k_cache, v_cache, k_new, v_new, slots, num_rows, num_kv_heads, head_dim,
+                         block_size, num_blocks, Strides{page_stride, head_stride, token_stride},
+                         src_token_stride, src_head_stride, stream);
+    });
 }
 
 pgd_status pgd_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,

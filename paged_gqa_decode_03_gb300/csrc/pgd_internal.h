@@ -244,7 +244,45 @@ struct VarlenParams {
                                   //   block index order
     int blk_page, blk_head;       // (page, KV head) -> block coordinate of the K/V maps
     uint64_t wait_budget_ns;
+    // trees of drafted tokens (the TREE instantiations; null otherwise)
+    int total_q;                  // rows of q and out
+    const int32_t *parents;       // [total_q] parent node of each query row, negative: none
+    __half *out_half;             // [total_q][Hq][D] the output as fp16, or null: `out` as fp32
 };
+
+// ---------------------------------------------------------------- the step around the cache
+// Page tables, slots, positions and lengths of a step, and the writes of its
+// K and V rows (pgd_kv.cu).
+constexpr unsigned kErrNoPage = 16u;      // a step needed more pages than the free list holds
+constexpr int kSlotCountCap = 1 << 30;    // row and page counts saturate here
+constexpr int kSlotMaxSeqs = 16384;       // requests of one call (their offsets sit in shared memory)
+constexpr int kSlotSmemMax = (2 * kSlotMaxSeqs + 1) * 4;
+
+struct SlotParams {
+    int32_t *slots, *positions;           // [N] (positions or null)
+    int32_t *cu_seqlens_q, *seq_lens;     // [S + 1], [S]
+    int32_t *free_end;                    // [1]
+    int32_t *block_tables;                // [S][MB]: read below, written from owned_s on
+    const int32_t *context_lens, *query_lens;  // [S]
+    const int32_t *free_pages;            // [num_free]
+    const int32_t *free_start;            // [1] or null (0)
+    unsigned *err;
+    int S, N, num_free, log2BS, MB, NB;
+    bool vector_slots, vector_positions;  // 16-byte aligned outputs
+};
+cudaError_t launch_kv_slots(const SlotParams &p, int num_sms, cudaStream_t stream);
+
+struct WriteParams {
+    uint16_t *k_cache, *v_cache;
+    const uint16_t *k_new, *v_new;
+    const int32_t *slots;                 // [rows]
+    unsigned *err;
+    int rows, Hkv, vec, log2BS, NB;       // vec: 16-byte pieces of a row (head_dim / 8)
+    int rows_per_cta;                     // set by the launcher
+    long long page_stride, head_stride, token_stride;   // halves
+    long long src_token_stride, src_head_stride;
+};
+cudaError_t launch_kv_write(WriteParams p, cudaStream_t stream);
 
 // Quantiser of rows into quantised pages (pgd_quantize.cu).
 cudaError_t launch_quantize(int head_dim, uint8_t *codes, uint16_t *meta, const uint16_t *src,
@@ -254,6 +292,12 @@ cudaError_t launch_quantize(int head_dim, uint8_t *codes, uint16_t *meta, const 
 cudaError_t launch_varlen(int head_dim, bool pairs, const CUtensorMap &tq, const CUtensorMap &tk,
                           const CUtensorMap &tv, const VarlenParams &p, int grid, int reduce_rows,
                           cudaStream_t stream);
+// Trees of drafted tokens over the cache (the TREE instantiations).
+constexpr unsigned kErrTree = 32u;     // a parent that is not an earlier node of its tree
+constexpr int kTreeMaxNodes = 256;     // nodes of one sequence's tree
+cudaError_t launch_tree(int head_dim, bool pairs, const CUtensorMap &tq, const CUtensorMap &tk,
+                        const CUtensorMap &tv, const VarlenParams &p, int grid, int reduce_rows,
+                        cudaStream_t stream);
 constexpr int kVarlenOrderKeys = 1024;  // stage counts the unit sort tells apart
 
 }  // namespace pgd
