@@ -525,6 +525,51 @@ pgd_status pgd_tree_plan(int num_seqs, int total_q, int max_q_len, int num_q_hea
                          int kv_partition, int *chosen_kv_partition, size_t *workspace_bytes);
 
 /*
+ * packed_gqa_prefill — causal attention over whole packed prompts, before
+ * their K and V are in any cache: q, k and v as the step's projections leave
+ * them.  (paged_gqa_varlen is the form for chunks behind cached tokens.)
+ *
+ * Prompt s is the rows cu_seqlens[s] .. cu_seqlens[s+1]-1 of q, k and v alike;
+ * for its row at position t and head h, which reads KV head
+ * h / (num_q_heads / num_kv_heads):
+ *     out[row][h][:] = softmax( q[row][h] . K^T * scale over positions <= t ) . V
+ *
+ * q            [total][num_q_heads][head_dim], k, v [total][num_kv_heads]
+ *              [head_dim] fp16, 16-byte aligned, each with its own token and
+ *              head stride (halves, positive multiples of 8): slices of one
+ *              fused projection's output need no copy
+ * cu_seqlens   [num_seqs + 1] int32, non-decreasing
+ * out          [total][num_q_heads][head_dim] contiguous, 16-byte aligned
+ * out_type     PGD_OUT_F32 or PGD_OUT_F16 (rounded to nearest).  The weights
+ *              are rounded to fp16 (relative 2^-11) before they multiply V,
+ *              sums are fp32.
+ * max_len      bound on every prompt's length
+ * workspace    NULL: library scratch (per call, also in a captured graph);
+ *              else at least pgd_prefill_plan's bytes, 256-byte aligned, not
+ *              used by anything else until the call's work is done
+ *
+ * head_dim 64/128/256, groups of up to 128 query heads.  Rows that belong to no
+ * prompt are left as they were (not written).  A prompt that is longer than
+ * max_len, has a negative length or does not lie inside total is skipped and
+ * sets PGD_DEVERR_QUERY_LEN.  Other prompts' rows may hold anything; within
+ * one prompt an infinity or NaN in V is not hidden from earlier rows of the same
+ * 128 keys by their weight of 0.
+ */
+pgd_status packed_gqa_prefill(void *out, int out_type, const uint16_t *q, const uint16_t *k,
+                              const uint16_t *v, const int32_t *cu_seqlens, float scale,
+                              int num_seqs, int total, int max_len, int num_q_heads,
+                              int num_kv_heads, int head_dim, int64_t q_token_stride,
+                              int64_t q_head_stride, int64_t k_token_stride,
+                              int64_t k_head_stride, int64_t v_token_stride,
+                              int64_t v_head_stride, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/* Scratch bytes a packed_gqa_prefill call with these sizes needs (the list of
+ * its tiles, longest first).  Pure arithmetic. */
+pgd_status pgd_prefill_plan(int num_seqs, int total, int num_q_heads, int num_kv_heads,
+                            int head_dim, size_t *workspace_bytes);
+
+/*
  * paged_kv_slots — a step's page tables, slots, positions and lengths from the
  * requests' token counts, on the GPU: what paged_kv_write / paged_kv_quantize
  * (slots) and paged_gqa_varlen / paged_gqa_tree (cu_seqlens_q, seq_lens,

@@ -31,8 +31,8 @@ __all__ = ["paged_gqa_decode", "paged_gqa_decode_ex", "paged_gqa_decode_noalloc"
            "paged_gqa_decode_append", "paged_gqa_decode_strided", "kv_strides",
            "paged_gqa_varlen", "pgd_varlen_plan", "paged_gqa_decode_q8",
            "paged_gqa_decode_q8_append", "paged_gqa_decode_q8_strided", "q8_strides",
-           "paged_kv_quantize", "paged_gqa_tree", "pgd_tree_plan", "paged_kv_slots",
-           "paged_kv_write", "pgd_plan", "pgd_workspace_size", "pgd_release",
+           "paged_kv_quantize", "paged_gqa_tree", "pgd_tree_plan",
+           "packed_gqa_prefill", "pgd_prefill_plan", "paged_kv_slots", "paged_kv_write", "pgd_plan", "pgd_workspace_size", "pgd_release",
            "pgd_last_partition_size",
            "pgd_last_error", "pgd_check_device_error", "pgd_set_timing_events",
            "pgd_test_stall_next_decode", "pgd_test_fail_next_reduce",
@@ -70,6 +70,8 @@ SIGNATURES = {
     "paged_gqa_decode_q8_strided": (_I, [_P] * 10 + [_F] + [_I] * 8 + [_L] * 6 + [_P, _Z, _P]),
     "paged_gqa_tree": (_I, [_P, _I] + [_P] * 7 + [_F] + [_I] * 9 + [_L] * 3 + [_I, _P, _Z, _P]),
     "pgd_tree_plan": (_I, [_I] * 9 + [ctypes.POINTER(_I), ctypes.POINTER(_Z)]),
+    "packed_gqa_prefill": (_I, [_P, _I] + [_P] * 4 + [_F] + [_I] * 6 + [_L] * 6 + [_P, _Z, _P]),
+    "pgd_prefill_plan": (_I, [_I] * 5 + [ctypes.POINTER(_Z)]),
     "paged_kv_slots": (_I, [_P] * 10 + [_I] * 6 + [_P]),
     "paged_kv_write": (_I, [_P] * 5 + [_I] * 5 + [_L] * 5 + [_P]),
     "pgd_plan": (_I, [_I] * 7 + [ctypes.POINTER(_I), ctypes.POINTER(_Z)]),
@@ -584,6 +586,54 @@ def pgd_tree_plan(num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, head_
     return pk.value, b.value
 
 
+def _packed_strides(t, name):
+    """(token, head) strides of rows [tokens, heads, head_dim] of contiguous
+    head_dim (the stride of a dimension of one element says nothing)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a float16 CUDA tensor")
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name} must have 3 dimensions and contiguous rows of head_dim")
+    T, H, D = t.shape
+    head = t.stride(1) if H > 1 else D
+    return (t.stride(0) if T > 1 else H * head), head
+
+
+def packed_gqa_prefill(out, q, k, v, cu_seqlens, scale, max_len: int, workspace=None,
+                       stream=None) -> None:
+    """Causal attention over whole packed prompts (rows cu_seqlens[s] ..
+    cu_seqlens[s+1]-1 of q [total, Hq, D] and k, v [total, Hkv, D], fp16 with
+    contiguous rows of head_dim and any token and head strides) into ``out``
+    (contiguous [total, Hq, D], float16 or float32)."""
+    lib = load_library()
+    kind = _out_type(out)
+    _check(out, "out", out.dtype, 3)
+    _check(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    qs, ks, vs = _packed_strides(q, "q"), _packed_strides(k, "k"), _packed_strides(v, "v")
+    T, Hq, D = q.shape
+    if out.shape != q.shape or k.shape[0] != T or k.shape[2] != D or v.shape != k.shape:
+        raise ValueError("inconsistent shapes of out, q, k, v")
+    if cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens holds num_seqs + 1 values")
+    ws_bytes = 0
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    dev = _one_device(q, out, k, v, cu_seqlens, workspace)
+    _on(dev, lib.packed_gqa_prefill, out.data_ptr(), kind, q.data_ptr(), k.data_ptr(),
+        v.data_ptr(), cu_seqlens.data_ptr(), float(scale), cu_seqlens.shape[0] - 1, T,
+        int(max_len), Hq, k.shape[1], D, *qs, *ks, *vs,
+        workspace.data_ptr() if workspace is not None else None, ws_bytes, stream=stream)
+
+
+def pgd_prefill_plan(num_seqs, total, num_q_heads, num_kv_heads, head_dim) -> int:
+    """Scratch bytes of a packed_gqa_prefill call (needs no GPU)."""
+    b = ctypes.c_size_t(0)
+    _raise(load_library().pgd_prefill_plan(num_seqs, total, num_q_heads, num_kv_heads, head_dim,
+                                           ctypes.byref(b)))
+    return b.value
+
+
 def paged_kv_slots(slots, cu_seqlens_q, seq_lens, free_end, block_tables, context_lens,
                    query_lens, free_pages, block_size: int, num_blocks: int, free_start=None,
                    positions=None, stream=None) -> None:
@@ -629,15 +679,13 @@ def paged_kv_write(k_cache, v_cache, k_new, v_new, slots, layout=None, stream=No
     head-major [NB, Hkv, BS, D], or any tensors with ``layout =
     (num_kv_heads, block_size, num_blocks, strides)``."""
     lib = load_library()
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.float16 or not t.is_cuda:
-            raise TypeError(f"{name} must be a float16 CUDA tensor")
-        if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
-            raise ValueError(f"{name} must be [N, num_kv_heads, head_dim] with contiguous rows")
+    src = _packed_strides(k_new, "k_new")
+    if _packed_strides(v_new, "v_new") != src:
+        raise ValueError("k_new and v_new must have the same strides")
     _check(slots, "slots", torch.int32, 1)
     N, Hkv, D = k_new.shape
-    if v_new.shape != k_new.shape or v_new.stride() != k_new.stride() or slots.shape[0] != N:
-        raise ValueError("k_new and v_new must have the same shape and strides, and a slot per row")
+    if v_new.shape != k_new.shape or slots.shape[0] != N:
+        raise ValueError("k_new and v_new must have the same shape, and a slot per row")
     if layout is None:
         _check(k_cache, "k_cache", torch.float16, 4)
         _check(v_cache, "v_cache", torch.float16, 4)
@@ -653,12 +701,9 @@ def paged_kv_write(k_cache, v_cache, k_new, v_new, slots, layout=None, stream=No
         _check_rows_inside(v_cache, "v_cache", NB, Hkv, BS, D, strides)
         sp, sh, st = (int(x) for x in strides)
     dev = _one_device(k_new, v_new, slots, k_cache, v_cache)
-    # (the stride of a dimension of one element says nothing)
-    from_token = k_new.stride(0) if N > 1 else Hkv * D
-    from_head = k_new.stride(1) if Hkv > 1 else D
     _on(dev, lib.paged_kv_write, k_cache.data_ptr(), v_cache.data_ptr(), k_new.data_ptr(),
-        v_new.data_ptr(), slots.data_ptr(), N, Hkv, D, int(BS), int(NB), sp, sh, st, from_token,
-        from_head, stream=stream)
+        v_new.data_ptr(), slots.data_ptr(), N, Hkv, D, int(BS), int(NB), sp, sh, st, *src,
+        stream=stream)
 
 
 NOALLOC_SCRATCH_BYTES = 64 << 20  # PGD_NOALLOC_SCRATCH_BYTES of include/pgd.h

@@ -1475,6 +1475,155 @@ pgd_status run_write(uint16_t *k_cache, uint16_t *v_cache, const uint16_t *k_new
     return PGD_OK;
 }
 
+// ------------------------------------------------------------------ packed prompts
+// One of q, k, v of a packed batch: rows [total][heads][D] at any token and head
+// strides (halves), as a 4-D tensor.  Keys (box_heads 0): 64 halves x tokens x
+// D/64 slabs (128 bytes apart) x heads, a box being `box_tokens` tokens of
+// `box_slabs` slabs of one head, landing as [slab][token][128 B].  Queries: 64
+// halves x heads x tokens x slabs, a box being `box_heads` heads of
+// `box_tokens` tokens of one slab, landing as [token][head][128 B].
+pgd_status encode_packed_map(CUtensorMap *map, const void *base, int total, int heads, int D,
+                             long long token_stride, long long head_stride, int box_tokens,
+                             int box_slabs, int box_heads)
+{
+    EncodeTiledFn fn;
+    pgd_status st = encode_fn(&fn);
+    if (st)
+        return st;
+    const bool keys = box_heads == 0;
+    const cuuint64_t T = (cuuint64_t)total, H = (cuuint64_t)heads, L = (cuuint64_t)(D / 64);
+    const cuuint64_t ts = (cuuint64_t)token_stride * 2, hs = (cuuint64_t)head_stride * 2;
+    cuuint64_t dims[4] = {64, keys ? T : H, keys ? L : T, keys ? H : L};
+    cuuint64_t strides[3] = {keys ? ts : hs, keys ? 128 : ts, keys ? hs : 128};
+    cuuint32_t box[4] = {64, (cuuint32_t)(keys ? box_tokens : box_heads),
+                         (cuuint32_t)(keys ? box_slabs : box_tokens), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(PGD_ERR_CUDA, "cuTensorMapEncodeTiled (packed rows) failed (CUresult %d)", (int)r);
+    return PGD_OK;
+}
+
+struct PrefillPlan {
+    int G, TQ, span, max_tiles;
+    size_t ws_bytes;  // [256 B: tile count][tiles]
+};
+
+pgd_status make_prefill_plan(int S, int total, int Hq, int Hkv, int D, PrefillPlan *pp)
+{
+    if (S < 0 || total < 0)
+        return fail(PGD_ERR_INVALID_ARG, "num_seqs %d, total %d", S, total);
+    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0)
+        return fail(PGD_ERR_INVALID_ARG, "head counts %d / %d", Hq, Hkv);
+    if (Hq / Hkv > 128)
+        return fail(PGD_ERR_UNSUPPORTED, "GQA group of %d query heads exceeds 128", Hq / Hkv);
+    if (!supported_head_dim(D))
+        return fail(PGD_ERR_UNSUPPORTED, "head_dim %d not in {64, 128, 256}", D);
+    pp->G = Hq / Hkv;
+    pp->TQ = 128 / pp->G;
+    pp->span = D == 256 ? pp->TQ : 2 * pp->TQ;
+    // disjoint prompts: whole spans of all rows, and one begun per prompt
+    const long long tiles = (long long)total / pp->span + S;
+    if (tiles * Hkv >= (1ll << 30))
+        return fail(PGD_ERR_UNSUPPORTED, "%lld work units", tiles * Hkv);
+    pp->max_tiles = (int)tiles;
+    pp->ws_bytes = total && S ? 256 + align256((size_t)tiles * 16) : 0;
+    if (pp->ws_bytes > kMaxWorkspaceBytes)
+        return fail(PGD_ERR_WORKSPACE, "scratch of %zu bytes needed, above the %zu-byte cap",
+                    pp->ws_bytes, kMaxWorkspaceBytes);
+    return PGD_OK;
+}
+
+struct PackedStrides {
+    long long q_token, q_head, k_token, k_head, v_token, v_head;
+};
+
+pgd_status run_prefill(float *out, uint16_t *out_half, const uint16_t *q, const uint16_t *k,
+                       const uint16_t *v, const int32_t *cu_seqlens, float scale, int S, int total,
+                       int max_len, int Hq, int Hkv, int D, const PackedStrides &x,
+                       void *workspace, size_t ws_bytes, void *stream_v)
+{
+    PrefillPlan pp;
+    pgd_status st = make_prefill_plan(S, total, Hq, Hkv, D, &pp);
+    if (st)
+        return st;
+    if (max_len < 0)
+        return fail(PGD_ERR_INVALID_ARG, "max_len %d < 0", max_len);
+    for (long long s : {x.q_token, x.q_head, x.k_token, x.k_head, x.v_token, x.v_head})
+        if (s <= 0 || s % 8 != 0 || s >= (1ll << 39))
+            return fail(PGD_ERR_INVALID_ARG,
+                        "stride %lld: positive multiples of 8 halves below 2^39", s);
+    if (!std::isfinite(scale))
+        return fail(PGD_ERR_INVALID_ARG, "scale is not finite");
+    if (S == 0 || total == 0) {
+        t_last_error.clear();
+        return PGD_OK;
+    }
+    const void *dst = out_half ? static_cast<const void *>(out_half) : out;
+    if (!dst || !q || !k || !v || !cu_seqlens)
+        return fail(PGD_ERR_INVALID_ARG, "null array argument");
+    if (!aligned(dst, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(cu_seqlens, 4))
+        return fail(PGD_ERR_INVALID_ARG, "out, q, k and v must be 16-byte aligned, cu_seqlens 4");
+    char *ws = static_cast<char *>(workspace);
+    const bool own = workspace == nullptr;
+    if (!own && (ws_bytes < pp.ws_bytes || !aligned(ws, 256)))
+        return fail(PGD_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) given, %zu needed",
+                    ws_bytes, pp.ws_bytes);
+    DeviceState *ds;
+    if ((st = device_state(&ds)))
+        return st;
+    CUtensorMap tq, tk, tv;
+    const bool wide = D == 256;  // K by slabs of 128 keys, V by 32 keys of all slabs
+    if ((st = encode_packed_map(&tq, q, total, Hq, D, x.q_token, x.q_head, pp.TQ, 1, pp.G)) ||
+        (st = encode_packed_map(&tk, k, total, Hkv, D, x.k_token, x.k_head, 128, wide ? 1 : D / 64,
+                                0)) ||
+        (st = encode_packed_map(&tv, v, total, Hkv, D, x.v_token, x.v_head, wide ? 32 : 128, D / 64,
+                                0)))
+        return st;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    cudaError_t e;
+    if (own) {
+        cudaMemPool_t pool;
+        if ((st = device_pool(*ds, &pool)))
+            return st;
+        if ((e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), pp.ws_bytes, pool,
+                                         stream)) != cudaSuccess)
+            return cuda_fail(e, "scratch allocation");
+    }
+    PrefillParams p = {};
+    p.out = out;
+    p.out_half = reinterpret_cast<__half *>(out_half);
+    p.cu_seqlens = cu_seqlens;
+    p.num_tiles = reinterpret_cast<int *>(ws);
+    p.tiles = reinterpret_cast<int4 *>(ws + 256);
+    p.err = ds->err_word;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.S = S;
+    p.total = total;
+    p.max_len = max_len;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = pp.G;
+    p.TQ = pp.TQ;
+    p.span = pp.span;
+    p.max_tiles = pp.max_tiles;
+    p.wait_budget_ns = kWaitBudgetNs;
+    const int grid = (int)std::min<long long>(ds->num_sms, (long long)pp.max_tiles * Hkv);
+    e = launch_prefill(D, tq, tk, tv, p, grid, stream);
+    if (own) {
+        const cudaError_t e2 = cudaFreeAsync(ws, stream);
+        if (e == cudaSuccess)
+            e = e2;
+    }
+    if (e != cudaSuccess)
+        return cuda_fail(e, "kernel launch");
+    t_last_error.clear();
+    return PGD_OK;
+}
+
 // Runs a C entry's body: nothing it throws (an allocation of the host's that
 // failed) leaves the library.
 template <class F> pgd_status guarded(F &&body) noexcept
@@ -1813,6 +1962,43 @@ pgd_status pgd_tree_plan(int num_seqs, int total_q, int max_q_len, int num_q_hea
             *chosen_kv_partition = vp.PK;
         if (workspace_bytes)
             *workspace_bytes = vp.ws_bytes;
+        return PGD_OK;
+    });
+}
+
+pgd_status packed_gqa_prefill(void *out, int out_type, const uint16_t *q, const uint16_t *k,
+                              const uint16_t *v, const int32_t *cu_seqlens, float scale,
+                              int num_seqs, int total, int max_len, int num_q_heads,
+                              int num_kv_heads, int head_dim, int64_t q_token_stride,
+                              int64_t q_head_stride, int64_t k_token_stride,
+                              int64_t k_head_stride, int64_t v_token_stride,
+                              int64_t v_head_stride, void *workspace, size_t workspace_bytes,
+                              void *stream)
+{
+    return guarded([&]() -> pgd_status {
+        if (out_type != PGD_OUT_F32 && out_type != PGD_OUT_F16)
+            return fail(PGD_ERR_INVALID_ARG, "out_type %d: PGD_OUT_F32 or PGD_OUT_F16", out_type);
+        const bool half = out_type == PGD_OUT_F16;
+        return run_prefill(half ? nullptr : static_cast<float *>(out),
+                           half ? static_cast<uint16_t *>(out) : nullptr, q, k, v, cu_seqlens,
+                           scale, num_seqs, total, max_len, num_q_heads, num_kv_heads, head_dim,
+                           {q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+                            v_token_stride, v_head_stride},
+                           workspace, workspace_bytes, stream);
+    });
+}
+
+pgd_status pgd_prefill_plan(int num_seqs, int total, int num_q_heads, int num_kv_heads,
+                            int head_dim, size_t *workspace_bytes)
+{
+    return guarded([&]() -> pgd_status {
+        PrefillPlan pp;
+        const pgd_status st =
+            make_prefill_plan(num_seqs, total, num_q_heads, num_kv_heads, head_dim, &pp);
+        if (st)
+            return st;
+        if (workspace_bytes)
+            *workspace_bytes = pp.ws_bytes;
         return PGD_OK;
     });
 }

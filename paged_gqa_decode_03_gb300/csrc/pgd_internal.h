@@ -250,6 +250,27 @@ struct VarlenParams {
     __half *out_half;             // [total_q][Hq][D] the output as fp16, or null: `out` as fp32
 };
 
+// ---------------------------------------------------------------- packed prompts
+// Causal attention over whole packed prompts (pgd_prefill.cu).
+constexpr int kPrefillOrderKeys = 1024;  // stage counts the sort tells apart
+
+struct PrefillParams {
+    float *out;                   // [total][Hq][D], or null with
+    __half *out_half;             //   out_half, the output as fp16
+    const int32_t *cu_seqlens;    // [S + 1]
+    int4 *tiles;                  // scratch: [max_tiles], longest first
+    int *num_tiles;               // scratch
+    unsigned *err;
+    float scale_log2;
+    int S, total, max_len, Hq, Hkv, G;
+    int TQ, span;                 // tokens of a tile, and of a unit (one tile or a pair)
+    int max_tiles;
+    uint64_t wait_budget_ns;
+};
+cudaError_t launch_prefill(int head_dim, const CUtensorMap &tq, const CUtensorMap &tk,
+                           const CUtensorMap &tv, const PrefillParams &p, int grid,
+                           cudaStream_t stream);
+
 // ---------------------------------------------------------------- the step around the cache
 // Page tables, slots, positions and lengths of a step, and the writes of its
 // K and V rows (pgd_kv.cu).

@@ -1,0 +1,1000 @@
+// Causal attention over whole packed prompts whose K and V are still rows of
+// the projection's output, not yet pages of a cache (packed_gqa_prefill), on
+// the 5th-generation tensor cores.
+//
+// For query head h of KV head g = h / G and the token at position t of its
+// prompt, out = sum_{u <= t} p_u v_u / sum_u p_u with p_u = exp2(s_u - m), s_u =
+// q . k_u * scale * log2(e): one pass over the keys with a running maximum m
+// and sum.  A tile is 128 rows: TQ = 128 / G tokens x the G heads of one KV
+// head, so that every K and V byte serves the group.  Work is 4 D operations
+// per row and key on operands that come from L2 almost always: the tensor
+// cores are what bounds a long prompt.
+#include <algorithm>
+
+#include "pgd_device.cuh"
+#include "pgd_internal.h"
+
+namespace pgd {
+
+namespace {
+
+constexpr int kNT = 128;               // keys per stage
+constexpr int kSlab = 128 * 128;       // bytes of 128 rows of one 64-wide slab of head_dim
+
+// The tiles of a call in decreasing order of their stages (a counting sort):
+// {first row of q, position of that row, rows left in the prompt, first row of
+// the prompt} per tile (or pair of tiles) of `span` tokens, for every KV head
+// alike.  The CTAs of the attention kernel deal them out like cards, back and
+// forth, so the long ones are spread evenly and the short ones fill the end.
+__global__ void __launch_bounds__(kPrefillOrderKeys)
+    packed_prefill_order_kernel(const PrefillParams p)
+{
+    __shared__ int cnt[kPrefillOrderKeys];
+    __shared__ int warp_tot[kPrefillOrderKeys / 32];
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    cnt[t] = 0;
+    __syncthreads();
+    // calls f(key, i0, n, row0) for every tile, a warp per prompt
+    auto each = [&](auto &&f) {
+        for (int s = w; s < p.S; s += kPrefillOrderKeys / 32) {
+            const int row0 = __ldg(p.cu_seqlens + s);
+            const int n = __ldg(p.cu_seqlens + s + 1) - row0;
+            if (n < 0 || n > p.max_len || row0 < 0 || row0 > p.total - n) {
+                if (lane == 0)
+                    atomicOr(p.err, kErrQueryLen);
+                continue;
+            }
+            for (int i0 = lane * p.span; i0 < n; i0 += 32 * p.span)
+                f(min((min(i0 + p.span, n) + kNT - 1) / kNT, kPrefillOrderKeys - 1), i0, n, row0);
+        }
+    };
+    each([&](int key, int, int, int) { atomicAdd(&cnt[key], 1); });
+    __syncthreads();
+    // exclusive prefix sum over the keys from the largest down: thread t owns
+    // key kPrefillOrderKeys - 1 - t
+    const int k = kPrefillOrderKeys - 1 - t;
+    const int c = cnt[k];
+    int inc = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(~0u, inc, off);
+        if (lane >= off)
+            inc += y;
+    }
+    if (lane == 31)
+        warp_tot[w] = inc;
+    __syncthreads();
+    if (w == 0) {
+        const int own = warp_tot[lane];
+        int x = own;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(~0u, x, off);
+            if (lane >= off)
+                x += y;
+        }
+        warp_tot[lane] = x - own;
+        if (lane == 31) {
+            // prompts that overlap can have more tiles than the rows allow
+            if ((unsigned)x > (unsigned)p.max_tiles)
+                atomicOr(p.err, kErrQueryLen);
+            *p.num_tiles = max(0, min(x, p.max_tiles));
+        }
+    }
+    __syncthreads();
+    cnt[k] = warp_tot[w] + inc - c;
+    __syncthreads();
+    each([&](int key, int i0, int n, int row0) {
+        const int at = atomicAdd(&cnt[key], 1);
+        if ((unsigned)at < (unsigned)p.max_tiles)
+            p.tiles[at] = make_int4(row0 + i0, i0, n - i0, row0);
+    });
+}
+
+// Turn k of CTA b takes unit k * grid + b, every other turn in the opposite
+// direction.
+__device__ __forceinline__ int unit_of(int k)
+{
+    const int b = (int)blockIdx.x, grid = (int)gridDim.x;
+    return k * grid + ((k & 1) ? grid - 1 - b : b);
+}
+
+__device__ __forceinline__ void store_row8(const PrefillParams &p, size_t at, const float *v,
+                                           float inv)
+{
+    if (p.out_half) {
+        uint4 w;
+        w.x = pack_half2(v[0] * inv, v[1] * inv);
+        w.y = pack_half2(v[2] * inv, v[3] * inv);
+        w.z = pack_half2(v[4] * inv, v[5] * inv);
+        w.w = pack_half2(v[6] * inv, v[7] * inv);
+        *reinterpret_cast<uint4 *>(p.out_half + at) = w;
+    } else {
+        *reinterpret_cast<float4 *>(p.out + at) =
+            make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+        *reinterpret_cast<float4 *>(p.out + at + 4) =
+            make_float4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    }
+}
+
+}  // namespace
+
+// packed_prefill_pair_kernel<D> (head_dim 64, 128) — persistent, one CTA per
+// SM, each unit a pair of consecutive 128-row tiles A and B of one KV head that
+// share every K and V stage.
+//
+// Tensor memory (512 columns): O of A and B (2 D), P of A and B as fp16 (2 x
+// 64), and the scores: 128 columns a buffer.  At head_dim 128 that leaves ONE
+// score buffer for both tiles, and that is enough: a tile's softmax reads its
+// 128 scores into registers in one round trip (~300 cycles) and hands the
+// buffer back, long before its exponentials are done, and the tensor pipe has
+// a P V product (512 cycles) to do meanwhile.  So the pipe runs S_A(j+1),
+// P_A(j) V_j, S_B(j+1), P_B(j) V_j without a gap: S(j+1) does not wait for P(j)
+// V_j, nor P V for a softmax that has just begun — a tile's softmax (about
+// 1200 cycles) has the whole 2048-cycle period minus its own S.
+//   * warp 0, one thread: Q tiles, K and V stages by tensor copies (one per
+//     stage; K and V in rings of their own)
+//   * warp 1, one thread: the products
+//   * warps 4-7 / 8-11: softmax of tile A / B, a thread per row
+template <int D> struct PairShape;
+template <> struct PairShape<64> {
+    static constexpr int NK = 4, NV = 4, SBUF = 2;
+};
+template <> struct PairShape<128> {
+    static constexpr int NK = 2, NV = 3, SBUF = 1;
+};
+constexpr int kPairThreads = 384;
+
+template <int D> constexpr size_t pair_smem_bytes()
+{
+    return size_t(2) * 128 * D * 2 + size_t(PairShape<D>::NK + PairShape<D>::NV) * kNT * D * 2 + 1024;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    packed_prefill_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                               const __grid_constant__ CUtensorMap tmap_k,
+                               const __grid_constant__ CUtensorMap tmap_v, const PrefillParams p)
+{
+    constexpr int NK = PairShape<D>::NK, NV = PairShape<D>::NV, SBUF = PairShape<D>::SBUF;
+    constexpr int SLABS = D / 64;
+    constexpr int KV_TILE = kNT * D * 2;
+    constexpr int Q_TILE = 128 * D * 2;
+    constexpr uint32_t S_COL = 2 * D, P_COL = S_COL + SBUF * kNT;
+    static_assert(P_COL + 128 <= 512, "tensor memory");
+    constexpr uint32_t IDESC_S = tc_idesc_f16(128, kNT, 0, 0);
+    constexpr uint32_t IDESC_O = tc_idesc_f16(128, D, 0, 1);
+
+    extern __shared__ uint8_t dyn_smem[];
+    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV],
+        v_empty[NV], s_full[2], s_free[2], p_full[2], o_done[2], o_free[2], mma_done;
+    __shared__ uint32_t tmem_base_s;
+    __shared__ int abort_flag;
+
+    const uint32_t dyn_base = smem_addr(dyn_smem);
+    const uint32_t base = (dyn_base + 1023u) & ~1023u;
+    uint8_t *const base_ptr = dyn_smem + (base - dyn_base);
+    const uint32_t q_s = base, k_s = q_s + 2 * Q_TILE, v_s = k_s + NK * KV_TILE;
+    uint8_t *const v_ptr = base_ptr + 2 * Q_TILE + NK * KV_TILE;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&q_full), 1);
+        mbar_init(smem_addr(&q_empty), 1);
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(smem_addr(&k_full[i]), 1);
+            mbar_init(smem_addr(&k_empty[i]), 1);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(smem_addr(&v_full[i]), 1);
+            mbar_init(smem_addr(&v_empty[i]), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_addr(&s_full[x]), 1);
+            mbar_init(smem_addr(&s_free[x]), 4);
+            mbar_init(smem_addr(&p_full[x]), 4);
+            mbar_init(smem_addr(&o_done[x]), 1);
+            mbar_init(smem_addr(&o_free[x]), 4);
+        }
+        mbar_init(smem_addr(&mma_done), 1);
+        abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmap_q);
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
+    }
+    if (warp == 1)
+        tc_alloc(smem_addr(&tmem_base_s), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    griddep_wait();  // the list of tiles
+    const int units = *p.num_tiles * p.Hkv;
+    const int turns = (units + (int)gridDim.x - 1) / (int)gridDim.x;
+
+    auto give_up = [&]() {
+        if (!abort_flag)
+            atomicOr(p.err, kErrTimeout);
+        abort_flag = 1;
+    };
+    // stages of the two tiles of a unit: tile A holds tokens i0 .. i0+TQ-1 of
+    // the prompt, B the next TQ; left: the prompt's tokens from i0 on
+    auto stages = [&](const int4 &u, int x) {
+        const int from = x * p.TQ;
+        return u.z > from ? (u.y + min(u.z, from + p.TQ) + kNT - 1) / kNT : 0;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ======================================================== copies
+            const uint64_t pol = l2_evict_last_policy();
+            int nk = 0, nv = 0, nq = 0;   // copies issued so far
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, int parity) {
+                return mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns);
+            };
+            auto load_k = [&](int row, int g) {
+                const int st = nk % NK;
+                if (!wait(&k_empty[st], ((nk / NK) & 1) ^ 1))
+                    return false;
+                const uint32_t bar = smem_addr(&k_full[st]);
+                mbar_arrive_expect_tx(bar, KV_TILE);
+                tma_load_4d(k_s + st * KV_TILE, &tmap_k, 0, row, 0, g, bar, pol);
+                ++nk;
+                return true;
+            };
+            auto load_v = [&](int row, int g) {
+                const int st = nv % NV;
+                if (!wait(&v_empty[st], ((nv / NV) & 1) ^ 1))
+                    return false;
+                const uint32_t bar = smem_addr(&v_full[st]);
+                mbar_arrive_expect_tx(bar, KV_TILE);
+                tma_load_4d(v_s + st * KV_TILE, &tmap_v, 0, row, 0, g, bar, pol);
+                ++nv;
+                return true;
+            };
+            for (int k = 0; k < turns && ok; ++k) {
+                const int ui = unit_of(k);
+                if (ui >= units)
+                    continue;
+                const int4 u = __ldg(p.tiles + ui / p.Hkv);
+                const int g = ui % p.Hkv;
+                const int nt = max(stages(u, 0), stages(u, 1));
+                // the unit's first K goes out before its Q, whose place is
+                // free only after the last unit's last S
+                ok = load_k(u.w, g) && wait(&q_empty, (nq & 1) ^ 1);
+                if (!ok)
+                    break;
+                const int ntq = u.z > p.TQ ? 2 : 1;
+                const uint32_t bar = smem_addr(&q_full);
+                mbar_arrive_expect_tx(bar, ntq * SLABS * p.TQ * p.G * 128);
+                for (int x = 0; x < ntq; ++x)
+                    for (int sl = 0; sl < SLABS; ++sl)
+                        tma_load_4d(q_s + x * Q_TILE + sl * kSlab, &tmap_q, 0, g * p.G,
+                                    u.x + x * p.TQ, sl, bar);
+                ++nq;
+                ok = load_v(u.w, g);
+                for (int j = 1; j < nt && ok; ++j)
+                    ok = load_k(u.w + j * kNT, g) && load_v(u.w + j * kNT, g);
+            }
+            if (!ok) {
+                give_up();
+                // let the copies in flight land before the CTA exits
+                if (nq)
+                    mbar_wait_bounded(smem_addr(&q_full), (nq - 1) & 1, nullptr, p.wait_budget_ns);
+                for (int i = max(0, nk - NK); i < nk; ++i)
+                    mbar_wait_bounded(smem_addr(&k_full[i % NK]), (i / NK) & 1, nullptr,
+                                      p.wait_budget_ns);
+                for (int i = max(0, nv - NV); i < nv; ++i)
+                    mbar_wait_bounded(smem_addr(&v_full[i % NV]), (i / NV) & 1, nullptr,
+                                      p.wait_budget_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ======================================================== products
+            const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
+            const uint64_t k_desc = tc_sdesc(k_s, 16, 1024);
+            const uint64_t v_desc = tc_sdesc(v_s, kSlab, 1024);
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, int parity) {
+                if (ok && !mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns))
+                    ok = false;
+                return ok;
+            };
+            int nk = 0, nv = 0, nq = 0;              // K and V stages, Q pairs used up
+            int uses[2] = {0, 0};                    // of each score buffer
+            int np[2] = {0, 0}, no[2] = {0, 0};      // P V products, units of each tile
+            // S_x = Q_x K^T of K stage number ki
+            auto issue_s = [&](int x, int ki) {
+                const int b = SBUF == 2 ? x : 0;
+                if (!wait(&k_full[ki % NK], (ki / NK) & 1) ||
+                    (uses[b] && !wait(&s_free[b], (uses[b] - 1) & 1)))
+                    return;
+                ++uses[b];
+                tc_fence_after();
+                const uint64_t ks = k_desc + (((ki % NK) * KV_TILE) >> 4);
+                const uint64_t qx = q_desc + ((x * Q_TILE) >> 4);
+                const uint32_t d = tmem + S_COL + b * kNT;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma(d, qx + (((kk / 4) * kSlab + (kk % 4) * 32) >> 4),
+                           ks + (((kk / 4) * kSlab + (kk % 4) * 32) >> 4), IDESC_S, kk > 0);
+                tc_commit(smem_addr(&s_full[x]));
+            };
+            // O_x += P_x V of V stage number vi
+            auto issue_pv = [&](int x, int vi, bool first) {
+                if (!wait(&v_full[vi % NV], (vi / NV) & 1) || !wait(&p_full[x], np[x] & 1) ||
+                    (first && no[x] && !wait(&o_free[x], (no[x] - 1) & 1)))
+                    return;
+                ++np[x];
+                if (first)
+                    ++no[x];
+                tc_fence_after();
+                const uint64_t vs = v_desc + (((vi % NV) * KV_TILE) >> 4);
+                const uint32_t d = tmem + x * D, a = tmem + P_COL + x * 64;
+#pragma unroll
+                for (int kk = 0; kk < kNT / 16; ++kk)
+                    tc_mma_ta(d, a + kk * 8, vs + ((kk * 2048) >> 4), IDESC_O, !first || kk > 0);
+                tc_commit(smem_addr(&o_done[x]));
+            };
+            for (int k = 0; k < turns && ok; ++k) {
+                const int ui = unit_of(k);
+                if (ui >= units)
+                    continue;
+                const int4 u = __ldg(p.tiles + ui / p.Hkv);
+                const int nt[2] = {stages(u, 0), stages(u, 1)};
+                const int nmax = max(nt[0], nt[1]);
+                const int last = nt[1] > 0 ? 1 : 0;  // B's range contains A's: the last reader
+                if (!wait(&q_full, nq & 1))
+                    break;
+                ++nq;
+                for (int j = -1; j < nmax && ok; ++j) {
+                    for (int x = 0; x < 2; ++x) {
+                        if (j + 1 < nt[x]) {
+                            issue_s(x, nk + j + 1);
+                            if (x == last) {
+                                tc_commit(smem_addr(&k_empty[(nk + j + 1) % NK]));
+                                if (j + 2 == nmax)
+                                    tc_commit(smem_addr(&q_empty));
+                            }
+                        }
+                        if (j >= 0 && j < nt[x]) {
+                            issue_pv(x, nv + j, j == 0);
+                            if (x == last)
+                                tc_commit(smem_addr(&v_empty[(nv + j) % NV]));
+                        }
+                    }
+                }
+                nk += nmax;
+                nv += nmax;
+            }
+            if (!ok)
+                give_up();
+            // every product issued here has completed before the memory is freed
+            tc_commit(smem_addr(&mma_done));
+            mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ============================================================ softmax
+        const int x = (warp - 4) >> 2;
+        const int quarter = warp & 3;
+        const int r = 32 * quarter + lane;  // this thread's row of the tile
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
+        const uint32_t s_col = S_COL + (SBUF == 2 ? x : 0) * kNT, o_col = x * D,
+                       p_col = P_COL + x * 64;
+        uint64_t *const s_free_x = &s_free[SBUF == 2 ? x : 0];
+        const int ti = r / p.G, hj = r - ti * p.G;
+        // a scale of 0 runs as 1e-30: exp2 of every score is then 1 in fp32
+        // (the mean over the range, as for 0) while masked scores, infinite
+        // with the sign that scales to -inf, still give 0
+        const float sc = p.scale_log2 == 0.f ? 1e-30f : p.scale_log2;
+        const bool neg = sc < 0.f;
+        const float masked = neg ? INFINITY : -INFINITY;
+        const float2 sc2 = make_float2(sc, sc);
+        int ns = 0, nv = 0;  // S tiles of this tile, V stages of the CTA, so far
+        bool ok = true;
+        for (int k = 0; k < turns && ok; ++k) {
+            const int ui = unit_of(k);
+            if (ui >= units)
+                continue;
+            const int4 u = __ldg(p.tiles + ui / p.Hkv);
+            const int g = ui % p.Hkv;
+            const int nt0 = stages(u, 0), ntx = stages(u, x);
+            const int left = min(p.TQ, u.z - x * p.TQ);  // tokens of this tile
+            const int n = u.y + u.z;                     // tokens of the prompt
+            const bool row_ok = r < p.TQ * p.G && ti < left;
+            const int lim = row_ok ? u.y + x * p.TQ + ti : -1;  // this row's position
+            float m_ref = -INFINITY, l = 0.f;
+            for (int j = 0; j < ntx; ++j, ++ns) {
+                const int t0 = j * kNT;
+                // wait outcomes are warp-uniform: tensor-memory loads and
+                // stores are warp-collective
+                if (!__all_sync(~0u, mbar_wait_bounded(smem_addr(&s_full[x]), ns & 1, &abort_flag,
+                                                       p.wait_budget_ns))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float v[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tc_ld32(t_lane + s_col + 32 * c, v[c]);
+                tc_wait_ld();
+                // the scores are in registers: the buffer is the other tile's
+                tc_fence_before();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(s_free_x));
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tc_ld_ready(v[c]);
+                if (t0 + kNT - 1 > lim) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[c][i] = t0 + 32 * c + i > lim ? masked : v[c][i];
+                }
+                float ec[4];  // four independent chains of three-input extremes
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    ec[c] = masked;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        ec[c] = neg ? fmin3(ec[c], v[c][i], v[c][i + 1])
+                                    : fmax3(ec[c], v[c][i], v[c][i + 1]);
+                }
+                const float e = neg ? fmin3(ec[0], ec[1], fminf(ec[2], ec[3]))
+                                    : fmax3(ec[0], ec[1], fmaxf(ec[2], ec[3]));
+                const float mt = e == masked ? -INFINITY : e * sc;
+                // the reference maximum moves only by more than 8 (log2
+                // units): p stays below 2^8, well inside fp16, and O is
+                // rescaled rarely
+                bool rescale = false;
+                float alpha = 1.f;
+                if (mt > m_ref + 8.f) {
+                    rescale = m_ref != -INFINITY;
+                    alpha = rescale ? ex2(m_ref - mt) : 1.f;
+                    m_ref = mt;
+                }
+                const float off = m_ref == -INFINITY ? 0.f : -m_ref;
+                const float2 off2 = make_float2(off, off);
+                float2 sum2 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float2 a = ffma2(make_float2(v[2 * h + c][i], v[2 * h + c][i + 1]), sc2,
+                                             off2);
+                            a.x = ex2(a.x);
+                            a.y = ex2(a.y);
+                            pk[16 * c + i / 2] = pack_half2(a.x, a.y);
+                            sum2 = fadd2(sum2, a);
+                        }
+                    if (h == 0 && j > 0) {
+                        // this tile's last P V is done with P (and O may be rescaled)
+                        if (!__all_sync(~0u, mbar_wait_bounded(smem_addr(&o_done[x]), (ns - 1) & 1,
+                                                               &abort_flag, p.wait_budget_ns))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    tc_st32u(t_lane + p_col + 32 * h, pk);
+                }
+                if (!ok)
+                    break;
+                if (j > 0 && __any_sync(~0u, rescale)) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        float o[32];
+                        tc_ld32(t_lane + o_col + 32 * c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] *= alpha;
+                        tc_st32(t_lane + o_col + 32 * c, o);
+                    }
+                }
+                // rows of the stage behind the prompt belong to the next one
+                // and may hold anything: the first tile to use the stage
+                // zeroes them in V (their weights are 0, which does not hide
+                // a NaN)
+                const bool zero_v = t0 + kNT > n && (x == 0 || j >= nt0);
+                if (zero_v) {
+                    const int st = (nv + j) % NV;
+                    mbar_wait_bounded(smem_addr(&v_full[st]), ((nv + j) / NV) & 1, nullptr,
+                                      p.wait_budget_ns);
+                    uint8_t *vs = v_ptr + st * KV_TILE;
+                    const int za = n - t0;
+                    for (int idx = r; idx < (kNT - za) * SLABS * 8; idx += 128) {
+                        const int row = za + idx / (SLABS * 8), c = idx % (SLABS * 8);
+                        *reinterpret_cast<uint4 *>(vs + (c >> 3) * kSlab + row * 128 +
+                                                   (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                tc_wait_st();
+                if (zero_v)
+                    fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&p_full[x]));
+                l = l * alpha + (sum2.x + sum2.y);
+            }
+            // ---- out = O / l
+            if (ok && ntx > 0) {
+                ok = __all_sync(~0u, mbar_wait_bounded(smem_addr(&o_done[x]), (ns - 1) & 1,
+                                                       &abort_flag, p.wait_budget_ns));
+                if (ok) {
+                    tc_fence_after();
+                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    const size_t at =
+                        ((size_t)(u.x + x * p.TQ + ti) * p.Hq + (size_t)g * p.G + hj) * D;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        float o[32];
+                        tc_ld32(t_lane + o_col + 32 * c, o);
+                        tc_wait_ld();
+                        if (c == D / 32 - 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(smem_addr(&o_free[x]));
+                        }
+                        if (row_ok)
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8)
+                                store_row8(p, at + 32 * c + i, o + i, inv);
+                    }
+                }
+            }
+            nv += max(nt0, stages(u, 1));
+        }
+        if (!ok)
+            give_up();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+// packed_prefill_wide_kernel (head_dim 256) — persistent, one tile per unit: O
+// takes 256 tensor-memory columns, two score buffers the other 256 (P over the
+// scores it came from), so S(j+1) runs while the softmax works on S(j).  K and
+// V move in pieces of 16 KB, K by 64-wide slabs of its 128 keys, V by 32 keys of
+// all of head_dim, so that beside the 64 KB of Q nine of them fit and each is
+// free again after its own products: a stage's copies are never waited for as
+// a whole.  Eight softmax warps: rows r by halves of a stage's keys.
+constexpr int kWideThreads = 384;
+constexpr int kWideNK = 5, kWideNV = 4;  // pieces
+constexpr int kWideD = 256;
+constexpr size_t kWideSmem = size_t(4) * kSlab + size_t(kWideNK + kWideNV) * kSlab + 1024;
+
+__global__ void __launch_bounds__(kWideThreads, 1)
+    packed_prefill_wide_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                               const __grid_constant__ CUtensorMap tmap_k,
+                               const __grid_constant__ CUtensorMap tmap_v, const PrefillParams p)
+{
+    constexpr int D = kWideD, NK = kWideNK, NV = kWideNV, SLABS = 4, VP = 4;
+    constexpr int PIECE = kSlab, VKEYS = kNT / VP;
+    constexpr uint32_t S_COL = 256;
+    constexpr uint32_t IDESC_S = tc_idesc_f16(128, kNT, 0, 0);
+    constexpr uint32_t IDESC_O = tc_idesc_f16(128, D, 0, 1);
+
+    extern __shared__ uint8_t dyn_smem[];
+    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV],
+        v_empty[NV], s_full[2], p_full, o_done, o_free, mma_done;
+    __shared__ uint32_t tmem_base_s;
+    __shared__ int abort_flag;
+    __shared__ float pair_red[2][2][128];  // [parity][half][row]: the halves' exchange
+
+    const uint32_t dyn_base = smem_addr(dyn_smem);
+    const uint32_t base = (dyn_base + 1023u) & ~1023u;
+    uint8_t *const base_ptr = dyn_smem + (base - dyn_base);
+    const uint32_t q_s = base, k_s = q_s + SLABS * kSlab, v_s = k_s + NK * PIECE;
+    uint8_t *const v_ptr = base_ptr + SLABS * kSlab + NK * PIECE;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&q_full), 1);
+        mbar_init(smem_addr(&q_empty), 1);
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(smem_addr(&k_full[i]), 1);
+            mbar_init(smem_addr(&k_empty[i]), 1);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(smem_addr(&v_full[i]), 1);
+            mbar_init(smem_addr(&v_empty[i]), 1);
+        }
+        mbar_init(smem_addr(&s_full[0]), 1);
+        mbar_init(smem_addr(&s_full[1]), 1);
+        mbar_init(smem_addr(&p_full), 8);
+        mbar_init(smem_addr(&o_done), 1);
+        mbar_init(smem_addr(&o_free), 8);
+        mbar_init(smem_addr(&mma_done), 1);
+        abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmap_q);
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
+    }
+    if (warp == 1)
+        tc_alloc(smem_addr(&tmem_base_s), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    griddep_wait();  // the list of tiles
+    const int units = *p.num_tiles * p.Hkv;
+    const int turns = (units + (int)gridDim.x - 1) / (int)gridDim.x;
+
+    auto give_up = [&]() {
+        if (!abort_flag)
+            atomicOr(p.err, kErrTimeout);
+        abort_flag = 1;
+    };
+    auto stages = [&](const int4 &u) { return (u.y + min(u.z, p.TQ) + kNT - 1) / kNT; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ======================================================== copies
+            const uint64_t pol = l2_evict_last_policy();
+            int nk = 0, nv = 0, nq = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, int parity) {
+                return mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns);
+            };
+            auto load_k = [&](int row, int g, int slab) {
+                const int st = nk % NK;
+                if (!wait(&k_empty[st], ((nk / NK) & 1) ^ 1))
+                    return false;
+                const uint32_t bar = smem_addr(&k_full[st]);
+                mbar_arrive_expect_tx(bar, PIECE);
+                tma_load_4d(k_s + st * PIECE, &tmap_k, 0, row, slab, g, bar, pol);
+                ++nk;
+                return true;
+            };
+            auto load_v = [&](int row, int g) {
+                const int st = nv % NV;
+                if (!wait(&v_empty[st], ((nv / NV) & 1) ^ 1))
+                    return false;
+                const uint32_t bar = smem_addr(&v_full[st]);
+                mbar_arrive_expect_tx(bar, PIECE);
+                tma_load_4d(v_s + st * PIECE, &tmap_v, 0, row, 0, g, bar, pol);
+                ++nv;
+                return true;
+            };
+            for (int k = 0; k < turns && ok; ++k) {
+                const int ui = unit_of(k);
+                if (ui >= units)
+                    continue;
+                const int4 u = __ldg(p.tiles + ui / p.Hkv);
+                const int g = ui % p.Hkv, nt = stages(u);
+                for (int sl = 0; sl < SLABS && ok; ++sl)
+                    ok = load_k(u.w, g, sl);
+                ok = ok && wait(&q_empty, (nq & 1) ^ 1);
+                if (!ok)
+                    break;
+                const uint32_t bar = smem_addr(&q_full);
+                mbar_arrive_expect_tx(bar, SLABS * p.TQ * p.G * 128);
+                for (int sl = 0; sl < SLABS; ++sl)
+                    tma_load_4d(q_s + sl * kSlab, &tmap_q, 0, g * p.G, u.x, sl, bar);
+                ++nq;
+                // in the order of use: K of stage j + 1 before V of stage j
+                for (int j = 0; j < nt && ok; ++j) {
+                    for (int sl = 0; j + 1 < nt && sl < SLABS && ok; ++sl)
+                        ok = load_k(u.w + (j + 1) * kNT, g, sl);
+                    for (int i = 0; i < VP && ok; ++i)
+                        ok = load_v(u.w + j * kNT + i * VKEYS, g);
+                }
+            }
+            if (!ok) {
+                give_up();
+                if (nq)
+                    mbar_wait_bounded(smem_addr(&q_full), (nq - 1) & 1, nullptr, p.wait_budget_ns);
+                for (int i = max(0, nk - NK); i < nk; ++i)
+                    mbar_wait_bounded(smem_addr(&k_full[i % NK]), (i / NK) & 1, nullptr,
+                                      p.wait_budget_ns);
+                for (int i = max(0, nv - NV); i < nv; ++i)
+                    mbar_wait_bounded(smem_addr(&v_full[i % NV]), (i / NV) & 1, nullptr,
+                                      p.wait_budget_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ======================================================== products
+            const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
+            const uint64_t k_desc = tc_sdesc(k_s, 16, 1024);
+            const uint64_t v_desc = tc_sdesc(v_s, VKEYS * 128, 1024);
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, int parity) {
+                if (ok && !mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns))
+                    ok = false;
+                return ok;
+            };
+            int nk = 0, nv = 0, nq = 0, ns = 0, np = 0, no = 0;
+            auto issue_s = [&](bool last) {
+                const uint32_t d = tmem + S_COL + (ns & 1) * kNT;
+                for (int sl = 0; sl < SLABS; ++sl, ++nk) {
+                    const int st = nk % NK;
+                    if (!wait(&k_full[st], (nk / NK) & 1))
+                        return;
+                    tc_fence_after();
+                    const uint64_t ks = k_desc + ((st * PIECE) >> 4);
+                    const uint64_t qs = q_desc + ((sl * kSlab) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma(d, qs + ((kk * 32) >> 4), ks + ((kk * 32) >> 4), IDESC_S,
+                               sl > 0 || kk > 0);
+                    tc_commit(smem_addr(&k_empty[st]));
+                }
+                tc_commit(smem_addr(&s_full[ns & 1]));
+                if (last)
+                    tc_commit(smem_addr(&q_empty));
+                ++ns;
+            };
+            auto issue_pv = [&](bool first) {
+                if (!wait(&p_full, np & 1) || (first && no && !wait(&o_free, (no - 1) & 1)))
+                    return;
+                if (first)
+                    ++no;
+                const uint32_t a = tmem + S_COL + (np & 1) * kNT;
+                for (int i = 0; i < VP; ++i, ++nv) {
+                    const int st = nv % NV;
+                    if (!wait(&v_full[st], (nv / NV) & 1))
+                        return;
+                    tc_fence_after();
+                    const uint64_t vs = v_desc + ((st * PIECE) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < VKEYS / 16; ++kk)
+                        tc_mma_ta(tmem, a + (i * (VKEYS / 16) + kk) * 8, vs + ((kk * 2048) >> 4),
+                                  IDESC_O, !first || i > 0 || kk > 0);
+                    tc_commit(smem_addr(&v_empty[st]));
+                }
+                tc_commit(smem_addr(&o_done));
+                ++np;
+            };
+            for (int k = 0; k < turns && ok; ++k) {
+                const int ui = unit_of(k);
+                if (ui >= units)
+                    continue;
+                const int4 u = __ldg(p.tiles + ui / p.Hkv);
+                const int nt = stages(u);
+                if (!wait(&q_full, nq & 1))
+                    break;
+                ++nq;
+                for (int j = -1; j < nt && ok; ++j) {
+                    // S(j+1) takes the buffer of P(j-1), whose product was issued before
+                    if (j + 1 < nt)
+                        issue_s(j + 2 == nt);
+                    if (j >= 0 && ok)
+                        issue_pv(j == 0);
+                }
+            }
+            if (!ok)
+                give_up();
+            tc_commit(smem_addr(&mma_done));
+            mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ============================================================ softmax
+        constexpr int HC = kNT / 2, HD = D / 2;
+        const int quarter = warp & 3;
+        const int half = (warp - 4) >> 2;
+        const int r = 32 * quarter + lane;
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
+        const uint32_t pair_bar = 1 + quarter;
+        const int ti = r / p.G, hj = r - ti * p.G;
+        const float sc = p.scale_log2 == 0.f ? 1e-30f : p.scale_log2;
+        const bool neg = sc < 0.f;
+        const float masked = neg ? INFINITY : -INFINITY;
+        const float2 sc2 = make_float2(sc, sc);
+        int ns = 0, nv = 0;
+        bool ok = true;
+        // after a failed wait the loops keep running without doing work, so
+        // that the two warps of a pair meet at every named barrier
+        auto wait = [&](uint64_t *bar, int parity) {
+            if (ok && !__all_sync(~0u, mbar_wait_bounded(smem_addr(bar), parity, &abort_flag,
+                                                         p.wait_budget_ns))) {
+                ok = false;
+                give_up();
+            }
+        };
+        for (int k = 0; k < turns; ++k) {
+            const int ui = unit_of(k);
+            if (ui >= units)
+                continue;
+            const int4 u = __ldg(p.tiles + ui / p.Hkv);
+            const int g = ui % p.Hkv, nt = stages(u), n = u.y + u.z;
+            const bool row_ok = r < p.TQ * p.G && ti < min(p.TQ, u.z);
+            const int lim = row_ok ? u.y + ti : -1;
+            float m_ref = -INFINITY, l = 0.f;
+            for (int j = 0; j < nt; ++j, ++ns, nv += VP) {
+                const int t0 = j * kNT, c0 = t0 + half * HC;
+                const uint32_t s_col = S_COL + (ns & 1) * kNT;
+                wait(&s_full[ns & 1], (ns >> 1) & 1);
+                float v[2][32];
+                float e = masked;
+                if (ok) {
+                    tc_fence_after();
+                    tc_ld32(t_lane + s_col + half * HC, v[0]);
+                    tc_ld32(t_lane + s_col + half * HC + 32, v[1]);
+                    tc_wait_ld();
+                    tc_ld_ready(v[0]);
+                    tc_ld_ready(v[1]);
+                    if (c0 + HC - 1 > lim) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[c][i] = c0 + 32 * c + i > lim ? masked : v[c][i];
+                    }
+                    float ec[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        ec[c] = masked;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float a = v[c >> 1][16 * (c & 1) + i],
+                                        b = v[c >> 1][16 * (c & 1) + i + 1];
+                            ec[c] = neg ? fmin3(ec[c], a, b) : fmax3(ec[c], a, b);
+                        }
+                    }
+                    e = neg ? fmin3(ec[0], ec[1], fminf(ec[2], ec[3]))
+                            : fmax3(ec[0], ec[1], fmaxf(ec[2], ec[3]));
+                }
+                pair_red[ns & 1][half][r] = e;
+                tc_fence_before();
+                named_barrier_sync(pair_bar, 64);
+                tc_fence_after();
+                const float e2 = pair_red[ns & 1][half ^ 1][r];
+                if (!ok)
+                    continue;
+                e = neg ? fminf(e, e2) : fmaxf(e, e2);
+                const float mt = e == masked ? -INFINITY : e * sc;
+                bool rescale = false;
+                float alpha = 1.f;
+                if (mt > m_ref + 8.f) {
+                    rescale = m_ref != -INFINITY;
+                    alpha = rescale ? ex2(m_ref - mt) : 1.f;
+                    m_ref = mt;
+                }
+                const float off = m_ref == -INFINITY ? 0.f : -m_ref;
+                const float2 off2 = make_float2(off, off);
+                float2 sum2 = make_float2(0.f, 0.f);
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float2 a = ffma2(make_float2(v[c][i], v[c][i + 1]), sc2, off2);
+                        a.x = ex2(a.x);
+                        a.y = ex2(a.y);
+                        pk[16 * c + i / 2] = pack_half2(a.x, a.y);
+                        sum2 = fadd2(sum2, a);
+                    }
+                l = l * alpha + (sum2.x + sum2.y);
+                // both halves have read their scores (the barrier above): P over them
+                tc_st32u(t_lane + s_col + half * 32, pk);
+                if (j > 0) {
+                    wait(&o_done, (ns - 1) & 1);  // O may be rescaled
+                    if (!ok)
+                        continue;
+                    tc_fence_after();
+                    if (__any_sync(~0u, rescale)) {
+#pragma unroll 1
+                        for (int c = 0; c < HD / 32; ++c) {
+                            float o[32];
+                            tc_ld32(t_lane + half * HD + 32 * c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] *= alpha;
+                            tc_st32(t_lane + half * HD + 32 * c, o);
+                        }
+                    }
+                }
+                const bool zero_v = t0 + kNT > n;
+                if (zero_v) {
+                    const int za = n - t0;  // first key behind the prompt
+                    for (int i = za / VKEYS; i < VP; ++i)
+                        mbar_wait_bounded(smem_addr(&v_full[(nv + i) % NV]), ((nv + i) / NV) & 1,
+                                          nullptr, p.wait_budget_ns);
+                    for (int idx = half * 128 + r; idx < (kNT - za) * SLABS * 8; idx += 256) {
+                        const int key = za + idx / (SLABS * 8), c = idx % (SLABS * 8);
+                        const int st = (nv + key / VKEYS) % NV, row = key % VKEYS;
+                        *reinterpret_cast<uint4 *>(v_ptr + st * PIECE + (c >> 3) * (VKEYS * 128) +
+                                                   row * 128 + (c & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                }
+                tc_wait_st();
+                if (zero_v)
+                    fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&p_full));
+            }
+            wait(&o_done, (ns - 1) & 1);
+            // the row's exp-sum from both halves, then each half writes its columns
+            // (through the last stage's slot: its readers are done, since o_done
+            // came after every warp's p_full, and the next stage takes the other)
+            pair_red[(ns & 1) ^ 1][half][r] = l;
+            named_barrier_sync(pair_bar, 64);
+            const float lt = l + pair_red[(ns & 1) ^ 1][half ^ 1][r];
+            if (!ok)
+                continue;
+            tc_fence_after();
+            const float inv = lt > 0.f ? 1.f / lt : 0.f;
+            const size_t at =
+                ((size_t)(u.x + ti) * p.Hq + (size_t)g * p.G + hj) * D + half * HD;
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+                float o[32];
+                tc_ld32(t_lane + half * HD + 32 * c, o);
+                tc_wait_ld();
+                if (c == HD / 32 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&o_free));
+                }
+                if (row_ok)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        store_row8(p, at + 32 * c + i, o + i, inv);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+cudaError_t launch_prefill(int head_dim, const CUtensorMap &tq, const CUtensorMap &tk,
+                           const CUtensorMap &tv, const PrefillParams &p, int grid,
+                           cudaStream_t stream)
+{
+    auto kernel = head_dim == 64    ? packed_prefill_pair_kernel<64>
+                  : head_dim == 128 ? packed_prefill_pair_kernel<128>
+                                    : packed_prefill_wide_kernel;
+    const size_t smem = head_dim == 64    ? pair_smem_bytes<64>()
+                        : head_dim == 128 ? pair_smem_bytes<128>()
+                                          : kWideSmem;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess)
+        return e;
+    packed_prefill_order_kernel<<<1, kPrefillOrderKeys, 0, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess)
+        return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(head_dim == 256 ? kWideThreads : kPairThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, p);
+}
+
+}  // namespace pgd

@@ -45,15 +45,6 @@
 
 namespace pgd {
 
-// L2 policy for data that other CTAs read again soon: kept ahead of the
-// other lines (the tile pairs of one sequence and KV head read the same pages)
-__device__ __forceinline__ uint64_t l2_evict_last_policy()
-{
-    uint64_t pol;
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
-    return pol;
-}
-
 // Ancestor bits of the nodes of one tree: bit j of row i is set where node i
 // sees node j (its ancestors and itself).  Rows of nine words: the ninth stays
 // zero for the funnel shift, and the odd stride spreads the rows over the banks.

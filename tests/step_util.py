@@ -24,26 +24,21 @@ def attention(q, k, v, seen, scale):
     """softmax(q k^T scale) v over ``seen``: q [n, H, D], k, v [L, Hkv, D] (any
     float type), seen bool [n, L].  Returns (out, A), float64 [n, H, D]; a row
     that sees nothing is zero."""
-    q, k, v = (np.asarray(x.detach().cpu() if isinstance(x, torch.Tensor) else x)
-               .astype(np.float64) for x in (q, k, v))
-    seen = np.asarray(seen)
+    dev = q.device
+    q, k, v = (x.detach().double() for x in (q, k, v))
+    seen = torch.as_tensor(seen, device=dev)
     n, H, D = q.shape
-    Hkv = k.shape[1]
-    out = np.zeros((n, H, D))
-    A = np.zeros((n, H, D))
-    for i in range(n):
-        at = np.flatnonzero(seen[i])
-        if at.size == 0:
-            continue
-        for g in range(Hkv):
-            kg, vg = k[at, g], v[at, g]
-            rows = q[i, g * (H // Hkv):(g + 1) * (H // Hkv)]
-            z = rows @ kg.T * scale
-            w = np.exp(z - z.max(axis=1, keepdims=True))
-            w /= w.sum(axis=1, keepdims=True)
-            out[i, g * (H // Hkv):(g + 1) * (H // Hkv)] = w @ vg
-            A[i, g * (H // Hkv):(g + 1) * (H // Hkv)] = w @ np.abs(vg)
-    return out, A
+    G = H // k.shape[1]
+    out = torch.zeros((n, H, D), dtype=torch.float64, device=dev)
+    A = torch.zeros_like(out)
+    empty = ~seen.any(1)
+    for h in range(H):
+        z = (q[:, h] @ k[:, h // G].T * scale).masked_fill(~seen, -torch.inf)
+        w = torch.exp(z - z.amax(1, keepdim=True).masked_fill(empty[:, None], 0.0))
+        w = w / w.sum(1, keepdim=True).masked_fill(empty[:, None], 1.0)
+        out[:, h] = w @ v[:, h // G]
+        A[:, h] = w @ v[:, h // G].abs()
+    return out.cpu().numpy(), A.cpu().numpy()
 
 
 def bound(out, A, L, D, vmax, half, scale=None):
