@@ -18,6 +18,16 @@ namespace pgd {
 
 namespace {
 
+// Registers per thread of a warpgroup (its four warps together).
+template <int N> __device__ __forceinline__ void regs_give()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_take()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 constexpr int kNT = 128;               // keys per stage
 constexpr int kSlab = 128 * 128;       // bytes of 128 rows of one 64-wide slab of head_dim
 
@@ -119,6 +129,32 @@ __device__ __forceinline__ void store_row8(const PrefillParams &p, size_t at, co
 
 }  // namespace
 
+// The largest (smallest, for a negative scale) of a row's 128 scores: four
+// independent chains of three-input extremes.  The sign is the call's, so it is
+// a branch around either loop: a choice per element would triple the work.
+__device__ __forceinline__ float extreme128(const float (&v)[4][32], bool least)
+{
+    float e[4];
+    if (!least) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            e[c] = fmaxf(v[c][0], v[c][1]);
+#pragma unroll
+            for (int i = 2; i < 32; i += 2)
+                e[c] = fmax3(e[c], v[c][i], v[c][i + 1]);
+        }
+        return fmax3(e[0], e[1], fmaxf(e[2], e[3]));
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        e[c] = fminf(v[c][0], v[c][1]);
+#pragma unroll
+        for (int i = 2; i < 32; i += 2)
+            e[c] = fmin3(e[c], v[c][i], v[c][i + 1]);
+    }
+    return fmin3(e[0], e[1], fminf(e[2], e[3]));
+}
+
 // packed_prefill_pair_kernel<D> (head_dim 64, 128) — persistent, one CTA per
 // SM, each unit a pair of consecutive 128-row tiles A and B of one KV head that
 // share every K and V stage.
@@ -134,7 +170,11 @@ __device__ __forceinline__ void store_row8(const PrefillParams &p, size_t at, co
 // 1200 cycles) has the whole 2048-cycle period minus its own S.
 //   * warp 0, one thread: Q tiles, K and V stages by tensor copies (one per
 //     stage; K and V in rings of their own)
-//   * warp 1, one thread: the products
+//   * warp 1, one thread: the scores; warp 2, one thread: the outputs.  The pipe
+//     queues only a few products and a thread spends about 70 cycles on each
+//     barrier it tests, so one thread for both kept the pipe idle half the
+//     time (a period of 4150 cycles; a thread per tile: 3300, S_A(j+1)'s wait
+//     for the buffer holding up P_A(j) V_j).
 //   * warps 4-7 / 8-11: softmax of tile A / B, a thread per row
 template <int D> struct PairShape;
 template <> struct PairShape<64> {
@@ -170,6 +210,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         v_empty[NV], s_full[2], s_free[2], p_full[2], o_done[2], o_free[2], mma_done;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag;
+    __shared__ volatile int s_issued[2];  // S products issued for each tile
 
     const uint32_t dyn_base = smem_addr(dyn_smem);
     const uint32_t base = (dyn_base + 1023u) & ~1023u;
@@ -196,7 +237,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(smem_addr(&o_done[x]), 1);
             mbar_init(smem_addr(&o_free[x]), 4);
         }
-        mbar_init(smem_addr(&mma_done), 1);
+        mbar_init(smem_addr(&mma_done), 2);
+        s_issued[0] = s_issued[1] = 0;
         abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tmap_q);
@@ -225,7 +267,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         return u.z > from ? (u.y + min(u.z, from + p.TQ) + kNT - 1) / kNT : 0;
     };
 
-    if (warp == 0) {
+    // the softmax warps hold a row's 128 scores and half of its weights: they
+    // take registers that the copying and issuing warps do not need (128 x 80 +
+    // 256 x 208 of the 384 x 168 of the launch)
+    if (warp < 4) {
+      regs_give<80>();
+      if (warp == 0) {
         if (lane == 0) {
             // ======================================================== copies
             const uint64_t pol = l2_evict_last_policy();
@@ -292,11 +339,64 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+      } else if (warp == 1) {
         if (lane == 0) {
-            // ======================================================== products
+            // ======================================================== scores
             const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
             const uint64_t k_desc = tc_sdesc(k_s, 16, 1024);
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, int parity) {
+                if (ok && !mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns))
+                    ok = false;
+                return ok;
+            };
+            int nk = 0, nq = 0;        // K stages, Q pairs used up
+            int uses[2] = {0, 0};      // of each score buffer
+            int ns[2] = {0, 0};        // S products of each tile
+            for (int k = 0; k < turns && ok; ++k) {
+                const int ui = unit_of(k);
+                if (ui >= units)
+                    continue;
+                const int4 u = __ldg(p.tiles + ui / p.Hkv);
+                const int nt0 = stages(u, 0), nt1 = stages(u, 1), nmax = max(nt0, nt1);
+                wait(&q_full, nq & 1);
+                ++nq;
+                for (int j = 0; j < nmax && ok; ++j, ++nk) {
+                    const int st = nk % NK;
+                    wait(&k_full[st], (nk / NK) & 1);
+                    const uint64_t ks = k_desc + ((st * KV_TILE) >> 4);
+                    for (int x = 0; x < 2; ++x) {
+                        if (j >= (x ? nt1 : nt0))
+                            continue;
+                        // the buffer's last scores have been read
+                        const int b = SBUF == 2 ? x : 0;
+                        if (uses[b] && !wait(&s_free[b], (uses[b] - 1) & 1))
+                            break;
+                        ++uses[b];
+                        tc_fence_after();
+                        const uint64_t qx = q_desc + ((x * Q_TILE) >> 4);
+                        const uint32_t d = tmem + S_COL + b * kNT;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc_mma(d, qx + (((kk / 4) * kSlab + (kk % 4) * 32) >> 4),
+                                   ks + (((kk / 4) * kSlab + (kk % 4) * 32) >> 4), IDESC_S, kk > 0);
+                        tc_commit(smem_addr(&s_full[x]));
+                        s_issued[x] = ++ns[x];
+                    }
+                    tc_commit(smem_addr(&k_empty[st]));
+                }
+                tc_commit(smem_addr(&q_empty));
+            }
+            if (!ok)
+                give_up();
+            // every product issued has completed before the memory is freed
+            tc_commit(smem_addr(&mma_done));
+            mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
+        }
+        __syncwarp();
+      } else if (warp == 2) {
+        if (lane == 0) {
+            // ======================================================== outputs
             const uint64_t v_desc = tc_sdesc(v_s, kSlab, 1024);
             bool ok = true;
             auto wait = [&](uint64_t *bar, int parity) {
@@ -304,81 +404,54 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     ok = false;
                 return ok;
             };
-            int nk = 0, nv = 0, nq = 0;              // K and V stages, Q pairs used up
-            int uses[2] = {0, 0};                    // of each score buffer
-            int np[2] = {0, 0}, no[2] = {0, 0};      // P V products, units of each tile
-            // S_x = Q_x K^T of K stage number ki
-            auto issue_s = [&](int x, int ki) {
-                const int b = SBUF == 2 ? x : 0;
-                if (!wait(&k_full[ki % NK], (ki / NK) & 1) ||
-                    (uses[b] && !wait(&s_free[b], (uses[b] - 1) & 1)))
-                    return;
-                ++uses[b];
-                tc_fence_after();
-                const uint64_t ks = k_desc + (((ki % NK) * KV_TILE) >> 4);
-                const uint64_t qx = q_desc + ((x * Q_TILE) >> 4);
-                const uint32_t d = tmem + S_COL + b * kNT;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma(d, qx + (((kk / 4) * kSlab + (kk % 4) * 32) >> 4),
-                           ks + (((kk / 4) * kSlab + (kk % 4) * 32) >> 4), IDESC_S, kk > 0);
-                tc_commit(smem_addr(&s_full[x]));
-            };
-            // O_x += P_x V of V stage number vi
-            auto issue_pv = [&](int x, int vi, bool first) {
-                if (!wait(&v_full[vi % NV], (vi / NV) & 1) || !wait(&p_full[x], np[x] & 1) ||
-                    (first && no[x] && !wait(&o_free[x], (no[x] - 1) & 1)))
-                    return;
-                ++np[x];
-                if (first)
-                    ++no[x];
-                tc_fence_after();
-                const uint64_t vs = v_desc + (((vi % NV) * KV_TILE) >> 4);
-                const uint32_t d = tmem + x * D, a = tmem + P_COL + x * 64;
-#pragma unroll
-                for (int kk = 0; kk < kNT / 16; ++kk)
-                    tc_mma_ta(d, a + kk * 8, vs + ((kk * 2048) >> 4), IDESC_O, !first || kk > 0);
-                tc_commit(smem_addr(&o_done[x]));
-            };
+            int nv = 0;                           // V stages used up
+            int np[2] = {0, 0}, no[2] = {0, 0};   // P V products, units of each tile
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
                 if (ui >= units)
                     continue;
                 const int4 u = __ldg(p.tiles + ui / p.Hkv);
-                const int nt[2] = {stages(u, 0), stages(u, 1)};
-                const int nmax = max(nt[0], nt[1]);
-                const int last = nt[1] > 0 ? 1 : 0;  // B's range contains A's: the last reader
-                if (!wait(&q_full, nq & 1))
-                    break;
-                ++nq;
-                for (int j = -1; j < nmax && ok; ++j) {
+                const int nt0 = stages(u, 0), nt1 = stages(u, 1), nmax = max(nt0, nt1);
+                for (int j = 0; j < nmax && ok; ++j, ++nv) {
+                    const int st = nv % NV;
+                    wait(&v_full[st], (nv / NV) & 1);
+                    const uint64_t vs = v_desc + ((st * KV_TILE) >> 4);
                     for (int x = 0; x < 2; ++x) {
-                        if (j + 1 < nt[x]) {
-                            issue_s(x, nk + j + 1);
-                            if (x == last) {
-                                tc_commit(smem_addr(&k_empty[(nk + j + 1) % NK]));
-                                if (j + 2 == nmax)
-                                    tc_commit(smem_addr(&q_empty));
-                            }
-                        }
-                        if (j >= 0 && j < nt[x]) {
-                            issue_pv(x, nv + j, j == 0);
-                            if (x == last)
-                                tc_commit(smem_addr(&v_empty[(nv + j) % NV]));
-                        }
+                        if (j >= (x ? nt1 : nt0))
+                            continue;
+                        // the last unit's output has been read
+                        if (j == 0 && no[x]++ && !wait(&o_free[x], no[x] & 1))
+                            break;
+                        if (!wait(&p_full[x], np[x] & 1))
+                            break;
+                        ++np[x];
+                        // let the tile's next scores go first: they are on the
+                        // path that sets the period, this product is not.  Only
+                        // a matter of order, so the look is short and goes on
+                        // either way.
+                        if (j + 1 < (x ? nt1 : nt0))
+                            for (int i = 0; i < 16 && s_issued[x] <= np[x]; ++i)
+                                ;
+                        tc_fence_after();
+                        const uint32_t o = tmem + x * D, a = tmem + P_COL + x * 64;
+#pragma unroll
+                        for (int kk = 0; kk < kNT / 16; ++kk)
+                            tc_mma_ta(o, a + kk * 8, vs + ((kk * 2048) >> 4), IDESC_O,
+                                      j > 0 || kk > 0);
+                        tc_commit(smem_addr(&o_done[x]));
                     }
+                    tc_commit(smem_addr(&v_empty[st]));
                 }
-                nk += nmax;
-                nv += nmax;
             }
             if (!ok)
                 give_up();
-            // every product issued here has completed before the memory is freed
             tc_commit(smem_addr(&mma_done));
             mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
         }
         __syncwarp();
-    } else if (warp >= 4) {
+      }
+    } else {
+        regs_take<208>();
         // ============================================================ softmax
         const int x = (warp - 4) >> 2;
         const int quarter = warp & 3;
@@ -386,7 +459,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t s_col = S_COL + (SBUF == 2 ? x : 0) * kNT, o_col = x * D,
                        p_col = P_COL + x * 64;
-        uint64_t *const s_free_x = &s_free[SBUF == 2 ? x : 0];
         const int ti = r / p.G, hj = r - ti * p.G;
         // a scale of 0 runs as 1e-30: exp2 of every score is then 1 in fp32
         // (the mean over the range, as for 0) while masked scores, infinite
@@ -403,7 +475,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 continue;
             const int4 u = __ldg(p.tiles + ui / p.Hkv);
             const int g = ui % p.Hkv;
-            const int nt0 = stages(u, 0), ntx = stages(u, x);
+            const int nt0 = stages(u, 0), nt1 = stages(u, 1), ntx = x ? nt1 : nt0;
             const int left = min(p.TQ, u.z - x * p.TQ);  // tokens of this tile
             const int n = u.y + u.z;                     // tokens of the prompt
             const bool row_ok = r < p.TQ * p.G && ti < left;
@@ -424,10 +496,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 for (int c = 0; c < 4; ++c)
                     tc_ld32(t_lane + s_col + 32 * c, v[c]);
                 tc_wait_ld();
-                // the scores are in registers: the buffer is the other tile's
+                // the scores are in registers: the buffer takes the next ones
                 tc_fence_before();
                 if (lane == 0)
-                    mbar_arrive(smem_addr(s_free_x));
+                    mbar_arrive(smem_addr(&s_free[SBUF == 2 ? x : 0]));
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     tc_ld_ready(v[c]);
@@ -438,17 +510,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         for (int i = 0; i < 32; ++i)
                             v[c][i] = t0 + 32 * c + i > lim ? masked : v[c][i];
                 }
-                float ec[4];  // four independent chains of three-input extremes
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    ec[c] = masked;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        ec[c] = neg ? fmin3(ec[c], v[c][i], v[c][i + 1])
-                                    : fmax3(ec[c], v[c][i], v[c][i + 1]);
-                }
-                const float e = neg ? fmin3(ec[0], ec[1], fminf(ec[2], ec[3]))
-                                    : fmax3(ec[0], ec[1], fmaxf(ec[2], ec[3]));
+                // has this tile's last P V ended?  (asked here, used below)
+                const bool pv_over =
+                    j == 0 || mbar_try_wait(smem_addr(&o_done[x]), (ns - 1) & 1);
+                const float e = extreme128(v, neg);
                 const float mt = e == masked ? -INFINITY : e * sc;
                 // the reference maximum moves only by more than 8 (log2
                 // units): p stays below 2^8, well inside fp16, and O is
@@ -479,7 +544,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         }
                     if (h == 0 && j > 0) {
                         // this tile's last P V is done with P (and O may be rescaled)
-                        if (!__all_sync(~0u, mbar_wait_bounded(smem_addr(&o_done[x]), (ns - 1) & 1,
+                        if (!__all_sync(~0u, pv_over) &&
+                            !__all_sync(~0u, mbar_wait_bounded(smem_addr(&o_done[x]), (ns - 1) & 1,
                                                                &abort_flag, p.wait_budget_ns))) {
                             ok = false;
                             break;
@@ -503,10 +569,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                 }
                 // rows of the stage behind the prompt belong to the next one
-                // and may hold anything: the first tile to use the stage
-                // zeroes them in V (their weights are 0, which does not hide
-                // a NaN)
-                const bool zero_v = t0 + kNT > n && (x == 0 || j >= nt0);
+                // and may hold anything: zero them in V (their weights are 0,
+                // which does not hide a NaN).  Each tile does so before its own
+                // product; the other's writes the same zeros.
+                const bool zero_v = t0 + kNT > n;
                 if (zero_v) {
                     const int st = (nv + j) % NV;
                     mbar_wait_bounded(smem_addr(&v_full[st]), ((nv + j) / NV) & 1, nullptr,
@@ -555,7 +621,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                 }
             }
-            nv += max(nt0, stages(u, 1));
+            nv += max(nt0, nt1);
         }
         if (!ok)
             give_up();
