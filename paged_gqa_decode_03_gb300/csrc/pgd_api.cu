@@ -1610,6 +1610,7 @@ pgd_status run_prefill(float *out, uint16_t *out_half, const uint16_t *q, const 
     p.TQ = pp.TQ;
     p.span = pp.span;
     p.max_tiles = pp.max_tiles;
+    p.wide_rows = aligned(dst, 32);
     p.wait_budget_ns = kWaitBudgetNs;
     const int grid = (int)std::min<long long>(ds->num_sms, (long long)pp.max_tiles * Hkv);
     e = launch_prefill(D, tq, tk, tv, p, grid, stream);

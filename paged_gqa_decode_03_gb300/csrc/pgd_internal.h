@@ -265,6 +265,7 @@ struct PrefillParams {
     int S, total, max_len, Hq, Hkv, G;
     int TQ, span;                 // tokens of a tile, and of a unit (one tile or a pair)
     int max_tiles;
+    bool wide_rows;               // the output starts on a 32-byte border
     uint64_t wait_budget_ns;
 };
 cudaError_t launch_prefill(int head_dim, const CUtensorMap &tq, const CUtensorMap &tk,

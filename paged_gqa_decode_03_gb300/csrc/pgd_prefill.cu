@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kPrefillOrderKeys)
     __shared__ int cnt[kPrefillOrderKeys];
     __shared__ int warp_tot[kPrefillOrderKeys / 32];
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    griddep_launch_dependents();  // their set-up may pass meanwhile
     cnt[t] = 0;
     __syncthreads();
     // calls f(key, i0, n, row0) for every tile, a warp per prompt
@@ -109,25 +110,132 @@ __device__ __forceinline__ int unit_of(int k)
     return k * grid + ((k & 1) ? grid - 1 - b : b);
 }
 
-__device__ __forceinline__ void store_row8(const PrefillParams &p, size_t at, const float *v,
-                                           float inv)
+__device__ __forceinline__ int4 tile_of(const PrefillParams &p, int k, int units)
 {
+    const int ui = unit_of(k);
+    return ui < units ? __ldg(p.tiles + ui / p.Hkv) : make_int4(0, 0, 0, 0);
+}
+
+// Rows of the output from the registers of a warp: lane r holds 32 words (fp32
+// values, or pairs of fp16) of row r.  Written as they are, every store would
+// touch 32 rows, a line each; so each four lanes first exchange eight-word
+// pieces (a 4 x 4 transpose by two butterflies), after which the four hold one
+// row's 128 bytes, of four rows in turn, and a store touches 8 lines.
+struct RowOut {
+    char *at[4];   // where rows 4 * (lane / 4) + 0 .. 3 of the warp begin, or null
+};
+
+__device__ __forceinline__ void store_words(const RowOut &o, uint32_t (&w)[32], int byte, int lane,
+                                            bool wide)
+{
+    const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {  // pieces (0, 1) and (2, 3) with lane ^ 1
+            const uint32_t got =
+                __shfl_xor_sync(~0u, odd ? w[8 * q + i] : w[8 * (q + 1) + i], 1);
+            w[8 * q + i] = odd ? got : w[8 * q + i];
+            w[8 * (q + 1) + i] = odd ? w[8 * (q + 1) + i] : got;
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {     // pieces (0, 2) and (1, 3) with lane ^ 2
+            const uint32_t got =
+                __shfl_xor_sync(~0u, high ? w[8 * q + i] : w[8 * (q + 2) + i], 2);
+            w[8 * q + i] = high ? got : w[8 * q + i];
+            w[8 * (q + 2) + i] = high ? w[8 * (q + 2) + i] : got;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (o.at[q]) {
+            char *dst = o.at[q] + byte + 32 * (lane & 3);
+            if (wide) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
+                             "r"(w[8 * q]), "r"(w[8 * q + 1]), "r"(w[8 * q + 2]), "r"(w[8 * q + 3]),
+                             "r"(w[8 * q + 4]), "r"(w[8 * q + 5]), "r"(w[8 * q + 6]),
+                             "r"(w[8 * q + 7])
+                             : "memory");
+            } else {  // an output that starts on 16 bytes only
+                *reinterpret_cast<uint4 *>(dst) =
+                    make_uint4(w[8 * q], w[8 * q + 1], w[8 * q + 2], w[8 * q + 3]);
+                *reinterpret_cast<uint4 *>(dst + 16) =
+                    make_uint4(w[8 * q + 4], w[8 * q + 5], w[8 * q + 6], w[8 * q + 7]);
+            }
+        }
+}
+
+// COLS columns of O from tensor memory (from column `col` of the tile's O on,
+// at `taddr`), scaled by the row's 1 / l, to the output; `last` runs once
+// the last value has been read.
+template <int COLS, class F>
+__device__ __forceinline__ void write_rows(const PrefillParams &p, const RowOut &o, uint32_t taddr,
+                                           int col, float inv, int lane, F &&last)
+{
+    float v[32];
+    uint32_t w[32];
     if (p.out_half) {
-        uint4 w;
-        w.x = pack_half2(v[0] * inv, v[1] * inv);
-        w.y = pack_half2(v[2] * inv, v[3] * inv);
-        w.z = pack_half2(v[4] * inv, v[5] * inv);
-        w.w = pack_half2(v[6] * inv, v[7] * inv);
-        *reinterpret_cast<uint4 *>(p.out_half + at) = w;
+#pragma unroll 1
+        for (int c = 0; c < COLS; c += 64) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                tc_ld32(taddr + c + 32 * h, v);
+                tc_wait_ld();
+                tc_ld_ready(v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    w[16 * h + i] = pack_half2(v[2 * i] * inv, v[2 * i + 1] * inv);
+            }
+            if (c + 64 == COLS)
+                last();
+            store_words(o, w, (col + c) * 2, lane, p.wide_rows);
+        }
     } else {
-        *reinterpret_cast<float4 *>(p.out + at) =
-            make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-        *reinterpret_cast<float4 *>(p.out + at + 4) =
-            make_float4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+#pragma unroll 1
+        for (int c = 0; c < COLS; c += 32) {
+            tc_ld32(taddr + c, v);
+            tc_wait_ld();
+            tc_ld_ready(v);
+            if (c + 32 == COLS)
+                last();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                w[i] = __float_as_uint(v[i] * inv);
+            store_words(o, w, (col + c) * 4, lane, p.wide_rows);
+        }
     }
 }
 
+// The rows of a warp's quarter of a tile whose first token is row `token` of
+// the output; `left`: the tile's tokens.
+__device__ __forceinline__ RowOut rows_out(const PrefillParams &p, int token, int left, int g,
+                                           int quarter, int lane, int D)
+{
+    RowOut o;
+    char *base = p.out_half ? reinterpret_cast<char *>(p.out_half) : reinterpret_cast<char *>(p.out);
+    const int size = p.out_half ? 2 : 4;
+    int r = 32 * quarter + (lane & ~3);
+    int ti = r / p.G, h = r - ti * p.G;
+#pragma unroll
+    for (int q = 0; q < 4; ++q, ++r) {
+        o.at[q] = r < p.TQ * p.G && ti < left
+                      ? base + (((size_t)(token + ti) * p.Hq + (size_t)g * p.G + h) * D) * size
+                      : nullptr;
+        if (++h == p.G) {
+            h = 0;
+            ++ti;
+        }
+    }
+    return o;
+}
+
 }  // namespace
+
+// The lowest n bits (none for n <= 0, all 32 for n >= 32).
+__device__ __forceinline__ uint32_t first_bits(int n)
+{
+    return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+}
 
 // The largest (smallest, for a negative scale) of a row's 128 scores: four
 // independent chains of three-input extremes.  The sign is the call's, so it is
@@ -301,11 +409,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 ++nv;
                 return true;
             };
+            int4 next = tile_of(p, 0, units);
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
+                const int4 u = next;
+                next = tile_of(p, k + 1, units);
                 if (ui >= units)
                     continue;
-                const int4 u = __ldg(p.tiles + ui / p.Hkv);
                 const int g = ui % p.Hkv;
                 const int nt = max(stages(u, 0), stages(u, 1));
                 // the unit's first K goes out before its Q, whose place is
@@ -353,11 +463,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int nk = 0, nq = 0;        // K stages, Q pairs used up
             int uses[2] = {0, 0};      // of each score buffer
             int ns[2] = {0, 0};        // S products of each tile
+            int4 next = tile_of(p, 0, units);
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
+                const int4 u = next;
+                next = tile_of(p, k + 1, units);
                 if (ui >= units)
                     continue;
-                const int4 u = __ldg(p.tiles + ui / p.Hkv);
                 const int nt0 = stages(u, 0), nt1 = stages(u, 1), nmax = max(nt0, nt1);
                 wait(&q_full, nq & 1);
                 ++nq;
@@ -406,11 +518,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             };
             int nv = 0;                           // V stages used up
             int np[2] = {0, 0}, no[2] = {0, 0};   // P V products, units of each tile
+            int4 next = tile_of(p, 0, units);
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
+                const int4 u = next;
+                next = tile_of(p, k + 1, units);
                 if (ui >= units)
                     continue;
-                const int4 u = __ldg(p.tiles + ui / p.Hkv);
                 const int nt0 = stages(u, 0), nt1 = stages(u, 1), nmax = max(nt0, nt1);
                 for (int j = 0; j < nmax && ok; ++j, ++nv) {
                     const int st = nv % NV;
@@ -459,7 +573,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t s_col = S_COL + (SBUF == 2 ? x : 0) * kNT, o_col = x * D,
                        p_col = P_COL + x * 64;
-        const int ti = r / p.G, hj = r - ti * p.G;
+        const int ti = r / p.G;
         // a scale of 0 runs as 1e-30: exp2 of every score is then 1 in fp32
         // (the mean over the range, as for 0) while masked scores, infinite
         // with the sign that scales to -inf, still give 0
@@ -469,17 +583,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const float2 sc2 = make_float2(sc, sc);
         int ns = 0, nv = 0;  // S tiles of this tile, V stages of the CTA, so far
         bool ok = true;
+        int4 next = tile_of(p, 0, units);
         for (int k = 0; k < turns && ok; ++k) {
             const int ui = unit_of(k);
+            const int4 u = next;
+            next = tile_of(p, k + 1, units);  // a turn ahead: its latency passes meanwhile
             if (ui >= units)
                 continue;
-            const int4 u = __ldg(p.tiles + ui / p.Hkv);
             const int g = ui % p.Hkv;
             const int nt0 = stages(u, 0), nt1 = stages(u, 1), ntx = x ? nt1 : nt0;
             const int left = min(p.TQ, u.z - x * p.TQ);  // tokens of this tile
             const int n = u.y + u.z;                     // tokens of the prompt
             const bool row_ok = r < p.TQ * p.G && ti < left;
-            const int lim = row_ok ? u.y + x * p.TQ + ti : -1;  // this row's position
+            const int lo = u.y + x * p.TQ;          // position of the tile's first token
+            const int lim = row_ok ? lo + ti : -1;  // and of this row's
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < ntx; ++j, ++ns) {
                 const int t0 = j * kNT;
@@ -503,12 +620,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     tc_ld_ready(v[c]);
-                if (t0 + kNT - 1 > lim) {
+                // where the causal border crosses this stage: 32 keys at a time
+                if (t0 + kNT - 1 > lo) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
+                        if (t0 + 32 * c + 31 > lo) {
+                            const uint32_t seen = first_bits(lim + 1 - (t0 + 32 * c));
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[c][i] = t0 + 32 * c + i > lim ? masked : v[c][i];
+                            for (int i = 0; i < 32; ++i)
+                                v[c][i] = (seen >> i) & 1u ? v[c][i] : masked;
+                        }
                 }
                 // has this tile's last P V ended?  (asked here, used below)
                 const bool pv_over =
@@ -521,7 +642,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 bool rescale = false;
                 float alpha = 1.f;
                 if (mt > m_ref + 8.f) {
-                    rescale = m_ref != -INFINITY;
+                    rescale = row_ok && m_ref != -INFINITY;
                     alpha = rescale ? ex2(m_ref - mt) : 1.f;
                     m_ref = mt;
                 }
@@ -532,7 +653,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 for (int h = 0; h < 2; ++h) {
                     uint32_t pk[32];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             float2 a = ffma2(make_float2(v[2 * h + c][i], v[2 * h + c][i + 1]), sc2,
@@ -542,6 +663,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             pk[16 * c + i / 2] = pack_half2(a.x, a.y);
                             sum2 = fadd2(sum2, a);
                         }
+                    }
                     if (h == 0 && j > 0) {
                         // this tile's last P V is done with P (and O may be rescaled)
                         if (!__all_sync(~0u, pv_over) &&
@@ -601,24 +723,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (ok) {
                     tc_fence_after();
                     const float inv = l > 0.f ? 1.f / l : 0.f;
-                    const size_t at =
-                        ((size_t)(u.x + x * p.TQ + ti) * p.Hq + (size_t)g * p.G + hj) * D;
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        tc_ld32(t_lane + o_col + 32 * c, o);
-                        tc_wait_ld();
-                        if (c == D / 32 - 1) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive(smem_addr(&o_free[x]));
-                        }
-                        if (row_ok)
-#pragma unroll
-                            for (int i = 0; i < 32; i += 8)
-                                store_row8(p, at + 32 * c + i, o + i, inv);
-                    }
+                    const RowOut rows = rows_out(p, u.x + x * p.TQ, left, g, quarter, lane, D);
+                    write_rows<D>(p, rows, t_lane + o_col, 0, inv, lane, [&] {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_addr(&o_free[x]));
+                    });
                 }
             }
             nv += max(nt0, nt1);
@@ -740,11 +851,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 ++nv;
                 return true;
             };
+            int4 next = tile_of(p, 0, units);
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
+                const int4 u = next;
+                next = tile_of(p, k + 1, units);
                 if (ui >= units)
                     continue;
-                const int4 u = __ldg(p.tiles + ui / p.Hkv);
                 const int g = ui % p.Hkv, nt = stages(u);
                 for (int sl = 0; sl < SLABS && ok; ++sl)
                     ok = load_k(u.w, g, sl);
@@ -831,11 +944,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 tc_commit(smem_addr(&o_done));
                 ++np;
             };
+            int4 next = tile_of(p, 0, units);
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
+                const int4 u = next;
+                next = tile_of(p, k + 1, units);
                 if (ui >= units)
                     continue;
-                const int4 u = __ldg(p.tiles + ui / p.Hkv);
                 const int nt = stages(u);
                 if (!wait(&q_full, nq & 1))
                     break;
@@ -862,7 +977,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int r = 32 * quarter + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t pair_bar = 1 + quarter;
-        const int ti = r / p.G, hj = r - ti * p.G;
+        const int ti = r / p.G;
         const float sc = p.scale_log2 == 0.f ? 1e-30f : p.scale_log2;
         const bool neg = sc < 0.f;
         const float masked = neg ? INFINITY : -INFINITY;
@@ -878,11 +993,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 give_up();
             }
         };
+        int4 next = tile_of(p, 0, units);
         for (int k = 0; k < turns; ++k) {
             const int ui = unit_of(k);
+            const int4 u = next;
+            next = tile_of(p, k + 1, units);
             if (ui >= units)
                 continue;
-            const int4 u = __ldg(p.tiles + ui / p.Hkv);
             const int g = ui % p.Hkv, nt = stages(u), n = u.y + u.z;
             const bool row_ok = r < p.TQ * p.G && ti < min(p.TQ, u.z);
             const int lim = row_ok ? u.y + ti : -1;
@@ -1005,24 +1122,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 continue;
             tc_fence_after();
             const float inv = lt > 0.f ? 1.f / lt : 0.f;
-            const size_t at =
-                ((size_t)(u.x + ti) * p.Hq + (size_t)g * p.G + hj) * D + half * HD;
-#pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
-                float o[32];
-                tc_ld32(t_lane + half * HD + 32 * c, o);
-                tc_wait_ld();
-                if (c == HD / 32 - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(smem_addr(&o_free));
-                }
-                if (row_ok)
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        store_row8(p, at + 32 * c + i, o + i, inv);
-            }
+            const RowOut rows = rows_out(p, u.x, min(p.TQ, u.z), g, quarter, lane, D);
+            write_rows<HD>(p, rows, t_lane + half * HD, half * HD, inv, lane, [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&o_free));
+            });
         }
     }
     tc_fence_before();
