@@ -499,24 +499,55 @@ def paged_kv_quantize(codes, meta, src, slots, stream=None) -> None:
     _raise(st)
 
 
-def _one_device(*tensors):
-    """The device all of a call's tensors are on (the launch goes there)."""
-    dev = tensors[0].device
+# The step's calls below are a few microseconds of GPU work each, so their
+# argument checks are written to cost little where all is well: one expression
+# of cheap attribute reads, and the checks that name the culprit only when
+# that is false.
+_F16, _I32 = torch.float16, torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _fits(t, dtype, ndim):
+    return t.dtype is dtype and t.is_cuda and t.dim() == ndim and t.is_contiguous()
+
+
+def _check_all(*specs):
+    """Raises for the first (tensor, name, dtype, ndim) that does not fit;
+    None passes where the name ends in "?"."""
+    for t, name, dtype, ndim in specs:
+        if t is not None or not name.endswith("?"):
+            _check(t, name.rstrip("?"), dtype, ndim)
+
+
+def _one_device(index, *tensors):
+    """All of a call's tensors are on the CUDA device ``index`` (the launch goes there)."""
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    return dev
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on CUDA devices {index} and {t.get_device()}")
 
 
-def _on(dev, fn, *args, stream=None):
-    """Calls the library with ``dev`` as the current device."""
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, _stream_handle(stream, dev))
+def _on(index, fn, *args, stream=None):
+    """Calls the library with CUDA device ``index`` as the current one."""
+    if stream is None and _raw_stream is not None:
+        handle = _raw_stream(index)
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream_handle(stream, dev))
+        handle = _stream_handle(stream, index)
+    if index == torch.cuda.current_device():
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, handle)
     if st:
         _raise(st)
+
+
+def _workspace(workspace):
+    """(pointer, bytes) of an optional workspace."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _out_type(out):
@@ -534,23 +565,23 @@ def paged_gqa_tree(out, q, cu_seqlens_q, parents, k_cache, v_cache, block_tables
     TREE_MAX_NODES), but row i sees the tokens before the tree, its ancestors
     by ``parents`` (int32 [total_q]: an earlier node of the same tree, or
     negative for none) and itself.  ``out`` is float32 or float16."""
-    lib = load_library()
+    lib = _lib or load_library()
     kind = _out_type(out)
-    _check(q, "q", torch.float16, 3)
-    _check(out, "out", out.dtype, 3)
-    _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
-    _check(parents, "parents", torch.int32, 1)
-    _check(block_tables, "block_tables", torch.int32, 2)
-    _check(seq_lens, "seq_lens", torch.int32, 1)
+    if not (_fits(q, _F16, 3) and _fits(out, out.dtype, 3) and _fits(cu_seqlens_q, _I32, 1)
+            and _fits(parents, _I32, 1) and _fits(block_tables, _I32, 2)
+            and _fits(seq_lens, _I32, 1)):
+        _check_all((q, "q", _F16, 3), (out, "out", out.dtype, 3),
+                   (cu_seqlens_q, "cu_seqlens_q", _I32, 1), (parents, "parents", _I32, 1),
+                   (block_tables, "block_tables", _I32, 2), (seq_lens, "seq_lens", _I32, 1))
     T, Hq, D = q.shape
-    S = seq_lens.shape[0]
-    if (out.shape != q.shape or cu_seqlens_q.shape[0] != S + 1 or block_tables.shape[0] != S
-            or parents.shape[0] != T):
+    S, MB = block_tables.shape
+    if (out.shape != q.shape or cu_seqlens_q.size(0) != S + 1 or seq_lens.size(0) != S
+            or parents.size(0) != T):
         raise ValueError("inconsistent shapes of q, out, cu_seqlens_q, parents, block_tables, "
                          "seq_lens")
     if layout is None:
-        _check(k_cache, "k_cache", torch.float16, 4)
-        _check(v_cache, "v_cache", torch.float16, 4)
+        if not (_fits(k_cache, _F16, 4) and _fits(v_cache, _F16, 4)):
+            _check_all((k_cache, "k_cache", _F16, 4), (v_cache, "v_cache", _F16, 4))
         NB, Hkv, BS, D2 = k_cache.shape
         if v_cache.shape != k_cache.shape or D2 != D:
             raise ValueError("k_cache / v_cache shapes")
@@ -560,18 +591,14 @@ def paged_gqa_tree(out, q, cu_seqlens_q, parents, k_cache, v_cache, block_tables
         _check_rows_inside(k_cache, "k_cache", NB, Hkv, BS, D, strides)
         _check_rows_inside(v_cache, "v_cache", NB, Hkv, BS, D, strides)
         sp, sh, st = (int(x) for x in strides)
-    ws_bytes = 0
-    if workspace is not None:
-        if not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    dev = _one_device(q, out, cu_seqlens_q, parents, k_cache, v_cache, block_tables, seq_lens,
-                      workspace)
+    ws, ws_bytes = _workspace(workspace)
+    dev = q.get_device()
+    _one_device(dev, out, cu_seqlens_q, parents, k_cache, v_cache, block_tables, seq_lens,
+                workspace)
     _on(dev, lib.paged_gqa_tree, out.data_ptr(), kind, q.data_ptr(), cu_seqlens_q.data_ptr(),
         parents.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-        seq_lens.data_ptr(), float(scale), S, T, int(max_q_len), Hq, int(Hkv), D, int(BS),
-        block_tables.shape[1], int(NB), sp, sh, st, int(kv_partition),
-        workspace.data_ptr() if workspace is not None else None, ws_bytes, stream=stream)
+        seq_lens.data_ptr(), float(scale), S, T, int(max_q_len), Hq, int(Hkv), D, int(BS), MB,
+        int(NB), sp, sh, st, int(kv_partition), ws, ws_bytes, stream=stream)
 
 
 def pgd_tree_plan(num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
@@ -589,13 +616,14 @@ def pgd_tree_plan(num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, head_
 def _packed_strides(t, name):
     """(token, head) strides of rows [tokens, heads, head_dim] of contiguous
     head_dim (the stride of a dimension of one element says nothing)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float16 or not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or t.dtype is not _F16 or not t.is_cuda:
         raise TypeError(f"{name} must be a float16 CUDA tensor")
-    if t.dim() != 3 or t.stride(2) != 1:
+    strides = t.stride()
+    if len(strides) != 3 or strides[2] != 1:
         raise ValueError(f"{name} must have 3 dimensions and contiguous rows of head_dim")
     T, H, D = t.shape
-    head = t.stride(1) if H > 1 else D
-    return (t.stride(0) if T > 1 else H * head), head
+    head = strides[1] if H > 1 else D
+    return (strides[0] if T > 1 else H * head), head
 
 
 def packed_gqa_prefill(out, q, k, v, cu_seqlens, scale, max_len: int, workspace=None,
@@ -604,26 +632,24 @@ def packed_gqa_prefill(out, q, k, v, cu_seqlens, scale, max_len: int, workspace=
     cu_seqlens[s+1]-1 of q [total, Hq, D] and k, v [total, Hkv, D], fp16 with
     contiguous rows of head_dim and any token and head strides) into ``out``
     (contiguous [total, Hq, D], float16 or float32)."""
-    lib = load_library()
+    lib = _lib or load_library()
     kind = _out_type(out)
-    _check(out, "out", out.dtype, 3)
-    _check(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    if not (_fits(out, out.dtype, 3) and _fits(cu_seqlens, _I32, 1)):
+        _check_all((out, "out", out.dtype, 3), (cu_seqlens, "cu_seqlens", _I32, 1))
     qs, ks, vs = _packed_strides(q, "q"), _packed_strides(k, "k"), _packed_strides(v, "v")
     T, Hq, D = q.shape
-    if out.shape != q.shape or k.shape[0] != T or k.shape[2] != D or v.shape != k.shape:
+    T2, Hkv, D2 = k.shape
+    if out.shape != q.shape or T2 != T or D2 != D or v.shape != k.shape:
         raise ValueError("inconsistent shapes of out, q, k, v")
-    if cu_seqlens.shape[0] < 1:
+    S = cu_seqlens.size(0) - 1
+    if S < 0:
         raise ValueError("cu_seqlens holds num_seqs + 1 values")
-    ws_bytes = 0
-    if workspace is not None:
-        if not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    dev = _one_device(q, out, k, v, cu_seqlens, workspace)
+    ws, ws_bytes = _workspace(workspace)
+    dev = q.get_device()
+    _one_device(dev, out, k, v, cu_seqlens, workspace)
     _on(dev, lib.packed_gqa_prefill, out.data_ptr(), kind, q.data_ptr(), k.data_ptr(),
-        v.data_ptr(), cu_seqlens.data_ptr(), float(scale), cu_seqlens.shape[0] - 1, T,
-        int(max_len), Hq, k.shape[1], D, *qs, *ks, *vs,
-        workspace.data_ptr() if workspace is not None else None, ws_bytes, stream=stream)
+        v.data_ptr(), cu_seqlens.data_ptr(), float(scale), S, T, int(max_len), Hq, Hkv, D, *qs,
+        *ks, *vs, ws, ws_bytes, stream=stream)
 
 
 def pgd_prefill_plan(num_seqs, total, num_q_heads, num_kv_heads, head_dim) -> int:
@@ -644,31 +670,36 @@ def paged_kv_slots(slots, cu_seqlens_q, seq_lens, free_end, block_tables, contex
     entered in ``block_tables``; ``cu_seqlens_q``, ``seq_lens``, ``free_end``
     (int32 [1]), ``slots`` and ``positions`` (int32 [rows], or None) are
     written, with -1 in the rows behind the last request."""
-    lib = load_library()
-    for t, name in ((slots, "slots"), (cu_seqlens_q, "cu_seqlens_q"), (seq_lens, "seq_lens"),
-                    (free_end, "free_end"), (context_lens, "context_lens"),
-                    (query_lens, "query_lens"), (free_pages, "free_pages"),
-                    (free_start, "free_start"), (positions, "positions")):
-        if t is not None or name not in ("free_start", "positions"):
-            _check(t, name, torch.int32, 1)
-    _check(block_tables, "block_tables", torch.int32, 2)
-    S, N = context_lens.shape[0], slots.shape[0]
-    if (query_lens.shape[0] != S or seq_lens.shape[0] != S or block_tables.shape[0] != S
-            or cu_seqlens_q.shape[0] != S + 1):
+    lib = _lib or load_library()
+    if not (_fits(slots, _I32, 1) and _fits(cu_seqlens_q, _I32, 1) and _fits(seq_lens, _I32, 1)
+            and _fits(free_end, _I32, 1) and _fits(context_lens, _I32, 1)
+            and _fits(query_lens, _I32, 1) and _fits(free_pages, _I32, 1)
+            and _fits(block_tables, _I32, 2) and (free_start is None or _fits(free_start, _I32, 1))
+            and (positions is None or _fits(positions, _I32, 1))):
+        _check_all((slots, "slots", _I32, 1), (cu_seqlens_q, "cu_seqlens_q", _I32, 1),
+                   (seq_lens, "seq_lens", _I32, 1), (free_end, "free_end", _I32, 1),
+                   (context_lens, "context_lens", _I32, 1), (query_lens, "query_lens", _I32, 1),
+                   (free_pages, "free_pages", _I32, 1), (block_tables, "block_tables", _I32, 2),
+                   (free_start, "free_start?", _I32, 1), (positions, "positions?", _I32, 1))
+    S, MB = block_tables.shape
+    N = slots.size(0)
+    if (context_lens.size(0) != S or query_lens.size(0) != S or seq_lens.size(0) != S
+            or cu_seqlens_q.size(0) != S + 1):
         raise ValueError("inconsistent shapes of context_lens, query_lens, seq_lens, "
                          "cu_seqlens_q, block_tables")
-    if positions is not None and positions.shape[0] != N:
+    if positions is not None and positions.size(0) != N:
         raise ValueError("positions must have a value per slot")
-    if free_end.shape[0] != 1 or (free_start is not None and free_start.shape[0] != 1):
+    if free_end.size(0) != 1 or (free_start is not None and free_start.size(0) != 1):
         raise ValueError("free_start and free_end hold one value")
-    dev = _one_device(slots, cu_seqlens_q, seq_lens, free_end, block_tables, context_lens,
-                      query_lens, free_pages, free_start, positions)
+    dev = slots.get_device()
+    _one_device(dev, cu_seqlens_q, seq_lens, free_end, block_tables, context_lens, query_lens,
+                free_pages, free_start, positions)
     _on(dev, lib.paged_kv_slots, slots.data_ptr(),
-        positions.data_ptr() if positions is not None else None, cu_seqlens_q.data_ptr(),
+        None if positions is None else positions.data_ptr(), cu_seqlens_q.data_ptr(),
         seq_lens.data_ptr(), free_end.data_ptr(), block_tables.data_ptr(),
         context_lens.data_ptr(), query_lens.data_ptr(), free_pages.data_ptr(),
-        free_start.data_ptr() if free_start is not None else None, S, N, free_pages.shape[0],
-        int(block_size), block_tables.shape[1], int(num_blocks), stream=stream)
+        None if free_start is None else free_start.data_ptr(), S, N, free_pages.size(0),
+        int(block_size), MB, int(num_blocks), stream=stream)
 
 
 def paged_kv_write(k_cache, v_cache, k_new, v_new, slots, layout=None, stream=None) -> None:
@@ -678,17 +709,18 @@ def paged_kv_write(k_cache, v_cache, k_new, v_new, slots, layout=None, stream=No
     block_size + row (int32 [N], distinct; negative: skipped).  Caches
     head-major [NB, Hkv, BS, D], or any tensors with ``layout =
     (num_kv_heads, block_size, num_blocks, strides)``."""
-    lib = load_library()
+    lib = _lib or load_library()
     src = _packed_strides(k_new, "k_new")
     if _packed_strides(v_new, "v_new") != src:
         raise ValueError("k_new and v_new must have the same strides")
-    _check(slots, "slots", torch.int32, 1)
+    if not _fits(slots, _I32, 1):
+        _check(slots, "slots", _I32, 1)
     N, Hkv, D = k_new.shape
-    if v_new.shape != k_new.shape or slots.shape[0] != N:
+    if v_new.shape != k_new.shape or slots.size(0) != N:
         raise ValueError("k_new and v_new must have the same shape, and a slot per row")
     if layout is None:
-        _check(k_cache, "k_cache", torch.float16, 4)
-        _check(v_cache, "v_cache", torch.float16, 4)
+        if not (_fits(k_cache, _F16, 4) and _fits(v_cache, _F16, 4)):
+            _check_all((k_cache, "k_cache", _F16, 4), (v_cache, "v_cache", _F16, 4))
         NB, H2, BS, D2 = k_cache.shape
         if v_cache.shape != k_cache.shape or D2 != D or H2 != Hkv:
             raise ValueError("inconsistent shapes of k_cache, v_cache, k_new")
@@ -700,7 +732,8 @@ def paged_kv_write(k_cache, v_cache, k_new, v_new, slots, layout=None, stream=No
         _check_rows_inside(k_cache, "k_cache", NB, Hkv, BS, D, strides)
         _check_rows_inside(v_cache, "v_cache", NB, Hkv, BS, D, strides)
         sp, sh, st = (int(x) for x in strides)
-    dev = _one_device(k_new, v_new, slots, k_cache, v_cache)
+    dev = slots.get_device()
+    _one_device(dev, k_new, v_new, k_cache, v_cache)
     _on(dev, lib.paged_kv_write, k_cache.data_ptr(), v_cache.data_ptr(), k_new.data_ptr(),
         v_new.data_ptr(), slots.data_ptr(), N, Hkv, D, int(BS), int(NB), sp, sh, st, *src,
         stream=stream)
