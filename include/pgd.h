@@ -478,11 +478,11 @@ pgd_status pgd_varlen_plan(int num_seqs, int total_q, int max_q_len, int num_q_h
 /*
  * paged_gqa_tree — attention of trees of drafted tokens over the paged cache:
  * the verification step of speculative decoding with more than one
- * continuation per sequence.  Arguments, layouts, scratch and checks are those
- * of paged_gqa_varlen (one row of q per drafted token, K and V of all of them
- * already in the cache as the sequence's newest n_s tokens, in row order); what
- * a row sees is not every earlier token but the tokens before the tree, its
- * ancestors and itself:
+ * continuation per sequence.  Arguments, layouts and checks are those of
+ * paged_gqa_varlen without kv_partition (one row of q per drafted token, K and V
+ * of all of them already in the cache as the sequence's newest n_s tokens, in
+ * row order); what a row sees is not every earlier token but the tokens before
+ * the tree, its ancestors and itself:
  *     out[r][h][:] = softmax( q[r][h] . K^T * scale over t < seq_lens[s] - n_s,
  *                             the ancestors of r, and r ) . V
  *
@@ -495,6 +495,8 @@ pgd_status pgd_varlen_plan(int num_seqs, int total_q, int max_q_len, int num_q_h
  *            In both, the weights are rounded to fp16 (relative 2^-11) before
  *            they multiply V, as in paged_gqa_varlen; sums are fp32.
  * max_q_len  bound on every n_s, at most PGD_TREE_MAX_NODES.
+ * workspace  NULL: library scratch; else at least pgd_tree_plan's bytes, 256-byte
+ *            aligned, not used by anything else until the call's work is done.
  *
  * parents[i] = i - 1 is paged_gqa_varlen's causal form.  A sequence whose query
  * rows are inconsistent (PGD_DEVERR_QUERY_LEN, also where they do not lie
@@ -516,13 +518,15 @@ pgd_status paged_gqa_tree(void *out, int out_type, const uint16_t *q, const int3
                           int num_seqs, int total_q, int max_q_len, int num_q_heads,
                           int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
                           int num_blocks, int64_t page_stride, int64_t head_stride,
-                          int64_t token_stride, int kv_partition, void *workspace,
-                          size_t workspace_bytes, void *stream);
+                          int64_t token_stride, void *workspace, size_t workspace_bytes,
+                          void *stream);
 
-/* pgd_varlen_plan for paged_gqa_tree. */
+/* Scratch bytes a paged_gqa_tree call with these sizes needs on the current
+ * device: the pieces of the units that its even division of the work cuts (at
+ * most 45 MB, whatever the batch). */
 pgd_status pgd_tree_plan(int num_seqs, int total_q, int max_q_len, int num_q_heads,
                          int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
-                         int kv_partition, int *chosen_kv_partition, size_t *workspace_bytes);
+                         size_t *workspace_bytes);
 
 /*
  * packed_gqa_prefill — causal attention over whole packed prompts, before

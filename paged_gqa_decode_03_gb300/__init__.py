@@ -68,8 +68,8 @@ SIGNATURES = {
     "paged_gqa_decode_q8_append": (_I, [_P] * 10 + [_F] + [_I] * 8 + [_P]),
     "paged_kv_quantize": (_I, [_P] * 4 + [_I] * 5 + [_P]),
     "paged_gqa_decode_q8_strided": (_I, [_P] * 10 + [_F] + [_I] * 8 + [_L] * 6 + [_P, _Z, _P]),
-    "paged_gqa_tree": (_I, [_P, _I] + [_P] * 7 + [_F] + [_I] * 9 + [_L] * 3 + [_I, _P, _Z, _P]),
-    "pgd_tree_plan": (_I, [_I] * 9 + [ctypes.POINTER(_I), ctypes.POINTER(_Z)]),
+    "paged_gqa_tree": (_I, [_P, _I] + [_P] * 7 + [_F] + [_I] * 9 + [_L] * 3 + [_P, _Z, _P]),
+    "pgd_tree_plan": (_I, [_I] * 8 + [ctypes.POINTER(_Z)]),
     "packed_gqa_prefill": (_I, [_P, _I] + [_P] * 4 + [_F] + [_I] * 6 + [_L] * 6 + [_P, _Z, _P]),
     "pgd_prefill_plan": (_I, [_I] * 5 + [ctypes.POINTER(_Z)]),
     "paged_kv_slots": (_I, [_P] * 10 + [_I] * 6 + [_P]),
@@ -557,8 +557,7 @@ def _out_type(out):
 
 
 def paged_gqa_tree(out, q, cu_seqlens_q, parents, k_cache, v_cache, block_tables, seq_lens, scale,
-                   max_q_len: int, kv_partition: int = 0, layout=None, workspace=None,
-                   stream=None) -> None:
+                   max_q_len: int, layout=None, workspace=None, stream=None) -> None:
     """Attention of trees of drafted tokens over the paged cache.  As
     ``paged_gqa_varlen`` (q: [total_q, Hq, D]; sequence s owns rows
     cu_seqlens_q[s]..cu_seqlens_q[s+1]-1, its newest tokens, at most
@@ -598,19 +597,17 @@ def paged_gqa_tree(out, q, cu_seqlens_q, parents, k_cache, v_cache, block_tables
     _on(dev, lib.paged_gqa_tree, out.data_ptr(), kind, q.data_ptr(), cu_seqlens_q.data_ptr(),
         parents.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), float(scale), S, T, int(max_q_len), Hq, int(Hkv), D, int(BS), MB,
-        int(NB), sp, sh, st, int(kv_partition), ws, ws_bytes, stream=stream)
+        int(NB), sp, sh, st, ws, ws_bytes, stream=stream)
 
 
 def pgd_tree_plan(num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
-                  max_blocks_per_seq, kv_partition=0):
-    """(KV partition used, scratch bytes needed) of a paged_gqa_tree call."""
-    lib = load_library()
-    pk = ctypes.c_int(0)
+                  max_blocks_per_seq) -> int:
+    """Scratch bytes of a paged_gqa_tree call on the current device."""
     b = ctypes.c_size_t(0)
-    _raise(lib.pgd_tree_plan(num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim,
-                             block_size, max_blocks_per_seq, kv_partition, ctypes.byref(pk),
-                             ctypes.byref(b)))
-    return pk.value, b.value
+    _raise(load_library().pgd_tree_plan(num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads,
+                                        head_dim, block_size, max_blocks_per_seq,
+                                        ctypes.byref(b)))
+    return b.value
 
 
 def _packed_strides(t, name):

@@ -19,8 +19,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpgd.so")
 SOURCES = ["pgd_api.cu", "pgd_kernels_d64.cu", "pgd_kernels_d128.cu", "pgd_kernels_d256.cu", "pgd_quantize.cu",
-           "pgd_varlen.cu", "pgd_kv.cu", "pgd_prefill.cu"]
-HEADERS = ["pgd_device.cuh", "pgd_internal.h", "pgd_kernels.cuh"]
+           "pgd_varlen.cu", "pgd_kv.cu", "pgd_prefill.cu",
+           "pgd_tree.cu"]
+HEADERS = ["pgd_device.cuh", "pgd_internal.h", "pgd_kernels.cuh", "pgd_rows.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          f"-I{os.path.join(ROOT, 'include')}"]

@@ -59,6 +59,7 @@ struct DeviceState {
     cudaError_t init_error = cudaSuccess;
     int num_sms = 0;
     int ctas[3][3][5] = {};         // [kind: fp16, quantised, MQ][head_dim 64/128/256][block size]
+    int tree_clusters[3][3] = {};   // [head_dim][cluster of 1, 2, 4 CTAs]
     unsigned *err_word = nullptr;   // address of g_device_error on this device
     std::mutex pool_mu;             // the pool is made on first library-owned scratch
     cudaMemPool_t pool = nullptr;   //   (and again after pgd_release): stream-ordered scratch
@@ -100,6 +101,12 @@ cudaError_t init_device(int dev, DeviceState &st)
             if ((e = occupancy_d256(kBlockSizes[i], kind, &st.ctas[kind][2][i])) != cudaSuccess)
                 return e;
         }
+    for (int i = 0; i < 9; ++i)
+        if ((e = tree_clusters(64 << (i / 3), 1 << (i % 3), &st.tree_clusters[i / 3][i % 3])) !=
+            cudaSuccess)
+            return e;
+    if ((e = prefill_set_up()) != cudaSuccess)
+        return e;
     return cudaGetSymbolAddress(reinterpret_cast<void **>(&st.err_word), g_device_error);
 }
 
@@ -1063,10 +1070,8 @@ int varlen_tokens_per_stage(int D) { return D == 64 ? VShape<64>::NT : D == 128 
 // per (sequence, KV head); the KV range is cut into partitions of PK tokens
 // only when the tiles alone (counted at max_q_len) would not give every SM
 // two units.  Scratch (partials) only when some row spans two partitions.
-// tree: trees of drafted tokens (paged_gqa_tree), on the tensor-core kernels
-// at every size.
 pgd_status make_varlen_plan(int S, int total_q, int max_q, int Hq, int Hkv, int D, int BS,
-                            int MB, int kv_partition, VarlenPlan *vp, bool tree = false)
+                            int MB, int kv_partition, VarlenPlan *vp)
 {
     pgd_status st;
     if (S < 0)
@@ -1085,9 +1090,6 @@ pgd_status make_varlen_plan(int S, int total_q, int max_q, int Hq, int Hkv, int 
         return fail(PGD_ERR_UNSUPPORTED, "length bound %lld above 2^30", (long long)MB * BS);
     if (total_q < 0 || max_q < 0 || (total_q > 0 && max_q < 1))
         return fail(PGD_ERR_INVALID_ARG, "total_q %d / max_q_len %d", total_q, max_q);
-    if (tree && max_q > kTreeMaxNodes)
-        return fail(PGD_ERR_UNSUPPORTED, "max_q_len %d: trees of up to %d nodes", max_q,
-                    kTreeMaxNodes);
     vp->NT = varlen_tokens_per_stage(D);
     if (kv_partition < 0 || (kv_partition > 0 && kv_partition % vp->NT != 0))
         return fail(PGD_ERR_INVALID_ARG, "kv_partition %d: 0 or a positive multiple of %d",
@@ -1101,7 +1103,7 @@ pgd_status make_varlen_plan(int S, int total_q, int max_q, int Hq, int Hkv, int 
     // read each K/V byte for only a few rows: an HBM-bound scan, which the
     // decode kernel's MQ form does (one n8 column tile of mma.sync, partitions of
     // 256 / 512 tokens chosen as for the decode, partials per query row).
-    vp->mq = !tree && D <= 128 && vp->G <= kMaxGroup && max_q >= 1 &&
+    vp->mq = D <= 128 && vp->G <= kMaxGroup && max_q >= 1 &&
              (long long)max_q * vp->G <= kMaxCols &&
              (kv_partition == 0 || kv_partition == kPartitionSmall ||
               kv_partition == kPartitionLarge);
@@ -1174,43 +1176,29 @@ pgd_status make_varlen_plan(int S, int total_q, int max_q, int Hq, int Hkv, int 
     return PGD_OK;
 }
 
-// What a call over trees of drafted tokens has beside the plain form's
-// arguments (then `out` is null): the parents and either output.
-struct TreeArgs {
-    const int32_t *parents;
-    float *out;
-    uint16_t *out_half;
-};
-
 pgd_status run_varlen(float *out, const uint16_t *q, const int32_t *cu_q, const uint16_t *k_cache,
                       const uint16_t *v_cache, const int32_t *block_tables,
                       const int32_t *seq_lens, float scale, int S, int total_q, int max_q, int Hq,
                       int Hkv, int D, int BS, int MB, int NB, const Strides &kv_strides,
-                      int kv_partition, void *workspace, size_t ws_bytes, void *stream_v,
-                      const TreeArgs *tree = nullptr)
+                      int kv_partition, void *workspace, size_t ws_bytes, void *stream_v)
 {
     VarlenPlan vp;
-    pgd_status st = make_varlen_plan(S, total_q, max_q, Hq, Hkv, D, BS, MB, kv_partition, &vp,
-                                     tree != nullptr);
+    pgd_status st = make_varlen_plan(S, total_q, max_q, Hq, Hkv, D, BS, MB, kv_partition, &vp);
     if (st)
         return st;
     if (S == 0 || total_q == 0) {
         t_last_error.clear();
         return PGD_OK;
     }
-    const void *dst = tree && tree->out_half ? static_cast<const void *>(tree->out_half)
-                      : tree                 ? tree->out
-                                             : out;
-    if (!dst || (tree && !tree->parents) || !q || !cu_q || !k_cache || !v_cache || !block_tables || !seq_lens)
+    if (!out || !q || !cu_q || !k_cache || !v_cache || !block_tables || !seq_lens)
         return fail(PGD_ERR_INVALID_ARG, "null array argument");
     if (!std::isfinite(scale))
         return fail(PGD_ERR_INVALID_ARG, "scale is not finite");
     if (NB <= 0)
         return fail(PGD_ERR_INVALID_ARG, "num_blocks %d <= 0", NB);
-    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(dst, 16))
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
         return fail(PGD_ERR_INVALID_ARG, "q, k_cache, v_cache and out must be 16-byte aligned");
-    if (!aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
-        (tree && !aligned(tree->parents, 4)))
+    if (!aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4))
         return fail(PGD_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
     if ((st = check_strides(kv_strides, D)))
         return st;
@@ -1253,10 +1241,7 @@ pgd_status run_varlen(float *out, const uint16_t *q, const int32_t *cu_q, const 
         return st;
     }
     VarlenParams p = {};
-    p.out = tree ? tree->out : out;
-    p.out_half = tree ? reinterpret_cast<__half *>(tree->out_half) : nullptr;
-    p.parents = tree ? tree->parents : nullptr;
-    p.total_q = total_q;
+    p.out = out;
     p.cu_q = cu_q;
     p.block_tables = block_tables;
     p.seq_lens = seq_lens;
@@ -1283,8 +1268,8 @@ pgd_status run_varlen(float *out, const uint16_t *q, const int32_t *cu_q, const 
     p.blk_head = (int)(kv_strides.head / blk_u);
     p.max_q = max_q;
     p.wait_budget_ns = kWaitBudgetNs;
-    e = (tree ? launch_tree : launch_varlen)(D, vp.pairs, tq, *tk, *tv, p, (int)vp.grid,
-                                             vp.NP > 1 ? total_q * Hq : 0, stream);
+    e = launch_varlen(D, vp.pairs, tq, *tk, *tv, p, (int)vp.grid, vp.NP > 1 ? total_q * Hq : 0,
+                      stream);
     if (own && ws) {
         cudaError_t e2 = cudaFreeAsync(ws, stream);
         if (e == cudaSuccess)
@@ -1347,6 +1332,154 @@ HostStaging host_staging(int S, int Hq, int D, int MB)
     h.out = h.sl + align256((size_t)S * 4);
     h.bytes = h.out + align256((size_t)S * Hq * D * 4);
     return h;
+}
+
+// ------------------------------------------------------------------ trees of drafted tokens
+struct TreePlan {
+    int G, TQ, cs, clusters, NT;
+    size_t ws_bytes, off_ml, off_cut;  // pieces' outputs, (maximum, exp-sum)s, cuts
+};
+
+// A cluster has as many CTAs as the largest tree has 128-row tiles (1, 2 or 4:
+// tiles past the fourth are further groups); as many clusters as are resident
+// at once, or as there can be stages.
+pgd_status make_tree_plan(int S, int total_q, int max_q, int Hq, int Hkv, int D, int BS, int MB,
+                          TreePlan *tp)
+{
+    if (S < 0 || total_q < 0 || max_q < 0 || (total_q > 0 && max_q < 1))
+        return fail(PGD_ERR_INVALID_ARG, "num_seqs %d, total_q %d, max_q_len %d", S, total_q, max_q);
+    if (max_q > kTreeMaxNodes)
+        return fail(PGD_ERR_UNSUPPORTED, "max_q_len %d: trees of up to %d nodes", max_q,
+                    kTreeMaxNodes);
+    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0)
+        return fail(PGD_ERR_INVALID_ARG, "head counts %d / %d", Hq, Hkv);
+    if (Hq / Hkv > 128)
+        return fail(PGD_ERR_UNSUPPORTED, "GQA group of %d query heads exceeds 128", Hq / Hkv);
+    if (!supported_head_dim(D))
+        return fail(PGD_ERR_UNSUPPORTED, "head_dim %d not in {64, 128, 256}", D);
+    if (!supported_block_size(BS))
+        return fail(PGD_ERR_UNSUPPORTED, "block_size %d not in {8, 16, 32, 64, 128}", BS);
+    if (MB <= 0)
+        return fail(PGD_ERR_INVALID_ARG, "max_blocks_per_seq %d <= 0", MB);
+    if ((long long)MB * BS > (1ll << 30))
+        return fail(PGD_ERR_UNSUPPORTED, "length bound %lld above 2^30", (long long)MB * BS);
+    DeviceState *ds;
+    pgd_status st;
+    if ((st = device_state(&ds)))
+        return st;
+    tp->G = Hq / Hkv;
+    tp->TQ = 128 / tp->G;
+    tp->NT = D == 64 ? TreeShape<64>::NT : D == 128 ? TreeShape<128>::NT : TreeShape<256>::NT;
+    const int tiles = std::max(1, (max_q + tp->TQ - 1) / tp->TQ);
+    const int c = tiles == 1 ? 0 : tiles == 2 ? 1 : 2;
+    tp->cs = 1 << c;
+    const int resident = ds->tree_clusters[d_index(D)][c];
+    if (resident < 1)
+        return fail(PGD_ERR_UNSUPPORTED, "a cluster of %d thread blocks does not fit", tp->cs);
+    const long long stages = (long long)S * Hkv * ((tiles + tp->cs - 1) / tp->cs) *
+                             (((long long)MB * BS + tp->NT - 1) / tp->NT);
+    tp->clusters = (int)std::max(1ll, std::min<long long>(resident, stages));
+    const size_t rows = (size_t)2 * tp->clusters * tp->cs * 128;
+    tp->off_ml = align256(rows * D * 4);
+    tp->off_cut = tp->off_ml + align256(rows * 8);
+    tp->ws_bytes = S && total_q ? tp->off_cut + align256((size_t)tp->clusters * 16) : 0;
+    return PGD_OK;
+}
+
+pgd_status run_tree(void *out, bool half, const uint16_t *q, const int32_t *cu_q,
+                    const int32_t *parents, const uint16_t *k_cache, const uint16_t *v_cache,
+                    const int32_t *block_tables, const int32_t *seq_lens, float scale, int S,
+                    int total_q, int max_q, int Hq, int Hkv, int D, int BS, int MB, int NB,
+                    const Strides &kv_strides, void *workspace, size_t ws_bytes, void *stream_v)
+{
+    TreePlan tp;
+    pgd_status st = make_tree_plan(S, total_q, max_q, Hq, Hkv, D, BS, MB, &tp);
+    if (st)
+        return st;
+    if (S == 0 || total_q == 0) {
+        t_last_error.clear();
+        return PGD_OK;
+    }
+    if (!out || !q || !cu_q || !parents || !k_cache || !v_cache || !block_tables || !seq_lens)
+        return fail(PGD_ERR_INVALID_ARG, "null array argument");
+    if (!std::isfinite(scale))
+        return fail(PGD_ERR_INVALID_ARG, "scale is not finite");
+    if (NB <= 0)
+        return fail(PGD_ERR_INVALID_ARG, "num_blocks %d <= 0", NB);
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
+        return fail(PGD_ERR_INVALID_ARG, "q, k_cache, v_cache and out must be 16-byte aligned");
+    if (!aligned(cu_q, 4) || !aligned(parents, 4) || !aligned(block_tables, 4) ||
+        !aligned(seq_lens, 4))
+        return fail(PGD_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+    if ((st = check_strides(kv_strides, D)))
+        return st;
+    char *ws = static_cast<char *>(workspace);
+    const bool own = workspace == nullptr;
+    if (!own && (ws_bytes < tp.ws_bytes || !aligned(ws, 256)))
+        return fail(PGD_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) given, %zu needed",
+                    ws_bytes, tp.ws_bytes);
+    DeviceState *ds;
+    if ((st = device_state(&ds)))
+        return st;
+    CUtensorMap tq;
+    const CacheGeom geom = {NB, Hkv, BS, D, kv_strides.page, kv_strides.head, kv_strides.token};
+    const CUtensorMap *tk = nullptr, *tv = nullptr;
+    long long blk_u, blk_n;
+    const int box_rows = std::min(BS, tp.NT / tp.cs);
+    if ((st = group_blocks(geom, &blk_u, &blk_n)) ||
+        (st = encode_q_map(&tq, q, total_q, Hq, D, tp.G, tp.TQ)) ||
+        (st = cache_maps(k_cache, v_cache, geom, box_rows / 8, 1, &tk, &tv)))
+        return st;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    cudaError_t e;
+    if (own) {
+        cudaMemPool_t pool;
+        if ((st = device_pool(*ds, &pool)))
+            return st;
+        if ((e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), tp.ws_bytes, pool,
+                                         stream)) != cudaSuccess)
+            return cuda_fail(e, "scratch allocation");
+    }
+    TreeParams p = {};
+    p.out = out;
+    p.out_half = half;
+    p.wide_rows = aligned(out, 32);
+    p.cu_q = cu_q;
+    p.parents = parents;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.part_o = reinterpret_cast<float *>(ws);
+    p.part_ml = reinterpret_cast<float2 *>(ws + tp.off_ml);
+    p.cut = reinterpret_cast<int4 *>(ws + tp.off_cut);
+    p.err = ds->err_word;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.S = S;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = tp.G;
+    p.TQ = tp.TQ;
+    p.total_q = total_q;
+    p.max_q = max_q;
+    p.MB = MB;
+    p.NB = NB;
+    p.BS = BS;
+    p.log2BS = 3 + bs_index(BS);
+    p.cs = tp.cs;
+    p.clusters = tp.clusters;
+    p.box_rows = box_rows;
+    p.blk_page = (int)(kv_strides.page / blk_u);
+    p.blk_head = (int)(kv_strides.head / blk_u);
+    p.wait_budget_ns = kWaitBudgetNs;
+    e = launch_tree(D, tq, *tk, *tv, p, stream);
+    if (own) {
+        const cudaError_t e2 = cudaFreeAsync(ws, stream);
+        if (e == cudaSuccess)
+            e = e2;
+    }
+    if (e != cudaSuccess)
+        return cuda_fail(e, "kernel launch");
+    t_last_error.clear();
+    return PGD_OK;
 }
 
 // ------------------------------------------------------------------ the step around the cache
@@ -1931,38 +2064,33 @@ pgd_status paged_gqa_tree(void *out, int out_type, const uint16_t *q, const int3
                           int num_seqs, int total_q, int max_q_len, int num_q_heads,
                           int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
                           int num_blocks, int64_t page_stride, int64_t head_stride,
-                          int64_t token_stride, int kv_partition, void *workspace,
-                          size_t workspace_bytes, void *stream)
+                          int64_t token_stride, void *workspace, size_t workspace_bytes,
+                          void *stream)
 {
     return guarded([&]() -> pgd_status {
         if (out_type != PGD_OUT_F32 && out_type != PGD_OUT_F16)
             return fail(PGD_ERR_INVALID_ARG, "out_type %d: PGD_OUT_F32 or PGD_OUT_F16", out_type);
-        const bool half = out_type == PGD_OUT_F16;
-        const TreeArgs tree = {parents, half ? nullptr : static_cast<float *>(out),
-                               half ? static_cast<uint16_t *>(out) : nullptr};
-        return run_varlen(nullptr, q, cu_seqlens_q, k_cache, v_cache, block_tables, seq_lens, scale,
-                          num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim,
-                          block_size, max_blocks_per_seq, num_blocks,
-                          Strides{page_stride, head_stride, token_stride}, kv_partition, workspace,
-                          workspace_bytes, stream, &tree);
+        return run_tree(out, out_type == PGD_OUT_F16, q, cu_seqlens_q, parents, k_cache, v_cache,
+                        block_tables, seq_lens, scale, num_seqs, total_q, max_q_len, num_q_heads,
+                        num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks,
+                        Strides{page_stride, head_stride, token_stride}, workspace,
+                        workspace_bytes, stream);
     });
 }
 
 pgd_status pgd_tree_plan(int num_seqs, int total_q, int max_q_len, int num_q_heads,
                          int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
-                         int kv_partition, int *chosen_kv_partition, size_t *workspace_bytes)
+                         size_t *workspace_bytes)
 {
     return guarded([&]() -> pgd_status {
-        VarlenPlan vp;
-        pgd_status st = make_varlen_plan(num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads,
-                                         head_dim, block_size, max_blocks_per_seq, kv_partition,
-                                         &vp, true);
+        TreePlan tp;
+        const pgd_status st = make_tree_plan(num_seqs, total_q, max_q_len, num_q_heads,
+                                             num_kv_heads, head_dim, block_size,
+                                             max_blocks_per_seq, &tp);
         if (st)
             return st;
-        if (chosen_kv_partition)
-            *chosen_kv_partition = vp.PK;
         if (workspace_bytes)
-            *workspace_bytes = vp.ws_bytes;
+            *workspace_bytes = tp.ws_bytes;
         return PGD_OK;
     });
 }

@@ -244,11 +244,52 @@ struct VarlenParams {
                                   //   block index order
     int blk_page, blk_head;       // (page, KV head) -> block coordinate of the K/V maps
     uint64_t wait_budget_ns;
-    // trees of drafted tokens (the TREE instantiations; null otherwise)
-    int total_q;                  // rows of q and out
-    const int32_t *parents;       // [total_q] parent node of each query row, negative: none
-    __half *out_half;             // [total_q][Hq][D] the output as fp16, or null: `out` as fp32
 };
+
+// ---------------------------------------------------------------- trees of drafted tokens
+// Attention of trees of drafted tokens over the paged cache (pgd_tree.cu).
+constexpr unsigned kErrTree = 32u;     // a parent that is not an earlier node of its tree
+constexpr int kTreeMaxNodes = 256;     // nodes of one sequence's tree
+constexpr int kTreeMaxCluster = 4;     // tiles that share a cluster's K and V stages
+
+// Tokens per K or V stage, and stages of each ring, per head_dim (beside the Q
+// tile and the trees' bits in 227 KB).
+template <int D> struct TreeShape;
+template <> struct TreeShape<64> {
+    static constexpr int NT = 128, NK = 4, NV = 4;
+};
+template <> struct TreeShape<128> {
+    static constexpr int NT = 128, NK = 2, NV = 3;
+};
+template <> struct TreeShape<256> {
+    static constexpr int NT = 64, NK = 2, NV = 2;
+};
+
+struct TreeParams {
+    void *out;                    // [total_q][Hq][D], fp16 (out_half) or fp32
+    bool out_half, wide_rows;     // wide_rows: it starts on a 32-byte border
+    const int32_t *cu_q;          // [S+1]
+    const int32_t *parents;       // [total_q] parent node of each row, negative: none
+    const int32_t *block_tables;  // [S][MB]
+    const int32_t *seq_lens;      // [S]
+    // scratch: the pieces of the units that are cut, two per cluster, each 128
+    // rows per tile of the cluster, and where the cut units begin
+    float *part_o;                // [2 * clusters][cs][128][D] sums of p v
+    float2 *part_ml;              // [2 * clusters][cs][128] (reference maximum, exp-sum)
+    int4 *cut;                    // [clusters] {sequence or -1, KV head, tile group, last cluster}
+    unsigned *err;
+    float scale_log2;
+    int S, Hq, Hkv, G, TQ, total_q, max_q, MB, NB, BS, log2BS;
+    int cs, clusters;             // CTAs of a cluster (tiles that share stages), clusters
+    int box_rows;                 // tokens of one page copy
+    int blk_page, blk_head;       // (page, KV head) -> block coordinate of the K/V maps
+    uint64_t wait_budget_ns;
+};
+// Clusters of cs CTAs that are resident at once on the current device (also the
+// kernel's set-up there: once before its launches).
+cudaError_t tree_clusters(int head_dim, int cs, int *clusters);
+cudaError_t launch_tree(int head_dim, const CUtensorMap &tq, const CUtensorMap &tk,
+                        const CUtensorMap &tv, const TreeParams &p, cudaStream_t stream);
 
 // ---------------------------------------------------------------- packed prompts
 // Causal attention over whole packed prompts (pgd_prefill.cu).
@@ -268,6 +309,7 @@ struct PrefillParams {
     bool wide_rows;               // the output starts on a 32-byte border
     uint64_t wait_budget_ns;
 };
+cudaError_t prefill_set_up();  // on the current device, once before its launches
 cudaError_t launch_prefill(int head_dim, const CUtensorMap &tq, const CUtensorMap &tk,
                            const CUtensorMap &tv, const PrefillParams &p, int grid,
                            cudaStream_t stream);
@@ -314,12 +356,6 @@ cudaError_t launch_quantize(int head_dim, uint8_t *codes, uint16_t *meta, const 
 cudaError_t launch_varlen(int head_dim, bool pairs, const CUtensorMap &tq, const CUtensorMap &tk,
                           const CUtensorMap &tv, const VarlenParams &p, int grid, int reduce_rows,
                           cudaStream_t stream);
-// Trees of drafted tokens over the cache (the TREE instantiations).
-constexpr unsigned kErrTree = 32u;     // a parent that is not an earlier node of its tree
-constexpr int kTreeMaxNodes = 256;     // nodes of one sequence's tree
-cudaError_t launch_tree(int head_dim, bool pairs, const CUtensorMap &tq, const CUtensorMap &tk,
-                        const CUtensorMap &tv, const VarlenParams &p, int grid, int reduce_rows,
-                        cudaStream_t stream);
 constexpr int kVarlenOrderKeys = 1024;  // stage counts the unit sort tells apart
 
 }  // namespace pgd

@@ -13,6 +13,7 @@
 
 #include "pgd_device.cuh"
 #include "pgd_internal.h"
+#include "pgd_rows.cuh"
 
 namespace pgd {
 
@@ -114,119 +115,6 @@ __device__ __forceinline__ int4 tile_of(const PrefillParams &p, int k, int units
 {
     const int ui = unit_of(k);
     return ui < units ? __ldg(p.tiles + ui / p.Hkv) : make_int4(0, 0, 0, 0);
-}
-
-// Rows of the output from the registers of a warp: lane r holds 32 words (fp32
-// values, or pairs of fp16) of row r.  Written as they are, every store would
-// touch 32 rows, a line each; so each four lanes first exchange eight-word
-// pieces (a 4 x 4 transpose by two butterflies), after which the four hold one
-// row's 128 bytes, of four rows in turn, and a store touches 8 lines.
-struct RowOut {
-    char *at[4];   // where rows 4 * (lane / 4) + 0 .. 3 of the warp begin, or null
-};
-
-__device__ __forceinline__ void store_words(const RowOut &o, uint32_t (&w)[32], int byte, int lane,
-                                            bool wide)
-{
-    const bool odd = lane & 1, high = lane & 2;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int q = 0; q < 4; q += 2) {  // pieces (0, 1) and (2, 3) with lane ^ 1
-            const uint32_t got =
-                __shfl_xor_sync(~0u, odd ? w[8 * q + i] : w[8 * (q + 1) + i], 1);
-            w[8 * q + i] = odd ? got : w[8 * q + i];
-            w[8 * (q + 1) + i] = odd ? w[8 * (q + 1) + i] : got;
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {     // pieces (0, 2) and (1, 3) with lane ^ 2
-            const uint32_t got =
-                __shfl_xor_sync(~0u, high ? w[8 * q + i] : w[8 * (q + 2) + i], 2);
-            w[8 * q + i] = high ? got : w[8 * q + i];
-            w[8 * (q + 2) + i] = high ? w[8 * (q + 2) + i] : got;
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        if (o.at[q]) {
-            char *dst = o.at[q] + byte + 32 * (lane & 3);
-            if (wide) {
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
-                             "r"(w[8 * q]), "r"(w[8 * q + 1]), "r"(w[8 * q + 2]), "r"(w[8 * q + 3]),
-                             "r"(w[8 * q + 4]), "r"(w[8 * q + 5]), "r"(w[8 * q + 6]),
-                             "r"(w[8 * q + 7])
-                             : "memory");
-            } else {  // an output that starts on 16 bytes only
-                *reinterpret_cast<uint4 *>(dst) =
-                    make_uint4(w[8 * q], w[8 * q + 1], w[8 * q + 2], w[8 * q + 3]);
-                *reinterpret_cast<uint4 *>(dst + 16) =
-                    make_uint4(w[8 * q + 4], w[8 * q + 5], w[8 * q + 6], w[8 * q + 7]);
-            }
-        }
-}
-
-// COLS columns of O from tensor memory (from column `col` of the tile's O on,
-// at `taddr`), scaled by the row's 1 / l, to the output; `last` runs once
-// the last value has been read.
-template <int COLS, class F>
-__device__ __forceinline__ void write_rows(const PrefillParams &p, const RowOut &o, uint32_t taddr,
-                                           int col, float inv, int lane, F &&last)
-{
-    float v[32];
-    uint32_t w[32];
-    if (p.out_half) {
-#pragma unroll 1
-        for (int c = 0; c < COLS; c += 64) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                tc_ld32(taddr + c + 32 * h, v);
-                tc_wait_ld();
-                tc_ld_ready(v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    w[16 * h + i] = pack_half2(v[2 * i] * inv, v[2 * i + 1] * inv);
-            }
-            if (c + 64 == COLS)
-                last();
-            store_words(o, w, (col + c) * 2, lane, p.wide_rows);
-        }
-    } else {
-#pragma unroll 1
-        for (int c = 0; c < COLS; c += 32) {
-            tc_ld32(taddr + c, v);
-            tc_wait_ld();
-            tc_ld_ready(v);
-            if (c + 32 == COLS)
-                last();
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                w[i] = __float_as_uint(v[i] * inv);
-            store_words(o, w, (col + c) * 4, lane, p.wide_rows);
-        }
-    }
-}
-
-// The rows of a warp's quarter of a tile whose first token is row `token` of
-// the output; `left`: the tile's tokens.
-__device__ __forceinline__ RowOut rows_out(const PrefillParams &p, int token, int left, int g,
-                                           int quarter, int lane, int D)
-{
-    RowOut o;
-    char *base = p.out_half ? reinterpret_cast<char *>(p.out_half) : reinterpret_cast<char *>(p.out);
-    const int size = p.out_half ? 2 : 4;
-    int r = 32 * quarter + (lane & ~3);
-    int ti = r / p.G, h = r - ti * p.G;
-#pragma unroll
-    for (int q = 0; q < 4; ++q, ++r) {
-        o.at[q] = r < p.TQ * p.G && ti < left
-                      ? base + (((size_t)(token + ti) * p.Hq + (size_t)g * p.G + h) * D) * size
-                      : nullptr;
-        if (++h == p.G) {
-            h = 0;
-            ++ti;
-        }
-    }
-    return o;
 }
 
 }  // namespace
@@ -363,6 +251,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int units = *p.num_tiles * p.Hkv;
     const int turns = (units + (int)gridDim.x - 1) / (int)gridDim.x;
 
+    const bool half_out = p.out_half != nullptr;
+    void *const out = half_out ? static_cast<void *>(p.out_half) : p.out;
+    const size_t row_bytes = (size_t)D * (half_out ? 2 : 4);
     auto give_up = [&]() {
         if (!abort_flag)
             atomicOr(p.err, kErrTimeout);
@@ -723,8 +614,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (ok) {
                     tc_fence_after();
                     const float inv = l > 0.f ? 1.f / l : 0.f;
-                    const RowOut rows = rows_out(p, u.x + x * p.TQ, left, g, quarter, lane, D);
-                    write_rows<D>(p, rows, t_lane + o_col, 0, inv, lane, [&] {
+                    const RowOut rows = rows_out(out, row_bytes, p.Hq, p.G, p.TQ, u.x + x * p.TQ,
+                                                 left, g, quarter, lane);
+                    write_rows<D>(rows, half_out, p.wide_rows, t_lane + o_col, 0, inv, lane, [&] {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
@@ -815,6 +707,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int units = *p.num_tiles * p.Hkv;
     const int turns = (units + (int)gridDim.x - 1) / (int)gridDim.x;
 
+    const bool half_out = p.out_half != nullptr;
+    void *const out = half_out ? static_cast<void *>(p.out_half) : p.out;
+    const size_t row_bytes = (size_t)D * (half_out ? 2 : 4);
     auto give_up = [&]() {
         if (!abort_flag)
             atomicOr(p.err, kErrTimeout);
@@ -1122,8 +1017,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 continue;
             tc_fence_after();
             const float inv = lt > 0.f ? 1.f / lt : 0.f;
-            const RowOut rows = rows_out(p, u.x, min(p.TQ, u.z), g, quarter, lane, D);
-            write_rows<HD>(p, rows, t_lane + half * HD, half * HD, inv, lane, [&] {
+            const RowOut rows = rows_out(out, row_bytes, p.Hq, p.G, p.TQ, u.x, min(p.TQ, u.z), g,
+                                         quarter, lane);
+            write_rows<HD>(rows, half_out, p.wide_rows, t_lane + half * HD, half * HD, inv, lane, [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
@@ -1139,6 +1035,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
 }
 
+cudaError_t prefill_set_up()
+{
+    const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(packed_prefill_pair_kernel<64>, most,
+                                  (int)pair_smem_bytes<64>())) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(packed_prefill_pair_kernel<128>, most,
+                                  (int)pair_smem_bytes<128>())) != cudaSuccess)
+        return e;
+    return cudaFuncSetAttribute(packed_prefill_wide_kernel, most, (int)kWideSmem);
+}
+
 cudaError_t launch_prefill(int head_dim, const CUtensorMap &tq, const CUtensorMap &tk,
                            const CUtensorMap &tv, const PrefillParams &p, int grid,
                            cudaStream_t stream)
@@ -1149,10 +1057,7 @@ cudaError_t launch_prefill(int head_dim, const CUtensorMap &tq, const CUtensorMa
     const size_t smem = head_dim == 64    ? pair_smem_bytes<64>()
                         : head_dim == 128 ? pair_smem_bytes<128>()
                                           : kWideSmem;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess)
-        return e;
+    cudaError_t e;
     packed_prefill_order_kernel<<<1, kPrefillOrderKeys, 0, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;

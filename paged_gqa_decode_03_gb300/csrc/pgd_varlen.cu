@@ -30,104 +30,12 @@
 //     exp-sum, normalised output, "Four speed-up tricks", 4).
 // paged_varlen_reduce_kernel<D> — merges the partials of rows that span more
 //   than one KV partition.
-//
-// TREE instantiations (paged_gqa_tree): a sequence's newest n_s tokens are the
-// nodes of a tree of drafted tokens, node i with parent parents[row] < i (or
-// none), and row i attends the tokens before the tree, its ancestors and
-// itself.  Ancestors have smaller indices, so the causal bound of the plain
-// form stays an upper bound on what a row sees: ranges, stages, partitions and
-// the order of units are the same, and only the stages that reach into the
-// tree mask by the row's ancestor bits.  The softmax warps build those bits
-// (one word per 32 nodes) in shared memory by pointer doubling while the first
-// K copies are in flight: log2(n_s) rounds, whatever the tree's depth.
 #include "pgd_device.cuh"
 #include "pgd_internal.h"
 
 namespace pgd {
 
-// Ancestor bits of the nodes of one tree: bit j of row i is set where node i
-// sees node j (its ancestors and itself).  Rows of nine words: the ninth stays
-// zero for the funnel shift, and the odd stride spreads the rows over the banks.
-template <bool TREE> struct TreeBits {
-    uint32_t bits[kTreeMaxNodes][kTreeMaxNodes / 32 + 1];
-    int16_t up[kTreeMaxNodes];  // the doubled parent link, -1 past the root
-};
-template <> struct TreeBits<false> {
-};
-
-// Built by the 256 softmax threads (tid 0..255 = node) together; `bar` is
-// their named barrier.  A parent that is not an earlier node counts as none
-// and is flagged (every negative value means none).
-__device__ __forceinline__ void build_tree_bits(TreeBits<true> &tree, const int32_t *parents, int n,
-                                                int tid, uint32_t bar, unsigned *err)
-{
-    constexpr int W = kTreeMaxNodes / 32;
-    if (tid < n) {
-        int up = __ldg(parents + tid);
-        if (up >= tid) {
-            atomicOr(err, kErrTree);
-            up = -1;
-        }
-        tree.up[tid] = (int16_t)max(up, -1);
-#pragma unroll
-        for (int w = 0; w <= W; ++w)
-            tree.bits[tid][w] = w == (tid >> 5) ? 1u << (tid & 31) : 0u;
-    }
-    named_barrier_sync(bar, 256);
-    const int words = (n + 31) >> 5;
-    for (int reach = 1; reach < n; reach <<= 1) {
-        const int up = tid < n ? tree.up[tid] : -1;
-        uint32_t other[W];
-        int next = -1;
-        if (up >= 0) {
-            next = tree.up[up];
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                other[w] = w < words ? tree.bits[up][w] : 0u;
-        }
-        named_barrier_sync(bar, 256);
-        if (up >= 0) {
-            tree.up[tid] = (int16_t)next;
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                if (w < words)
-                    tree.bits[tid][w] |= other[w];
-        }
-        named_barrier_sync(bar, 256);
-    }
-}
-
-// Which of the 32 tokens from node index j0 on (negative: before the tree,
-// where every token is seen) node i sees.
-__device__ __forceinline__ uint32_t tree_word(const TreeBits<true> &tree, int i, int j0)
-{
-    if (j0 <= -32)
-        return ~0u;
-    if (j0 < 0)
-        return (tree.bits[i][0] << -j0) | ((1u << -j0) - 1u);
-    if (j0 >= kTreeMaxNodes)
-        return 0u;
-    return __funnelshift_r(tree.bits[i][j0 >> 5], tree.bits[i][(j0 >> 5) + 1], j0 & 31);
-}
-
-// The query rows of a sequence lie inside q and out.
-__device__ __forceinline__ bool rows_inside(const VarlenParams &p, int row0, int n)
-{
-    return row0 >= 0 && row0 <= p.total_q && n <= p.total_q - row0;
-}
-
-// Eight consecutive output values of a row as fp16 (rounded to nearest).
-__device__ __forceinline__ void store_out8(__half *dst, const float *v, float inv)
-{
-    uint4 w;
-    w.x = pack_half2(v[0] * inv, v[1] * inv);
-    w.y = pack_half2(v[2] * inv, v[3] * inv);
-    w.z = pack_half2(v[4] * inv, v[5] * inv);
-    w.w = pack_half2(v[6] * inv, v[7] * inv);
-    *reinterpret_cast<uint4 *>(dst) = w;
-}
-
-template <int D, bool TREE>
+template <int D>
 __global__ void __launch_bounds__(kVarlenThreads, 1)
     paged_varlen_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         const __grid_constant__ CUtensorMap tmap_k,
@@ -149,7 +57,6 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag;
     __shared__ float pair_red[2][2][128];  // [tile parity][half][row]: softmax pair exchange
-    __shared__ TreeBits<TREE> tree;
 
     // ---- the unit: (sequence, KV head, query tile, KV partition); query
     // tiles in decreasing order so the longest causal ranges start first
@@ -165,7 +72,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
     L = L < 0 ? 0 : (L > maxlen ? maxlen : L);
     const int row0 = __ldg(p.cu_q + s);
     int n = __ldg(p.cu_q + s + 1) - row0;
-    if (n < 0 || n > L || n > p.max_q || (TREE && !rows_inside(p, row0, n))) {
+    if (n < 0 || n > L || n > p.max_q) {
         if (qt == p.QT - 1 && g == 0 && part == 0 && threadIdx.x == 0)
             atomicOr(p.err, kErrQueryLen);
         n = 0;
@@ -405,9 +312,6 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
         const int last_page_end = ((L + p.BS - 1) / p.BS) * p.BS;
-        if constexpr (TREE)
-            if (kv_hi > L - n)
-                build_tree_bits(tree, p.parents + row0, n, threadIdx.x - 64, 5, p.err);
         for (int jj = 0; jj < ntiles; ++jj) {
             const int t0 = (j0 + jj) * NT;
             const int c0 = t0 + half * HC;            // first token of this half
@@ -437,23 +341,12 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
             // row's last token.  The extreme is taken on raw scores: the max
             // for a scale >= 0, the min for a negative one, with masked
             // scores set to the value that scales to -inf.
-            const bool masked_tile = c0 + HC - 1 > lim || (TREE && c0 + HC > L - n);
+            const bool masked_tile = c0 + HC - 1 > lim;
             const bool none = lim < c0;  // this row sees no token of this half
             if (masked_tile && !none) {
-                if constexpr (TREE) {
-                    // (the row's bits: none past the row's own node, so none past lim)
 #pragma unroll
-                    for (int c = 0; c < HC / 32; ++c) {
-                        const uint32_t seen = tree_word(tree, i0 + ti, c0 + 32 * c - (L - n));
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            x[32 * c + i] = (seen >> i) & 1u ? x[32 * c + i] : masked;
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < HC; ++c)
-                        x[c] = c0 + c <= lim ? x[c] : masked;
-                }
+                for (int c = 0; c < HC; ++c)
+                    x[c] = c0 + c <= lim ? x[c] : masked;
             }
             float e = masked;
             if (none || !ok) {
@@ -590,17 +483,12 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
             const size_t rowh = ((size_t)(row0 + i0 + ti) * p.Hq + (size_t)g * p.G + hj);
             const float inv = lt > 0.f ? 1.f / lt : 0.f;
             float *dst = (direct ? p.out + rowh * D : p.ws_o + (rowh * p.NP + part) * D) + half * HD;
-            const bool halves = TREE && direct && p.out_half;
 #pragma unroll 1
             for (int c = 0; c < HD / 32; ++c) {
                 float v[32];
                 tc_ld32(t_lane + O_COL + half * HD + 32 * c, v);
                 tc_wait_ld();
-                if (has && halves) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        store_out8(p.out_half + rowh * D + half * HD + 32 * c + i, v + i, inv);
-                } else if (has) {
+                if (has) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         *reinterpret_cast<float4 *>(dst + 32 * c + i) =
@@ -641,7 +529,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
 //     the same lazy reference max as paged_varlen_kernel; S_j completing
 //     implies P_{j-1} V_{j-1} completed, so O may be rescaled then without
 //     another wait.
-template <int D, bool TREE>
+template <int D>
 __global__ void __launch_bounds__(kVarlenThreads, 1)
     paged_varlen_pair_kernel(const __grid_constant__ CUtensorMap tmap_q,
                              const __grid_constant__ CUtensorMap tmap_k,
@@ -664,7 +552,6 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
         v_empty[NSTG], s_full[2], p_full[2], o_done[2], mma_done;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag;
-    __shared__ TreeBits<TREE> tree;
 
     // ---- the unit: (sequence, KV head, query-tile pair, KV partition);
     // pairs in decreasing order so the longest causal ranges start first
@@ -680,7 +567,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
     L = L < 0 ? 0 : (L > maxlen ? maxlen : L);
     const int row0 = __ldg(p.cu_q + s);
     int n = __ldg(p.cu_q + s + 1) - row0;
-    if (n < 0 || n > L || n > p.max_q || (TREE && !rows_inside(p, row0, n))) {
+    if (n < 0 || n > L || n > p.max_q) {
         if (qp == p.QP - 1 && g == 0 && part == 0 && threadIdx.x == 0)
             atomicOr(p.err, kErrQueryLen);
         n = 0;
@@ -940,9 +827,6 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
         const int last_page_end = ((L + p.BS - 1) / p.BS) * p.BS;
-        if constexpr (TREE)
-            if (max(kv_hi[0], kv_hi[1]) > L - n)
-                build_tree_bits(tree, p.parents + row0, n, threadIdx.x - 64, 1, p.err);
         for (int jj = 0; jj < ntx; ++jj) {
             const int t0 = (j0 + jj) * NT;
             // wait outcomes are warp-uniform: tensor-memory loads and stores
@@ -966,17 +850,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 tc_ld_ready(v[c]);
-            if (TREE && row_ok && t0 + NT > L - n) {
-                if constexpr (TREE) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t seen = tree_word(tree, i0x + ti, t0 + 32 * c - (L - n));
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[c][i] = (seen >> i) & 1u ? v[c][i] : masked;
-                    }
-                }
-            } else if (t0 + NT - 1 > lim) {
+            if (t0 + NT - 1 > lim) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -1086,17 +960,12 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
             const size_t rowh = ((size_t)(row0 + i0x + ti) * p.Hq + (size_t)g * p.G + hj);
             const float inv = l > 0.f ? 1.f / l : 0.f;
             float *dst = direct ? p.out + rowh * D : p.ws_o + (rowh * p.NP + part) * D;
-            const bool halves = TREE && direct && p.out_half;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 float v[32];
                 tc_ld32(t_lane + o_col + 32 * c, v);
                 tc_wait_ld();
-                if (has && halves) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        store_out8(p.out_half + rowh * D + 32 * c + i, v + i, inv);
-                } else if (has) {
+                if (has) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         *reinterpret_cast<float4 *>(dst + 32 * c + i) =
@@ -1190,7 +1059,7 @@ __global__ void __launch_bounds__(kVarlenOrderKeys)
 
 // One CTA per (query row, head) whose causal range spans more than one KV
 // partition: out = sum_i w_i o_i / sum_i w_i with w_i = l_i * exp2(m_i - max m).
-template <int D, bool TREE>
+template <int D>
 __global__ void __launch_bounds__(128) paged_varlen_reduce_kernel(const VarlenParams p)
 {
     const int rowh = blockIdx.x;
@@ -1209,9 +1078,7 @@ __global__ void __launch_bounds__(128) paged_varlen_reduce_kernel(const VarlenPa
     L = L < 0 ? 0 : (L > maxlen ? maxlen : L);
     const int row0 = __ldg(p.cu_q + s);
     const int n = __ldg(p.cu_q + s + 1) - row0;
-    // (TREE: rows behind the last sequence belong to none and stay as they are)
-    const bool bad = n < 0 || n > L || n > p.max_q ||
-                     (TREE && (!rows_inside(p, row0, n) || r < row0 || r - row0 >= n));
+    const bool bad = n < 0 || n > L || n > p.max_q;
     const int pos = L - n + (r - row0);
     const int np = bad ? 1 : pos / p.PK + 1;
     griddep_wait();
@@ -1243,26 +1110,21 @@ __global__ void __launch_bounds__(128) paged_varlen_reduce_kernel(const VarlenPa
     const float inv = den > 0.f ? 1.f / den : 0.f;
 #pragma unroll
     for (int k = 0; k < (D + 127) / 128; ++k)
-        if (threadIdx.x + 128 * k < D) {
-            const size_t at = (size_t)rowh * D + threadIdx.x + 128 * k;
-            if (TREE && p.out_half)
-                p.out_half[at] = __float2half_rn(acc[k] * inv);
-            else
-                p.out[at] = acc[k] * inv;
-        }
+        if (threadIdx.x + 128 * k < D)
+            p.out[(size_t)rowh * D + threadIdx.x + 128 * k] = acc[k] * inv;
 }
 
-template <int D, bool TREE>
+template <int D>
 cudaError_t launch_varlen_impl(bool pairs, const CUtensorMap &tq, const CUtensorMap &tk,
                                const CUtensorMap &tv, const VarlenParams &p, int grid,
                                int reduce_rows, cudaStream_t stream)
 {
     // head_dim 256 has one kernel (two tiles' scores and outputs would not
     // fit in tensor memory)
-    auto kernel = paged_varlen_kernel<D, TREE>;
+    auto kernel = paged_varlen_kernel<D>;
     if constexpr (varlen_pairs<D>())
         if (pairs)
-            kernel = paged_varlen_pair_kernel<D, TREE>;
+            kernel = paged_varlen_pair_kernel<D>;
     const size_t smem = varlen_smem_bytes<D>(pairs && varlen_pairs<D>());
     static bool attr_done[2][64] = {};
     int dev = 0;
@@ -1299,38 +1161,23 @@ cudaError_t launch_varlen_impl(bool pairs, const CUtensorMap &tq, const CUtensor
     rcfg.stream = stream;
     rcfg.attrs = attr;
     rcfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&rcfg, paged_varlen_reduce_kernel<D, TREE>, p);
-}
-
-template <bool TREE>
-cudaError_t launch_varlen_dim(int head_dim, bool pairs, const CUtensorMap &tq,
-                              const CUtensorMap &tk, const CUtensorMap &tv, const VarlenParams &p,
-                              int grid, int reduce_rows, cudaStream_t stream)
-{
-    switch (head_dim) {
-    case 64:
-        return launch_varlen_impl<64, TREE>(pairs, tq, tk, tv, p, grid, reduce_rows, stream);
-    case 128:
-        return launch_varlen_impl<128, TREE>(pairs, tq, tk, tv, p, grid, reduce_rows, stream);
-    case 256:
-        return launch_varlen_impl<256, TREE>(pairs, tq, tk, tv, p, grid, reduce_rows, stream);
-    default:
-        return cudaErrorInvalidValue;
-    }
+    return cudaLaunchKernelEx(&rcfg, paged_varlen_reduce_kernel<D>, p);
 }
 
 cudaError_t launch_varlen(int head_dim, bool pairs, const CUtensorMap &tq, const CUtensorMap &tk,
                           const CUtensorMap &tv, const VarlenParams &p, int grid, int reduce_rows,
                           cudaStream_t stream)
 {
-    return launch_varlen_dim<false>(head_dim, pairs, tq, tk, tv, p, grid, reduce_rows, stream);
-}
-
-cudaError_t launch_tree(int head_dim, bool pairs, const CUtensorMap &tq, const CUtensorMap &tk,
-                        const CUtensorMap &tv, const VarlenParams &p, int grid, int reduce_rows,
-                        cudaStream_t stream)
-{
-    return launch_varlen_dim<true>(head_dim, pairs, tq, tk, tv, p, grid, reduce_rows, stream);
+    switch (head_dim) {
+    case 64:
+        return launch_varlen_impl<64>(pairs, tq, tk, tv, p, grid, reduce_rows, stream);
+    case 128:
+        return launch_varlen_impl<128>(pairs, tq, tk, tv, p, grid, reduce_rows, stream);
+    case 256:
+        return launch_varlen_impl<256>(pairs, tq, tk, tv, p, grid, reduce_rows, stream);
+    default:
+        return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace pgd

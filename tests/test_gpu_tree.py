@@ -89,12 +89,10 @@ def test_chain_is_the_causal_form(D):
     out = run(w, parents, dtype=torch.float32)
     check(out, w, trees, ctx, "chain")
     plain = torch.empty_like(out)
-    # a forced partition keeps the plain form on the same kernels
     pgd.paged_gqa_varlen(plain, w.q, w.cu_seqlens_q, w.k_cache, w.v_cache, w.block_tables,
-                         w.seq_lens, w.scale, w.max_q_len, kv_partition=1024)
-    again = run(w, parents, dtype=torch.float32, kv_partition=1024)
+                         w.seq_lens, w.scale, w.max_q_len)
     torch.cuda.synchronize()
-    assert torch.equal(again, plain)
+    check(plain, w, trees, ctx, "the causal form")
 
 
 def test_deep_and_wide_trees():
@@ -107,16 +105,27 @@ def test_deep_and_wide_trees():
     check(run(w, parents), w, trees, ctx, "deep and wide")
 
 
-@pytest.mark.parametrize("D,PK", [(128, 128), (64, 256), (256, 64)])
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
-def test_split_kv_with_the_tree_across_partitions(D, PK, dtype):
-    """The partition border falls inside the tree: rows that see nothing of a
-    partition leave an empty partial."""
-    ctx, n = [PK - 5, 2 * PK - 1, 3 * PK, 10], [40, 130, 7, 256]
-    w, trees, parents = case(ctx, n, 8, 2, D, 16, seed=PK)
-    out = run(w, parents, dtype=dtype, kv_partition=PK)
-    assert pgd.pgd_last_partition_size() == PK
-    check(out, w, trees, ctx, f"split {PK}")
+@pytest.mark.parametrize("Hkv", [1, 3])
+def test_work_cut_inside_trees(D, dtype, Hkv):
+    """Few heads and long contexts: every unit is cut into many pieces, some of
+    them inside its tree, where rows may see nothing of a piece."""
+    ctx, n = [4000, 1, 777, 2048 - 13], [40, 130, 7, 256]
+    w, trees, parents = case(ctx, n, 4 * Hkv, Hkv, D, 16, seed=D + Hkv)
+    check(run(w, parents, dtype=dtype), w, trees, ctx, f"cut D{D}")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("S", [1, 3, 400])
+def test_many_and_few_sequences(D, S):
+    """Runs that hold many units, sequences without nodes between them."""
+    rng = random.Random(S)
+    ctx = [rng.randrange(0, 300) for _ in range(S)]
+    n = [rng.choice([0, 1, 2, 5, 33]) for _ in range(S)]
+    n[0] = 3
+    w, trees, parents = case(ctx, n, 8, 2, D, 8, seed=S)
+    check(run(w, parents), w, trees, ctx, f"S {S}", seqs=range(0, S, 1 if S < 9 else 37))
 
 
 def test_workspace_layouts_and_repeats():
@@ -124,10 +133,12 @@ def test_workspace_layouts_and_repeats():
     w, trees, parents = case(ctx, n, 16, 4, 128, 16, seed=4)
     base = run(w, parents)
     check(base, w, trees, ctx, "base")
-    _, need = pgd.pgd_tree_plan(w.S, w.total_q, w.max_q_len, w.Hq, w.Hkv, w.D, w.BS,
-                                w.block_tables.shape[1])
-    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=DEV)
+    need = pgd.pgd_tree_plan(w.S, w.total_q, w.max_q_len, w.Hq, w.Hkv, w.D, w.BS,
+                             w.block_tables.shape[1])
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)   # no initial value needed
     assert torch.equal(run(w, parents, workspace=ws), base)
+    with pytest.raises(pgd.PGDError):
+        run(w, parents, workspace=ws[: need - 1])
     kt, vt = (c.permute(0, 2, 1, 3).contiguous() for c in (w.k_cache, w.v_cache))
     strides = pgd.kv_strides("token_major", w.Hkv, w.BS, w.D)
     got = run(w, parents, k=kt, v=vt, layout=(w.Hkv, w.BS, w.NB, strides))
@@ -148,13 +159,13 @@ def test_padded_rows_and_empty_sequences_stay():
     """More rows than the sequences own, and a sequence without any."""
     ctx, n = [300, 40, 5, 1200], [4, 0, 6, 50]
     w, trees, parents = case(ctx, n, 8, 2, 128, 16, seed=6)
-    for PK in (0, 128):
+    for _ in range(2):
         out = torch.full((w.total_q + 9, w.Hq, w.D), 7.0, dtype=torch.float16, device=DEV)
         q = torch.cat([w.q, torch.full((9, w.Hq, w.D), float("nan"), dtype=torch.float16,
                                        device=DEV)])
         pp = torch.cat([parents, torch.full((9,), 3, dtype=torch.int32, device=DEV)])
         pgd.paged_gqa_tree(out, q, w.cu_seqlens_q, pp, w.k_cache, w.v_cache, w.block_tables,
-                           w.seq_lens, w.scale, w.max_q_len, kv_partition=PK)
+                           w.seq_lens, w.scale, w.max_q_len)
         torch.cuda.synchronize()
         check(out[: w.total_q], w, trees, ctx, "padded")
         assert (out[w.total_q:] == 7.0).all()

@@ -70,18 +70,18 @@ def test_write_of_no_rows_needs_no_arrays(lib):
 
 
 def tree(lib, out_type=1, T=40, max_q=16, S=4, Hq=32, Hkv=8, D=128, BS=16, MB=64, NB=1024,
-         scale=0.1, strides=None, PK=0, ptrs=(A,) * 8, ws=NULL, ws_bytes=0):
+         scale=0.1, strides=None, ptrs=(A,) * 8, ws=NULL, ws_bytes=0):
     strides = strides or (Hkv * BS * D, BS * D, D)
     out, q, cu, parents, k, v, bt, sl = ptrs
     return lib.paged_gqa_tree(out, out_type, q, cu, parents, k, v, bt, sl, ctypes.c_float(scale), S,
-                              T, max_q, Hq, Hkv, D, BS, MB, NB, *strides, PK, ws, ws_bytes, NULL)
+                              T, max_q, Hq, Hkv, D, BS, MB, NB, *strides, ws, ws_bytes, NULL)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(out_type=2), INVALID), (dict(out_type=-1), INVALID), (dict(max_q=257), UNSUPPORTED),
     (dict(D=96), UNSUPPORTED), (dict(BS=4), UNSUPPORTED), (dict(Hq=30), INVALID),
     (dict(Hq=129 * 8), UNSUPPORTED), (dict(MB=0), INVALID), (dict(T=-1), INVALID),
-    (dict(T=4, max_q=0), INVALID), (dict(S=-1), INVALID), (dict(PK=100), INVALID),
+    (dict(T=4, max_q=0), INVALID), (dict(S=-1), INVALID), (dict(MB=1 << 28), UNSUPPORTED),
 ])
 def test_tree_sizes_refused(lib, kw, status):
     assert tree(lib, **kw) == status
@@ -116,7 +116,7 @@ def test_binding_refusals():
     (dict(ptrs=(A, A, A, ODD, A, A, A, A)), INVALID),
     (dict(ptrs=(NULL, A, A, A, A, A, A, A)), INVALID),
     (dict(ptrs=(ctypes.c_void_p((1 << 20) + 8), A, A, A, A, A, A, A)), INVALID),
-    (dict(PK=128, ws=A, ws_bytes=16), WORKSPACE),
+    (dict(ws=A, ws_bytes=16), WORKSPACE),
 ])
 def test_tree_refusals_behind_the_plan(lib, kw, status):
     assert tree(lib, **kw) == status
