@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
     extern __shared__ uint8_t dyn_smem[];
     __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV],
-        v_empty[NV], s_full[2], p_full, o_done, o_free, mma_done;
+        v_empty[NV], s_full[2], p_full, o_done[2], o_free, mma_done;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag;
     __shared__ float pair_red[2][2][128];  // [parity][half][row]: the halves' exchange
@@ -688,9 +688,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         mbar_init(smem_addr(&s_full[0]), 1);
         mbar_init(smem_addr(&s_full[1]), 1);
         mbar_init(smem_addr(&p_full), 8);
-        mbar_init(smem_addr(&o_done), 1);
+        mbar_init(smem_addr(&o_done[0]), 1);
+        mbar_init(smem_addr(&o_done[1]), 1);
         mbar_init(smem_addr(&o_free), 8);
-        mbar_init(smem_addr(&mma_done), 1);
+        mbar_init(smem_addr(&mma_done), 2);
         abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tmap_q);
@@ -785,81 +786,88 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 2) {
         if (lane == 0) {
             // ======================================================== products
-            const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
-            const uint64_t k_desc = tc_sdesc(k_s, 16, 1024);
-            const uint64_t v_desc = tc_sdesc(v_s, VKEYS * 128, 1024);
+            // (scores and outputs by a thread each, as in the pair kernel)
             bool ok = true;
             auto wait = [&](uint64_t *bar, int parity) {
                 if (ok && !mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns))
                     ok = false;
                 return ok;
             };
-            int nk = 0, nv = 0, nq = 0, ns = 0, np = 0, no = 0;
-            auto issue_s = [&](bool last) {
-                const uint32_t d = tmem + S_COL + (ns & 1) * kNT;
-                for (int sl = 0; sl < SLABS; ++sl, ++nk) {
-                    const int st = nk % NK;
-                    if (!wait(&k_full[st], (nk / NK) & 1))
-                        return;
-                    tc_fence_after();
-                    const uint64_t ks = k_desc + ((st * PIECE) >> 4);
-                    const uint64_t qs = q_desc + ((sl * kSlab) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma(d, qs + ((kk * 32) >> 4), ks + ((kk * 32) >> 4), IDESC_S,
-                               sl > 0 || kk > 0);
-                    tc_commit(smem_addr(&k_empty[st]));
-                }
-                tc_commit(smem_addr(&s_full[ns & 1]));
-                if (last)
-                    tc_commit(smem_addr(&q_empty));
-                ++ns;
-            };
-            auto issue_pv = [&](bool first) {
-                if (!wait(&p_full, np & 1) || (first && no && !wait(&o_free, (no - 1) & 1)))
-                    return;
-                if (first)
-                    ++no;
-                const uint32_t a = tmem + S_COL + (np & 1) * kNT;
-                for (int i = 0; i < VP; ++i, ++nv) {
-                    const int st = nv % NV;
-                    if (!wait(&v_full[st], (nv / NV) & 1))
-                        return;
-                    tc_fence_after();
-                    const uint64_t vs = v_desc + ((st * PIECE) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < VKEYS / 16; ++kk)
-                        tc_mma_ta(tmem, a + (i * (VKEYS / 16) + kk) * 8, vs + ((kk * 2048) >> 4),
-                                  IDESC_O, !first || i > 0 || kk > 0);
-                    tc_commit(smem_addr(&v_empty[st]));
-                }
-                tc_commit(smem_addr(&o_done));
-                ++np;
-            };
             int4 next = tile_of(p, 0, units);
-            for (int k = 0; k < turns && ok; ++k) {
-                const int ui = unit_of(k);
-                const int4 u = next;
-                next = tile_of(p, k + 1, units);
-                if (ui >= units)
-                    continue;
-                const int nt = stages(u);
-                if (!wait(&q_full, nq & 1))
-                    break;
-                ++nq;
-                for (int j = -1; j < nt && ok; ++j) {
-                    // S(j+1) takes the buffer of P(j-1), whose product was issued before
-                    if (j + 1 < nt)
-                        issue_s(j + 2 == nt);
-                    if (j >= 0 && ok)
-                        issue_pv(j == 0);
+            if (warp == 1) {
+                const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
+                const uint64_t k_desc = tc_sdesc(k_s, 16, 1024);
+                int nk = 0, nq = 0, ns = 0;
+                for (int k = 0; k < turns && ok; ++k) {
+                    const int ui = unit_of(k);
+                    const int4 u = next;
+                    next = tile_of(p, k + 1, units);
+                    if (ui >= units)
+                        continue;
+                    const int nt = stages(u);
+                    wait(&q_full, nq & 1);
+                    ++nq;
+                    for (int j = 0; j < nt && ok; ++j, ++ns) {
+                        // into the buffer of P(ns - 2), once its product is over
+                        if (ns >= 2)
+                            wait(&o_done[ns & 1], ((ns >> 1) & 1) ^ 1);
+                        const uint32_t d = tmem + S_COL + (ns & 1) * kNT;
+                        for (int sl = 0; sl < SLABS; ++sl, ++nk) {
+                            const int st = nk % NK;
+                            if (!wait(&k_full[st], (nk / NK) & 1))
+                                break;
+                            tc_fence_after();
+                            const uint64_t ks = k_desc + ((st * PIECE) >> 4);
+                            const uint64_t qs = q_desc + ((sl * kSlab) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc_mma(d, qs + ((kk * 32) >> 4), ks + ((kk * 32) >> 4), IDESC_S,
+                                       sl > 0 || kk > 0);
+                            tc_commit(smem_addr(&k_empty[st]));
+                        }
+                        tc_commit(smem_addr(&s_full[ns & 1]));
+                    }
+                    tc_commit(smem_addr(&q_empty));
+                }
+            } else {
+                const uint64_t v_desc = tc_sdesc(v_s, VKEYS * 128, 1024);
+                int nv = 0, np = 0, no = 0;
+                for (int k = 0; k < turns && ok; ++k) {
+                    const int ui = unit_of(k);
+                    const int4 u = next;
+                    next = tile_of(p, k + 1, units);
+                    if (ui >= units)
+                        continue;
+                    const int nt = stages(u);
+                    // the last unit's output has been read
+                    if (no++ && !wait(&o_free, no & 1))
+                        break;
+                    for (int j = 0; j < nt && ok; ++j, ++np) {
+                        if (!wait(&p_full, np & 1))
+                            break;
+                        const uint32_t a = tmem + S_COL + (np & 1) * kNT;
+                        for (int i = 0; i < VP; ++i, ++nv) {
+                            const int st = nv % NV;
+                            if (!wait(&v_full[st], (nv / NV) & 1))
+                                break;
+                            tc_fence_after();
+                            const uint64_t vs = v_desc + ((st * PIECE) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < VKEYS / 16; ++kk)
+                                tc_mma_ta(tmem, a + (i * (VKEYS / 16) + kk) * 8,
+                                          vs + ((kk * 2048) >> 4), IDESC_O, j > 0 || i > 0 || kk > 0);
+                            tc_commit(smem_addr(&v_empty[st]));
+                        }
+                        tc_commit(smem_addr(&o_done[np & 1]));
+                    }
                 }
             }
             if (!ok)
                 give_up();
+            // every product issued has completed before the memory is freed
             tc_commit(smem_addr(&mma_done));
             mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
         }
@@ -967,7 +975,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 // both halves have read their scores (the barrier above): P over them
                 tc_st32u(t_lane + s_col + half * 32, pk);
                 if (j > 0) {
-                    wait(&o_done, (ns - 1) & 1);  // O may be rescaled
+                    wait(&o_done[(ns - 1) & 1], ((ns - 1) >> 1) & 1);  // O may be rescaled
                     if (!ok)
                         continue;
                     tc_fence_after();
@@ -1006,7 +1014,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 if (lane == 0)
                     mbar_arrive(smem_addr(&p_full));
             }
-            wait(&o_done, (ns - 1) & 1);
+            wait(&o_done[(ns - 1) & 1], ((ns - 1) >> 1) & 1);
             // the row's exp-sum from both halves, then each half writes its columns
             // (through the last stage's slot: its readers are done, since o_done
             // came after every warp's p_full, and the next stage takes the other)

@@ -32,8 +32,9 @@ namespace pgd {
 
 namespace {
 
-constexpr int kTreeThreads = 352;  // K copies, products, 8 softmax warps, V copies
-constexpr int kTreeVWarp = 10;
+// warp 0 K copies, 1 scores, 2-9 softmax, 10 V copies, 11 outputs
+constexpr int kTreeThreads = 384;
+constexpr int kTreeVWarp = 10, kTreeOWarp = 11;
 constexpr int kTreeWords = kTreeMaxNodes / 32;
 
 template <int D> constexpr size_t tree_smem_bytes()
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
     extern __shared__ uint8_t dyn_smem[];
     __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV],
-        v_empty[NV], s_full[2], p_full, o_done, o_free, mma_done;
+        v_empty[NV], s_full[2], p_full, o_done[2], o_free, mma_done;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag;
     __shared__ float pair_red[2][2][128];  // [parity][half][row]: the halves' exchange
@@ -250,9 +251,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         mbar_init(smem_addr(&s_full[0]), 1);
         mbar_init(smem_addr(&s_full[1]), 1);
         mbar_init(smem_addr(&p_full), 8);
-        mbar_init(smem_addr(&o_done), 1);
+        mbar_init(smem_addr(&o_done[0]), 1);
+        mbar_init(smem_addr(&o_done[1]), 1);
         mbar_init(smem_addr(&o_free), 8);
-        mbar_init(smem_addr(&mma_done), 1);
+        mbar_init(smem_addr(&mma_done), 2);
         abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tmap_q);
@@ -398,12 +400,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                   p.wait_budget_ns);
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == kTreeOWarp) {
         if (lane == 0) {
             // ======================================================== products
-            const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
-            const uint64_t k_desc = tc_sdesc(k_s, 16, GROUP);
-            const uint64_t v_desc = tc_sdesc(v_s, 1024, GROUP);
+            // scores by one thread, outputs by another: a thread spends some
+            // 1400 cycles a stage on its barriers and commits, the products of
+            // a stage take about as long, and one thread for both would be
+            // slower than the copies
             bool ok = true;
             auto wait = [&](uint64_t *bar, int parity) {
                 if (ok && !mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns))
@@ -416,16 +419,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 else
                     tc_commit(smem_addr(bar));
             };
-            int ns = 0, np = 0, nq = 0, no = 0;  // S and P V products, Q tiles, units
-            for (; walk.more() && ok; walk.next(p)) {
-                const int nt = walk.t_end - walk.t;
-                wait(&q_full, nq & 1);
-                ++nq;
-                for (int j = -1; j < nt && ok; ++j) {
-                    if (j + 1 < nt) {
-                        // into the buffer of P(j - 1), whose product was issued before
+            if (warp == 1) {
+                const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
+                const uint64_t k_desc = tc_sdesc(k_s, 16, GROUP);
+                int ns = 0, nq = 0;  // S products, Q tiles
+                for (; walk.more() && ok; walk.next(p)) {
+                    wait(&q_full, nq & 1);
+                    ++nq;
+                    for (int t = walk.t; t < walk.t_end; ++t, ++ns) {
+                        // into the buffer of P(ns - 2), once its product is over
                         const int st = ns % NK;
-                        if (!wait(&k_full[st], (ns / NK) & 1))
+                        if ((ns >= 2 && !wait(&o_done[ns & 1], ((ns >> 1) & 1) ^ 1)) ||
+                            !wait(&k_full[st], (ns / NK) & 1))
                             break;
                         tc_fence_after();
                         const uint64_t ks = k_desc + ((st * KV_TILE) >> 4);
@@ -436,14 +441,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                    ks + (((kk / 4) * 1024 + (kk % 4) * 32) >> 4), IDESC_S, kk > 0);
                         tc_commit(smem_addr(&s_full[ns & 1]));
                         release(&k_empty[st]);
-                        if (j + 2 == nt)
-                            tc_commit(smem_addr(&q_empty));
-                        ++ns;
                     }
-                    if (j >= 0) {
+                    tc_commit(smem_addr(&q_empty));
+                }
+            } else {
+                const uint64_t v_desc = tc_sdesc(v_s, 1024, GROUP);
+                int np = 0, no = 0;  // P V products, units
+                for (; walk.more() && ok; walk.next(p)) {
+                    // the last unit's output has been read
+                    if (no++ && !wait(&o_free, no & 1))
+                        break;
+                    for (int t = walk.t; t < walk.t_end; ++t, ++np) {
                         const int st = np % NV;
-                        if (j == 0 && no++ && !wait(&o_free, no & 1))
-                            break;
                         if (!wait(&v_full[st], (np / NV) & 1) || !wait(&p_full, np & 1))
                             break;
                         tc_fence_after();
@@ -452,10 +461,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < NT / 16; ++kk)
                             tc_mma_ta(tmem + O_COL, a + kk * 8, vs + ((kk * 2 * GROUP) >> 4),
-                                      IDESC_O, j > 0 || kk > 0);
-                        tc_commit(smem_addr(&o_done));
+                                      IDESC_O, t > walk.t || kk > 0);
+                        tc_commit(smem_addr(&o_done[np & 1]));
                         release(&v_empty[st]);
-                        ++np;
                     }
                 }
             }
@@ -608,7 +616,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 else
                     tc_st16u(t_lane + s_col + half * 16, pk);
                 if (t > walk.t) {
-                    wait(&o_done, (ns - 1) & 1);  // O may be rescaled
+                    wait(&o_done[(ns - 1) & 1], ((ns - 1) >> 1) & 1);  // O may be rescaled
                     if (!ok)
                         continue;
                     tc_fence_after();
@@ -649,7 +657,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (lane == 0)
                     mbar_arrive(smem_addr(&p_full));
             }
-            wait(&o_done, (ns - 1) & 1);
+            wait(&o_done[(ns - 1) & 1], ((ns - 1) >> 1) & 1);
             // the row's exp-sum from both halves, then each half writes its
             // columns (through the last stage's slot: its readers are done,
             // since o_done came after every warp's p_full, and the next stage
