@@ -59,7 +59,7 @@ struct DeviceState {
     cudaError_t init_error = cudaSuccess;
     int num_sms = 0;
     int ctas[3][3][5] = {};         // [kind: fp16, quantised, MQ][head_dim 64/128/256][block size]
-    int tree_clusters[3][3] = {};   // [head_dim][cluster of 1, 2, 4 CTAs]
+    int tree_runs[3][2] = {};       // [head_dim][pairs]: resident runs of the tree kernel
     unsigned *err_word = nullptr;   // address of g_device_error on this device
     std::mutex pool_mu;             // the pool is made on first library-owned scratch
     cudaMemPool_t pool = nullptr;   //   (and again after pgd_release): stream-ordered scratch
@@ -101,9 +101,8 @@ cudaError_t init_device(int dev, DeviceState &st)
             if ((e = occupancy_d256(kBlockSizes[i], kind, &st.ctas[kind][2][i])) != cudaSuccess)
                 return e;
         }
-    for (int i = 0; i < 9; ++i)
-        if ((e = tree_clusters(64 << (i / 3), 1 << (i % 3), &st.tree_clusters[i / 3][i % 3])) !=
-            cudaSuccess)
+    for (int i = 0; i < 6; ++i)
+        if ((e = tree_resident(64 << (i / 2), i % 2, &st.tree_runs[i / 2][i % 2])) != cudaSuccess)
             return e;
     if ((e = prefill_set_up()) != cudaSuccess)
         return e;
@@ -407,7 +406,7 @@ pgd_status group_blocks(const CacheGeom &g, long long *u, long long *blocks)
 }
 
 pgd_status encode_cache_map_groups(CUtensorMap *map, const void *base, const CacheGeom &g,
-                                   int box_groups)
+                                   int box_groups, int box_slabs = 0)
 {
     EncodeTiledFn fn;
     pgd_status st = encode_fn(&fn);
@@ -419,7 +418,8 @@ pgd_status encode_cache_map_groups(CUtensorMap *map, const void *base, const Cac
     cuuint64_t dims[5] = {64, 8, (cuuint64_t)(g.D / 64), (cuuint64_t)(g.BS / 8), (cuuint64_t)blocks};
     cuuint64_t strides[4] = {(cuuint64_t)g.token_stride * 2, 128, (cuuint64_t)g.token_stride * 16,
                              (cuuint64_t)u * 2};
-    cuuint32_t box[5] = {64, 8, (cuuint32_t)(g.D / 64), (cuuint32_t)box_groups, 1};
+    cuuint32_t box[5] = {64, 8, (cuuint32_t)(box_slabs ? box_slabs : g.D / 64),
+                         (cuuint32_t)box_groups, 1};
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void *>(base), dims,
                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -554,7 +554,7 @@ pgd_status cache_maps(const void *k, const void *v, const CacheGeom &geom, int b
     // kinds: 0 fp16 rows, 1 fp16 8-row groups, 2 codes, 3 head-major pairs,
     // 6 pairs of 16-byte rows at any strides; both arrays in one map: 4
     // codes (head-major), 5 head-major pairs, 7 pairs of 16-byte rows, 8
-    // codes with adjacent heads
+    // codes with adjacent heads; 9 fp16 8-row groups, K and V in pieces of their own
     if (kind == 4 || kind == 5 || kind == 7 || kind == 8) {
         const uintptr_t ka = reinterpret_cast<uintptr_t>(k), va = reinterpret_cast<uintptr_t>(v);
         const long long stride = (long long)(ka < va ? va - ka : ka - va);
@@ -578,6 +578,10 @@ pgd_status cache_maps(const void *k, const void *v, const CacheGeom &geom, int b
             return encode_code_map(m, base, geom, box);
         case 6:
             return encode_meta_rows_map(m, base, 0, geom, box);
+        case 9:  // (slabs of a K and a V copy, 8-row groups of a K and a V copy)
+            return m == &c.tk
+                       ? encode_cache_map_groups(m, base, geom, (box >> 8) & 255, box & 15)
+                       : encode_cache_map_groups(m, base, geom, box >> 16, (box >> 4) & 15);
         default:
             return encode_meta_map(m, base, geom, box);
         }
@@ -1336,13 +1340,13 @@ HostStaging host_staging(int S, int Hq, int D, int MB)
 
 // ------------------------------------------------------------------ trees of drafted tokens
 struct TreePlan {
-    int G, TQ, cs, clusters, NT;
+    int G, TQ, cs, runs;
     size_t ws_bytes, off_ml, off_cut;  // pieces' outputs, (maximum, exp-sum)s, cuts
 };
 
-// A cluster has as many CTAs as the largest tree has 128-row tiles (1, 2 or 4:
-// tiles past the fourth are further groups); as many clusters as are resident
-// at once, or as there can be stages.
+// Trees of more than one 128-row tile are worked on by pairs of CTAs (head_dim 128
+// and 256; tiles past the second are further units); as many runs of the work as
+// are resident at once, or as there can be stages.
 pgd_status make_tree_plan(int S, int total_q, int max_q, int Hq, int Hkv, int D, int BS, int MB,
                           TreePlan *tp)
 {
@@ -1369,21 +1373,45 @@ pgd_status make_tree_plan(int S, int total_q, int max_q, int Hq, int Hkv, int D,
         return st;
     tp->G = Hq / Hkv;
     tp->TQ = 128 / tp->G;
-    tp->NT = D == 64 ? TreeShape<64>::NT : D == 128 ? TreeShape<128>::NT : TreeShape<256>::NT;
     const int tiles = std::max(1, (max_q + tp->TQ - 1) / tp->TQ);
-    const int c = tiles == 1 ? 0 : tiles == 2 ? 1 : 2;
-    tp->cs = 1 << c;
-    const int resident = ds->tree_clusters[d_index(D)][c];
+    const int resident = ds->tree_runs[d_index(D)][tiles > 1 && D > 64];
+    tp->cs = tiles > 1 && D > 64 ? 2 : 1;
     if (resident < 1)
-        return fail(PGD_ERR_UNSUPPORTED, "a cluster of %d thread blocks does not fit", tp->cs);
+        return fail(PGD_ERR_UNSUPPORTED, "the tree kernel does not fit on this device");
     const long long stages = (long long)S * Hkv * ((tiles + tp->cs - 1) / tp->cs) *
-                             (((long long)MB * BS + tp->NT - 1) / tp->NT);
-    tp->clusters = (int)std::max(1ll, std::min<long long>(resident, stages));
-    const size_t rows = (size_t)2 * tp->clusters * tp->cs * 128;
+                             (((long long)MB * BS + kTreeNT - 1) / kTreeNT);
+    tp->runs = (int)std::max(1ll, std::min<long long>(resident, stages));
+    const size_t rows = (size_t)2 * tp->runs * tp->cs * 128;
     tp->off_ml = align256(rows * D * 4);
     tp->off_cut = tp->off_ml + align256(rows * 8);
-    tp->ws_bytes = S && total_q ? tp->off_cut + align256((size_t)tp->clusters * 16) : 0;
+    tp->ws_bytes = S && total_q ? tp->off_cut + align256((size_t)tp->runs * 16) : 0;
     return PGD_OK;
+}
+
+// What a copy of the tree kernel's brings: tokens at most and slabs, of K and V.
+struct TreeCopies {
+    int k_keys, k_slabs, v_keys, v_slabs;
+};
+template <int D, bool PAIR> TreeCopies tree_copies_of()
+{
+    using T = TreePieces<D, PAIR>;
+    return {T::KKEYS, T::KSLABS, T::VKEYS, T::VSLABS};
+}
+TreeCopies tree_copies(int D, bool pair)
+{
+    return D == 64    ? tree_copies_of<64, false>()
+           : D == 128 ? (pair ? tree_copies_of<128, true>() : tree_copies_of<128, false>())
+                      : (pair ? tree_copies_of<256, true>() : tree_copies_of<256, false>());
+}
+
+// The page-group views of K and V that the tree kernel copies from, kept with
+// the other kinds' (kind 9: `box` holds the four sizes).
+pgd_status tree_maps(const void *k, const void *v, const CacheGeom &geom, const TreeCopies &copies,
+                     int k_groups, int v_groups, const CUtensorMap **tk, const CUtensorMap **tv)
+{
+    return cache_maps(k, v, geom,
+                      copies.k_slabs | copies.v_slabs << 4 | k_groups << 8 | v_groups << 16, 9, tk,
+                      tv);
 }
 
 pgd_status run_tree(void *out, bool half, const uint16_t *q, const int32_t *cu_q,
@@ -1425,10 +1453,12 @@ pgd_status run_tree(void *out, bool half, const uint16_t *q, const int32_t *cu_q
     const CacheGeom geom = {NB, Hkv, BS, D, kv_strides.page, kv_strides.head, kv_strides.token};
     const CUtensorMap *tk = nullptr, *tv = nullptr;
     long long blk_u, blk_n;
-    const int box_rows = std::min(BS, tp.NT / tp.cs);
+    // a copy is a page of a piece (or the piece, where pages are longer)
+    const TreeCopies copies = tree_copies(D, tp.cs == 2);
+    const int k_rows = std::min(BS, copies.k_keys), v_rows = std::min(BS, copies.v_keys);
     if ((st = group_blocks(geom, &blk_u, &blk_n)) ||
         (st = encode_q_map(&tq, q, total_q, Hq, D, tp.G, tp.TQ)) ||
-        (st = cache_maps(k_cache, v_cache, geom, box_rows / 8, 1, &tk, &tv)))
+        (st = tree_maps(k_cache, v_cache, geom, copies, k_rows / 8, v_rows / 8, &tk, &tv)))
         return st;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
     cudaError_t e;
@@ -1465,8 +1495,9 @@ pgd_status run_tree(void *out, bool half, const uint16_t *q, const int32_t *cu_q
     p.BS = BS;
     p.log2BS = 3 + bs_index(BS);
     p.cs = tp.cs;
-    p.clusters = tp.clusters;
-    p.box_rows = box_rows;
+    p.runs = tp.runs;
+    p.k_rows = k_rows;
+    p.v_rows = v_rows;
     p.blk_page = (int)(kv_strides.page / blk_u);
     p.blk_head = (int)(kv_strides.head / blk_u);
     p.wait_budget_ns = kWaitBudgetNs;

@@ -250,19 +250,36 @@ struct VarlenParams {
 // Attention of trees of drafted tokens over the paged cache (pgd_tree.cu).
 constexpr unsigned kErrTree = 32u;     // a parent that is not an earlier node of its tree
 constexpr int kTreeMaxNodes = 256;     // nodes of one sequence's tree
-constexpr int kTreeMaxCluster = 4;     // tiles that share a cluster's K and V stages
 
-// Tokens per K or V stage, and stages of each ring, per head_dim (beside the Q
-// tile and the trees' bits in 227 KB).
-template <int D> struct TreeShape;
-template <> struct TreeShape<64> {
-    static constexpr int NT = 128, NK = 4, NV = 4;
+// A stage is kTreeNT tokens.  With trees of more than one tile (head_dim 128 and
+// 256) two CTAs work on two tiles as a pair of the tensor cores, each copying half
+// of every stage: half of K's tokens, half of V's head_dim.  KP, VP: the pieces in
+// which a CTA's part of K and of V is copied and used; NK, NV: pieces in the rings
+// (what 227 KB leave beside the Q tile and the trees' bits).
+constexpr int kTreeNT = 128;
+template <int D, bool PAIR> struct TreeShape;
+template <> struct TreeShape<64, false> {
+    static constexpr int KP = 1, VP = 1, NK = 4, NV = 4;
 };
-template <> struct TreeShape<128> {
-    static constexpr int NT = 128, NK = 2, NV = 3;
+template <> struct TreeShape<128, false> {
+    static constexpr int KP = 1, VP = 1, NK = 2, NV = 3;
 };
-template <> struct TreeShape<256> {
-    static constexpr int NT = 64, NK = 2, NV = 2;
+template <> struct TreeShape<256, false> {  // K by 64-wide slabs, V by 32 tokens
+    static constexpr int KP = 4, VP = 4, NK = 5, NV = 4;
+};
+template <> struct TreeShape<128, true> {
+    static constexpr int KP = 1, VP = 1, NK = 4, NV = 6;
+};
+template <> struct TreeShape<256, true> {   // K by two slabs, V by 64 tokens
+    static constexpr int KP = 2, VP = 2, NK = 4, NV = 5;
+};
+// Tokens of K and slabs of V that a CTA copies of a stage, and slabs of a K piece
+// and tokens of a V piece.
+template <int D, bool PAIR> struct TreePieces {
+    using S = TreeShape<D, PAIR>;
+    static constexpr int KKEYS = PAIR ? kTreeNT / 2 : kTreeNT, KSLABS = D / 64 / S::KP;
+    static constexpr int VSLABS = PAIR ? D / 128 : D / 64, VKEYS = kTreeNT / S::VP;
+    static constexpr int K_BYTES = KKEYS * KSLABS * 128, V_BYTES = VKEYS * VSLABS * 128;
 };
 
 struct TreeParams {
@@ -272,22 +289,22 @@ struct TreeParams {
     const int32_t *parents;       // [total_q] parent node of each row, negative: none
     const int32_t *block_tables;  // [S][MB]
     const int32_t *seq_lens;      // [S]
-    // scratch: the pieces of the units that are cut, two per cluster, each 128
-    // rows per tile of the cluster, and where the cut units begin
-    float *part_o;                // [2 * clusters][cs][128][D] sums of p v
-    float2 *part_ml;              // [2 * clusters][cs][128] (reference maximum, exp-sum)
-    int4 *cut;                    // [clusters] {sequence or -1, KV head, tile group, last cluster}
+    // scratch: the pieces of the units that are cut, two per run, each 128 rows
+    // per tile of the unit, and where the cut units begin
+    float *part_o;                // [2 * runs][cs][128][D] sums of p v
+    float2 *part_ml;              // [2 * runs][cs][128] (reference maximum, exp-sum)
+    int4 *cut;                    // [runs] {sequence or -1, KV head, tile group, last run}
     unsigned *err;
     float scale_log2;
     int S, Hq, Hkv, G, TQ, total_q, max_q, MB, NB, BS, log2BS;
-    int cs, clusters;             // CTAs of a cluster (tiles that share stages), clusters
-    int box_rows;                 // tokens of one page copy
+    int cs, runs;                 // tiles (CTAs) that work together, 1 or 2; runs of work
+    int k_rows, v_rows;           // tokens of one page copy of K and of V
     int blk_page, blk_head;       // (page, KV head) -> block coordinate of the K/V maps
     uint64_t wait_budget_ns;
 };
-// Clusters of cs CTAs that are resident at once on the current device (also the
-// kernel's set-up there: once before its launches).
-cudaError_t tree_clusters(int head_dim, int cs, int *clusters);
+// Runs that are resident at once on the current device, of one CTA or of a pair (0
+// where no kernel is built); also the kernel's set-up there, once before its launches.
+cudaError_t tree_resident(int head_dim, bool pair, int *runs);
 cudaError_t launch_tree(int head_dim, const CUtensorMap &tq, const CUtensorMap &tk,
                         const CUtensorMap &tv, const TreeParams &p, cudaStream_t stream);
 

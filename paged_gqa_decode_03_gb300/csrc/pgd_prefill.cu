@@ -19,16 +19,6 @@ namespace pgd {
 
 namespace {
 
-// Registers per thread of a warpgroup (its four warps together).
-template <int N> __device__ __forceinline__ void regs_give()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N> __device__ __forceinline__ void regs_take()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 constexpr int kNT = 128;               // keys per stage
 constexpr int kSlab = 128 * 128;       // bytes of 128 rows of one 64-wide slab of head_dim
 

@@ -12,18 +12,27 @@
 // Every K and V byte serves at most a few hundred rows, so the call is bound by
 // the K and V bytes from HBM; everything below is about keeping all SMs reading
 // until the end:
-//   * A unit is one (sequence, KV head, group of tiles); a tile is 128 rows (TQ =
-//     128 / G nodes x the G heads of the KV head).  Where trees have more rows
-//     than one tile, the tiles of a group are the CTAs of a cluster: each loads
-//     its share of every stage and multicasts it to all, so that a byte leaves
-//     L2 once for the group.
+//   * A unit is one (sequence, KV head, one or two tiles); a tile is 128 rows (TQ =
+//     128 / G nodes x the G heads of the KV head).  An SM takes in some 55 GB/s
+//     whatever the copies, 152 of them 8.3 TB/s: little more than HBM gives, so a
+//     byte must not go to two SMs.  Where trees have more rows than one tile,
+//     two CTAs work on two tiles as a pair (tcgen05 cta_group::2): one product of
+//     256 rows, whose B operand is split over the two, so that each copies half of
+//     every stage (half of K's tokens, half of V's head_dim) and both use all of it.
+//     (Two CTAs of a cluster that each hold all of a stage, copied by multicast:
+//     338 us against HBM's 201 on 32 sequences of 8 k to 32 k tokens at
+//     head_dim 256.)
 //   * The stages of all units, one after the other, are cut into equal runs, one
-//     per resident cluster: no cluster has more than a stage more than another,
-//     whatever the lengths.  A unit that is cut leaves pieces (reference maximum,
-//     exp-sum, unscaled output; at most two per cluster, so the scratch does not
-//     grow with the batch), which a second kernel joins.
+//     per resident CTA or pair: no run has more than another, whatever the
+//     lengths.  A unit that is cut leaves pieces (reference maximum, exp-sum,
+//     unscaled output; at most two per run, so the scratch does not grow with the
+//     batch), which a second kernel joins.
 //   * The K and V rings run on from unit to unit, so a unit's start and end
 //     pass while the next unit's stages are already coming in.
+//   * Scores and outputs are issued by a thread each: a thread spends some 1400
+//     cycles a stage on its barriers and commits, the products of a stage take
+//     about as long, and one thread for both was slower than the copies
+//     (2900 cycles a stage at head_dim 128, of which HBM leaves 3040).
 #include "pgd_device.cuh"
 #include "pgd_internal.h"
 #include "pgd_rows.cuh"
@@ -32,15 +41,15 @@ namespace pgd {
 
 namespace {
 
-// warp 0 K copies, 1 scores, 2-9 softmax, 10 V copies, 11 outputs
+// warp 0 Q and K copies, 1 V copies, 2 scores, 3 outputs, 4-11 softmax
 constexpr int kTreeThreads = 384;
-constexpr int kTreeVWarp = 10, kTreeOWarp = 11;
+constexpr int kTreeVWarp = 1, kTreeSWarp = 2, kTreeOWarp = 3;
 constexpr int kTreeWords = kTreeMaxNodes / 32;
 
-template <int D> constexpr size_t tree_smem_bytes()
+template <int D, bool PAIR> constexpr size_t tree_smem_bytes()
 {
-    return size_t(128) * D * 2 +
-           size_t(TreeShape<D>::NK + TreeShape<D>::NV) * TreeShape<D>::NT * D * 2 + 1024;
+    return size_t(128) * D * 2 + size_t(TreeShape<D, PAIR>::NK) * TreePieces<D, PAIR>::K_BYTES +
+           size_t(TreeShape<D, PAIR>::NV) * TreePieces<D, PAIR>::V_BYTES + 1024;
 }
 
 // Ancestor bits: bit j of row i is set where node i sees node j.  Nine words a
@@ -113,7 +122,7 @@ struct TreeSeq {
     bool bad;
 };
 
-template <int NT> __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s)
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s)
 {
     TreeSeq q;
     const int maxlen = p.MB << p.log2BS;
@@ -124,50 +133,69 @@ template <int NT> __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &
     q.bad = q.n < 0 || q.n > q.L || q.n > p.max_q || q.row0 < 0 || q.row0 > p.total_q - q.n;
     if (q.bad)
         q.n = 0;
-    q.T = (q.L + NT - 1) / NT;
+    q.T = (q.L + kTreeNT - 1) / kTreeNT;
     q.groups = ((q.n + p.TQ - 1) / p.TQ + p.cs - 1) / p.cs;
     return q;
 }
-__device__ __forceinline__ long long tree_stages(const TreeParams &p, const TreeSeq &q)
+// What a unit counts in the division of the work: its stages, and as much again
+// as a unit costs beside them (its start and end: measured at 2800 to 4100 cycles,
+// a stage being some 2900).
+constexpr int kTreeUnitCost = 1;
+__device__ __forceinline__ long long tree_cost(const TreeParams &p, const TreeSeq &q)
 {
-    return (long long)q.groups * p.Hkv * q.T;
+    return q.T ? (long long)q.groups * p.Hkv * (q.T + kTreeUnitCost) : 0;
 }
 
-// The cluster's run through the stages of all units, a unit (or the part of it
-// that the run holds) at a time.  Every role walks its own copy.
-template <int NT> struct TreeWalk {
+// A run [x0, x1) of the cost of all units, a unit (or the part of it that the
+// run holds) at a time: stage t of a unit that begins at cost c lies at c +
+// kTreeUnitCost + t, so a cut before it begins the unit in the next run.  Every
+// role walks its own copy.
+struct TreeWalk {
     TreeSeq q;
-    int s, v, t, t_end;      // sequence, unit within it, stages [t, t_end)
-    long long left;          // stages of the run from t on
+    int s, v, t, t_end;  // sequence, unit within it, stages [t, t_end)
+    long long at, x1;    // where unit v begins, and the run's end
 
-    __device__ __forceinline__ TreeWalk(const TreeParams &p, int s0, long long skip, long long run)
+    __device__ __forceinline__ TreeWalk(const TreeParams &p, int s0, long long begin, long long x0,
+                                        long long x1_)
     {
         s = s0;
-        left = run;
-        t = t_end = v = 0;
-        if (left <= 0)
+        x1 = at = x1_;
+        v = t = t_end = 0;
+        if (x0 >= x1)
             return;
-        q = tree_seq<NT>(p, s);
-        v = (int)(skip / q.T);
-        t = (int)(skip - (long long)v * q.T);
-        t_end = (int)min((long long)q.T, t + left);
+        q = tree_seq(p, s);  // begin: where the sequence's first unit begins
+        v = (int)((x0 - begin) / (q.T + kTreeUnitCost));
+        at = begin + (long long)v * (q.T + kTreeUnitCost);
+        t = (int)max(0ll, x0 - at - kTreeUnitCost);
+        set_end();
     }
-    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void set_end()
+    {
+        t_end = (int)min((long long)q.T, x1 - at - kTreeUnitCost);
+        if (t_end <= t)  // the run ends before the unit's first stage
+            at = x1;
+    }
+    __device__ __forceinline__ bool more() const { return at < x1; }
     __device__ __forceinline__ int head() const { return v / q.groups; }
     __device__ __forceinline__ int group() const { return v % q.groups; }
     __device__ __forceinline__ void next(const TreeParams &p)
     {
-        left -= t_end - t;
-        if (left <= 0)
+        at += q.T + kTreeUnitCost;
+        if (at >= x1)
             return;
-        t = 0;  // stages are left, so the unit has ended
+        t = 0;
         if (++v == q.groups * p.Hkv) {
             v = 0;
             do
-                q = tree_seq<NT>(p, ++s);
-            while (tree_stages(p, q) == 0);
+                q = tree_seq(p, ++s);
+            while (tree_cost(p, q) == 0);
         }
-        t_end = (int)min((long long)q.T, left);
+        set_end();
+    }
+    // the run that holds the unit's last stage, of `runs` equal ones of `total`
+    __device__ __forceinline__ int last_run(long long total, int runs) const
+    {
+        return (int)(((at + q.T + kTreeUnitCost) * runs - 1) / total);
     }
 };
 
@@ -200,129 +228,151 @@ __device__ __forceinline__ long long block_prefix(long long x, long long *warp_s
 
 }  // namespace
 
-template <int D>
+template <int D, bool PAIR>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
                       const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const TreeParams p)
 {
-    constexpr int NT = TreeShape<D>::NT, NK = TreeShape<D>::NK, NV = TreeShape<D>::NV;
-    constexpr int SLABS = D / 64;
-    constexpr int GROUP = SLABS * 1024;  // one 8-row group of K or V, all slabs
-    constexpr int KV_TILE = NT * D * 2;
-    constexpr int Q_SLAB = 128 * 128;
+    using P = TreePieces<D, PAIR>;
+    constexpr int NT = kTreeNT, CS = PAIR ? 2 : 1;
+    constexpr int NK = TreeShape<D, PAIR>::NK, NV = TreeShape<D, PAIR>::NV;
+    constexpr int KP = TreeShape<D, PAIR>::KP, VP = TreeShape<D, PAIR>::VP;
+    static_assert(NK >= KP && NV >= VP, "a stage's pieces fit the rings");
+    constexpr int KKEYS = P::KKEYS, KSLABS = P::KSLABS, VKEYS = P::VKEYS, VSLABS = P::VSLABS;
+    constexpr int K_BYTES = P::K_BYTES, V_BYTES = P::V_BYTES;
+    constexpr int KGROUP = KSLABS * 1024, VGROUP = VSLABS * 1024;  // 8 rows of a piece
+    constexpr int SLABS = D / 64, Q_SLAB = 128 * 128;
     constexpr uint32_t O_COL = 0, S_COL = D;  // tensor memory: O, two score buffers
     static_assert(S_COL + 2 * NT <= 512, "tensor memory");
-    constexpr uint32_t IDESC_S = tc_idesc_f16(128, NT, 0, 0);
-    constexpr uint32_t IDESC_O = tc_idesc_f16(128, D, 0, 1);
+    constexpr uint32_t IDESC_S = tc_idesc_f16(128 * CS, NT, 0, 0);
+    constexpr uint32_t IDESC_O = tc_idesc_f16(128 * CS, D, 0, 1);
 
     extern __shared__ uint8_t dyn_smem[];
+    // (of a pair, the even CTA's q_full, k_full, v_full, p_full and o_free count for both)
     __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV],
-        v_empty[NV], s_full[2], p_full, o_done[2], o_free, mma_done;
+        v_empty[NV], v_here, s_full[2], p_full, o_done[2], o_free, mma_done;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag;
     __shared__ float pair_red[2][2][128];  // [parity][half][row]: the halves' exchange
     __shared__ TreeBits tree;
-    __shared__ long long warp_sum[kTreeThreads / 32], run_skip;
+    __shared__ long long warp_sum[kTreeThreads / 32], run_begin;
     __shared__ int run_seq;
 
     const uint32_t dyn_base = smem_addr(dyn_smem);
     const uint32_t base = (dyn_base + 1023u) & ~1023u;
     uint8_t *const base_ptr = dyn_smem + (base - dyn_base);
-    const uint32_t q_s = base, k_s = q_s + 128 * D * 2, v_s = k_s + NK * KV_TILE;
-    uint8_t *const v_ptr = base_ptr + 128 * D * 2 + NK * KV_TILE;
+    const uint32_t q_s = base, k_s = q_s + 128 * D * 2, v_s = k_s + NK * K_BYTES;
+    uint8_t *const v_ptr = base_ptr + 128 * D * 2 + NK * K_BYTES;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = p.cs > 1 ? (int)cluster_rank() : 0;
-    const int cluster = (int)blockIdx.x / p.cs;
-    const uint16_t everyone = (uint16_t)((1u << p.cs) - 1u);
+    const int rank = PAIR ? (int)cluster_rank() : 0;
+    const int run = (int)blockIdx.x / CS;
     if (threadIdx.x == 0) {
         mbar_init(smem_addr(&q_full), 1);
         mbar_init(smem_addr(&q_empty), 1);
-        // a stage's place is free once every CTA that it is copied to has used it
         for (int i = 0; i < NK; ++i) {
             mbar_init(smem_addr(&k_full[i]), 1);
-            mbar_init(smem_addr(&k_empty[i]), p.cs);
+            mbar_init(smem_addr(&k_empty[i]), 1);
         }
         for (int i = 0; i < NV; ++i) {
             mbar_init(smem_addr(&v_full[i]), 1);
-            mbar_init(smem_addr(&v_empty[i]), p.cs);
+            mbar_init(smem_addr(&v_empty[i]), 1);
         }
         mbar_init(smem_addr(&s_full[0]), 1);
         mbar_init(smem_addr(&s_full[1]), 1);
-        mbar_init(smem_addr(&p_full), 8);
+        mbar_init(smem_addr(&p_full), 8 * CS);
         mbar_init(smem_addr(&o_done[0]), 1);
         mbar_init(smem_addr(&o_done[1]), 1);
-        mbar_init(smem_addr(&o_free), 8);
+        mbar_init(smem_addr(&o_free), 8 * CS);
         mbar_init(smem_addr(&mma_done), 2);
+        mbar_init(smem_addr(&v_here), 1);
         abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tmap_q);
         prefetch_tensormap(&tmap_k);
         prefetch_tensormap(&tmap_v);
     }
-    if (warp == 1)
-        tc_alloc(smem_addr(&tmem_base_s), 512);
+    if (warp == 0) {
+        if constexpr (PAIR)
+            tc_alloc_pair(smem_addr(&tmem_base_s), 512);
+        else
+            tc_alloc(smem_addr(&tmem_base_s), 512);
+    }
 
-    // ---- the run: stages [x0, x1) of all; the sequence that holds x0
-    long long total = 0;
+    // ---- the run: [x0, x1) of the cost of all units; the sequence that holds x0
+    long long total = 0, mine = 0, before = 0;  // before: this thread's (last) sequence
     for (int s0 = 0; s0 < p.S; s0 += kTreeThreads) {
         const int s = s0 + (int)threadIdx.x;
-        long long mine = 0, all;
+        long long all;
+        mine = 0;
         if (s < p.S) {
-            const TreeSeq q = tree_seq<NT>(p, s);
+            const TreeSeq q = tree_seq(p, s);
             if (q.bad && blockIdx.x == 0)
                 atomicOr(p.err, kErrQueryLen);
-            mine = tree_stages(p, q);
+            mine = tree_cost(p, q);
         }
-        block_prefix(mine, warp_sum, &all);
+        before = total + block_prefix(mine, warp_sum, &all);
         total += all;
     }
-    const long long x0 = total * cluster / p.clusters, x1 = total * (cluster + 1) / p.clusters;
-    if (x1 > x0) {
-        long long before = 0;
-        for (int s0 = 0; s0 < p.S && before <= x0; s0 += kTreeThreads) {
+    const long long x0 = total * run / p.runs, x1 = total * (run + 1) / p.runs;
+    if (x1 > x0 && p.S <= kTreeThreads) {
+        if (mine > 0 && before <= x0 && x0 < before + mine) {
+            run_seq = (int)threadIdx.x;
+            run_begin = before;
+        }
+    } else if (x1 > x0) {
+        long long past = 0;
+        for (int s0 = 0; s0 < p.S && past <= x0; s0 += kTreeThreads) {
             const int s = s0 + (int)threadIdx.x;
-            const long long mine = s < p.S ? tree_stages(p, tree_seq<NT>(p, s)) : 0;
+            const long long here = s < p.S ? tree_cost(p, tree_seq(p, s)) : 0;
             long long all;
-            const long long at = before + block_prefix(mine, warp_sum, &all);
-            if (mine > 0 && at <= x0 && x0 < at + mine) {
+            const long long at = past + block_prefix(here, warp_sum, &all);
+            if (here > 0 && at <= x0 && x0 < at + here) {
                 run_seq = s;
-                run_skip = x0 - at;
+                run_begin = at;
             }
-            before += all;
+            past += all;
         }
     }
     tc_fence_before();
-    if (p.cs > 1)
-        cluster_sync();  // every CTA's barriers exist
+    if constexpr (PAIR)
+        cluster_sync();  // both CTAs' barriers exist
     else
         __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
     griddep_launch_dependents();
-    TreeWalk<NT> walk(p, x1 > x0 ? run_seq : 0, x1 > x0 ? run_skip : 0, x1 - x0);
+    TreeWalk walk(p, x1 > x0 ? run_seq : 0, x1 > x0 ? run_begin : 0, x0, x1);
 
     auto give_up = [&]() {
         if (!abort_flag)
             atomicOr(p.err, kErrTimeout);
         abort_flag = 1;
     };
+    // a barrier of the CTA that issues the products
+    auto lead = [&](uint64_t *bar) {
+        return PAIR ? cluster_addr(smem_addr(bar), 0) : smem_addr(bar);
+    };
 
-    if (warp == 0 || warp == kTreeVWarp) {
+    if (warp < 4) {
+      regs_give<104>();  // to the softmax warps (128 x 104 + 256 x 200 of 384 x 168)
+      if (warp == 0 || warp == kTreeVWarp) {
         // ============================================================ copies
-        // warp 0: Q tiles and K, warp 10: V.  A stage is a copy per page (or
-        // part of one); the cluster's CTAs take equal shares of them, lane c
-        // the share's copy c.
+        // warp 0: Q tiles and K, warp 1: V.  A piece is a copy per page (or one
+        // copy, where pages are longer): lane c issues copy c.
         const bool is_v = warp == kTreeVWarp;
         const uint64_t pol = l2_evict_first_policy();
         const CUtensorMap *map = is_v ? &tmap_v : &tmap_k;
         uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
-        const int slots = is_v ? NV : NK;
+        const int slots = is_v ? NV : NK, bytes = is_v ? V_BYTES : K_BYTES;
         const uint32_t ring = is_v ? v_s : k_s;
-        const int share = NT / p.box_rows / p.cs;
-        const int copy = rank * share + lane;  // this lane's copy
-        const int from = copy * p.box_rows;    // its first token within a stage
+        const int rows = is_v ? p.v_rows : p.k_rows;
+        const int copies = (is_v ? VKEYS : KKEYS) / rows;
+        // this lane's first token of a piece, and its place there; of a pair, K's
+        // second half of the tokens belongs to the odd CTA
+        const int row = lane * rows, from = row + (is_v ? 0 : rank * KKEYS % NT);
+        const uint32_t place = (row / 8) * (is_v ? VGROUP : KGROUP);
         int nst = 0, nq = 0;
         bool ok = true;
         for (; walk.more() && ok; walk.next(p)) {
@@ -330,157 +380,183 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const int g = walk.head();
             const int npages = (q.L + p.BS - 1) >> p.log2BS;
             const int32_t *bt = p.block_tables + (size_t)walk.s * p.MB;
-            auto block_of = [&](int t) -> int {  // block coordinate, -1: none (reads zeros)
-                const int pg = (t * NT + from) >> p.log2BS;
+            auto block_of = [&](int token) -> int {  // block coordinate, -1: none (reads zeros)
+                const int pg = (token + from) >> p.log2BS;
                 int b = -1;
-                if (lane < share && pg < npages) {
+                if (lane < copies && pg < npages) {
                     const int id = __ldg(bt + pg);
                     if ((unsigned)id < (unsigned)p.NB)
                         b = id * p.blk_page + g * p.blk_head;
-                    else if (!is_v)
+                    else
                         atomicOr(p.err, kErrPageRange);
                 }
                 return b;
             };
-            int blk_next = block_of(walk.t);
-            for (int t = walk.t; t < walk.t_end; ++t) {
-                const int st = nst % slots;
+            // K's pieces are slabs of a stage's tokens, V's are tokens
+            const int step = is_v ? VKEYS : NT, end = walk.t_end * NT;
+            int blk_next = block_of(walk.t * NT);
+            for (int token = walk.t * NT; token < end && ok; token += step) {
                 const int blk = blk_next;
-                if (t + 1 < walk.t_end)
-                    blk_next = block_of(t + 1);  // in flight while this stage waits
-                bool w = true;
-                if (lane == 0)
-                    w = mbar_wait_bounded(smem_addr(&empty[st]), ((nst / slots) & 1) ^ 1,
-                                          &abort_flag, p.wait_budget_ns);
-                ok = __shfl_sync(~0u, w, 0);
-                if (!ok)
-                    break;
-                const uint32_t bar = smem_addr(&full[st]);
-                if (lane == 0)
-                    mbar_arrive_expect_tx(bar, KV_TILE);
-                __syncwarp();
-                if (lane < share) {
-                    const uint32_t dst = ring + st * KV_TILE + (from / 8) * GROUP;
-                    const int grp = ((t * NT + from) & (p.BS - 1)) >> 3;
-                    if (p.cs > 1)
-                        tma_load_5d_multicast(dst, map, 0, 0, 0, grp, blk, bar, everyone, pol);
-                    else
-                        tma_load_5d(dst, map, 0, 0, 0, grp, blk, bar, pol);
+                if (token + step < end)
+                    blk_next = block_of(token + step);  // in flight while this one waits
+                const int grp = ((token + from) & (p.BS - 1)) >> 3;
+                for (int kp = 0; kp < (is_v ? 1 : KP); ++kp, ++nst) {
+                    const int st = nst % slots;
+                    bool w = true;
+                    if (lane == 0)
+                        w = mbar_wait_bounded(smem_addr(&empty[st]), ((nst / slots) & 1) ^ 1,
+                                              &abort_flag, p.wait_budget_ns);
+                    ok = __shfl_sync(~0u, w, 0);
+                    if (!ok)
+                        break;
+                    if (lane == 0 && rank == 0)  // for both CTAs' copies
+                        mbar_arrive_expect_tx(smem_addr(&full[st]), CS * bytes);
+                    __syncwarp();
+                    if (lane < copies) {
+                        const uint32_t dst = ring + st * bytes + place;
+                        const int slab = is_v ? rank * VSLABS : kp * KSLABS;
+                        if constexpr (PAIR)
+                            tma_load_5d_pair(dst, map, 0, 0, slab, grp, blk, lead(&full[st]), pol);
+                        else
+                            tma_load_5d(dst, map, 0, 0, slab, grp, blk, smem_addr(&full[st]), pol);
+                    }
                 }
-                ++nst;
-                if (!is_v && t == walk.t) {
+                if (ok && !is_v && token == walk.t * NT) {
                     // Q after the unit's first K: its place is free only after
                     // the last unit's last scores
+                    bool w = true;
                     if (lane == 0) {
                         w = mbar_wait_bounded(smem_addr(&q_empty), (nq & 1) ^ 1, &abort_flag,
                                               p.wait_budget_ns);
                         if (w) {
-                            const uint32_t qb = smem_addr(&q_full);
-                            mbar_arrive_expect_tx(qb, SLABS * p.TQ * p.G * 128);
-                            const int tile = walk.group() * p.cs + rank;
-                            for (int sl = 0; sl < SLABS; ++sl)
-                                tma_load_4d(q_s + sl * Q_SLAB, &tmap_q, 0, g * p.G,
-                                            q.row0 + tile * p.TQ, sl, qb);
+                            if (rank == 0)
+                                mbar_arrive_expect_tx(smem_addr(&q_full),
+                                                      CS * SLABS * p.TQ * p.G * 128);
+                            const int first = q.row0 + (walk.group() * CS + rank) * p.TQ;
+                            for (int sl = 0; sl < SLABS; ++sl) {
+                                if constexpr (PAIR)
+                                    tma_load_4d_pair(q_s + sl * Q_SLAB, &tmap_q, 0, g * p.G, first,
+                                                     sl, lead(&q_full));
+                                else
+                                    tma_load_4d(q_s + sl * Q_SLAB, &tmap_q, 0, g * p.G, first, sl,
+                                                smem_addr(&q_full));
+                            }
                         }
                     }
                     ok = __shfl_sync(~0u, w, 0);
-                    if (!ok)
-                        break;
-                    ++nq;
+                    if (ok)
+                        ++nq;
                 }
             }
         }
         if (!ok && lane == 0) {
             give_up();
-            // let the copies in flight land before the CTA exits
-            if (nq)
+            // let the copies in flight land before the CTA exits (of a pair, the
+            // even CTA's barriers count both CTAs' copies, and neither leaves alone)
+            if (nq && rank == 0)
                 mbar_wait_bounded(smem_addr(&q_full), (nq - 1) & 1, nullptr, p.wait_budget_ns);
-            for (int i = max(0, nst - slots); i < nst; ++i)
+            for (int i = max(0, nst - slots); i < nst && rank == 0; ++i)
                 mbar_wait_bounded(smem_addr(&full[i % slots]), (i / slots) & 1, nullptr,
                                   p.wait_budget_ns);
         }
-        __syncwarp();
-    } else if (warp == 1 || warp == kTreeOWarp) {
-        if (lane == 0) {
-            // ======================================================== products
-            // scores by one thread, outputs by another: a thread spends some
-            // 1400 cycles a stage on its barriers and commits, the products of
-            // a stage take about as long, and one thread for both would be
-            // slower than the copies
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, int parity) {
-                if (ok && !mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns))
-                    ok = false;
-                return ok;
-            };
-            auto release = [&](uint64_t *bar) {
-                if (p.cs > 1)
-                    tc_commit_multicast(smem_addr(bar), everyone);
-                else
-                    tc_commit(smem_addr(bar));
-            };
-            if (warp == 1) {
-                const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
-                const uint64_t k_desc = tc_sdesc(k_s, 16, GROUP);
-                int ns = 0, nq = 0;  // S products, Q tiles
-                for (; walk.more() && ok; walk.next(p)) {
-                    wait(&q_full, nq & 1);
-                    ++nq;
-                    for (int t = walk.t; t < walk.t_end; ++t, ++ns) {
-                        // into the buffer of P(ns - 2), once its product is over
-                        const int st = ns % NK;
-                        if ((ns >= 2 && !wait(&o_done[ns & 1], ((ns >> 1) & 1) ^ 1)) ||
-                            !wait(&k_full[st], (ns / NK) & 1))
+      } else if (lane == 0 && rank == 0) {
+        // ============================================================ products
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, int parity) {
+            if (ok && !mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns))
+                ok = false;
+            return ok;
+        };
+        auto commit = [&](uint64_t *bar) {  // in both CTAs of a pair
+            if constexpr (PAIR)
+                tc_commit_pair(smem_addr(bar));
+            else
+                tc_commit(smem_addr(bar));
+        };
+        if (warp == kTreeSWarp) {
+            const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
+            const uint64_t k_desc = tc_sdesc(k_s, 16, KGROUP);
+            int nk = 0, ns = 0, nq = 0;  // K pieces, S products, Q tiles
+            for (; walk.more() && ok; walk.next(p)) {
+                wait(&q_full, nq & 1);
+                ++nq;
+                for (int t = walk.t; t < walk.t_end && ok; ++t, ++ns) {
+                    // into the buffer of P(ns - 2), once its product is over
+                    if (ns >= 2)
+                        wait(&o_done[ns & 1], ((ns >> 1) & 1) ^ 1);
+                    const uint32_t d = tmem + S_COL + (ns & 1) * NT;
+                    for (int kp = 0; kp < KP; ++kp, ++nk) {
+                        const int st = nk % NK;
+                        if (!wait(&k_full[st], (nk / NK) & 1))
                             break;
                         tc_fence_after();
-                        const uint64_t ks = k_desc + ((st * KV_TILE) >> 4);
-                        const uint32_t d = tmem + S_COL + (ns & 1) * NT;
+                        const uint64_t ks = k_desc + ((st * K_BYTES) >> 4);
+                        const uint64_t qs = q_desc + ((kp * KSLABS * Q_SLAB) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            tc_mma(d, q_desc + (((kk / 4) * Q_SLAB + (kk % 4) * 32) >> 4),
-                                   ks + (((kk / 4) * 1024 + (kk % 4) * 32) >> 4), IDESC_S, kk > 0);
-                        tc_commit(smem_addr(&s_full[ns & 1]));
-                        release(&k_empty[st]);
+                        for (int kk = 0; kk < 4 * KSLABS; ++kk) {
+                            const uint64_t a = qs + (((kk / 4) * Q_SLAB + (kk % 4) * 32) >> 4);
+                            const uint64_t b = ks + (((kk / 4) * 1024 + (kk % 4) * 32) >> 4);
+                            if constexpr (PAIR)
+                                tc_mma_pair(d, a, b, IDESC_S, kp > 0 || kk > 0);
+                            else
+                                tc_mma(d, a, b, IDESC_S, kp > 0 || kk > 0);
+                        }
+                        commit(&k_empty[st]);
                     }
-                    tc_commit(smem_addr(&q_empty));
+                    commit(&s_full[ns & 1]);
                 }
-            } else {
-                const uint64_t v_desc = tc_sdesc(v_s, 1024, GROUP);
-                int np = 0, no = 0;  // P V products, units
-                for (; walk.more() && ok; walk.next(p)) {
-                    // the last unit's output has been read
-                    if (no++ && !wait(&o_free, no & 1))
+                commit(&q_empty);
+            }
+        } else {
+            const uint64_t v_desc = tc_sdesc(v_s, 1024, VGROUP);
+            int nv = 0, np = 0, no = 0;  // V pieces, P V products, units
+            for (; walk.more() && ok; walk.next(p)) {
+                // the last unit's output has been read
+                if (no++ && !wait(&o_free, no & 1))
+                    break;
+                for (int t = walk.t; t < walk.t_end && ok; ++t, ++np) {
+                    if (!wait(&p_full, np & 1))
                         break;
-                    for (int t = walk.t; t < walk.t_end; ++t, ++np) {
-                        const int st = np % NV;
-                        if (!wait(&v_full[st], (np / NV) & 1) || !wait(&p_full, np & 1))
+                    if constexpr (PAIR)
+                        fence_acquire_cluster();
+                    const uint32_t a = tmem + S_COL + (np & 1) * NT;
+                    for (int vp = 0; vp < VP; ++vp, ++nv) {
+                        const int st = nv % NV;
+                        if (!wait(&v_full[st], (nv / NV) & 1))
                             break;
                         tc_fence_after();
-                        const uint64_t vs = v_desc + ((st * KV_TILE) >> 4);
-                        const uint32_t a = tmem + S_COL + (np & 1) * NT;
+                        const uint64_t vs = v_desc + ((st * V_BYTES) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < NT / 16; ++kk)
-                            tc_mma_ta(tmem + O_COL, a + kk * 8, vs + ((kk * 2 * GROUP) >> 4),
-                                      IDESC_O, t > walk.t || kk > 0);
-                        tc_commit(smem_addr(&o_done[np & 1]));
-                        release(&v_empty[st]);
+                        for (int kk = 0; kk < VKEYS / 16; ++kk) {
+                            const uint32_t pa = a + (vp * (VKEYS / 16) + kk) * 8;
+                            const uint64_t b = vs + ((kk * 2 * VGROUP) >> 4);
+                            const bool more = t > walk.t || vp > 0 || kk > 0;
+                            if constexpr (PAIR)
+                                tc_mma_ta_pair(tmem + O_COL, pa, b, IDESC_O, more);
+                            else
+                                tc_mma_ta(tmem + O_COL, pa, b, IDESC_O, more);
+                        }
+                        commit(&v_empty[st]);
                     }
+                    commit(&o_done[np & 1]);
                 }
             }
-            if (!ok)
-                give_up();
-            // every product issued here has completed before the memory is freed
-            tc_commit(smem_addr(&mma_done));
-            mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
         }
-        __syncwarp();
+        if (!ok)
+            give_up();
+        // every product issued here has completed before the memory is freed
+        commit(&mma_done);
+        mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
+      }
+      __syncwarp();
     } else {
         // ============================================================ softmax
-        // warps 2-5 take the first half of a stage's tokens, warps 6-9 the
+        // warps 4-7 take the first half of a stage's tokens, warps 8-11 the
         // second, for the same rows: warp w reads tensor-memory quarter w & 3
+        regs_take<200>();
         constexpr int HC = NT / 2, HD = D / 2;
         const int quarter = warp & 3;
-        const int half = (warp - 2) >> 2;
+        const int half = (warp - 4) >> 2;
         const int r = 32 * quarter + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t pair_bar = 1 + quarter;
@@ -492,11 +568,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const bool neg = sc < 0.f;
         const float masked = neg ? INFINITY : -INFINITY;
         const float2 sc2 = make_float2(sc, sc);
-        const bool scribe = threadIdx.x == 64 && rank == 0;
+        const bool scribe = threadIdx.x == 128 && rank == 0;
         if (scribe)
-            p.cut[cluster] = make_int4(-1, 0, 0, 0);
-        if (!walk.more() && half == 0)  // an empty run (fewer stages than runs) between a unit's pieces
-            p.part_ml[((size_t)(2 * cluster) * p.cs + rank) * 128 + r] = make_float2(-INFINITY, 0.f);
+            p.cut[run] = make_int4(-1, 0, 0, 0);
+        if (!walk.more() && half == 0)  // a run without a stage, perhaps between a unit's pieces
+            p.part_ml[((size_t)(2 * run) * CS + rank) * 128 + r] = make_float2(-INFINITY, 0.f);
         int ns = 0, built = -1;
         bool ok = true;
         // after a failed wait the loops keep running without doing work, so
@@ -509,15 +585,35 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 give_up();
             }
         };
+        auto signal = [&](uint64_t *bar) {  // to the thread that issues the outputs
+            if constexpr (PAIR)
+                mbar_arrive_cluster(lead(bar));
+            else
+                mbar_arrive(smem_addr(bar));
+        };
+        // waits for V's pieces [a, b); of a pair, the even CTA's barriers count
+        // both CTAs' copies, and it tells the odd one
+        int told = 0;
+        auto wait_v = [&](int a, int b) {
+            if (PAIR && rank == 1) {
+                mbar_wait_bounded(smem_addr(&v_here), told++ & 1, &abort_flag, p.wait_budget_ns);
+                return;
+            }
+            for (int i = a; i < b; ++i)
+                mbar_wait_bounded(smem_addr(&v_full[i % NV]), (i / NV) & 1, &abort_flag,
+                                  p.wait_budget_ns);
+            if (PAIR && threadIdx.x == 128)
+                mbar_arrive_cluster(cluster_addr(smem_addr(&v_here), 1));
+        };
         for (; walk.more(); walk.next(p)) {
             const TreeSeq &q = walk.q;
-            const int g = walk.head(), tile = walk.group() * p.cs + rank;
+            const int g = walk.head(), tile = walk.group() * CS + rank;
             const int left = min(p.TQ, q.n - tile * p.TQ);  // nodes of this tile (or none)
             const bool row_ok = r < p.TQ * p.G && ti < left;
             const int node = tile * p.TQ + ti;
             const int prefix = q.L - q.n;
             if (walk.t_end * NT > prefix && built != walk.s) {
-                build_tree_bits(tree, p.parents + q.row0, q.n, threadIdx.x - 64, 5, p.err);
+                build_tree_bits(tree, p.parents + q.row0, q.n, threadIdx.x - 128, 5, p.err);
                 built = walk.s;
             }
             float m_ref = -INFINITY, l = 0.f;
@@ -548,10 +644,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                         }
                     }
                     // the extreme: the sign is the call's, a branch around two loops
-                    float ec[2 * (HC / 32)];
+                    float ec[4];
                     if (!neg) {
 #pragma unroll
-                        for (int c = 0; c < 2 * (HC / 32); ++c) {
+                        for (int c = 0; c < 4; ++c) {
                             ec[c] = v[c >> 1][16 * (c & 1)];
 #pragma unroll
                             for (int i = 1; i < 15; i += 2)
@@ -559,12 +655,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                               v[c >> 1][16 * (c & 1) + i + 1]);
                             ec[c] = fmaxf(ec[c], v[c >> 1][16 * (c & 1) + 15]);
                         }
-                        e = fmaxf(ec[0], ec[1]);
-                        if constexpr (HC == 64)
-                            e = fmax3(e, ec[2], ec[3]);
+                        e = fmax3(ec[0], ec[1], fmaxf(ec[2], ec[3]));
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 2 * (HC / 32); ++c) {
+                        for (int c = 0; c < 4; ++c) {
                             ec[c] = v[c >> 1][16 * (c & 1)];
 #pragma unroll
                             for (int i = 1; i < 15; i += 2)
@@ -572,9 +666,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                               v[c >> 1][16 * (c & 1) + i + 1]);
                             ec[c] = fminf(ec[c], v[c >> 1][16 * (c & 1) + 15]);
                         }
-                        e = fminf(ec[0], ec[1]);
-                        if constexpr (HC == 64)
-                            e = fmin3(e, ec[2], ec[3]);
+                        e = fmin3(ec[0], ec[1], fminf(ec[2], ec[3]));
                     }
                 }
                 pair_red[ns & 1][half][r] = e;
@@ -611,10 +703,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     }
                 l = l * alpha + (sum2.x + sum2.y);
                 // both halves have read their scores (the barrier above): P over them
-                if constexpr (HC == 64)
-                    tc_st32u(t_lane + s_col + half * 32, pk);
-                else
-                    tc_st16u(t_lane + s_col + half * 16, pk);
+                tc_st32u(t_lane + s_col + half * 32, pk);
                 if (t > walk.t) {
                     wait(&o_done[(ns - 1) & 1], ((ns - 1) >> 1) & 1);  // O may be rescaled
                     if (!ok)
@@ -637,15 +726,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 // them in V (their weights are 0, which does not hide a NaN)
                 const bool zero_v = t0 + NT > q.L;
                 if (zero_v) {
-                    const int st = ns % NV;
-                    mbar_wait_bounded(smem_addr(&v_full[st]), (ns / NV) & 1, nullptr,
-                                      p.wait_budget_ns);
-                    uint8_t *vs = v_ptr + st * KV_TILE;
-                    const int za = q.L - t0;
-                    for (int idx = half * 128 + r; idx < (NT - za) * SLABS * 8; idx += 256) {
-                        const int row = za + idx / (SLABS * 8), c = idx % (SLABS * 8);
-                        *reinterpret_cast<uint4 *>(vs + (row / 8) * GROUP + (c >> 3) * 1024 +
-                                                   (row % 8) * 128 + (c & 7) * 16) =
+                    const int za = q.L - t0;  // first row behind it
+                    wait_v(ns * VP + za / VKEYS, ns * VP + VP);
+                    for (int idx = half * 128 + r; idx < (NT - za) * VSLABS * 8; idx += 256) {
+                        const int row = za + idx / (VSLABS * 8), c = idx % (VSLABS * 8);
+                        const int st = (ns * VP + row / VKEYS) % NV, in = row % VKEYS;
+                        *reinterpret_cast<uint4 *>(v_ptr + st * V_BYTES + (in / 8) * VGROUP +
+                                                   (c >> 3) * 1024 + (in % 8) * 128 + (c & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
                     }
                 }
@@ -655,7 +742,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(smem_addr(&p_full));
+                    signal(&p_full);
             }
             wait(&o_done[(ns - 1) & 1], ((ns - 1) >> 1) & 1);
             // the row's exp-sum from both halves, then each half writes its
@@ -673,7 +760,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(smem_addr(&o_free));
+                    signal(&o_free);
             };
             // a store takes 64 columns at least: at head_dim 64 the first
             // half's warps write whole rows
@@ -689,7 +776,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                lt > 0.f ? 1.f / lt : 0.f, lane, read);
             } else {
                 // a piece: 0 where the unit began in an earlier run, else 1
-                const size_t piece = (size_t)(2 * cluster + (walk.t == 0)) * p.cs + rank;
+                const size_t piece = (size_t)(2 * run + (walk.t == 0)) * CS + rank;
                 RowOut rows;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -701,141 +788,162 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 write_rows<WC>(rows, false, true, t_lane + O_COL + col, col, 1.f, lane, read);
                 if (row_ok && half == 0)
                     p.part_ml[piece * 128 + r] = make_float2(m_ref, lt);
-                if (scribe && walk.t == 0) {
-                    // the run that holds the unit's last stage
-                    const long long end = x1 - walk.left + q.T;  // one past it
-                    p.cut[cluster] = make_int4(walk.s, g, walk.group(),
-                                               (int)((end * p.clusters - 1) / total));
-                }
+                if (scribe && walk.t == 0)
+                    p.cut[run] = make_int4(walk.s, g, walk.group(), walk.last_run(total, p.runs));
             }
         }
     }
     tc_fence_before();
-    if (p.cs > 1)
-        cluster_sync();  // no CTA leaves while another may still signal it
+    if constexpr (PAIR)
+        cluster_sync();  // neither CTA leaves while the other may still use its memory
     else
         __syncthreads();
-    if (warp == 1) {
+    if (warp == 0) {
         tc_fence_after();
-        tc_dealloc(tmem, 512);
+        if constexpr (PAIR)
+            tc_dealloc_pair(tmem, 512);
+        else
+            tc_dealloc(tmem, 512);
     }
+    if constexpr (PAIR)
+        cluster_sync();  // the memory is given back by both while both are there
 }
 
 // Joins the pieces of the unit that is cut at the end of run blockIdx.x (if one
 // is): its piece 1 there, then piece 0 of every later run up to the last.  A
 // row's output is sum_i w_i o_i / sum_i w_i l_i with w_i = exp2(m_i - max m).
-// CTA (run, tile, quarter): 32 rows, a warp per row in turn.
+// A warp per row: what it waits for is latency, so the rows go to as many warps
+// as there are and a row's pieces are loaded eight at a time (11 to 15 us with
+// 32 rows and one piece at a time per CTA of eight warps, 4 to 6 now).
 constexpr int kTreeJoinThreads = 256;
+constexpr int kTreeJoinRows = kTreeJoinThreads / 32;
 
 template <int D>
 __global__ void __launch_bounds__(kTreeJoinThreads) paged_tree_join_kernel(const TreeParams p)
 {
     constexpr int VPL = D / 32;  // values per lane
+    constexpr int AHEAD = 8;
     const int run = blockIdx.x, rank = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = kTreeJoinRows * blockIdx.z + warp, ti = r / p.G;
     griddep_wait();
     const int4 cut = p.cut[run];
-    if (cut.x < 0)
+    if (cut.x < 0 || r >= p.TQ * p.G)
         return;
     const int row0 = __ldg(p.cu_q + cut.x), n = __ldg(p.cu_q + cut.x + 1) - row0;
-    const int tile = cut.z * p.cs + rank;
-    for (int r = 32 * blockIdx.z + warp; r < 32 * (int)blockIdx.z + 32; r += kTreeJoinThreads / 32) {
-        const int ti = r / p.G, node = tile * p.TQ + ti;
-        if (r >= p.TQ * p.G || node >= n)
-            break;  // (rows in order: none after it either)
-        auto piece = [&](int i) -> size_t {
-            return ((size_t)(i == run ? 2 * run + 1 : 2 * i) * p.cs + rank) * 128 + r;
-        };
-        float top = -INFINITY;
-        for (int i = run + lane; i <= cut.w; i += 32)
-            top = fmaxf(top, p.part_ml[piece(i)].x);
+    const int node = (cut.z * p.cs + rank) * p.TQ + ti;
+    if (node >= n)
+        return;
+    auto piece = [&](int i) -> size_t {
+        return ((size_t)(i == run ? 2 * run + 1 : 2 * i) * p.cs + rank) * 128 + r;
+    };
+    float acc[VPL], den = 0.f, top = -INFINITY;
 #pragma unroll
-        for (int off = 16; off; off >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, off));
-        float acc[VPL], den = 0.f;
+    for (int k = 0; k < VPL; ++k)
+        acc[k] = 0.f;
+    for (int i0 = run; i0 <= cut.w; i0 += AHEAD) {
+        float2 ml[AHEAD], x[AHEAD][VPL / 2];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            ml[a] = make_float2(-INFINITY, 0.f);
+            if (i0 + a > cut.w)
+                continue;
+            const size_t at = piece(i0 + a);
+            ml[a] = p.part_ml[at];
+#pragma unroll
+            for (int k = 0; k < VPL / 2; ++k)
+                x[a][k] = *reinterpret_cast<const float2 *>(p.part_o + at * D + VPL * lane + 2 * k);
+        }
+        float m = top;
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+            m = fmaxf(m, ml[a].x);
+        if (m == -INFINITY)
+            continue;
+        const float keep = ex2(top - m);
+        den *= keep;
 #pragma unroll
         for (int k = 0; k < VPL; ++k)
-            acc[k] = 0.f;
-        for (int i = run; i <= cut.w; ++i) {
-            const float2 ml = p.part_ml[piece(i)];
-            if (ml.x == -INFINITY)  // the row sees nothing there
-                continue;
-            const float *o = p.part_o + piece(i) * D + VPL * lane;
-            const float w = ex2(ml.x - top);
-            den += w * ml.y;
+            acc[k] *= keep;
 #pragma unroll
-            for (int k = 0; k < VPL; k += 2) {
-                const float2 x = *reinterpret_cast<const float2 *>(o + k);
-                acc[k] += w * x.x;
-                acc[k + 1] += w * x.y;
+        for (int a = 0; a < AHEAD; ++a) {
+            if (ml[a].x == -INFINITY)  // nothing there, or nothing that the row sees
+                continue;
+            const float w = ex2(ml[a].x - m);
+            den += w * ml[a].y;
+#pragma unroll
+            for (int k = 0; k < VPL / 2; ++k) {
+                acc[2 * k] += w * x[a][k].x;
+                acc[2 * k + 1] += w * x[a][k].y;
             }
         }
-        const float inv = den > 0.f ? 1.f / den : 0.f;
-        const size_t at = ((size_t)(row0 + node) * p.Hq + (size_t)cut.y * p.G + (r - ti * p.G)) * D +
-                          VPL * lane;
+        top = m;
+    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const size_t at =
+        ((size_t)(row0 + node) * p.Hq + (size_t)cut.y * p.G + (r - ti * p.G)) * D + VPL * lane;
 #pragma unroll
-        for (int k = 0; k < VPL; k += 2) {
-            if (p.out_half)
-                *reinterpret_cast<uint32_t *>(static_cast<__half *>(p.out) + at + k) =
-                    pack_half2(acc[k] * inv, acc[k + 1] * inv);
-            else
-                *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at + k) =
-                    make_float2(acc[k] * inv, acc[k + 1] * inv);
-        }
+    for (int k = 0; k < VPL; k += 2) {
+        if (p.out_half)
+            *reinterpret_cast<uint32_t *>(static_cast<__half *>(p.out) + at + k) =
+                pack_half2(acc[k] * inv, acc[k + 1] * inv);
+        else
+            *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at + k) =
+                make_float2(acc[k] * inv, acc[k + 1] * inv);
     }
 }
 
 namespace {
 
-template <int D> void tree_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int cs)
+template <int D, bool PAIR> void tree_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr)
 {
     *cfg = {};
     cfg->blockDim = dim3(kTreeThreads);
-    cfg->dynamicSmemBytes = tree_smem_bytes<D>();
+    cfg->dynamicSmemBytes = tree_smem_bytes<D, PAIR>();
     attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = (unsigned)cs;
+    attr->val.clusterDim.x = 2;
     attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
     cfg->attrs = attr;
-    cfg->numAttrs = cs > 1 ? 1 : 0;
+    cfg->numAttrs = PAIR ? 1 : 0;
 }
 
-template <int D> cudaError_t tree_clusters_dim(int cs, int *clusters)
+template <int D, bool PAIR> cudaError_t tree_resident_of(int *runs)
 {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr;
-    tree_config<D>(&cfg, &attr, cs);
-    cudaError_t e = cudaFuncSetAttribute(paged_tree_kernel<D>,
+    tree_config<D, PAIR>(&cfg, &attr);
+    cudaError_t e = cudaFuncSetAttribute(paged_tree_kernel<D, PAIR>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess)
         return e;
-    if (cs == 1) {
-        int dev = 0;
-        if ((e = cudaGetDevice(&dev)) != cudaSuccess)
-            return e;
-        return cudaDeviceGetAttribute(clusters, cudaDevAttrMultiProcessorCount, dev);
+    if (PAIR) {
+        cfg.gridDim = dim3(2);
+        return cudaOccupancyMaxActiveClusters(runs, paged_tree_kernel<D, PAIR>, &cfg);
     }
-    cfg.gridDim = dim3((unsigned)cs);
-    return cudaOccupancyMaxActiveClusters(clusters, paged_tree_kernel<D>, &cfg);
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess)
+        return e;
+    return cudaDeviceGetAttribute(runs, cudaDevAttrMultiProcessorCount, dev);
 }
 
-template <int D>
-cudaError_t launch_tree_dim(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                            const TreeParams &p, cudaStream_t stream)
+template <int D, bool PAIR>
+cudaError_t launch_tree_of(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                           const TreeParams &p, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr;
-    tree_config<D>(&cfg, &attr, p.cs);
-    cfg.gridDim = dim3((unsigned)(p.clusters * p.cs));
+    tree_config<D, PAIR>(&cfg, &attr);
+    cfg.gridDim = dim3((unsigned)(p.runs * p.cs));
     cfg.stream = stream;
     cudaError_t e;
-    if ((e = cudaLaunchKernelEx(&cfg, paged_tree_kernel<D>, tq, tk, tv, p)) != cudaSuccess)
+    if ((e = cudaLaunchKernelEx(&cfg, paged_tree_kernel<D, PAIR>, tq, tk, tv, p)) != cudaSuccess)
         return e;
     cudaLaunchAttribute overlap;
     overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     overlap.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t join = {};
-    join.gridDim = dim3((unsigned)p.clusters, (unsigned)p.cs, 4);
+    join.gridDim = dim3((unsigned)p.runs, (unsigned)p.cs, 128 / kTreeJoinRows);
     join.blockDim = dim3(kTreeJoinThreads);
     join.stream = stream;
     join.attrs = &overlap;
@@ -845,19 +953,33 @@ cudaError_t launch_tree_dim(const CUtensorMap &tq, const CUtensorMap &tk, const 
 
 }  // namespace
 
-cudaError_t tree_clusters(int head_dim, int cs, int *clusters)
+cudaError_t tree_resident(int head_dim, bool pair, int *runs)
 {
-    return head_dim == 64    ? tree_clusters_dim<64>(cs, clusters)
-           : head_dim == 128 ? tree_clusters_dim<128>(cs, clusters)
-                             : tree_clusters_dim<256>(cs, clusters);
+    *runs = 0;
+    switch (head_dim) {
+    case 64:
+        return pair ? cudaSuccess : tree_resident_of<64, false>(runs);
+    case 128:
+        return pair ? tree_resident_of<128, true>(runs) : tree_resident_of<128, false>(runs);
+    default:
+        return pair ? tree_resident_of<256, true>(runs) : tree_resident_of<256, false>(runs);
+    }
 }
 
 cudaError_t launch_tree(int head_dim, const CUtensorMap &tq, const CUtensorMap &tk,
                         const CUtensorMap &tv, const TreeParams &p, cudaStream_t stream)
 {
-    return head_dim == 64    ? launch_tree_dim<64>(tq, tk, tv, p, stream)
-           : head_dim == 128 ? launch_tree_dim<128>(tq, tk, tv, p, stream)
-                             : launch_tree_dim<256>(tq, tk, tv, p, stream);
+    const bool pair = p.cs == 2;
+    switch (head_dim) {
+    case 64:
+        return launch_tree_of<64, false>(tq, tk, tv, p, stream);
+    case 128:
+        return pair ? launch_tree_of<128, true>(tq, tk, tv, p, stream)
+                    : launch_tree_of<128, false>(tq, tk, tv, p, stream);
+    default:
+        return pair ? launch_tree_of<256, true>(tq, tk, tv, p, stream)
+                    : launch_tree_of<256, false>(tq, tk, tv, p, stream);
+    }
 }
 
 }  // namespace pgd
