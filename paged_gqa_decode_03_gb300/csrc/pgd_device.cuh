@@ -458,18 +458,16 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank)
     return a;
 }
 
-// Arrival on a barrier of any CTA of the cluster (cluster_addr).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+// Arrival on a barrier of any CTA of the cluster (cluster_addr).  FAR: this
+// thread's own writes to shared memory are released to the whole cluster with it
+// (a fence of some 1500 cycles; tensor memory is ordered by the tcgen05 fences).
+template <bool FAR> __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                 : "memory");
-}
-
-// Orders what arrivals from other CTAs of the cluster released (after the wait
-// for their barrier) before this thread's further accesses.
-__device__ __forceinline__ void fence_acquire_cluster()
-{
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    if constexpr (FAR)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                     : "memory");
+    else
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ---------------------------------------------------------------- tensor cores of two SMs

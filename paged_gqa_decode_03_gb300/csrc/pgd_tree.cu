@@ -517,8 +517,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 for (int t = walk.t; t < walk.t_end && ok; ++t, ++np) {
                     if (!wait(&p_full, np & 1))
                         break;
-                    if constexpr (PAIR)
-                        fence_acquire_cluster();
                     const uint32_t a = tmem + S_COL + (np & 1) * NT;
                     for (int vp = 0; vp < VP; ++vp, ++nv) {
                         const int st = nv % NV;
@@ -585,9 +583,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 give_up();
             }
         };
-        auto signal = [&](uint64_t *bar) {  // to the thread that issues the outputs
-            if constexpr (PAIR)
-                mbar_arrive_cluster(lead(bar));
+        // to the thread that issues the outputs (far: also what was written to V)
+        auto signal = [&](uint64_t *bar, bool far) {
+            if (PAIR && far)
+                mbar_arrive_cluster<true>(lead(bar));
+            else if (PAIR)
+                mbar_arrive_cluster<false>(lead(bar));
             else
                 mbar_arrive(smem_addr(bar));
         };
@@ -603,7 +604,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 mbar_wait_bounded(smem_addr(&v_full[i % NV]), (i / NV) & 1, &abort_flag,
                                   p.wait_budget_ns);
             if (PAIR && threadIdx.x == 128)
-                mbar_arrive_cluster(cluster_addr(smem_addr(&v_here), 1));
+                mbar_arrive_cluster<true>(cluster_addr(smem_addr(&v_here), 1));
         };
         for (; walk.more(); walk.next(p)) {
             const TreeSeq &q = walk.q;
@@ -742,7 +743,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    signal(&p_full);
+                    signal(&p_full, zero_v);
             }
             wait(&o_done[(ns - 1) & 1], ((ns - 1) >> 1) & 1);
             // the row's exp-sum from both halves, then each half writes its
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    signal(&o_free);
+                    signal(&o_free, false);
             };
             // a store takes 64 columns at least: at head_dim 64 the first
             // half's warps write whole rows
