@@ -1380,6 +1380,10 @@ pgd_status make_tree_plan(int S, int total_q, int max_q, int Hq, int Hkv, int D,
         return fail(PGD_ERR_UNSUPPORTED, "the tree kernel does not fit on this device");
     const long long stages = (long long)S * Hkv * ((tiles + tp->cs - 1) / tp->cs) *
                              (((long long)MB * BS + kTreeNT - 1) / kTreeNT);
+    // (the kernel counts stages, and two more per unit, in 32-bit integers)
+    if (3 * stages >= (1ll << 31))
+        return fail(PGD_ERR_UNSUPPORTED, "batch of %d sequences x %d KV heads x %lld tokens too large",
+                    S, Hkv, (long long)MB * BS);
     tp->runs = (int)std::max(1ll, std::min<long long>(resident, stages));
     const size_t rows = (size_t)2 * tp->runs * tp->cs * 128;
     tp->off_ml = align256(rows * D * 4);

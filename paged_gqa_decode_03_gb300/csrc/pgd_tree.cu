@@ -137,13 +137,14 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s)
     q.groups = ((q.n + p.TQ - 1) / p.TQ + p.cs - 1) / p.cs;
     return q;
 }
-// What a unit counts in the division of the work: its stages, and as much again
-// as a unit costs beside them (its start and end: measured at 2800 to 4100 cycles,
-// a stage being some 2900).
-constexpr int kTreeUnitCost = 1;
-__device__ __forceinline__ long long tree_cost(const TreeParams &p, const TreeSeq &q)
+// What a unit counts in the division of the work: its stages, and what it costs
+// beside them (its start and end), in stages: with 0, 1, 2, 4, 6 a batch of 64
+// requests of 512 to 4096 tokens took 118, 116, 110, 110, 112 us, 32 of 8 k to
+// 32 k tokens 271, 269, 269, 277, 278.
+constexpr int kTreeUnitCost = 2;
+__device__ __forceinline__ int tree_cost(const TreeParams &p, const TreeSeq &q)
 {
-    return q.T ? (long long)q.groups * p.Hkv * (q.T + kTreeUnitCost) : 0;
+    return q.T ? q.groups * p.Hkv * (q.T + kTreeUnitCost) : 0;
 }
 
 // A run [x0, x1) of the cost of all units, a unit (or the part of it that the
@@ -153,10 +154,9 @@ __device__ __forceinline__ long long tree_cost(const TreeParams &p, const TreeSe
 struct TreeWalk {
     TreeSeq q;
     int s, v, t, t_end;  // sequence, unit within it, stages [t, t_end)
-    long long at, x1;    // where unit v begins, and the run's end
+    int at, x1;          // where unit v begins, and the run's end
 
-    __device__ __forceinline__ TreeWalk(const TreeParams &p, int s0, long long begin, long long x0,
-                                        long long x1_)
+    __device__ __forceinline__ TreeWalk(const TreeParams &p, int s0, int begin, int x0, int x1_)
     {
         s = s0;
         x1 = at = x1_;
@@ -164,14 +164,14 @@ struct TreeWalk {
         if (x0 >= x1)
             return;
         q = tree_seq(p, s);  // begin: where the sequence's first unit begins
-        v = (int)((x0 - begin) / (q.T + kTreeUnitCost));
-        at = begin + (long long)v * (q.T + kTreeUnitCost);
-        t = (int)max(0ll, x0 - at - kTreeUnitCost);
+        v = (x0 - begin) / (q.T + kTreeUnitCost);
+        at = begin + v * (q.T + kTreeUnitCost);
+        t = max(0, x0 - at - kTreeUnitCost);
         set_end();
     }
     __device__ __forceinline__ void set_end()
     {
-        t_end = (int)min((long long)q.T, x1 - at - kTreeUnitCost);
+        t_end = min(q.T, x1 - at - kTreeUnitCost);
         if (t_end <= t)  // the run ends before the unit's first stage
             at = x1;
     }
@@ -193,28 +193,28 @@ struct TreeWalk {
         set_end();
     }
     // the run that holds the unit's last stage, of `runs` equal ones of `total`
-    __device__ __forceinline__ int last_run(long long total, int runs) const
+    __device__ __forceinline__ int last_run(int total, int runs) const
     {
-        return (int)(((at + q.T + kTreeUnitCost) * runs - 1) / total);
+        return (int)(((long long)(at + q.T + kTreeUnitCost) * runs - 1) / total);
     }
 };
 
 // Sum over the CTA's threads before this one of `x`, and over all in *total.
-__device__ __forceinline__ long long block_prefix(long long x, long long *warp_sum, long long *total)
+__device__ __forceinline__ int block_prefix(int x, int *warp_sum, int *total)
 {
     constexpr int WARPS = kTreeThreads / 32;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    long long inc = x;
+    int inc = x;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const long long y = __shfl_up_sync(~0u, inc, off);
+        const int y = __shfl_up_sync(~0u, inc, off);
         if (lane >= off)
             inc += y;
     }
     if (lane == 31)
         warp_sum[w] = inc;
     __syncthreads();
-    long long before = 0, all = 0;
+    int before = 0, all = 0;
 #pragma unroll
     for (int i = 0; i < WARPS; ++i) {
         if (i < w)
@@ -256,8 +256,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     __shared__ int abort_flag;
     __shared__ float pair_red[2][2][128];  // [parity][half][row]: the halves' exchange
     __shared__ TreeBits tree;
-    __shared__ long long warp_sum[kTreeThreads / 32], run_begin;
-    __shared__ int run_seq;
+    __shared__ int warp_sum[kTreeThreads / 32], run_begin, run_seq;
 
     const uint32_t dyn_base = smem_addr(dyn_smem);
     const uint32_t base = (dyn_base + 1023u) & ~1023u;
@@ -301,10 +300,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
 
     // ---- the run: [x0, x1) of the cost of all units; the sequence that holds x0
-    long long total = 0, mine = 0, before = 0;  // before: this thread's (last) sequence
+    int total = 0, mine = 0, before = 0;  // before: this thread's (last) sequence
     for (int s0 = 0; s0 < p.S; s0 += kTreeThreads) {
         const int s = s0 + (int)threadIdx.x;
-        long long all;
+        int all;
         mine = 0;
         if (s < p.S) {
             const TreeSeq q = tree_seq(p, s);
@@ -315,19 +314,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         before = total + block_prefix(mine, warp_sum, &all);
         total += all;
     }
-    const long long x0 = total * run / p.runs, x1 = total * (run + 1) / p.runs;
+    const int x0 = (int)((long long)total * run / p.runs);
+    const int x1 = (int)((long long)total * (run + 1) / p.runs);
     if (x1 > x0 && p.S <= kTreeThreads) {
         if (mine > 0 && before <= x0 && x0 < before + mine) {
             run_seq = (int)threadIdx.x;
             run_begin = before;
         }
     } else if (x1 > x0) {
-        long long past = 0;
+        int past = 0;
         for (int s0 = 0; s0 < p.S && past <= x0; s0 += kTreeThreads) {
             const int s = s0 + (int)threadIdx.x;
-            const long long here = s < p.S ? tree_cost(p, tree_seq(p, s)) : 0;
-            long long all;
-            const long long at = past + block_prefix(here, warp_sum, &all);
+            const int here = s < p.S ? tree_cost(p, tree_seq(p, s)) : 0;
+            int all;
+            const int at = past + block_prefix(here, warp_sum, &all);
             if (here > 0 && at <= x0 && x0 < at + here) {
                 run_seq = s;
                 run_begin = at;
@@ -749,7 +749,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             // the row's exp-sum from both halves, then each half writes its
             // columns (through the last stage's slot: its readers are done,
             // since o_done came after every warp's p_full, and the next stage
-            // takes the other)
+            // takes the other).  No warp goes on to the next unit before that
+            // product is over: p_full, v_here and the V ring count on it (a
+            // phase further on would pass for the one before).
             pair_red[(ns & 1) ^ 1][half][r] = l;
             named_barrier_sync(pair_bar, 64);
             const float lt = l + pair_red[(ns & 1) ^ 1][half ^ 1][r];
