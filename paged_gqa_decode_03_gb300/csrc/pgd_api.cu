@@ -1361,6 +1361,8 @@ pgd_status make_tree_plan(int S, int total_q, int max_q, int Hq, int Hkv, int D,
         return fail(PGD_ERR_UNSUPPORTED, "GQA group of %d query heads exceeds 128", Hq / Hkv);
     if (!supported_head_dim(D))
         return fail(PGD_ERR_UNSUPPORTED, "head_dim %d not in {64, 128, 256}", D);
+    if (Hq > 65536)  // (a tile's rows span 128 / G tokens of Hq heads)
+        return fail(PGD_ERR_UNSUPPORTED, "num_q_heads %d above 65536", Hq);
     if (!supported_block_size(BS))
         return fail(PGD_ERR_UNSUPPORTED, "block_size %d not in {8, 16, 32, 64, 128}", BS);
     if (MB <= 0)
@@ -1675,8 +1677,8 @@ pgd_status encode_packed_map(CUtensorMap *map, const void *base, int total, int 
 }
 
 struct PrefillPlan {
-    int G, TQ, span, max_tiles;
-    size_t ws_bytes;  // [256 B: tile count][tiles]
+    int G, TQ, span, max_units;
+    size_t ws_bytes;  // [256 B: unit count][units]
 };
 
 pgd_status make_prefill_plan(int S, int total, int Hq, int Hkv, int D, PrefillPlan *pp)
@@ -1689,15 +1691,17 @@ pgd_status make_prefill_plan(int S, int total, int Hq, int Hkv, int D, PrefillPl
         return fail(PGD_ERR_UNSUPPORTED, "GQA group of %d query heads exceeds 128", Hq / Hkv);
     if (!supported_head_dim(D))
         return fail(PGD_ERR_UNSUPPORTED, "head_dim %d not in {64, 128, 256}", D);
+    if (Hq > 65536)  // (a tile's rows span 128 / G tokens of Hq heads)
+        return fail(PGD_ERR_UNSUPPORTED, "num_q_heads %d above 65536", Hq);
     pp->G = Hq / Hkv;
     pp->TQ = 128 / pp->G;
     pp->span = D == 256 ? pp->TQ : 2 * pp->TQ;
     // disjoint prompts: whole spans of all rows, and one begun per prompt
-    const long long tiles = (long long)total / pp->span + S;
-    if (tiles * Hkv >= (1ll << 30))
-        return fail(PGD_ERR_UNSUPPORTED, "%lld work units", tiles * Hkv);
-    pp->max_tiles = (int)tiles;
-    pp->ws_bytes = total && S ? 256 + align256((size_t)tiles * 16) : 0;
+    const long long units = ((long long)total / pp->span + S) * Hkv;
+    if (units >= (1ll << 30))
+        return fail(PGD_ERR_UNSUPPORTED, "%lld work units", units);
+    pp->max_units = (int)units;
+    pp->ws_bytes = total && S ? 256 + align256((size_t)units * 16) : 0;
     if (pp->ws_bytes > kMaxWorkspaceBytes)
         return fail(PGD_ERR_WORKSPACE, "scratch of %zu bytes needed, above the %zu-byte cap",
                     pp->ws_bytes, kMaxWorkspaceBytes);
@@ -1765,8 +1769,8 @@ pgd_status run_prefill(float *out, uint16_t *out_half, const uint16_t *q, const 
     p.out = out;
     p.out_half = reinterpret_cast<__half *>(out_half);
     p.cu_seqlens = cu_seqlens;
-    p.num_tiles = reinterpret_cast<int *>(ws);
-    p.tiles = reinterpret_cast<int4 *>(ws + 256);
+    p.num_units = reinterpret_cast<int *>(ws);
+    p.units = reinterpret_cast<int4 *>(ws + 256);
     p.err = ds->err_word;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.S = S;
@@ -1777,10 +1781,10 @@ pgd_status run_prefill(float *out, uint16_t *out_half, const uint16_t *q, const 
     p.G = pp.G;
     p.TQ = pp.TQ;
     p.span = pp.span;
-    p.max_tiles = pp.max_tiles;
+    p.max_units = pp.max_units;
     p.wide_rows = aligned(dst, 32);
     p.wait_budget_ns = kWaitBudgetNs;
-    const int grid = (int)std::min<long long>(ds->num_sms, (long long)pp.max_tiles * Hkv);
+    const int grid = std::min(ds->num_sms, pp.max_units);
     e = launch_prefill(D, tq, tk, tv, p, grid, stream);
     if (own) {
         const cudaError_t e2 = cudaFreeAsync(ws, stream);

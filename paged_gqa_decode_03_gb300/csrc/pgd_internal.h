@@ -316,13 +316,13 @@ struct PrefillParams {
     float *out;                   // [total][Hq][D], or null with
     __half *out_half;             //   out_half, the output as fp16
     const int32_t *cu_seqlens;    // [S + 1]
-    int4 *tiles;                  // scratch: [max_tiles], longest first
-    int *num_tiles;               // scratch
+    int4 *units;                  // scratch: [max_units], longest first
+    int *num_units;               // scratch
     unsigned *err;
     float scale_log2;
     int S, total, max_len, Hq, Hkv, G;
     int TQ, span;                 // tokens of a tile, and of a unit (one tile or a pair)
-    int max_tiles;
+    int max_units;
     bool wide_rows;               // the output starts on a 32-byte border
     uint64_t wait_budget_ns;
 };

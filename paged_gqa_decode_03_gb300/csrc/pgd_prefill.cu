@@ -22,10 +22,9 @@ namespace {
 constexpr int kNT = 128;               // keys per stage
 constexpr int kSlab = 128 * 128;       // bytes of 128 rows of one 64-wide slab of head_dim
 
-// The tiles of a call in decreasing order of their stages (a counting sort):
-// {first row of q, position of that row, rows left in the prompt, first row of
-// the prompt} per tile (or pair of tiles) of `span` tokens, for every KV head
-// alike.  The CTAs of the attention kernel deal them out like cards, back and
+// The units of a call in decreasing order of their stages (a counting sort):
+// {first row of q, position of that row, rows left in the prompt, KV head} per
+// tile (or pair of tiles) of `span` tokens and KV head.  The CTAs of the attention kernel deal them out like cards, back and
 // forth, so the long ones are spread evenly and the short ones fill the end.
 __global__ void __launch_bounds__(kPrefillOrderKeys)
     packed_prefill_order_kernel(const PrefillParams p)
@@ -50,7 +49,7 @@ __global__ void __launch_bounds__(kPrefillOrderKeys)
                 f(min((min(i0 + p.span, n) + kNT - 1) / kNT, kPrefillOrderKeys - 1), i0, n, row0);
         }
     };
-    each([&](int key, int, int, int) { atomicAdd(&cnt[key], 1); });
+    each([&](int key, int, int, int) { atomicAdd(&cnt[key], p.Hkv); });
     __syncthreads();
     // exclusive prefix sum over the keys from the largest down: thread t owns
     // key kPrefillOrderKeys - 1 - t
@@ -77,19 +76,20 @@ __global__ void __launch_bounds__(kPrefillOrderKeys)
         }
         warp_tot[lane] = x - own;
         if (lane == 31) {
-            // prompts that overlap can have more tiles than the rows allow
-            if ((unsigned)x > (unsigned)p.max_tiles)
+            // prompts that overlap can have more units than the rows allow
+            if ((unsigned)x > (unsigned)p.max_units)
                 atomicOr(p.err, kErrQueryLen);
-            *p.num_tiles = max(0, min(x, p.max_tiles));
+            *p.num_units = max(0, min(x, p.max_units));
         }
     }
     __syncthreads();
     cnt[k] = warp_tot[w] + inc - c;
     __syncthreads();
     each([&](int key, int i0, int n, int row0) {
-        const int at = atomicAdd(&cnt[key], 1);
-        if ((unsigned)at < (unsigned)p.max_tiles)
-            p.tiles[at] = make_int4(row0 + i0, i0, n - i0, row0);
+        const int at = atomicAdd(&cnt[key], p.Hkv);
+        for (int g = 0; g < p.Hkv; ++g)
+            if ((unsigned)(at + g) < (unsigned)p.max_units)
+                p.units[at + g] = make_int4(row0 + i0, i0, n - i0, g);
     });
 }
 
@@ -101,10 +101,10 @@ __device__ __forceinline__ int unit_of(int k)
     return k * grid + ((k & 1) ? grid - 1 - b : b);
 }
 
-__device__ __forceinline__ int4 tile_of(const PrefillParams &p, int k, int units)
+__device__ __forceinline__ int4 unit_at(const PrefillParams &p, int k, int units)
 {
     const int ui = unit_of(k);
-    return ui < units ? __ldg(p.tiles + ui / p.Hkv) : make_int4(0, 0, 0, 0);
+    return ui < units ? __ldg(p.units + ui) : make_int4(0, 0, 0, 0);
 }
 
 }  // namespace
@@ -237,12 +237,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
-    griddep_wait();  // the list of tiles
-    const int units = *p.num_tiles * p.Hkv;
+    griddep_wait();  // the list of units
+    const int units = *p.num_units;
     const int turns = (units + (int)gridDim.x - 1) / (int)gridDim.x;
 
     const bool half_out = p.out_half != nullptr;
-    void *const out = half_out ? static_cast<void *>(p.out_half) : p.out;
+    char *const out = half_out ? reinterpret_cast<char *>(p.out_half) : reinterpret_cast<char *>(p.out);
     const size_t row_bytes = (size_t)D * (half_out ? 2 : 4);
     auto give_up = [&]() {
         if (!abort_flag)
@@ -290,18 +290,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 ++nv;
                 return true;
             };
-            int4 next = tile_of(p, 0, units);
+            int4 next = unit_at(p, 0, units);
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
                 const int4 u = next;
-                next = tile_of(p, k + 1, units);
+                next = unit_at(p, k + 1, units);
                 if (ui >= units)
                     continue;
-                const int g = ui % p.Hkv;
+                const int g = u.w, row0 = u.x - u.y;  // KV head, the prompt's first row
                 const int nt = max(stages(u, 0), stages(u, 1));
                 // the unit's first K goes out before its Q, whose place is
                 // free only after the last unit's last S
-                ok = load_k(u.w, g) && wait(&q_empty, (nq & 1) ^ 1);
+                ok = load_k(row0, g) && wait(&q_empty, (nq & 1) ^ 1);
                 if (!ok)
                     break;
                 const int ntq = u.z > p.TQ ? 2 : 1;
@@ -312,9 +312,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         tma_load_4d(q_s + x * Q_TILE + sl * kSlab, &tmap_q, 0, g * p.G,
                                     u.x + x * p.TQ, sl, bar);
                 ++nq;
-                ok = load_v(u.w, g);
+                ok = load_v(row0, g);
                 for (int j = 1; j < nt && ok; ++j)
-                    ok = load_k(u.w + j * kNT, g) && load_v(u.w + j * kNT, g);
+                    ok = load_k(row0 + j * kNT, g) && load_v(row0 + j * kNT, g);
             }
             if (!ok) {
                 give_up();
@@ -344,11 +344,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int nk = 0, nq = 0;        // K stages, Q pairs used up
             int uses[2] = {0, 0};      // of each score buffer
             int ns[2] = {0, 0};        // S products of each tile
-            int4 next = tile_of(p, 0, units);
+            int4 next = unit_at(p, 0, units);
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
                 const int4 u = next;
-                next = tile_of(p, k + 1, units);
+                next = unit_at(p, k + 1, units);
                 if (ui >= units)
                     continue;
                 const int nt0 = stages(u, 0), nt1 = stages(u, 1), nmax = max(nt0, nt1);
@@ -399,11 +399,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             };
             int nv = 0;                           // V stages used up
             int np[2] = {0, 0}, no[2] = {0, 0};   // P V products, units of each tile
-            int4 next = tile_of(p, 0, units);
+            int4 next = unit_at(p, 0, units);
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
                 const int4 u = next;
-                next = tile_of(p, k + 1, units);
+                next = unit_at(p, k + 1, units);
                 if (ui >= units)
                     continue;
                 const int nt0 = stages(u, 0), nt1 = stages(u, 1), nmax = max(nt0, nt1);
@@ -462,16 +462,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const bool neg = sc < 0.f;
         const float masked = neg ? INFINITY : -INFINITY;
         const float2 sc2 = make_float2(sc, sc);
+        const RowPlaces places(row_bytes, p.Hq, p.G, p.TQ, quarter, lane);
         int ns = 0, nv = 0;  // S tiles of this tile, V stages of the CTA, so far
         bool ok = true;
-        int4 next = tile_of(p, 0, units);
+        int4 next = unit_at(p, 0, units);
         for (int k = 0; k < turns && ok; ++k) {
             const int ui = unit_of(k);
             const int4 u = next;
-            next = tile_of(p, k + 1, units);  // a turn ahead: its latency passes meanwhile
+            next = unit_at(p, k + 1, units);  // a turn ahead: its latency passes meanwhile
             if (ui >= units)
                 continue;
-            const int g = ui % p.Hkv;
+            const int g = u.w;
             const int nt0 = stages(u, 0), nt1 = stages(u, 1), ntx = x ? nt1 : nt0;
             const int left = min(p.TQ, u.z - x * p.TQ);  // tokens of this tile
             const int n = u.y + u.z;                     // tokens of the prompt
@@ -604,8 +605,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (ok) {
                     tc_fence_after();
                     const float inv = l > 0.f ? 1.f / l : 0.f;
-                    const RowOut rows = rows_out(out, row_bytes, p.Hq, p.G, p.TQ, u.x + x * p.TQ,
-                                                 left, g, quarter, lane);
+                    const RowOut rows =
+                        places.at(out + ((size_t)(u.x + x * p.TQ) * p.Hq + (size_t)g * p.G) *
+                                            row_bytes, left);
                     write_rows<D>(rows, half_out, p.wide_rows, t_lane + o_col, 0, inv, lane, [&] {
                         tc_fence_before();
                         __syncwarp();
@@ -694,12 +696,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
-    griddep_wait();  // the list of tiles
-    const int units = *p.num_tiles * p.Hkv;
+    griddep_wait();  // the list of units
+    const int units = *p.num_units;
     const int turns = (units + (int)gridDim.x - 1) / (int)gridDim.x;
 
     const bool half_out = p.out_half != nullptr;
-    void *const out = half_out ? static_cast<void *>(p.out_half) : p.out;
+    char *const out = half_out ? reinterpret_cast<char *>(p.out_half) : reinterpret_cast<char *>(p.out);
     const size_t row_bytes = (size_t)D * (half_out ? 2 : 4);
     auto give_up = [&]() {
         if (!abort_flag)
@@ -737,16 +739,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 ++nv;
                 return true;
             };
-            int4 next = tile_of(p, 0, units);
+            int4 next = unit_at(p, 0, units);
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
                 const int4 u = next;
-                next = tile_of(p, k + 1, units);
+                next = unit_at(p, k + 1, units);
                 if (ui >= units)
                     continue;
-                const int g = ui % p.Hkv, nt = stages(u);
+                const int g = u.w, nt = stages(u), row0 = u.x - u.y;
                 for (int sl = 0; sl < SLABS && ok; ++sl)
-                    ok = load_k(u.w, g, sl);
+                    ok = load_k(row0, g, sl);
                 ok = ok && wait(&q_empty, (nq & 1) ^ 1);
                 if (!ok)
                     break;
@@ -758,9 +760,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 // in the order of use: K of stage j + 1 before V of stage j
                 for (int j = 0; j < nt && ok; ++j) {
                     for (int sl = 0; j + 1 < nt && sl < SLABS && ok; ++sl)
-                        ok = load_k(u.w + (j + 1) * kNT, g, sl);
+                        ok = load_k(row0 + (j + 1) * kNT, g, sl);
                     for (int i = 0; i < VP && ok; ++i)
-                        ok = load_v(u.w + j * kNT + i * VKEYS, g);
+                        ok = load_v(row0 + j * kNT + i * VKEYS, g);
                 }
             }
             if (!ok) {
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     ok = false;
                 return ok;
             };
-            int4 next = tile_of(p, 0, units);
+            int4 next = unit_at(p, 0, units);
             if (warp == 1) {
                 const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
                 const uint64_t k_desc = tc_sdesc(k_s, 16, 1024);
@@ -794,7 +796,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 for (int k = 0; k < turns && ok; ++k) {
                     const int ui = unit_of(k);
                     const int4 u = next;
-                    next = tile_of(p, k + 1, units);
+                    next = unit_at(p, k + 1, units);
                     if (ui >= units)
                         continue;
                     const int nt = stages(u);
@@ -828,7 +830,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 for (int k = 0; k < turns && ok; ++k) {
                     const int ui = unit_of(k);
                     const int4 u = next;
-                    next = tile_of(p, k + 1, units);
+                    next = unit_at(p, k + 1, units);
                     if (ui >= units)
                         continue;
                     const int nt = stages(u);
@@ -875,6 +877,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const bool neg = sc < 0.f;
         const float masked = neg ? INFINITY : -INFINITY;
         const float2 sc2 = make_float2(sc, sc);
+        const RowPlaces places(row_bytes, p.Hq, p.G, p.TQ, quarter, lane);
         int ns = 0, nv = 0;
         bool ok = true;
         // after a failed wait the loops keep running without doing work, so
@@ -886,14 +889,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 give_up();
             }
         };
-        int4 next = tile_of(p, 0, units);
+        int4 next = unit_at(p, 0, units);
         for (int k = 0; k < turns; ++k) {
             const int ui = unit_of(k);
             const int4 u = next;
-            next = tile_of(p, k + 1, units);
+            next = unit_at(p, k + 1, units);
             if (ui >= units)
                 continue;
-            const int g = ui % p.Hkv, nt = stages(u), n = u.y + u.z;
+            const int g = u.w, nt = stages(u), n = u.y + u.z;
             const bool row_ok = r < p.TQ * p.G && ti < min(p.TQ, u.z);
             const int lim = row_ok ? u.y + ti : -1;
             float m_ref = -INFINITY, l = 0.f;
@@ -1015,8 +1018,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 continue;
             tc_fence_after();
             const float inv = lt > 0.f ? 1.f / lt : 0.f;
-            const RowOut rows = rows_out(out, row_bytes, p.Hq, p.G, p.TQ, u.x, min(p.TQ, u.z), g,
-                                         quarter, lane);
+            const RowOut rows = places.at(
+                out + ((size_t)u.x * p.Hq + (size_t)g * p.G) * row_bytes, min(p.TQ, u.z));
             write_rows<HD>(rows, half_out, p.wide_rows, t_lane + half * HD, half * HD, inv, lane, [&] {
                 tc_fence_before();
                 __syncwarp();

@@ -96,27 +96,37 @@ __device__ __forceinline__ void write_rows(const RowOut &o, bool half, bool wide
     }
 }
 
-// The rows of a warp's quarter of a tile (TQ tokens x the G heads of KV head g)
-// whose first token is row `token` of out [tokens][Hq][row_bytes]; `left`: the
-// tile's tokens.
-__device__ __forceinline__ RowOut rows_out(void *out, size_t row_bytes, int Hq, int G, int TQ,
-                                           int token, int left, int g, int quarter, int lane)
-{
-    RowOut o;
-    int r = 32 * quarter + (lane & ~3);
-    int ti = r / G, h = r - ti * G;
+// Where the rows of a warp's quarter of a tile (TQ tokens x the G heads of a KV
+// head) lie in out [tokens][Hq][row_bytes], from the tile's first token and head
+// on: the same for every tile, so worked out once.
+struct RowPlaces {
+    uint32_t off[4];  // bytes, in units of 16
+    uint32_t token;   // the rows' tokens within the tile, a byte each (255: none)
+    __device__ __forceinline__ RowPlaces(size_t row_bytes, int Hq, int G, int TQ, int quarter,
+                                         int lane)
+    {
+        int r = 32 * quarter + (lane & ~3);
+        int ti = r / G, h = r - ti * G;
+        token = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q, ++r) {
-        o.at[q] = r < TQ * G && ti < left
-                      ? static_cast<char *>(out) +
-                            ((size_t)(token + ti) * Hq + (size_t)g * G + h) * row_bytes
-                      : nullptr;
-        if (++h == G) {
-            h = 0;
-            ++ti;
+        for (int q = 0; q < 4; ++q, ++r) {
+            off[q] = (uint32_t)(((size_t)ti * Hq + h) * row_bytes / 16);
+            token |= (r < TQ * G ? (uint32_t)ti : 255u) << (8 * q);
+            if (++h == G) {
+                h = 0;
+                ++ti;
+            }
         }
     }
-    return o;
-}
+    // the rows of a tile of `left` tokens (at most 128) that begins at `first`
+    __device__ __forceinline__ RowOut at(char *first, int left) const
+    {
+        RowOut o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            o.at[q] = (int)((token >> (8 * q)) & 255u) < left ? first + 16 * (size_t)off[q] : nullptr;
+        return o;
+    }
+};
 
 }  // namespace pgd

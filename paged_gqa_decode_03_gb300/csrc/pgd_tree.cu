@@ -571,6 +571,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             p.cut[run] = make_int4(-1, 0, 0, 0);
         if (!walk.more() && half == 0)  // a run without a stage, perhaps between a unit's pieces
             p.part_ml[((size_t)(2 * run) * CS + rank) * 128 + r] = make_float2(-INFINITY, 0.f);
+        const size_t row_bytes = (size_t)D * (p.out_half ? 2 : 4);
+        const RowPlaces places(row_bytes, p.Hq, p.G, p.TQ, quarter, lane);
         int ns = 0, built = -1;
         bool ok = true;
         // after a failed wait the loops keep running without doing work, so
@@ -772,9 +774,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (D == 64 && half == 1) {
                 read();
             } else if (whole) {
-                const RowOut rows =
-                    rows_out(p.out, (size_t)D * (p.out_half ? 2 : 4), p.Hq, p.G, p.TQ,
-                             q.row0 + tile * p.TQ, left, g, quarter, lane);
+                const RowOut rows = places.at(
+                    static_cast<char *>(p.out) +
+                        ((size_t)(q.row0 + tile * p.TQ) * p.Hq + (size_t)g * p.G) * row_bytes, left);
                 write_rows<WC>(rows, p.out_half, p.wide_rows, t_lane + O_COL + col, col,
                                lt > 0.f ? 1.f / lt : 0.f, lane, read);
             } else {
