@@ -148,6 +148,21 @@ def test_strides_outputs_and_workspaces_agree():
         run(c, workspace=ws[: need - 1])
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_output_on_a_16_byte_border(D, dtype):
+    c = case([140, 33], 8, 2, D, seed=14)
+    base = run(c, dtype=dtype)
+    size = base.element_size()
+    flat = torch.full((base.numel() + 32,), 7.0, dtype=dtype, device=DEV)
+    out = flat[16 // size: 16 // size + base.numel()].view(base.shape)
+    assert out.data_ptr() % 32 == 16
+    pgd.packed_gqa_prefill(out, c["q"], c["k"], c["v"], c["cu"], c["scale"], 140)
+    torch.cuda.synchronize()
+    assert torch.equal(out, base)
+    assert (flat[: 16 // size] == 7.0).all() and (flat[16 // size + base.numel():] == 7.0).all()
+
+
 def test_flags():
     c = case([100, 60, 40], 8, 2, 128, seed=13)
     good = run(c)

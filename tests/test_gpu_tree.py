@@ -155,6 +155,38 @@ def test_any_scale(scale):
     check(run(w, parents), w, trees, ctx, f"scale {scale}")
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_output_on_a_16_byte_border(D, dtype):
+    ctx, n = [900, 40, 5], [30, 9, 64]
+    w, trees, parents = case(ctx, n, 8, 2, D, 16, seed=5)
+    base = run(w, parents, dtype=dtype)
+    size = base.element_size()
+    flat = torch.full((base.numel() + 32,), 7.0, dtype=dtype, device=DEV)
+    out = flat[16 // size: 16 // size + base.numel()].view(base.shape)
+    pgd.paged_gqa_tree(out, w.q, w.cu_seqlens_q, parents, w.k_cache, w.v_cache, w.block_tables,
+                       w.seq_lens, w.scale, w.max_q_len)
+    torch.cuda.synchronize()
+    assert torch.equal(out, base)
+    assert (flat[: 16 // size] == 7.0).all() and (flat[16 // size + base.numel():] == 7.0).all()
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own scratch and outputs, over the same caches."""
+    ctx, n = [3000, 40, 2000, 700], [30, 9, 64, 200]
+    w, trees, parents = case(ctx, n, 16, 4, 128, 16, seed=15)
+    base = run(w, parents)
+    outs = [torch.zeros_like(base) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o, s in zip(outs, streams):
+            pgd.paged_gqa_tree(o, w.q, w.cu_seqlens_q, parents, w.k_cache, w.v_cache,
+                               w.block_tables, w.seq_lens, w.scale, w.max_q_len, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, base) for o in outs)
+
+
 def test_padded_rows_and_empty_sequences_stay():
     """More rows than the sequences own, and a sequence without any."""
     ctx, n = [300, 40, 5, 1200], [4, 0, 6, 50]

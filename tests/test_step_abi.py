@@ -1,5 +1,5 @@
 """Refusals of the step's entry points (paged_kv_slots, paged_kv_write,
-paged_gqa_tree), with the documented status, before anything reaches a GPU."""
+paged_gqa_tree, packed_gqa_prefill), with the documented status, before anything reaches a GPU."""
 import ctypes
 import math
 
@@ -94,6 +94,47 @@ def test_tree_reports_a_missing_device(lib):
     assert tree(lib) == 4
 
 
+def prefill(lib, out_type=1, S=2, T=40, max_len=30, Hq=32, Hkv=8, D=128, scale=0.1,
+            strides=(48 * 128, 128) * 3, ptrs=(A,) * 5, ws=NULL, ws_bytes=0):
+    out, q, k, v, cu = ptrs
+    return lib.packed_gqa_prefill(out, out_type, q, k, v, cu, ctypes.c_float(scale), S, T, max_len,
+                                  Hq, Hkv, D, *strides, ws, ws_bytes, NULL)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(out_type=7), INVALID), (dict(S=-1), INVALID), (dict(T=-1), INVALID),
+    (dict(max_len=-1), INVALID), (dict(Hq=30), INVALID), (dict(Hq=0), INVALID),
+    (dict(Hq=129 * 8), UNSUPPORTED), (dict(Hq=1 << 17, Hkv=1 << 17), UNSUPPORTED),
+    (dict(D=96), UNSUPPORTED), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID),
+    (dict(strides=(48 * 128 + 4, 128) + (48 * 128, 128) * 2), INVALID),
+    (dict(strides=(48 * 128, 128) * 2 + (48 * 128, 0)), INVALID),
+    (dict(strides=(48 * 128, 128) * 2 + (1 << 39, 128)), INVALID),
+    (dict(ptrs=(NULL, A, A, A, A)), INVALID), (dict(ptrs=(A, A, A, A, NULL)), INVALID),
+    (dict(ptrs=(A, ctypes.c_void_p((1 << 20) + 8), A, A, A)), INVALID),
+    (dict(ptrs=(A, A, A, A, ODD)), INVALID), (dict(ws=A, ws_bytes=256), WORKSPACE),
+    (dict(ws=ctypes.c_void_p((1 << 20) + 128), ws_bytes=1 << 20), WORKSPACE),
+    (dict(T=(1 << 31) - 1, Hkv=4096, Hq=4096), UNSUPPORTED),
+])
+def test_prefill_refusals(lib, kw, status):
+    assert prefill(lib, **kw) == status
+    assert lib.pgd_last_error().decode() != ""
+
+
+def test_prefill_of_nothing_needs_no_arrays(lib):
+    assert prefill(lib, T=0, ptrs=(NULL,) * 5) == 0
+    assert prefill(lib, S=0, ptrs=(NULL,) * 5) == 0
+
+
+def test_prefill_plan_closed_form():
+    """16 bytes per unit of 2 tiles of 128 / G tokens (one tile at head_dim 256) and KV
+    head, one begun per prompt, behind 256 bytes; regions rounded up to 256."""
+    assert pgd.pgd_prefill_plan(4, 8192, 32, 8, 128) == 256 + (8192 // 64 + 4) * 8 * 16
+    assert pgd.pgd_prefill_plan(3, 100, 24, 4, 256) == 256 + 512
+    assert pgd.pgd_prefill_plan(3, 0, 24, 4, 256) == 0
+    with pytest.raises(pgd.PGDError):
+        pgd.pgd_prefill_plan(3, 100, 24, 5, 256)
+
+
 def test_binding_refusals():
     i = torch.zeros(4, dtype=torch.int32)
     q = torch.zeros((4, 8, 128), dtype=torch.float16)
@@ -106,6 +147,10 @@ def test_binding_refusals():
         pgd.paged_gqa_tree(q, q, i, i, k, k, i.view(1, 4), i, 0.1, 4)
     with pytest.raises(TypeError, match="float32 or float16"):
         pgd.paged_gqa_tree(q.double(), q, i, i, k, k, i.view(1, 4), i, 0.1, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        pgd.packed_gqa_prefill(q, q, q, q, i, 0.1, 4)
+    with pytest.raises(TypeError, match="torch.Tensor|has no|float"):
+        pgd.packed_gqa_prefill(None, q, q, q, i, 0.1, 4)
 
 
 @pytest.mark.gpu
@@ -137,3 +182,12 @@ def test_binding_refuses_mixed_devices_and_shapes():
         pgd.paged_kv_write(k, k, q[:, :4], q[:, :4], i)                   # heads of the cache
     with pytest.raises(ValueError):
         pgd.paged_kv_slots(i, i, i, i[:1], i.view(4, 1), i, i, i, 16, 64)
+    with pytest.raises(ValueError, match="contiguous"):
+        pgd.packed_gqa_prefill(q, q.transpose(1, 2), q, q, i, 0.1, 4)
+    with pytest.raises(ValueError, match="shapes"):
+        pgd.packed_gqa_prefill(q, q, q[:3], q[:3], i, 0.1, 4)
+    with pytest.raises(ValueError):
+        pgd.packed_gqa_prefill(q, q, q, q, i[:0], 0.1, 4)
+    for bad in (i.float(), i.view(2, 2), None, [0, 1]):
+        with pytest.raises((TypeError, ValueError, AttributeError)):
+            pgd.packed_gqa_prefill(q, q, q, q, bad, 0.1, 4)
