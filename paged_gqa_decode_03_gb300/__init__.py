@@ -500,15 +500,27 @@ def paged_kv_quantize(codes, meta, src, slots, stream=None) -> None:
 
 
 # The step's calls below are a few microseconds of GPU work each, so their
-# argument checks are written to cost little where all is well: one expression
-# of cheap attribute reads, and the checks that name the culprit only when
-# that is false.
+# argument checks are written to cost little where all is well: a few cheap
+# attribute reads per tensor, and the checks that name the culprit only when
+# one is off (paged_kv_slots, with ten tensors: 8.6 us a call, of which the C
+# entry and its launch are 3.2).
 _F16, _I32 = torch.float16, torch.int32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _fits(t, dtype, ndim):
-    return t.dtype is dtype and t.is_cuda and t.dim() == ndim and t.is_contiguous()
+def _index(t):
+    """The CUDA device a call's launch goes to, by one of its tensors (-1: none)."""
+    return t.get_device() if isinstance(t, torch.Tensor) else -1
+
+
+def _fits(index, dtype, ndim, *tensors):
+    """All contiguous, of ``dtype`` and ``ndim``, on CUDA device ``index``."""
+    for t in tensors:
+        if (t.dtype is not dtype or t.get_device() != index or t.dim() != ndim
+                or not t.is_contiguous()):
+            return False
+    return index >= 0
 
 
 def _check_all(*specs):
@@ -532,7 +544,7 @@ def _on(index, fn, *args, stream=None):
         handle = _raw_stream(index)
     else:
         handle = _stream_handle(stream, index)
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         st = fn(*args, handle)
     else:
         with torch.cuda.device(index):
@@ -566,21 +578,24 @@ def paged_gqa_tree(out, q, cu_seqlens_q, parents, k_cache, v_cache, block_tables
     negative for none) and itself.  ``out`` is float32 or float16."""
     lib = _lib or load_library()
     kind = _out_type(out)
-    if not (_fits(q, _F16, 3) and _fits(out, out.dtype, 3) and _fits(cu_seqlens_q, _I32, 1)
-            and _fits(parents, _I32, 1) and _fits(block_tables, _I32, 2)
-            and _fits(seq_lens, _I32, 1)):
+    dev = _index(q)
+    if not (_fits(dev, _F16, 3, q) and _fits(dev, out.dtype, 3, out)
+            and _fits(dev, _I32, 1, cu_seqlens_q, parents, seq_lens)
+            and _fits(dev, _I32, 2, block_tables)):
         _check_all((q, "q", _F16, 3), (out, "out", out.dtype, 3),
                    (cu_seqlens_q, "cu_seqlens_q", _I32, 1), (parents, "parents", _I32, 1),
                    (block_tables, "block_tables", _I32, 2), (seq_lens, "seq_lens", _I32, 1))
+        _one_device(dev, out, cu_seqlens_q, parents, block_tables, seq_lens)
     T, Hq, D = q.shape
     S, MB = block_tables.shape
-    if (out.shape != q.shape or cu_seqlens_q.size(0) != S + 1 or seq_lens.size(0) != S
-            or parents.size(0) != T):
+    if (out.shape != q.shape or cu_seqlens_q.numel() != S + 1 or seq_lens.numel() != S
+            or parents.numel() != T):
         raise ValueError("inconsistent shapes of q, out, cu_seqlens_q, parents, block_tables, "
                          "seq_lens")
     if layout is None:
-        if not (_fits(k_cache, _F16, 4) and _fits(v_cache, _F16, 4)):
+        if not _fits(dev, _F16, 4, k_cache, v_cache):
             _check_all((k_cache, "k_cache", _F16, 4), (v_cache, "v_cache", _F16, 4))
+            _one_device(dev, k_cache, v_cache)
         NB, Hkv, BS, D2 = k_cache.shape
         if v_cache.shape != k_cache.shape or D2 != D:
             raise ValueError("k_cache / v_cache shapes")
@@ -589,11 +604,10 @@ def paged_gqa_tree(out, q, cu_seqlens_q, parents, k_cache, v_cache, block_tables
         Hkv, BS, NB, strides = layout
         _check_rows_inside(k_cache, "k_cache", NB, Hkv, BS, D, strides)
         _check_rows_inside(v_cache, "v_cache", NB, Hkv, BS, D, strides)
+        _one_device(dev, k_cache, v_cache)
         sp, sh, st = (int(x) for x in strides)
     ws, ws_bytes = _workspace(workspace)
-    dev = q.get_device()
-    _one_device(dev, out, cu_seqlens_q, parents, k_cache, v_cache, block_tables, seq_lens,
-                workspace)
+    _one_device(dev, workspace)
     _on(dev, lib.paged_gqa_tree, out.data_ptr(), kind, q.data_ptr(), cu_seqlens_q.data_ptr(),
         parents.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), float(scale), S, T, int(max_q_len), Hq, int(Hkv), D, int(BS), MB,
@@ -631,19 +645,21 @@ def packed_gqa_prefill(out, q, k, v, cu_seqlens, scale, max_len: int, workspace=
     (contiguous [total, Hq, D], float16 or float32)."""
     lib = _lib or load_library()
     kind = _out_type(out)
-    if not (_fits(out, out.dtype, 3) and _fits(cu_seqlens, _I32, 1)):
+    dev = _index(q)
+    if not (_fits(dev, out.dtype, 3, out) and _fits(dev, _I32, 1, cu_seqlens)):
         _check_all((out, "out", out.dtype, 3), (cu_seqlens, "cu_seqlens", _I32, 1))
+        _packed_strides(q, "q")
+        _one_device(dev, out, cu_seqlens)
     qs, ks, vs = _packed_strides(q, "q"), _packed_strides(k, "k"), _packed_strides(v, "v")
     T, Hq, D = q.shape
     T2, Hkv, D2 = k.shape
     if out.shape != q.shape or T2 != T or D2 != D or v.shape != k.shape:
         raise ValueError("inconsistent shapes of out, q, k, v")
-    S = cu_seqlens.size(0) - 1
+    S = cu_seqlens.numel() - 1
     if S < 0:
         raise ValueError("cu_seqlens holds num_seqs + 1 values")
     ws, ws_bytes = _workspace(workspace)
-    dev = q.get_device()
-    _one_device(dev, out, k, v, cu_seqlens, workspace)
+    _one_device(dev, k, v, workspace)
     _on(dev, lib.packed_gqa_prefill, out.data_ptr(), kind, q.data_ptr(), k.data_ptr(),
         v.data_ptr(), cu_seqlens.data_ptr(), float(scale), S, T, int(max_len), Hq, Hkv, D, *qs,
         *ks, *vs, ws, ws_bytes, stream=stream)
@@ -668,34 +684,34 @@ def paged_kv_slots(slots, cu_seqlens_q, seq_lens, free_end, block_tables, contex
     (int32 [1]), ``slots`` and ``positions`` (int32 [rows], or None) are
     written, with -1 in the rows behind the last request."""
     lib = _lib or load_library()
-    if not (_fits(slots, _I32, 1) and _fits(cu_seqlens_q, _I32, 1) and _fits(seq_lens, _I32, 1)
-            and _fits(free_end, _I32, 1) and _fits(context_lens, _I32, 1)
-            and _fits(query_lens, _I32, 1) and _fits(free_pages, _I32, 1)
-            and _fits(block_tables, _I32, 2) and (free_start is None or _fits(free_start, _I32, 1))
-            and (positions is None or _fits(positions, _I32, 1))):
+    dev = _index(slots)
+    if not (_fits(dev, _I32, 1, slots, cu_seqlens_q, seq_lens, free_end, context_lens, query_lens,
+                  free_pages)
+            and _fits(dev, _I32, 2, block_tables)
+            and (free_start is None or _fits(dev, _I32, 1, free_start))
+            and (positions is None or _fits(dev, _I32, 1, positions))):
         _check_all((slots, "slots", _I32, 1), (cu_seqlens_q, "cu_seqlens_q", _I32, 1),
                    (seq_lens, "seq_lens", _I32, 1), (free_end, "free_end", _I32, 1),
                    (context_lens, "context_lens", _I32, 1), (query_lens, "query_lens", _I32, 1),
                    (free_pages, "free_pages", _I32, 1), (block_tables, "block_tables", _I32, 2),
                    (free_start, "free_start?", _I32, 1), (positions, "positions?", _I32, 1))
+        _one_device(dev, cu_seqlens_q, seq_lens, free_end, block_tables, context_lens, query_lens,
+                    free_pages, free_start, positions)
     S, MB = block_tables.shape
-    N = slots.size(0)
-    if (context_lens.size(0) != S or query_lens.size(0) != S or seq_lens.size(0) != S
-            or cu_seqlens_q.size(0) != S + 1):
+    N = slots.numel()
+    if (context_lens.numel() != S or query_lens.numel() != S or seq_lens.numel() != S
+            or cu_seqlens_q.numel() != S + 1):
         raise ValueError("inconsistent shapes of context_lens, query_lens, seq_lens, "
                          "cu_seqlens_q, block_tables")
-    if positions is not None and positions.size(0) != N:
+    if positions is not None and positions.numel() != N:
         raise ValueError("positions must have a value per slot")
-    if free_end.size(0) != 1 or (free_start is not None and free_start.size(0) != 1):
+    if free_end.numel() != 1 or (free_start is not None and free_start.numel() != 1):
         raise ValueError("free_start and free_end hold one value")
-    dev = slots.get_device()
-    _one_device(dev, cu_seqlens_q, seq_lens, free_end, block_tables, context_lens, query_lens,
-                free_pages, free_start, positions)
     _on(dev, lib.paged_kv_slots, slots.data_ptr(),
         None if positions is None else positions.data_ptr(), cu_seqlens_q.data_ptr(),
         seq_lens.data_ptr(), free_end.data_ptr(), block_tables.data_ptr(),
         context_lens.data_ptr(), query_lens.data_ptr(), free_pages.data_ptr(),
-        None if free_start is None else free_start.data_ptr(), S, N, free_pages.size(0),
+        None if free_start is None else free_start.data_ptr(), S, N, free_pages.numel(),
         int(block_size), MB, int(num_blocks), stream=stream)
 
 
@@ -710,14 +726,16 @@ def paged_kv_write(k_cache, v_cache, k_new, v_new, slots, layout=None, stream=No
     src = _packed_strides(k_new, "k_new")
     if _packed_strides(v_new, "v_new") != src:
         raise ValueError("k_new and v_new must have the same strides")
-    if not _fits(slots, _I32, 1):
+    dev = _index(slots)
+    if not _fits(dev, _I32, 1, slots):
         _check(slots, "slots", _I32, 1)
     N, Hkv, D = k_new.shape
-    if v_new.shape != k_new.shape or slots.size(0) != N:
+    if v_new.shape != k_new.shape or slots.numel() != N:
         raise ValueError("k_new and v_new must have the same shape, and a slot per row")
     if layout is None:
-        if not (_fits(k_cache, _F16, 4) and _fits(v_cache, _F16, 4)):
+        if not _fits(dev, _F16, 4, k_cache, v_cache):
             _check_all((k_cache, "k_cache", _F16, 4), (v_cache, "v_cache", _F16, 4))
+            _one_device(dev, k_cache, v_cache)
         NB, H2, BS, D2 = k_cache.shape
         if v_cache.shape != k_cache.shape or D2 != D or H2 != Hkv:
             raise ValueError("inconsistent shapes of k_cache, v_cache, k_new")
@@ -728,9 +746,9 @@ def paged_kv_write(k_cache, v_cache, k_new, v_new, slots, layout=None, stream=No
             raise ValueError(f"layout of {H2} KV heads for rows of {Hkv}")
         _check_rows_inside(k_cache, "k_cache", NB, Hkv, BS, D, strides)
         _check_rows_inside(v_cache, "v_cache", NB, Hkv, BS, D, strides)
+        _one_device(dev, k_cache, v_cache)
         sp, sh, st = (int(x) for x in strides)
-    dev = slots.get_device()
-    _one_device(dev, k_new, v_new, k_cache, v_cache)
+    _one_device(dev, k_new, v_new)
     _on(dev, lib.paged_kv_write, k_cache.data_ptr(), v_cache.data_ptr(), k_new.data_ptr(),
         v_new.data_ptr(), slots.data_ptr(), N, Hkv, D, int(BS), int(NB), sp, sh, st, *src,
         stream=stream)
