@@ -503,9 +503,10 @@ pgd_status pgd_varlen_plan(int num_seqs, int total_q, int max_q_len, int num_q_h
  * inside total_q) is skipped; rows behind the last sequence (total_q above
  * cu_seqlens_q[num_seqs], a padded batch) are left as they were.  K and V rows
  * of one sequence's tree must be finite: a weight of 0 does not hide an
- * infinity or NaN in a sibling's V.  Library scratch, where there is any, is
- * per call (also in a captured graph), and there is no state between calls:
- * calls on different streams and replays of different graphs may overlap.
+ * infinity or NaN in a sibling's V.  out must not overlap an input.  Library
+ * scratch, where there is any, is per call (also in a captured graph), and
+ * there is no state between calls: calls on different streams and replays of
+ * different graphs may overlap.
  */
 #define PGD_OUT_F32 0
 #define PGD_OUT_F16 1
@@ -552,8 +553,8 @@ pgd_status pgd_tree_plan(int num_seqs, int total_q, int max_q_len, int num_q_hea
  *              else at least pgd_prefill_plan's bytes, 256-byte aligned, not
  *              used by anything else until the call's work is done
  *
- * head_dim 64/128/256, groups of up to 128 query heads.  Rows that belong to no
- * prompt are left as they were (not written).  A prompt that is longer than
+ * head_dim 64/128/256, groups of up to 128 query heads; out must not overlap
+ * an input.  Rows that belong to no prompt are left as they were (not written).  A prompt that is longer than
  * max_len, has a negative length or does not lie inside total is skipped and
  * sets PGD_DEVERR_QUERY_LEN.  Other prompts' rows may hold anything; within
  * one prompt an infinity or NaN in V is not hidden from earlier rows of the same
@@ -569,7 +570,7 @@ pgd_status packed_gqa_prefill(void *out, int out_type, const uint16_t *q, const 
                               void *stream);
 
 /* Scratch bytes a packed_gqa_prefill call with these sizes needs (the list of
- * its tiles, longest first).  Pure arithmetic. */
+ * its work units, longest first).  Pure arithmetic. */
 pgd_status pgd_prefill_plan(int num_seqs, int total, int num_q_heads, int num_kv_heads,
                             int head_dim, size_t *workspace_bytes);
 
@@ -707,7 +708,8 @@ pgd_status pgd_device_info(int head_dim, int block_size, int *num_sms, int *ctas
 /* Library version, major * 10000 + minor * 100 + patch (1.1.0: strided caches,
  * head_dim 64, block sizes 64 and 128; 1.2.0: several query tokens per
  * sequence; 1.3.0: quantised pages; 1.4.0: pgd_workspace_size, pgd_release,
- * paged_gqa_decode_host). */
+ * paged_gqa_decode_host; 1.5.0: paged_gqa_tree, packed_gqa_prefill,
+ * paged_kv_slots, paged_kv_write). */
 int pgd_version(void);
 
 #ifdef __cplusplus

@@ -2350,6 +2350,6 @@ pgd_status pgd_device_info(int head_dim, int block_size, int *num_sms, int *ctas
     return PGD_OK;
 }
 
-int pgd_version(void) { return 10400; }
+int pgd_version(void) { return 10500; }
 
 }  // extern "C"

@@ -24,8 +24,9 @@ constexpr int kSlab = 128 * 128;       // bytes of 128 rows of one 64-wide slab 
 
 // The units of a call in decreasing order of their stages (a counting sort):
 // {first row of q, position of that row, rows left in the prompt, KV head} per
-// tile (or pair of tiles) of `span` tokens and KV head.  The CTAs of the attention kernel deal them out like cards, back and
-// forth, so the long ones are spread evenly and the short ones fill the end.
+// tile (or pair of tiles) of `span` tokens and KV head.  The CTAs of the
+// attention kernel deal them out like cards, back and forth, so the long ones are
+// spread evenly and the short ones fill the end.
 __global__ void __launch_bounds__(kPrefillOrderKeys)
     packed_prefill_order_kernel(const PrefillParams p)
 {
@@ -152,8 +153,19 @@ __device__ __forceinline__ float extreme128(const float (&v)[4][32], bool least)
 // buffer back, long before its exponentials are done, and the tensor pipe has
 // a P V product (512 cycles) to do meanwhile.  So the pipe runs S_A(j+1),
 // P_A(j) V_j, S_B(j+1), P_B(j) V_j without a gap: S(j+1) does not wait for P(j)
-// V_j, nor P V for a softmax that has just begun — a tile's softmax (about
-// 1200 cycles) has the whole 2048-cycle period minus its own S.
+// V_j, nor P V for a softmax that has just begun.  Where a stage's cycles go,
+// by clock stamps: a period of 3150 for both tiles, of which the products take
+// 2048; between a tile's scores being whole and the other's being whole lie
+// 330 cycles of reading, 250 until the next product is issued and the 512 of
+// it behind what the pipe still holds.  A tile's softmax takes 2400 of the
+// period (reading 330, maximum 400, exponentials 900, P 200, barriers).
+// One prompt of 16381 tokens, 32 / 8 heads x 128: 1450 to 1515 us by the GPU's
+// clock at the time, 1450 to 1520 TFLOP/s; 4 x 2048 tokens: 115 us.  Tried
+// and slower: part of the exponentials as polynomials on the FMA pipes (a
+// quarter of them: 1450 -> 1690 us: the issue slots, not the special-function
+// unit, are short); two threads per row (16 softmax warps: 1630); the rows'
+// way out by four warps of their own (4 x 2048: 115 -> 127, O has no second
+// place to go on in); polling for o_done instead of waiting (1580).
 //   * warp 0, one thread: Q tiles, K and V stages by tensor copies (one per
 //     stage; K and V in rings of their own)
 //   * warp 1, one thread: the scores; warp 2, one thread: the outputs.  The pipe
@@ -636,6 +648,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // all of head_dim, so that beside the 64 KB of Q nine of them fit and each is
 // free again after its own products: a stage's copies are never waited for as
 // a whole.  Eight softmax warps: rows r by halves of a stage's keys.
+// A prompt of 8192 tokens, 16 / 2 heads: 405 us, 1360 TFLOP/s.  37 prompts of 1
+// to 512 tokens, 24 / 4 heads: 33 us, of which a unit's start and end are the
+// larger part: a unit of one token costs 4.6 us of its CTA's time.  Ending a
+// unit's last stage at its last key (copies and products by 32 keys) took 5 %
+// off the short prompts and added 5 % to the long one: not taken.
 constexpr int kWideThreads = 384;
 constexpr int kWideNK = 5, kWideNV = 4;  // pieces
 constexpr int kWideD = 256;
