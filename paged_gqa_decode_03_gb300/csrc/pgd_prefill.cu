@@ -267,6 +267,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int from = x * p.TQ;
         return u.z > from ? (u.y + min(u.z, from + p.TQ) + kNT - 1) / kNT : 0;
     };
+    // Steps of 16 keys that the output's product takes of the tile's last stage: up
+    // to its last key, by twos.  (8192 tokens at head_dim 64: 380 us with the
+    // whole stage, 363 by twos, 350 one by one; 16381 at 128: 1490, 1465, 1465;
+    // 190 prompts of 128 tokens: 96, 100, 105, the price of the branches.)
+    auto last_steps = [&](const int4 &u, int x) {
+        return ((u.y + min(u.z, (x + 1) * p.TQ) - 1) % kNT / 32 + 1) * 2;
+    };
 
     // the softmax warps hold a row's 128 scores and half of its weights: they
     // take registers that the copying and issuing warps do not need (128 x 80 +
@@ -441,10 +448,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                 ;
                         tc_fence_after();
                         const uint32_t o = tmem + x * D, a = tmem + P_COL + x * 64;
+                        const int steps = j + 1 < (x ? nt1 : nt0) ? kNT / 16 : last_steps(u, x);
 #pragma unroll
-                        for (int kk = 0; kk < kNT / 16; ++kk)
-                            tc_mma_ta(o, a + kk * 8, vs + ((kk * 2048) >> 4), IDESC_O,
-                                      j > 0 || kk > 0);
+                        for (int part = 0; part < kNT / 16; part += 2) {
+                            if (part >= steps)
+                                break;
+#pragma unroll
+                            for (int kk = part; kk < part + 2; ++kk)
+                                tc_mma_ta(o, a + kk * 8, vs + ((kk * 2048) >> 4), IDESC_O,
+                                          j > 0 || kk > 0);
+                        }
                         tc_commit(smem_addr(&o_done[x]));
                     }
                     tc_commit(smem_addr(&v_empty[st]));
@@ -584,18 +597,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         tc_st32(t_lane + o_col + 32 * c, o);
                     }
                 }
-                // rows of the stage behind the prompt belong to the next one
-                // and may hold anything: zero them in V (their weights are 0,
-                // which does not hide a NaN).  Each tile does so before its own
-                // product; the other's writes the same zeros.
-                const bool zero_v = t0 + kNT > n;
+                // rows behind the prompt belong to the next one and may hold
+                // anything: zero those of them in V that the tile's last product
+                // takes in (their weights are 0, which does not hide a NaN).
+                // Each tile does so before its own product; the other's writes
+                // the same zeros.
+                const int za = n - t0, ze = j + 1 < ntx ? 0 : 16 * last_steps(u, x);
+                const bool zero_v = za < ze;
                 if (zero_v) {
                     const int st = (nv + j) % NV;
                     mbar_wait_bounded(smem_addr(&v_full[st]), ((nv + j) / NV) & 1, nullptr,
                                       p.wait_budget_ns);
                     uint8_t *vs = v_ptr + st * KV_TILE;
-                    const int za = n - t0;
-                    for (int idx = r; idx < (kNT - za) * SLABS * 8; idx += 128) {
+                    for (int idx = r; idx < (ze - za) * SLABS * 8; idx += 128) {
                         const int row = za + idx / (SLABS * 8), c = idx % (SLABS * 8);
                         *reinterpret_cast<uint4 *>(vs + (c >> 3) * kSlab + row * 128 +
                                                    (c & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -649,10 +663,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // free again after its own products: a stage's copies are never waited for as
 // a whole.  Eight softmax warps: rows r by halves of a stage's keys.
 // A prompt of 8192 tokens, 16 / 2 heads: 405 us, 1360 TFLOP/s.  37 prompts of 1
-// to 512 tokens, 24 / 4 heads: 33 us, of which a unit's start and end are the
-// larger part: a unit of one token costs 4.6 us of its CTA's time.  Ending a
-// unit's last stage at its last key (copies and products by 32 keys) took 5 %
-// off the short prompts and added 5 % to the long one: not taken.
+// to 512 tokens, 24 / 4 heads: 31 us, of which a unit's start and end are the
+// larger part: a unit of one token costs 4.1 us of its CTA's time.  The output's
+// product of a unit's last stage ends at the tile's last key, rounded up to 16,
+// so that of the rows behind a prompt 15 at most have to be zeroed (the whole
+// stage: 34.5 us).  Ending its copies and scores there as well added 5 % to the
+// long prompt: not taken.
 constexpr int kWideThreads = 384;
 constexpr int kWideNK = 5, kWideNV = 4;  // pieces
 constexpr int kWideD = 256;
@@ -726,6 +742,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         abort_flag = 1;
     };
     auto stages = [&](const int4 &u) { return (u.y + min(u.z, p.TQ) + kNT - 1) / kNT; };
+    auto last_steps = [&](const int4 &u) {
+        return (u.y + min(u.z, p.TQ) - 1) % kNT / 16 + 1;
+    };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -858,6 +877,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                         if (!wait(&p_full, np & 1))
                             break;
                         const uint32_t a = tmem + S_COL + (np & 1) * kNT;
+                        const int steps = j + 1 < nt ? kNT / 16 : last_steps(u);
                         for (int i = 0; i < VP; ++i, ++nv) {
                             const int st = nv % NV;
                             if (!wait(&v_full[st], (nv / NV) & 1))
@@ -866,7 +886,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                             const uint64_t vs = v_desc + ((st * PIECE) >> 4);
 #pragma unroll
                             for (int kk = 0; kk < VKEYS / 16; ++kk)
-                                tc_mma_ta(tmem, a + (i * (VKEYS / 16) + kk) * 8,
+                                if (i * (VKEYS / 16) + kk < steps)
+                                    tc_mma_ta(tmem, a + (i * (VKEYS / 16) + kk) * 8,
                                           vs + ((kk * 2048) >> 4), IDESC_O, j > 0 || i > 0 || kk > 0);
                             tc_commit(smem_addr(&v_empty[st]));
                         }
@@ -1002,13 +1023,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                         }
                     }
                 }
-                const bool zero_v = t0 + kNT > n;
+                const int za = n - t0, ze = j + 1 < nt ? 0 : 16 * last_steps(u);
+                const bool zero_v = za < ze;  // (as in the pair kernel)
                 if (zero_v) {
-                    const int za = n - t0;  // first key behind the prompt
-                    for (int i = za / VKEYS; i < VP; ++i)
-                        mbar_wait_bounded(smem_addr(&v_full[(nv + i) % NV]), ((nv + i) / NV) & 1,
-                                          nullptr, p.wait_budget_ns);
-                    for (int idx = half * 128 + r; idx < (kNT - za) * SLABS * 8; idx += 256) {
+                    mbar_wait_bounded(smem_addr(&v_full[(nv + za / VKEYS) % NV]),
+                                      ((nv + za / VKEYS) / NV) & 1, nullptr, p.wait_budget_ns);
+                    for (int idx = half * 128 + r; idx < (ze - za) * SLABS * 8; idx += 256) {
                         const int key = za + idx / (SLABS * 8), c = idx % (SLABS * 8);
                         const int st = (nv + key / VKEYS) % NV, row = key % VKEYS;
                         *reinterpret_cast<uint4 *>(v_ptr + st * PIECE + (c >> 3) * (VKEYS * 128) +
