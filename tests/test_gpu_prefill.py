@@ -201,3 +201,35 @@ def test_captured_and_replayed_beside_another_call():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, base) and torch.equal(out2, other)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_every_length_beside_prompts_of_nan(D):
+    """Prompts of 1 to 140 tokens, a prompt of NaN rows behind each: no weight of
+    0 meets them, wherever in a stage the prompt ends."""
+    lens = [n for k in range(1, 141) for n in (k, 3)]
+    c = case(lens, 4, 2, D, seed=21)
+    at = 0
+    for s, n in enumerate(lens):
+        if s % 2:
+            for t in (c["q"], c["k"], c["v"]):
+                t[at:at + n] = float("nan")
+        at += n
+    check(run(c), c, f"D{D}", prompts=set(range(0, len(lens), 2)))
+
+
+def test_rows_past_32_bit_offsets():
+    """q and out of more than 2^31 elements; groups of 128 heads."""
+    n, D = 6, 256
+    S = (2 ** 31 + 2 ** 24) // (128 * D * n)
+    T = S * n
+    q = torch.empty((T, 128, D), dtype=torch.float16, device=DEV).normal_()
+    k, v = (torch.randn((T, 1, D), device=DEV).half() for _ in range(2))
+    cu = torch.arange(S + 1, dtype=torch.int32, device=DEV) * n
+    out = torch.full_like(q, 7.0)
+    pgd.packed_gqa_prefill(out, q, k, v, cu, D ** -0.5, n)
+    torch.cuda.synchronize()
+    for s in (0, S // 2, S - 2, S - 1):
+        rows = slice(s * n, s * n + n)
+        ref, A = attention(q[rows], k[rows], v[rows], packed_seen(n), D ** -0.5)
+        assert_attention(out[rows], ref, A, n, D, float(v[rows].abs().max()), f"prompt {s}")

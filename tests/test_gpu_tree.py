@@ -246,3 +246,35 @@ def test_captured_and_replayed_on_another_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, base)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_every_length_before_rows_of_nan(D):
+    """Contexts of 0 to 139 tokens; the rows of the last page behind the sequence
+    hold NaN."""
+    ctx = list(range(140))
+    w, trees, parents = case(ctx, [1 + s % 9 for s in ctx], 4, 2, D, 32, seed=31)
+    k, v = w.k_cache.clone(), w.v_cache.clone()
+    for s, c in enumerate(ctx):
+        L = c + len(trees[s])
+        if L % 32:
+            page = int(w.block_tables[s, L // 32])
+            for t in (k, v):
+                t[page, :, L % 32:] = float("nan")
+    check(run(w, parents, k=k, v=v), w, trees, ctx, f"D{D}")
+
+
+def test_pages_past_32_bit_offsets():
+    """A cache whose used pages start past element 2^31."""
+    ctx, n = [300, 17, 64], [20, 33, 5]
+    w, trees, parents = case(ctx, n, 32, 8, 128, 16, seed=32)
+    used = w.k_cache.shape[0]
+    NB = (2 ** 31 + 2 ** 24) // (8 * 16 * 128) + used
+    big = [torch.empty((NB, 8, 16, 128), dtype=torch.float16, device=DEV) for _ in range(2)]
+    for t, c in zip(big, (w.k_cache, w.v_cache)):
+        t[NB - used:] = c
+    out = torch.empty((w.total_q, 32, 128), dtype=torch.float16, device=DEV)
+    pgd.paged_gqa_tree(out, w.q, w.cu_seqlens_q, parents, *big, w.block_tables + (NB - used),
+                       w.seq_lens, w.scale, w.max_q_len)
+    torch.cuda.synchronize()
+    check(out, w, trees, ctx, "far pages")
