@@ -53,20 +53,21 @@ FALLBACK_HBM_GBS = 6800.0
 # sources they were taken on (hash of csrc/ below), keyed by (workload,
 # partition size).
 TRAFFIC = {
-    # decode kernels (hash without pgd_varlen.cu)
-    "22686a0c259250ef": {("long_context", 512): 1_293_085_440 + 7_323_904,
-                         ("long_context", 256): 1_293_064_192 + 7_469_312,
-                         ("ragged_tails", 256): 888_242_432 + 6_854_144,
-                         ("serving_mix", 512): 1_212_329_984 + 6_878_464,
-                         ("batch_decode", 512): 633_321_472 + 5_394_432,
-                         ("batch_decode_q8", 512): 336_775_168 + 4_792_576,
-                         ("long_context_q8", 512): 687_138_560 + 6_665_216,
-                         ("ragged_tails_q8", 256): 472_754_688 + 6_605_056,
-                         ("serving_mix_q8", 512): 644_722_176 + 6_985_472},
-    # the several-query-token kernels (hash without the decode kernels' files)
-    "dca98565443fa7ab": {("chunked_prefill", 8320): 267_655_168 + 41_203_200,
-                         ("prefill", 2048): 102_982_400 + 83_275_008,
-                         ("spec_verify", 4096): 605_178_624 + 4_264_704},
+    # decode kernels (hash without pgd_varlen.cu and the step's operators)
+    "ca5c1dac27761114": {("long_context", 512): 1_293_067_264 + 6_864_896,
+                         ("long_context", 256): 1_293_185_024 + 7_358_208,
+                         ("ragged_tails", 256): 888_200_704 + 6_841_344,
+                         ("serving_mix", 512): 1_212_336_640 + 6_846_208,
+                         ("batch_decode", 512): 633_309_952 + 5_264_896,
+                         ("batch_decode_q8", 512): 336_819_456 + 4_822_272,
+                         ("long_context_q8", 512): 687_138_048 + 6_886_656,
+                         ("ragged_tails_q8", 256): 472_705_536 + 6_773_760,
+                         ("serving_mix_q8", 512): 644_734_976 + 7_085_824},
+    # the several-query-token kernels (hash without the decode kernels' files
+    # and the step's operators)
+    "581bd824679a3af2": {("chunked_prefill", 8320): 265_761_280 + 41_800_960,
+                         ("prefill", 2048): 103_046_656 + 82_970_368,
+                         ("spec_verify", 4096): 605_144_320 + 4_453_376},
 }
 
 
@@ -97,9 +98,9 @@ def _code_only(text):
 
 def kernel_source_hash(exclude=()):
     """Hash of the code of the CUDA sources (csrc/; comments and layout
-    left out), less the files in `exclude`: the decode kernels do not
-    include pgd_varlen.cu, so their traffic figure stays valid while only
-    that file changes."""
+    left out), less the files in `exclude`: the decode kernels include
+    neither pgd_varlen.cu nor the step's operators, so their traffic figure
+    stays valid while only those files change."""
     import glob
     import hashlib
     h = hashlib.sha256()
@@ -112,10 +113,12 @@ def kernel_source_hash(exclude=()):
     return h.hexdigest()[:16]
 
 
-DECODE_HASH_EXCLUDE = ("pgd_varlen.cu",)
+# the operators around the cache: kernels that no workload of this file runs
+STEP_FILES = ("pgd_kv.cu", "pgd_tree.cu", "pgd_prefill.cu", "pgd_rows.cuh")
+DECODE_HASH_EXCLUDE = ("pgd_varlen.cu",) + STEP_FILES
 # the several-query-token kernels include neither the decode kernels nor the quantiser
 VARLEN_HASH_EXCLUDE = ("pgd_kernels.cuh", "pgd_kernels_d64.cu", "pgd_kernels_d128.cu",
-                       "pgd_kernels_d256.cu", "pgd_quantize.cu")
+                       "pgd_kernels_d256.cu", "pgd_quantize.cu") + STEP_FILES
 
 
 def measured_peaks():
