@@ -21,6 +21,12 @@ namespace {
 
 constexpr int kNT = 128;               // keys per stage
 constexpr int kSlab = 128 * 128;       // bytes of 128 rows of one 64-wide slab of head_dim
+// Of the products' descriptor: -A for A.  With a negative scale the scores are
+// those of -q, and the softmax goes by |scale|: its loop then looks for the
+// largest score whatever the sign (a second loop for the smallest, although it
+// was not run, cost 4 x 2048 tokens 115 us instead of 111 by its place in the
+// code).
+constexpr uint32_t kNegateA = 1u << 13;
 
 // The units of a call in decreasing order of their stages (a counting sort):
 // {first row of q, position of that row, rows left in the prompt, KV head} per
@@ -116,30 +122,19 @@ __device__ __forceinline__ uint32_t first_bits(int n)
     return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-// The largest (smallest, for a negative scale) of a row's 128 scores: four
-// independent chains of three-input extremes.  The sign is the call's, so it is
-// a branch around either loop: a choice per element would triple the work.
-__device__ __forceinline__ float extreme128(const float (&v)[4][32], bool least)
+// The largest of a row's 128 scores: four independent chains of three-input
+// maxima.
+__device__ __forceinline__ float max128(const float (&v)[4][32])
 {
     float e[4];
-    if (!least) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            e[c] = fmaxf(v[c][0], v[c][1]);
-#pragma unroll
-            for (int i = 2; i < 32; i += 2)
-                e[c] = fmax3(e[c], v[c][i], v[c][i + 1]);
-        }
-        return fmax3(e[0], e[1], fmaxf(e[2], e[3]));
-    }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        e[c] = fminf(v[c][0], v[c][1]);
+        e[c] = fmaxf(v[c][0], v[c][1]);
 #pragma unroll
         for (int i = 2; i < 32; i += 2)
-            e[c] = fmin3(e[c], v[c][i], v[c][i + 1]);
+            e[c] = fmax3(e[c], v[c][i], v[c][i + 1]);
     }
-    return fmin3(e[0], e[1], fminf(e[2], e[3]));
+    return fmax3(e[0], e[1], fmaxf(e[2], e[3]));
 }
 
 // packed_prefill_pair_kernel<D> (head_dim 64, 128) — persistent, one CTA per
@@ -159,8 +154,8 @@ __device__ __forceinline__ float extreme128(const float (&v)[4][32], bool least)
 // 330 cycles of reading, 250 until the next product is issued and the 512 of
 // it behind what the pipe still holds.  A tile's softmax takes 2400 of the
 // period (reading 330, maximum 400, exponentials 900, P 200, barriers).
-// One prompt of 16381 tokens, 32 / 8 heads x 128: 1450 to 1515 us by the GPU's
-// clock at the time, 1450 to 1520 TFLOP/s; 4 x 2048 tokens: 115 us.  Tried
+// One prompt of 16381 tokens, 32 / 8 heads x 128: 1450 to 1500 us by the GPU's
+// clock at the time, 1450 to 1520 TFLOP/s; 4 x 2048 tokens: 111 us.  Tried
 // and slower: part of the exponentials as polynomials on the FMA pipes (a
 // quarter of them: 1450 -> 1690 us: the issue slots, not the special-function
 // unit, are short); two threads per row (16 softmax warps: 1630); the rows'
@@ -267,12 +262,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int from = x * p.TQ;
         return u.z > from ? (u.y + min(u.z, from + p.TQ) + kNT - 1) / kNT : 0;
     };
-    // Steps of 16 keys that the output's product takes of the tile's last stage: up
-    // to its last key, by twos.  (8192 tokens at head_dim 64: 380 us with the
-    // whole stage, 363 by twos, 350 one by one; 16381 at 128: 1490, 1465, 1465;
-    // 190 prompts of 128 tokens: 96, 100, 105, the price of the branches.)
+    // Steps of 16 keys that the output's product takes of the tile's last stage: at
+    // head_dim 64 up to its last key, by twos (8192 tokens: 341 us, with the
+    // whole stage 358), at 128 the whole stage (16381 tokens: 1462 us, by
+    // twos 1477; 190 prompts of 128 tokens: 96 and 95)
+    constexpr int PART = D == 64 ? 2 : kNT / 16;
     auto last_steps = [&](const int4 &u, int x) {
-        return ((u.y + min(u.z, (x + 1) * p.TQ) - 1) % kNT / 32 + 1) * 2;
+        return ((u.y + min(u.z, (x + 1) * p.TQ) - 1) % kNT / (16 * PART) + 1) * PART;
     };
 
     // the softmax warps hold a row's 128 scores and half of its weights: they
@@ -352,6 +348,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       } else if (warp == 1) {
         if (lane == 0) {
             // ======================================================== scores
+            const uint32_t idesc_s = IDESC_S | (p.scale_log2 < 0.f ? kNegateA : 0u);
             const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
             const uint64_t k_desc = tc_sdesc(k_s, 16, 1024);
             bool ok = true;
@@ -391,7 +388,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
                             tc_mma(d, qx + (((kk / 4) * kSlab + (kk % 4) * 32) >> 4),
-                                   ks + (((kk / 4) * kSlab + (kk % 4) * 32) >> 4), IDESC_S, kk > 0);
+                                   ks + (((kk / 4) * kSlab + (kk % 4) * 32) >> 4), idesc_s, kk > 0);
                         tc_commit(smem_addr(&s_full[x]));
                         s_issued[x] = ++ns[x];
                     }
@@ -450,11 +447,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         const uint32_t o = tmem + x * D, a = tmem + P_COL + x * 64;
                         const int steps = j + 1 < (x ? nt1 : nt0) ? kNT / 16 : last_steps(u, x);
 #pragma unroll
-                        for (int part = 0; part < kNT / 16; part += 2) {
+                        for (int part = 0; part < kNT / 16; part += PART) {
                             if (part >= steps)
                                 break;
 #pragma unroll
-                            for (int kk = part; kk < part + 2; ++kk)
+                            for (int kk = part; kk < part + PART; ++kk)
                                 tc_mma_ta(o, a + kk * 8, vs + ((kk * 2048) >> 4), IDESC_O,
                                           j > 0 || kk > 0);
                         }
@@ -481,11 +478,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                        p_col = P_COL + x * 64;
         const int ti = r / p.G;
         // a scale of 0 runs as 1e-30: exp2 of every score is then 1 in fp32
-        // (the mean over the range, as for 0) while masked scores, infinite
-        // with the sign that scales to -inf, still give 0
-        const float sc = p.scale_log2 == 0.f ? 1e-30f : p.scale_log2;
-        const bool neg = sc < 0.f;
-        const float masked = neg ? INFINITY : -INFINITY;
+        // (the mean over the range, as for 0) while masked scores, -inf, still
+        // give 0
+        const float sc = p.scale_log2 == 0.f ? 1e-30f : fabsf(p.scale_log2);
         const float2 sc2 = make_float2(sc, sc);
         const RowPlaces places(row_bytes, p.Hq, p.G, p.TQ, quarter, lane);
         int ns = 0, nv = 0;  // S tiles of this tile, V stages of the CTA, so far
@@ -535,14 +530,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             const uint32_t seen = first_bits(lim + 1 - (t0 + 32 * c));
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                v[c][i] = (seen >> i) & 1u ? v[c][i] : masked;
+                                v[c][i] = (seen >> i) & 1u ? v[c][i] : -INFINITY;
                         }
                 }
                 // has this tile's last P V ended?  (asked here, used below)
                 const bool pv_over =
                     j == 0 || mbar_try_wait(smem_addr(&o_done[x]), (ns - 1) & 1);
-                const float e = extreme128(v, neg);
-                const float mt = e == masked ? -INFINITY : e * sc;
+                const float mt = max128(v) * sc;
                 // the reference maximum moves only by more than 8 (log2
                 // units): p stays below 2^8, well inside fp16, and O is
                 // rescaled rarely
@@ -826,7 +820,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             };
             int4 next = unit_at(p, 0, units);
             if (warp == 1) {
-                const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
+                const uint32_t idesc_s = IDESC_S | (p.scale_log2 < 0.f ? kNegateA : 0u);
+            const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
                 const uint64_t k_desc = tc_sdesc(k_s, 16, 1024);
                 int nk = 0, nq = 0, ns = 0;
                 for (int k = 0; k < turns && ok; ++k) {
@@ -852,7 +847,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                             const uint64_t qs = q_desc + ((sl * kSlab) >> 4);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc_mma(d, qs + ((kk * 32) >> 4), ks + ((kk * 32) >> 4), IDESC_S,
+                                tc_mma(d, qs + ((kk * 32) >> 4), ks + ((kk * 32) >> 4), idesc_s,
                                        sl > 0 || kk > 0);
                             tc_commit(smem_addr(&k_empty[st]));
                         }
@@ -911,9 +906,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t pair_bar = 1 + quarter;
         const int ti = r / p.G;
-        const float sc = p.scale_log2 == 0.f ? 1e-30f : p.scale_log2;
-        const bool neg = sc < 0.f;
-        const float masked = neg ? INFINITY : -INFINITY;
+        const float sc = p.scale_log2 == 0.f ? 1e-30f : fabsf(p.scale_log2);
         const float2 sc2 = make_float2(sc, sc);
         const RowPlaces places(row_bytes, p.Hq, p.G, p.TQ, quarter, lane);
         int ns = 0, nv = 0;
@@ -943,7 +936,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 const uint32_t s_col = S_COL + (ns & 1) * kNT;
                 wait(&s_full[ns & 1], (ns >> 1) & 1);
                 float v[2][32];
-                float e = masked;
+                float e = -INFINITY;
                 if (ok) {
                     tc_fence_after();
                     tc_ld32(t_lane + s_col + half * HC, v[0]);
@@ -956,21 +949,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                         for (int c = 0; c < 2; ++c)
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                v[c][i] = c0 + 32 * c + i > lim ? masked : v[c][i];
+                                v[c][i] = c0 + 32 * c + i > lim ? -INFINITY : v[c][i];
                     }
                     float ec[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        ec[c] = masked;
+                        ec[c] = -INFINITY;
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             const float a = v[c >> 1][16 * (c & 1) + i],
                                         b = v[c >> 1][16 * (c & 1) + i + 1];
-                            ec[c] = neg ? fmin3(ec[c], a, b) : fmax3(ec[c], a, b);
+                            ec[c] = fmax3(ec[c], a, b);
                         }
                     }
-                    e = neg ? fmin3(ec[0], ec[1], fminf(ec[2], ec[3]))
-                            : fmax3(ec[0], ec[1], fmaxf(ec[2], ec[3]));
+                    e = fmax3(ec[0], ec[1], fmaxf(ec[2], ec[3]));
                 }
                 pair_red[ns & 1][half][r] = e;
                 tc_fence_before();
@@ -979,8 +971,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 const float e2 = pair_red[ns & 1][half ^ 1][r];
                 if (!ok)
                     continue;
-                e = neg ? fminf(e, e2) : fmaxf(e, e2);
-                const float mt = e == masked ? -INFINITY : e * sc;
+                const float mt = fmaxf(e, e2) * sc;
                 bool rescale = false;
                 float alpha = 1.f;
                 if (mt > m_ref + 8.f) {
