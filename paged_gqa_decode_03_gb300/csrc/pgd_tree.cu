@@ -22,7 +22,7 @@
 //     32 sequences of 8 k to 32 k tokens, 16 / 2 heads x 256: 270 us, 5.1 TB/s
 //     (two CTAs of a cluster that each hold all of a stage, copied by multicast:
 //     338 us); 64 of 512 to 4096 tokens, 32 / 8 heads x 128, single CTAs:
-//     110 us, 5.9 TB/s; one of 1000: 13 us, latency.
+//     107 us, 6.1 TB/s; one of 1000: 12.5 us, latency.
 //   * The stages of all units, one after the other, are cut into equal runs, one
 //     per resident CTA or pair: no run has more than another, whatever the
 //     lengths.  A unit that is cut leaves pieces (reference maximum, exp-sum,
@@ -44,7 +44,8 @@ namespace {
 
 // warp 0 Q and K copies, 1 V copies, 2 scores, 3 outputs, 4-11 softmax
 constexpr int kTreeThreads = 384;
-constexpr int kTreeVWarp = 1, kTreeSWarp = 2, kTreeOWarp = 3;
+constexpr uint32_t kTreeNegateA = 1u << 13;  // of the products' descriptor: -A for A
+constexpr int kTreeVWarp = 1, kTreeSWarp = 2;
 constexpr int kTreeWords = kTreeMaxNodes / 32;
 
 template <int D, bool PAIR> constexpr size_t tree_smem_bytes()
@@ -139,9 +140,9 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s)
     return q;
 }
 // What a unit counts in the division of the work: its stages, and what it costs
-// beside them (its start and end), in stages: with 0, 1, 2, 4, 6 a batch of 64
-// requests of 512 to 4096 tokens took 118, 116, 110, 110, 112 us, 32 of 8 k to
-// 32 k tokens 271, 269, 269, 277, 278.
+// beside them (its start and end), in stages: with 1, 2, 3, 4 a batch of 64
+// requests of 512 to 4096 tokens takes 106.6, 106.4, 106.5, 107 us (with 0 it
+// took 8 us more), 32 of 8 k to 32 k tokens 275 with any.
 constexpr int kTreeUnitCost = 2;
 __device__ __forceinline__ int tree_cost(const TreeParams &p, const TreeSeq &q)
 {
@@ -357,7 +358,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     };
 
     if (warp < 4) {
-      regs_give<104>();  // to the softmax warps (128 x 104 + 256 x 200 of 384 x 168)
+      // 8 each to the softmax warps (128 x 152 + 256 x 176 of the launch's 384 x
+      // 168): no role spills.  (128 x 104 + 256 x 200: the copying warps spill,
+      // 64 requests 111.5 us instead of 107.9.)
+      regs_give<152>();
       if (warp == 0 || warp == kTreeVWarp) {
         // ============================================================ copies
         // warp 0: Q tiles and K, warp 1: V.  A piece is a copy per page (or one
@@ -475,6 +479,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 tc_commit(smem_addr(bar));
         };
         if (warp == kTreeSWarp) {
+            // (a negative scale: -q for q)
+            const uint32_t idesc_s = IDESC_S | (p.scale_log2 < 0.f ? kTreeNegateA : 0u);
             const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
             const uint64_t k_desc = tc_sdesc(k_s, 16, KGROUP);
             int nk = 0, ns = 0, nq = 0;  // K pieces, S products, Q tiles
@@ -498,9 +504,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             const uint64_t a = qs + (((kk / 4) * Q_SLAB + (kk % 4) * 32) >> 4);
                             const uint64_t b = ks + (((kk / 4) * 1024 + (kk % 4) * 32) >> 4);
                             if constexpr (PAIR)
-                                tc_mma_pair(d, a, b, IDESC_S, kp > 0 || kk > 0);
+                                tc_mma_pair(d, a, b, idesc_s, kp > 0 || kk > 0);
                             else
-                                tc_mma(d, a, b, IDESC_S, kp > 0 || kk > 0);
+                                tc_mma(d, a, b, idesc_s, kp > 0 || kk > 0);
                         }
                         commit(&k_empty[st]);
                     }
@@ -552,7 +558,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // ============================================================ softmax
         // warps 4-7 take the first half of a stage's tokens, warps 8-11 the
         // second, for the same rows: warp w reads tensor-memory quarter w & 3
-        regs_take<200>();
+        regs_take<176>();
         constexpr int HC = NT / 2, HD = D / 2;
         const int quarter = warp & 3;
         const int half = (warp - 4) >> 2;
@@ -561,11 +567,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const uint32_t pair_bar = 1 + quarter;
         const int ti = r / p.G;
         // a scale of 0 runs as 1e-30: exp2 of every score is then 1 in fp32
-        // (the mean, as for 0) while masked scores, infinite with the sign that
-        // scales to -inf, still give 0
-        const float sc = p.scale_log2 == 0.f ? 1e-30f : p.scale_log2;
-        const bool neg = sc < 0.f;
-        const float masked = neg ? INFINITY : -INFINITY;
+        // (the mean, as for 0) while masked scores, -inf, still give 0; with a
+        // negative one the scores are those of -q
+        const float sc = p.scale_log2 == 0.f ? 1e-30f : fabsf(p.scale_log2);
         const float2 sc2 = make_float2(sc, sc);
         const bool scribe = threadIdx.x == 128 && rank == 0;
         if (scribe)
@@ -626,7 +630,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 const uint32_t s_col = S_COL + (ns & 1) * NT;
                 wait(&s_full[ns & 1], (ns >> 1) & 1);
                 float v[HC / 32][32];
-                float e = masked;
+                float e = -INFINITY;
                 if (ok) {
                     tc_fence_after();
 #pragma unroll
@@ -644,34 +648,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                 row_ok ? tree_word(tree, node, c0 + 32 * c - prefix) : 0u;
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                v[c][i] = (seen >> i) & 1u ? v[c][i] : masked;
+                                v[c][i] = (seen >> i) & 1u ? v[c][i] : -INFINITY;
                         }
                     }
-                    // the extreme: the sign is the call's, a branch around two loops
                     float ec[4];
-                    if (!neg) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            ec[c] = v[c >> 1][16 * (c & 1)];
+                    for (int c = 0; c < 4; ++c) {
+                        ec[c] = fmaxf(v[c >> 1][16 * (c & 1)], v[c >> 1][16 * (c & 1) + 1]);
 #pragma unroll
-                            for (int i = 1; i < 15; i += 2)
-                                ec[c] = fmax3(ec[c], v[c >> 1][16 * (c & 1) + i],
-                                              v[c >> 1][16 * (c & 1) + i + 1]);
-                            ec[c] = fmaxf(ec[c], v[c >> 1][16 * (c & 1) + 15]);
-                        }
-                        e = fmax3(ec[0], ec[1], fmaxf(ec[2], ec[3]));
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            ec[c] = v[c >> 1][16 * (c & 1)];
-#pragma unroll
-                            for (int i = 1; i < 15; i += 2)
-                                ec[c] = fmin3(ec[c], v[c >> 1][16 * (c & 1) + i],
-                                              v[c >> 1][16 * (c & 1) + i + 1]);
-                            ec[c] = fminf(ec[c], v[c >> 1][16 * (c & 1) + 15]);
-                        }
-                        e = fmin3(ec[0], ec[1], fminf(ec[2], ec[3]));
+                        for (int i = 2; i < 16; i += 2)
+                            ec[c] = fmax3(ec[c], v[c >> 1][16 * (c & 1) + i],
+                                          v[c >> 1][16 * (c & 1) + i + 1]);
                     }
+                    e = fmax3(ec[0], ec[1], fmaxf(ec[2], ec[3]));
                 }
                 pair_red[ns & 1][half][r] = e;
                 tc_fence_before();
@@ -680,8 +669,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 const float e2 = pair_red[ns & 1][half ^ 1][r];
                 if (!ok)
                     continue;
-                e = neg ? fminf(e, e2) : fmaxf(e, e2);
-                const float mt = e == masked ? -INFINITY : e * sc;
+                const float mt = fmaxf(e, e2) * sc;
                 // the reference maximum moves only by more than 8 (log2 units):
                 // p stays below 2^8, well inside fp16, and O is rescaled rarely
                 bool rescale = false;
