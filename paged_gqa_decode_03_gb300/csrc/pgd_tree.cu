@@ -358,9 +358,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     };
 
     if (warp < 4) {
-      // 8 each to the softmax warps (128 x 152 + 256 x 176 of the launch's 384 x
-      // 168): no role spills.  (128 x 104 + 256 x 200: the copying warps spill,
-      // 64 requests 111.5 us instead of 107.9.)
+      // to the softmax warps (128 x 152 + 256 x 176 of the launch's 384 x 168): at
+      // head_dim 64 and 128 no role spills.  (With 104 and 200 the copying warps
+      // did: 64 requests 111.5 us instead of 107.9.)
       regs_give<152>();
       if (warp == 0 || warp == kTreeVWarp) {
         // ============================================================ copies
