@@ -656,9 +656,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // all of head_dim, so that beside the 64 KB of Q nine of them fit and each is
 // free again after its own products: a stage's copies are never waited for as
 // a whole.  Eight softmax warps: rows r by halves of a stage's keys.
-// A prompt of 8192 tokens, 16 / 2 heads: 405 us, 1360 TFLOP/s.  37 prompts of 1
+// A prompt of 8192 tokens, 16 / 2 heads: 396 us, 1390 TFLOP/s.  37 prompts of 1
 // to 512 tokens, 24 / 4 heads: 31 us, of which a unit's start and end are the
-// larger part: a unit of one token costs 4.1 us of its CTA's time.  The output's
+// larger part: a unit of one token costs 3.8 us of its CTA's time.  The output's
 // product of a unit's last stage ends at the tile's last key, rounded up to 16,
 // so that of the rows behind a prompt 15 at most have to be zeroed (the whole
 // stage: 34.5 us).  Ending its copies and scores there as well added 5 % to the
@@ -740,7 +740,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         return (u.y + min(u.z, p.TQ) - 1) % kNT / 16 + 1;
     };
 
-    if (warp == 0) {
+    // (384 x 168 at the launch: 128 x 120 and 256 x 192, with which no role
+    // spills; 8192 tokens 396 us instead of 406, short prompts 31 instead of 32)
+    if (warp < 4) {
+      regs_give<120>();
+      if (warp == 0) {
         if (lane == 0) {
             // ======================================================== copies
             const uint64_t pol = l2_evict_last_policy();
@@ -808,7 +812,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 1 || warp == 2) {
+      } else if (warp == 1 || warp == 2) {
         if (lane == 0) {
             // ======================================================== products
             // (scores and outputs by a thread each, as in the pair kernel)
@@ -897,8 +901,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
         }
         __syncwarp();
-    } else if (warp >= 4) {
+      }
+    } else {
         // ============================================================ softmax
+        regs_take<192>();
         constexpr int HC = kNT / 2, HD = D / 2;
         const int quarter = warp & 3;
         const int half = (warp - 4) >> 2;
