@@ -216,7 +216,9 @@ __global__ void __launch_bounds__(kSlotThreads) paged_kv_slots_kernel(const Slot
 cudaError_t launch_kv_slots(const SlotParams &p, int num_sms, cudaStream_t stream)
 {
     const size_t smem = (2 * (size_t)p.S + 1) * sizeof(int);
-    if (smem > 48 * 1024) {
+    // a launch that has not asked for more gets 48 KB, the kernel's static
+    // arrays included: ask well before
+    if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(
             paged_kv_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotSmemMax);
         if (e != cudaSuccess)
