@@ -498,9 +498,10 @@ pgd_status pgd_varlen_plan(int num_seqs, int total_q, int max_q_len, int num_q_h
  * workspace  NULL: library scratch; else at least pgd_tree_plan's bytes, 256-byte
  *            aligned, not used by anything else until the call's work is done.
  *
- * parents[i] = i - 1 is paged_gqa_varlen's causal form.  A sequence whose query
- * rows are inconsistent (PGD_DEVERR_QUERY_LEN, also where they do not lie
- * inside total_q) is skipped; rows behind the last sequence (total_q above
+ * parents[i] = i - 1 is paged_gqa_varlen's causal form.  A sequence whose length
+ * is negative or past its table (PGD_DEVERR_SEQ_LEN) or whose query rows are
+ * inconsistent (PGD_DEVERR_QUERY_LEN, also where they do not lie inside
+ * total_q) is skipped, its rows are not written; rows behind the last sequence (total_q above
  * cu_seqlens_q[num_seqs], a padded batch) are left as they were.  K and V rows
  * of one sequence's tree must be finite: a weight of 0 does not hide an
  * infinity or NaN in a sibling's V.  out must not overlap an input.  Library

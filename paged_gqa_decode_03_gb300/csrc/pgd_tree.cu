@@ -118,23 +118,27 @@ __device__ __forceinline__ uint32_t tree_word(const TreeBits &tree, int i, int j
 }
 
 // What a sequence asks for: its length, first row, nodes (0 where its numbers do
-// not fit together), stages per unit and units.
+// not fit together or the table cannot hold its length: its tree is at the
+// length's end, so no other length will do), stages per unit and units.
 struct TreeSeq {
     int L, row0, n, T, groups;
-    bool bad;
+    unsigned bad;  // the device error bit of a sequence that is left out
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int s)
 {
     TreeSeq q;
     const int maxlen = p.MB << p.log2BS;
-    const int L = __ldg(p.seq_lens + s);
-    q.L = min(max(L, 0), maxlen);
+    q.L = __ldg(p.seq_lens + s);
     q.row0 = __ldg(p.cu_q + s);
     q.n = __ldg(p.cu_q + s + 1) - q.row0;
-    q.bad = q.n < 0 || q.n > q.L || q.n > p.max_q || q.row0 < 0 || q.row0 > p.total_q - q.n;
+    q.bad = 0;
+    if (q.L < 0 || q.L > maxlen)
+        q.bad = kErrSeqLen;
+    else if (q.n < 0 || q.n > q.L || q.n > p.max_q || q.row0 < 0 || q.row0 > p.total_q - q.n)
+        q.bad = kErrQueryLen;
     if (q.bad)
-        q.n = 0;
+        q.L = q.n = 0;
     q.T = (q.L + kTreeNT - 1) / kTreeNT;
     q.groups = ((q.n + p.TQ - 1) / p.TQ + p.cs - 1) / p.cs;
     return q;
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (s < p.S) {
             const TreeSeq q = tree_seq(p, s);
             if (q.bad && blockIdx.x == 0)
-                atomicOr(p.err, kErrQueryLen);
+                atomicOr(p.err, q.bad);
             mine = tree_cost(p, q);
         }
         before = total + block_prefix(mine, warp_sum, &all);

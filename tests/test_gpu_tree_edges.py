@@ -1,0 +1,73 @@
+"""Tree attention (paged_gqa_tree) where its inputs are out of the ordinary: lengths
+that do not fit the page table, rows of NaN, scores that grow from stage to
+stage, weights far below the largest, divisions over many sequences, bounds
+that are loose.  Plain 64-bit forms and bounds of step_util."""
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import paged_gqa_decode_03_gb300 as pgd
+from step_util import assert_attention, attention, bound, tree_seen
+from test_gpu_tree import case, check, run
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+    yield
+    assert pgd.pgd_check_device_error() == 0
+
+
+def gathered(w, s, L):
+    """K and V of sequence s in token order, [L, Hkv, D]."""
+    ids = w.block_tables[s, : -(-L // w.BS)].long()
+    return [c[ids].transpose(1, 2).reshape(-1, w.Hkv, w.D)[:L] for c in (w.k_cache, w.v_cache)]
+
+
+def set_keys(w, s, keys):
+    """Writes keys [L, Hkv, D] as sequence s's K rows."""
+    for t0 in range(0, keys.shape[0], w.BS):
+        rows = keys[t0: t0 + w.BS]
+        w.k_cache[int(w.block_tables[s, t0 // w.BS]), :, : rows.shape[0]] = rows.transpose(0, 1)
+
+
+# ------------------------------------------------------------------ lengths
+@pytest.mark.parametrize("D,n", [(64, 40), (128, 9), (128, 100), (256, 9), (256, 60)])
+def test_length_past_the_table_is_flagged_and_skipped(D, n):
+    ctx = [300, 45, 500]
+    w, trees, parents = case(ctx, [n, 5, n], 16, 4, D, 16, seed=41)
+    most = w.block_tables.shape[1] * 16
+    lens, cu = w.seq_lens.clone(), w.cu_seqlens_q.tolist()
+    for bad in (most + 1, 2 ** 31 - 1, -1, -2 ** 31):
+        lens[1] = bad
+        out = torch.full((w.total_q, w.Hq, D), 7.0, dtype=torch.float16, device=DEV)
+        pgd.paged_gqa_tree(out, w.q, w.cu_seqlens_q, parents, w.k_cache, w.v_cache,
+                           w.block_tables, lens, w.scale, w.max_q_len)
+        torch.cuda.synchronize()
+        bits = pgd.pgd_check_device_error()
+        assert bits & pgd.DEVERR_SEQ_LEN and not bits & ~(pgd.DEVERR_SEQ_LEN | pgd.DEVERR_QUERY_LEN)
+        assert (out[cu[1]:cu[2]] == 7.0).all()
+        check(out, w, trees, ctx, f"beside a length of {bad}", seqs=(0, 2))
+    # the largest length that fits is none of these
+    assert int(w.seq_lens.max()) <= most
+    run(w, parents)
+    assert pgd.pgd_check_device_error() == 0
+
+
+@pytest.mark.parametrize("bad", [-3, 10 ** 6])
+def test_bad_length_of_a_sequence_without_nodes_is_flagged(bad):
+    ctx, n = [300, 40, 60], [4, 0, 6]
+    w, trees, parents = case(ctx, n, 8, 2, 128, 16, seed=42)
+    w.seq_lens[1] = bad
+    out = run(w, parents)
+    assert pgd.pgd_check_device_error() == pgd.DEVERR_SEQ_LEN
+    check(out, w, trees, ctx, "beside it")
