@@ -69,11 +69,15 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
     const int s = u / p.Hkv;
     const int maxlen = p.MB * p.BS;
     int L = __ldg(p.seq_lens + s);
+    // one CTA of the sequence reports what is wrong with its numbers
+    const bool reports = qt == p.QT - 1 && g == 0 && part == 0 && threadIdx.x == 0;
+    if ((L < 0 || L > maxlen) && reports)
+        atomicOr(p.err, kErrSeqLen);
     L = L < 0 ? 0 : (L > maxlen ? maxlen : L);
     const int row0 = __ldg(p.cu_q + s);
     int n = __ldg(p.cu_q + s + 1) - row0;
     if (n < 0 || n > L || n > p.max_q) {
-        if (qt == p.QT - 1 && g == 0 && part == 0 && threadIdx.x == 0)
+        if (reports)
             atomicOr(p.err, kErrQueryLen);
         n = 0;
     }
@@ -564,11 +568,15 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
     const int s = u / p.Hkv;
     const int maxlen = p.MB * p.BS;
     int L = __ldg(p.seq_lens + s);
+    // one CTA of the sequence reports what is wrong with its numbers
+    const bool reports = qp == p.QP - 1 && g == 0 && part == 0 && threadIdx.x == 0;
+    if ((L < 0 || L > maxlen) && reports)
+        atomicOr(p.err, kErrSeqLen);
     L = L < 0 ? 0 : (L > maxlen ? maxlen : L);
     const int row0 = __ldg(p.cu_q + s);
     int n = __ldg(p.cu_q + s + 1) - row0;
     if (n < 0 || n > L || n > p.max_q) {
-        if (qp == p.QP - 1 && g == 0 && part == 0 && threadIdx.x == 0)
+        if (reports)
             atomicOr(p.err, kErrQueryLen);
         n = 0;
     }
