@@ -695,6 +695,16 @@ pgd_status pgd_test_stall_next_decode(const void *device_flag);
 pgd_status pgd_test_fail_next_reduce(int enable);
 
 /*
+ * pgd_test_fail_next_set_up — failure-injection test knob, on the host.  The
+ * kernels of paged_gqa_tree and packed_gqa_prefill are set up on a device by the
+ * first call that needs them.  When enable is non-zero, the next such set-up on
+ * this thread fails: its call returns PGD_ERR_CUDA, calls that need none are not
+ * affected, and the next call tries again.  enable = 0 cancels a pending
+ * request.  Tests only.
+ */
+pgd_status pgd_test_fail_next_set_up(int enable);
+
+/*
  * pgd_set_timing_events — measurement hook.  When both are non-NULL, every
  * later call on this thread records `before` (a cudaEvent_t) on its stream
  * just before the partition kernel and `after` just after it, so the kernel's
@@ -710,7 +720,7 @@ pgd_status pgd_device_info(int head_dim, int block_size, int *num_sms, int *ctas
  * head_dim 64, block sizes 64 and 128; 1.2.0: several query tokens per
  * sequence; 1.3.0: quantised pages; 1.4.0: pgd_workspace_size, pgd_release,
  * paged_gqa_decode_host; 1.5.0: paged_gqa_tree, packed_gqa_prefill,
- * paged_kv_slots, paged_kv_write). */
+ * paged_kv_slots, paged_kv_write; 1.5.1: pgd_test_fail_next_set_up). */
 int pgd_version(void);
 
 #ifdef __cplusplus

@@ -35,7 +35,7 @@ __all__ = ["paged_gqa_decode", "paged_gqa_decode_ex", "paged_gqa_decode_noalloc"
            "packed_gqa_prefill", "pgd_prefill_plan", "paged_kv_slots", "paged_kv_write", "pgd_plan", "pgd_workspace_size", "pgd_release",
            "pgd_last_partition_size",
            "pgd_last_error", "pgd_check_device_error", "pgd_set_timing_events",
-           "pgd_test_stall_next_decode", "pgd_test_fail_next_reduce",
+           "pgd_test_stall_next_decode", "pgd_test_fail_next_reduce", "pgd_test_fail_next_set_up",
            "pgd_device_info", "pgd_version", "PGDError", "library_path", "load_library"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -83,6 +83,7 @@ SIGNATURES = {
     "pgd_set_timing_events": (_I, [_P, _P]),
     "pgd_test_stall_next_decode": (_I, [_P]),
     "pgd_test_fail_next_reduce": (_I, [_I]),
+    "pgd_test_fail_next_set_up": (_I, [_I]),
     "pgd_device_info": (_I, [_I, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)]),
     "pgd_version": (_I, []),
 }
@@ -901,6 +902,12 @@ def pgd_test_fail_next_reduce(enable: bool = True) -> None:
     launches its partition kernel, withholds the reduce and reports
     PGD_ERR_CUDA (its output undefined); False cancels."""
     _raise(load_library().pgd_test_fail_next_reduce(1 if enable else 0))
+
+
+def pgd_test_fail_next_set_up(enable: bool = True) -> None:
+    """Failure-injection test knob: the next set-up of the tree or prompt
+    kernels on this thread fails its call with PGD_ERR_CUDA; False cancels."""
+    _raise(load_library().pgd_test_fail_next_set_up(1 if enable else 0))
 
 
 def pgd_device_info(head_dim: int, block_size: int):

@@ -34,6 +34,7 @@ thread_local cudaEvent_t t_ev_before = nullptr;
 thread_local cudaEvent_t t_ev_after = nullptr;
 thread_local const unsigned *t_stall_flag = nullptr;  // pgd_test_stall_next_decode
 thread_local bool t_skip_reduce = false;               // pgd_test_fail_next_reduce
+thread_local bool t_fail_set_up = false;               // pgd_test_fail_next_set_up
 
 pgd_status fail(pgd_status st, const char *fmt, ...)
 {
@@ -59,7 +60,10 @@ struct DeviceState {
     cudaError_t init_error = cudaSuccess;
     int num_sms = 0;
     int ctas[3][3][5] = {};         // [kind: fp16, quantised, MQ][head_dim 64/128/256][block size]
-    int tree_runs[3][2] = {};       // [head_dim][pairs]: resident runs of the tree kernel
+    // set up by the first call that needs them, so that no other call pays for
+    // them or fails with them
+    std::atomic<int> tree_runs[3][2] = {};       // [head_dim][pairs]: resident runs, 0: not set up
+    std::atomic<bool> prefill_ready[3] = {};     // [head_dim]
     unsigned *err_word = nullptr;   // address of g_device_error on this device
     std::mutex pool_mu;             // the pool is made on first library-owned scratch
     cudaMemPool_t pool = nullptr;   //   (and again after pgd_release): stream-ordered scratch
@@ -101,11 +105,6 @@ cudaError_t init_device(int dev, DeviceState &st)
             if ((e = occupancy_d256(kBlockSizes[i], kind, &st.ctas[kind][2][i])) != cudaSuccess)
                 return e;
         }
-    for (int i = 0; i < 6; ++i)
-        if ((e = tree_resident(64 << (i / 2), i % 2, &st.tree_runs[i / 2][i % 2])) != cudaSuccess)
-            return e;
-    if ((e = prefill_set_up()) != cudaSuccess)
-        return e;
     return cudaGetSymbolAddress(reinterpret_cast<void **>(&st.err_word), g_device_error);
 }
 
@@ -136,6 +135,44 @@ pgd_status device_state(DeviceState **out)
         return cuda_fail(st.init_error, "device set-up");
     *out = &st;
     return PGD_OK;
+}
+
+// Sets a kernel up on the current device by `f` (which a test may have fail).  A
+// failure is this call's alone: the next one tries again.
+template <class F> pgd_status set_up(const char *what, F &&f)
+{
+    const bool withheld = t_fail_set_up;
+    t_fail_set_up = false;
+    if (withheld)
+        return fail(PGD_ERR_CUDA, "%s: withheld by pgd_test_fail_next_set_up", what);
+    const cudaError_t e = f();
+    if (e == cudaSuccess)
+        return PGD_OK;
+    cudaGetLastError();  // no later call's launch is to find it
+    return cuda_fail(e, what);
+}
+
+pgd_status tree_runs(DeviceState &st, int D, bool pair, int *runs)
+{
+    std::atomic<int> &known = st.tree_runs[d_index(D)][pair];
+    if ((*runs = known.load(std::memory_order_acquire)) > 0)
+        return PGD_OK;
+    const pgd_status s =
+        set_up("set-up of the tree kernel", [&] { return tree_resident(D, pair, runs); });
+    if (!s)
+        known.store(*runs, std::memory_order_release);
+    return s;
+}
+
+pgd_status prefill_ready(DeviceState &st, int D)
+{
+    std::atomic<bool> &known = st.prefill_ready[d_index(D)];
+    if (known.load(std::memory_order_acquire))
+        return PGD_OK;
+    const pgd_status s = set_up("set-up of the prompt kernel", [&] { return prefill_set_up(D); });
+    if (!s)
+        known.store(true, std::memory_order_release);
+    return s;
 }
 
 // The library's scratch pool on the current device, created on first use
@@ -1376,8 +1413,10 @@ pgd_status make_tree_plan(int S, int total_q, int max_q, int Hq, int Hkv, int D,
     tp->G = Hq / Hkv;
     tp->TQ = 128 / tp->G;
     const int tiles = std::max(1, (max_q + tp->TQ - 1) / tp->TQ);
-    const int resident = ds->tree_runs[d_index(D)][tiles > 1 && D > 64];
+    int resident;
     tp->cs = tiles > 1 && D > 64 ? 2 : 1;
+    if ((st = tree_runs(*ds, D, tp->cs == 2, &resident)))
+        return st;
     if (resident < 1)
         return fail(PGD_ERR_UNSUPPORTED, "the tree kernel does not fit on this device");
     const long long stages = (long long)S * Hkv * ((tiles + tp->cs - 1) / tp->cs) *
@@ -1745,7 +1784,7 @@ pgd_status run_prefill(float *out, uint16_t *out_half, const uint16_t *q, const 
         return fail(PGD_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) given, %zu needed",
                     ws_bytes, pp.ws_bytes);
     DeviceState *ds;
-    if ((st = device_state(&ds)))
+    if ((st = device_state(&ds)) || (st = prefill_ready(*ds, D)))
         return st;
     CUtensorMap tq, tk, tv;
     const bool wide = D == 256;  // K by slabs of 128 keys, V by 32 keys of all slabs
@@ -2304,6 +2343,13 @@ pgd_status pgd_test_fail_next_reduce(int enable)
     return PGD_OK;
 }
 
+pgd_status pgd_test_fail_next_set_up(int enable)
+{
+    t_fail_set_up = enable != 0;
+    t_last_error.clear();
+    return PGD_OK;
+}
+
 pgd_status pgd_check_device_error(void *stream, unsigned *bits)
 {
     DeviceState *ds;
@@ -2350,6 +2396,6 @@ pgd_status pgd_device_info(int head_dim, int block_size, int *num_sms, int *ctas
     return PGD_OK;
 }
 
-int pgd_version(void) { return 10500; }
+int pgd_version(void) { return 10501; }
 
 }  // extern "C"

@@ -326,7 +326,8 @@ struct PrefillParams {
     bool wide_rows;               // the output starts on a 32-byte border
     uint64_t wait_budget_ns;
 };
-cudaError_t prefill_set_up();  // on the current device, once before its launches
+// On the current device, once before the launches of this head_dim.
+cudaError_t prefill_set_up(int head_dim);
 cudaError_t launch_prefill(int head_dim, const CUtensorMap &tq, const CUtensorMap &tk,
                            const CUtensorMap &tv, const PrefillParams &p, int grid,
                            cudaStream_t stream);

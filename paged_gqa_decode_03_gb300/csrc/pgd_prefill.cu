@@ -1070,16 +1070,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
 }
 
-cudaError_t prefill_set_up()
+cudaError_t prefill_set_up(int head_dim)
 {
     const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e;
-    if ((e = cudaFuncSetAttribute(packed_prefill_pair_kernel<64>, most,
-                                  (int)pair_smem_bytes<64>())) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(packed_prefill_pair_kernel<128>, most,
-                                  (int)pair_smem_bytes<128>())) != cudaSuccess)
-        return e;
-    return cudaFuncSetAttribute(packed_prefill_wide_kernel, most, (int)kWideSmem);
+    return head_dim == 64    ? cudaFuncSetAttribute(packed_prefill_pair_kernel<64>, most,
+                                                    (int)pair_smem_bytes<64>())
+           : head_dim == 128 ? cudaFuncSetAttribute(packed_prefill_pair_kernel<128>, most,
+                                                    (int)pair_smem_bytes<128>())
+                             : cudaFuncSetAttribute(packed_prefill_wide_kernel, most,
+                                                    (int)kWideSmem);
 }
 
 cudaError_t launch_prefill(int head_dim, const CUtensorMap &tq, const CUtensorMap &tk,
