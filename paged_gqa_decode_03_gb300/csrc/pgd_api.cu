@@ -108,7 +108,7 @@ cudaError_t init_device(int dev, DeviceState &st)
     return cudaGetSymbolAddress(reinterpret_cast<void **>(&st.err_word), g_device_error);
 }
 
-cudaError_t init_pool(int dev, DeviceState &st)
+cudaError_t create_pool(int dev, DeviceState &st)
 {
     cudaMemPoolProps props = {};
     props.allocType = cudaMemAllocationTypePinned;
@@ -119,6 +119,19 @@ cudaError_t init_pool(int dev, DeviceState &st)
         return e;
     uint64_t keep = ~0ull;  // keep freed scratch in the pool between calls
     return cudaMemPoolSetAttribute(st.pool, cudaMemPoolAttrReleaseThreshold, &keep);
+}
+
+cudaError_t init_pool(int dev, DeviceState &st)
+{
+    // The call that needs it first may be captured into a graph.  A pool is no part
+    // of any stream's work, so its creation is allowed there.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess)
+        return e;
+    e = create_pool(dev, st);
+    const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+    return e != cudaSuccess ? e : back;
 }
 
 pgd_status device_state(DeviceState **out)

@@ -90,6 +90,6 @@ def test_failed_set_up_is_one_calls_failure(D):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("when", ["after a decode"])
+@pytest.mark.parametrize("when", ["first of all", "after a decode"])
 def test_first_call_captured(D, when):
     own_process(CAPTURED, D, when)
