@@ -108,10 +108,12 @@ __device__ __forceinline__ int unit_of(int k)
     return k * grid + ((k & 1) ? grid - 1 - b : b);
 }
 
+// (A plain load: the order kernel may still be writing the list while this
+// kernel already runs, up to griddep_wait, so it is not read-only here.)
 __device__ __forceinline__ int4 unit_at(const PrefillParams &p, int k, int units)
 {
     const int ui = unit_of(k);
-    return ui < units ? __ldg(p.units + ui) : make_int4(0, 0, 0, 0);
+    return ui < units ? p.units[ui] : make_int4(0, 0, 0, 0);
 }
 
 }  // namespace
