@@ -587,6 +587,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         float o[32];
                         tc_ld32(t_lane + o_col + 32 * c, o);
                         tc_wait_ld();
+                        tc_ld_ready(o);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             o[i] *= alpha;
@@ -1015,6 +1016,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                             float o[32];
                             tc_ld32(t_lane + half * HD + 32 * c, o);
                             tc_wait_ld();
+                            tc_ld_ready(o);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 o[i] *= alpha;

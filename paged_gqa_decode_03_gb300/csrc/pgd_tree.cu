@@ -711,6 +711,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             float o[32];
                             tc_ld32(t_lane + O_COL + half * HD + 32 * c, o);
                             tc_wait_ld();
+                            tc_ld_ready(o);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 o[i] *= alpha;

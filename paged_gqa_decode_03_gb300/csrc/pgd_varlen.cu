@@ -328,18 +328,20 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
                 ok = false;
                 give_up();
             }
-            float x[HC];
+            float x[HC], raw[HC / 32][32];
             if (ok) {
                 tc_fence_after();
 #pragma unroll
+                for (int c = 0; c < HC / 32; ++c)
+                    tc_ld32(t_lane + S_COL + (jj & 1) * NT + half * HC + 32 * c, raw[c]);
+                tc_wait_ld();
+#pragma unroll
                 for (int c = 0; c < HC / 32; ++c) {
-                    float v[32];
-                    tc_ld32(t_lane + S_COL + (jj & 1) * NT + half * HC + 32 * c, v);
+                    tc_ld_ready(raw[c]);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        x[32 * c + i] = v[i];
+                        x[32 * c + i] = raw[c][i];
                 }
-                tc_wait_ld();
             }
             // causal / partition mask only where this half reaches past the
             // row's last token.  The extreme is taken on raw scores: the max
@@ -424,6 +426,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
                         float v[32];
                         tc_ld32(t_lane + O_COL + half * HD + 32 * c, v);
                         tc_wait_ld();
+                        tc_ld_ready(v);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             v[i] *= alpha;
@@ -492,6 +495,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
                 float v[32];
                 tc_ld32(t_lane + O_COL + half * HD + 32 * c, v);
                 tc_wait_ld();
+                tc_ld_ready(v);
                 if (has) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
@@ -919,6 +923,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
                     float v[32];
                     tc_ld32(t_lane + o_col + 32 * c, v);
                     tc_wait_ld();
+                    tc_ld_ready(v);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         v[i] *= alpha;
@@ -973,6 +978,7 @@ __global__ void __launch_bounds__(kVarlenThreads, 1)
                 float v[32];
                 tc_ld32(t_lane + o_col + 32 * c, v);
                 tc_wait_ld();
+                tc_ld_ready(v);
                 if (has) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)

@@ -71,3 +71,40 @@ def test_bad_length_of_a_sequence_without_nodes_is_flagged(bad):
     out = run(w, parents)
     assert pgd.pgd_check_device_error() == pgd.DEVERR_SEQ_LEN
     check(out, w, trees, ctx, "beside it")
+
+
+# ------------------------------------------------------------------ moving maxima
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nodes", [3, 30, 70])
+@pytest.mark.parametrize("S,ctx", [(1, 700), (9, 2800)])
+def test_growing_scores_rescale(D, nodes, S, ctx):
+    """Keys that grow along the sequence, so that a row's maximum moves by more
+    than 8 (log2) in every stage of 128 tokens: alone in its unit, in pairs of
+    tiles (more than 32 nodes of 4 heads), and in units cut between the stages."""
+    Hq, Hkv = 8, 2
+    w, trees, parents = case([ctx] * S, [nodes] * S, Hq, Hkv, D, 16, seed=44)
+    L, stages = ctx + nodes, -(-(ctx + nodes) // 128)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(D + nodes)
+    u = torch.sign(torch.randn((Hkv, D), generator=g, device=DEV))
+    w.q[:] = (u.repeat_interleave(4, 0)[None] + 0.05 * torch.randn(w.q.shape, generator=g, device=DEV)).half()
+    # a token's score is about scale * D * ramp: 10 log2 units more every 128
+    step = 10.0 * math.log(2) / (128 * w.scale * D)
+    ramp = torch.arange(L, device=DEV, dtype=torch.float32) * step
+    for s in range(S):
+        set_keys(w, s, (ramp[:, None, None] * u[None]).half())
+    out = run(w, parents, dtype=torch.float32)
+    for s in range(S):
+        rows = slice(s * nodes, (s + 1) * nodes)
+        k, v = gathered(w, s, L)
+        seen = tree_seen(trees[s], ctx)
+        ref, A = attention(w.q[rows], k, v, seen, w.scale)
+        z = torch.einsum("nd,ld->nl", w.q[rows][:, 0].double(), k[:, 0].double()) * w.scale
+        z = z.masked_fill(~torch.as_tensor(seen, device=DEV), -torch.inf) / math.log(2)
+        tops = torch.stack([z[:, 128 * t: 128 * t + 128].amax(1) for t in range(ctx // 128)], 1)
+        assert (tops.diff(dim=1) > 8).all()
+        # the score's own rounding (step_util) with sum |q k| scale of these rows
+        size = float((w.q[rows].abs().double().sum(2).max() * ramp[-1]) * w.scale) * (1 + 4 / D)
+        lim = bound(ref, A, L, D, float(v.abs().max()), False, size / D)
+        err = np.abs(out[rows].double().cpu().numpy() - ref)
+        assert (err <= lim).all(), f"{(err / lim).max()} times the bound, {stages} stages"

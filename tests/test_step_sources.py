@@ -28,3 +28,16 @@ def test_non_coherent_loads_are_of_the_callers_inputs(name):
     for that kernel's lifetime, so it may not be read through ld.global.nc."""
     read = set(re.findall(r"__ldg\(\s*(?:reinterpret_cast<[^>]*>\()?p\.(\w+)", source(name)))
     assert read and read <= INPUTS, read - INPUTS
+
+
+@pytest.mark.parametrize("name", ["pgd_prefill.cu", "pgd_tree.cu", "pgd_rows.cuh", "pgd_varlen.cu"])
+def test_tensor_memory_loads_are_used_behind_their_wait(name):
+    """tcgen05.ld is asynchronous: its registers may be read behind tcgen05.wait::ld
+    only.  The wait names no register, so arithmetic on them (which is not
+    volatile) may be moved in front of it unless tc_ld_ready, right behind the
+    wait, ties them to that place."""
+    parts = source(name).split("tc_wait_ld();")
+    assert len(parts) > 1
+    for behind in parts[1:]:
+        first_use = re.search(r"tc_ld_ready\(|\*=|make_float4|tc_st32|fmax|x\[32", behind)
+        assert first_use and first_use.group(0) == "tc_ld_ready(", behind[:300]
