@@ -785,8 +785,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                                      : nullptr;
                 }
                 write_rows<WC>(rows, false, true, t_lane + O_COL + col, col, 1.f, lane, read);
+                // (-inf says that there is nothing to join; scores that are all NaN
+                // leave it too, with a sum of NaN, which is to reach the output)
                 if (row_ok && half == 0)
-                    p.part_ml[piece * 128 + r] = make_float2(m_ref, lt);
+                    p.part_ml[piece * 128 + r] =
+                        make_float2(m_ref == -INFINITY && lt != 0.f ? 0.f : m_ref, lt);
                 if (scribe && walk.t == 0)
                     p.cut[run] = make_int4(walk.s, g, walk.group(), walk.last_run(total, p.runs));
             }

@@ -73,6 +73,32 @@ def test_bad_length_of_a_sequence_without_nodes_is_flagged(bad):
     check(out, w, trees, ctx, "beside it")
 
 
+# ------------------------------------------------------------------ NaN
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hkv,ctx", [(1, 3000), (4, 60)])
+def test_a_row_of_nan_is_nan_whole_or_cut(D, Hkv, ctx):
+    """A query row of NaN gives NaN, whether its unit is cut into pieces (one
+    KV head, long) or not; no other row notices."""
+    n = [9, 70]
+    w, trees, parents = case([ctx, ctx + 77], n, 4 * Hkv, Hkv, D, 16, seed=43)
+    w.q[3, 1] = float("nan")
+    w.q[50] = float("nan")
+    out = run(w, parents, dtype=torch.float32)
+    assert torch.isnan(out[3, 1]).all() and torch.isnan(out[50]).all()
+    keep = torch.ones(out.shape[:2], dtype=torch.bool)
+    keep[3, 1] = False
+    keep[50] = False
+    q = w.q.clone()
+    q[3, 1] = q[50] = 0.0
+    for s, rows in ((0, slice(0, 9)), (1, slice(9, 79))):
+        L = [ctx, ctx + 77][s] + n[s]
+        k, v = gathered(w, s, L)
+        ref, A = attention(q[rows], k, v, tree_seen(trees[s], L - n[s]), w.scale)
+        o = torch.where(keep[rows].to(DEV)[:, :, None], out[rows],
+                        torch.as_tensor(ref, device=DEV).float())
+        assert_attention(o, ref, A, L, D, float(v.abs().max()), f"sequence {s}", w.scale)
+
+
 # ------------------------------------------------------------------ moving maxima
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("nodes", [3, 30, 70])
