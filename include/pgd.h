@@ -492,8 +492,9 @@ pgd_status pgd_varlen_plan(int num_seqs, int total_q, int max_q_len, int num_q_h
  *            earlier node counts as none and sets PGD_DEVERR_TREE.
  * out        [total_q][num_q_heads][head_dim], 16-byte aligned
  * out_type   PGD_OUT_F32 or PGD_OUT_F16 (the fp32 result rounded to nearest).
- *            In both, the weights are rounded to fp16 (relative 2^-11) before
- *            they multiply V, as in paged_gqa_varlen; sums are fp32.
+ *            In both, the weights are rounded to fp16 before they multiply V:
+ *            by 2^-11 of themselves at most, or, below 2^-21 of the row's
+ *            largest, by 2^-32 of that; sums are fp32.
  * max_q_len  bound on every n_s, at most PGD_TREE_MAX_NODES.
  * workspace  NULL: library scratch; else at least pgd_tree_plan's bytes, 256-byte
  *            aligned, not used by anything else until the call's work is done.
@@ -547,8 +548,8 @@ pgd_status pgd_tree_plan(int num_seqs, int total_q, int max_q_len, int num_q_hea
  * cu_seqlens   [num_seqs + 1] int32, non-decreasing
  * out          [total][num_q_heads][head_dim] contiguous, 16-byte aligned
  * out_type     PGD_OUT_F32 or PGD_OUT_F16 (rounded to nearest).  The weights
- *              are rounded to fp16 (relative 2^-11) before they multiply V,
- *              sums are fp32.
+ *              are rounded to fp16 before they multiply V, in both, as in
+ *              paged_gqa_tree; sums are fp32.
  * max_len      bound on every prompt's length
  * workspace    NULL: library scratch (per call, also in a captured graph);
  *              else at least pgd_prefill_plan's bytes, 256-byte aligned, not

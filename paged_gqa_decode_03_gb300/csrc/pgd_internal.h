@@ -246,6 +246,19 @@ struct VarlenParams {
     uint64_t wait_budget_ns;
 };
 
+// ---------------------------------------------------------------- weights of the step's attention
+// Trees and packed prompts hold a weight p = 2^(score - reference) in fp16 for its
+// product with V (the tensor cores take A and B of one type, V is fp16, and fp16
+// has three bits more than bf16); scores, sums and outputs are fp32.  The
+// reference is set kRefBelow under the row's maximum and stays while the maximum
+// keeps within kRefRoom of it: p is at most 2^15, inside fp16's 65504, and is
+// a normal number, rounded by 2^-11 of itself, down to 2^-21 of the largest, below
+// that by 2^-32 of the largest at most.  (With the reference at the maximum those were
+// 2^-14 and 2^-25: thousands of small weights behind one large one lost
+// bits that the sum of the unrounded ones still held.)
+constexpr float kRefBelow = 7.f;
+constexpr float kRefRoom = 15.f;
+
 // ---------------------------------------------------------------- trees of drafted tokens
 // Attention of trees of drafted tokens over the paged cache (pgd_tree.cu).
 constexpr unsigned kErrTree = 32u;     // a parent that is not an earlier node of its tree

@@ -539,15 +539,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const bool pv_over =
                     j == 0 || mbar_try_wait(smem_addr(&o_done[x]), (ns - 1) & 1);
                 const float mt = max128(v) * sc;
-                // the reference maximum moves only by more than 8 (log2
-                // units): p stays below 2^8, well inside fp16, and O is
-                // rescaled rarely
+                // the reference moves only when the maximum has grown by more
+                // than 8 (log2 units): O is rescaled rarely
                 bool rescale = false;
                 float alpha = 1.f;
-                if (mt > m_ref + 8.f) {
+                if (mt > m_ref + kRefRoom) {
+                    const float ref = mt - kRefBelow;
                     rescale = row_ok && m_ref != -INFINITY;
-                    alpha = rescale ? ex2(m_ref - mt) : 1.f;
-                    m_ref = mt;
+                    alpha = rescale ? ex2(m_ref - ref) : 1.f;
+                    m_ref = ref;
                 }
                 const float off = m_ref == -INFINITY ? 0.f : -m_ref;
                 const float2 off2 = make_float2(off, off);
@@ -983,10 +983,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 const float mt = fmaxf(e, e2) * sc;
                 bool rescale = false;
                 float alpha = 1.f;
-                if (mt > m_ref + 8.f) {
+                if (mt > m_ref + kRefRoom) {
+                    const float ref = mt - kRefBelow;
                     rescale = m_ref != -INFINITY;
-                    alpha = rescale ? ex2(m_ref - mt) : 1.f;
-                    m_ref = mt;
+                    alpha = rescale ? ex2(m_ref - ref) : 1.f;
+                    m_ref = ref;
                 }
                 const float off = m_ref == -INFINITY ? 0.f : -m_ref;
                 const float2 off2 = make_float2(off, off);

@@ -674,14 +674,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 if (!ok)
                     continue;
                 const float mt = fmaxf(e, e2) * sc;
-                // the reference maximum moves only by more than 8 (log2 units):
-                // p stays below 2^8, well inside fp16, and O is rescaled rarely
+                // the reference moves only when the maximum has grown by more
+                // than 8 (log2 units): O is rescaled rarely
                 bool rescale = false;
                 float alpha = 1.f;
-                if (mt > m_ref + 8.f) {
+                if (mt > m_ref + kRefRoom) {
+                    const float ref = mt - kRefBelow;
                     rescale = row_ok && m_ref != -INFINITY;
-                    alpha = rescale ? ex2(m_ref - mt) : 1.f;
-                    m_ref = mt;
+                    alpha = rescale ? ex2(m_ref - ref) : 1.f;
+                    m_ref = ref;
                 }
                 const float off = m_ref == -INFINITY ? 0.f : -m_ref;
                 const float2 off2 = make_float2(off, off);

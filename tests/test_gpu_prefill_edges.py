@@ -25,6 +25,25 @@ def _built():
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+def test_weights_far_below_the_largest(D):
+    """The first token takes nearly all of the weight and its V is 0; the others' weights
+    are 2^-24.4 of it.  Weights may be off by 2^-11 of themselves or 2^-32 of
+    the largest, whichever is more."""
+    n = 2000
+    c = case([n], 8, 2, D, seed=52)
+    q, k, v = (torch.zeros((n, h, D), dtype=torch.float16, device=DEV) for h in (8, 2, 2))
+    q[..., 0] = 1.0
+    k[1:, :, 0] = -24.375
+    v[1:] = 1.0
+    c.update(q=q, k=k, v=v, scale=math.log(2))
+    out = run(c, dtype=torch.float32)
+    ref, A = attention(q, k, v, packed_seen(n), c["scale"])
+    lim = (2.0 ** -11 + 2 * (2.0 ** -18 + n * 2.0 ** -24)) * A + n * 2.0 ** -32
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert (err <= lim).all(), (err / lim).max()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_rows_of_nan(D):
     """A query row of NaN gives NaN, no other row notices."""
     c = case([300, 40], 8, 2, D, seed=53)

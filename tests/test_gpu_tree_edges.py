@@ -134,3 +134,29 @@ def test_growing_scores_rescale(D, nodes, S, ctx):
         lim = bound(ref, A, L, D, float(v.abs().max()), False, size / D)
         err = np.abs(out[rows].double().cpu().numpy() - ref)
         assert (err <= lim).all(), f"{(err / lim).max()} times the bound, {stages} stages"
+
+
+# ------------------------------------------------------------------ small weights
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nodes", [2, 60])
+def test_weights_far_below_the_largest(D, nodes):
+    """One token takes nearly all of the weight and its V is 0; the others' weights are
+    2^-24.4 of it.  Weights may be off by 2^-11 of themselves or 2^-32 of the
+    largest, whichever is more."""
+    ctx = 2000
+    w, trees, parents = case([ctx], [nodes], 8, 2, D, 16, seed=45)
+    w.q.zero_()
+    w.q[..., 0] = 1.0
+    w.base.scale = math.log(2)
+    keys = torch.zeros((ctx + nodes, 2, D), dtype=torch.float16, device=DEV)
+    keys[1:, :, 0] = -24.375
+    set_keys(w, 0, keys)
+    w.v_cache.fill_(1.0)
+    w.v_cache[int(w.block_tables[0, 0]), :, 0] = 0.0
+    out = run(w, parents, dtype=torch.float32)
+    k, v = gathered(w, 0, ctx + nodes)
+    ref, A = attention(w.q, k, v, tree_seen(trees[0], ctx), w.scale)
+    L = ctx + nodes
+    lim = (2.0 ** -11 + 2 * (2.0 ** -18 + L * 2.0 ** -24)) * A + L * 2.0 ** -32
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert (err <= lim).all(), (err / lim).max()
