@@ -652,6 +652,15 @@ pgd_status paged_kv_write(uint16_t *k_cache, uint16_t *v_cache, const uint16_t *
                           int64_t page_stride, int64_t head_stride, int64_t token_stride,
                           int64_t src_token_stride, int64_t src_head_stride, void *stream);
 
+/* The same with strides of their own for k_new and v_new, as packed_gqa_prefill
+ * takes them. */
+pgd_status paged_kv_write_strided(uint16_t *k_cache, uint16_t *v_cache, const uint16_t *k_new,
+                                  const uint16_t *v_new, const int32_t *slots, int num_rows,
+                                  int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                  int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                                  int64_t k_token_stride, int64_t k_head_stride,
+                                  int64_t v_token_stride, int64_t v_head_stride, void *stream);
+
 /* Partition size used by this thread's last successful call (0 if none);
  * the diagnostic of the pages' "Hands-on" section. */
 int pgd_last_partition_size(void);
@@ -721,7 +730,8 @@ pgd_status pgd_device_info(int head_dim, int block_size, int *num_sms, int *ctas
  * head_dim 64, block sizes 64 and 128; 1.2.0: several query tokens per
  * sequence; 1.3.0: quantised pages; 1.4.0: pgd_workspace_size, pgd_release,
  * paged_gqa_decode_host; 1.5.0: paged_gqa_tree, packed_gqa_prefill,
- * paged_kv_slots, paged_kv_write; 1.5.1: pgd_test_fail_next_set_up). */
+ * paged_kv_slots, paged_kv_write; 1.5.1: paged_kv_write_strided,
+ * pgd_test_fail_next_set_up). */
 int pgd_version(void);
 
 #ifdef __cplusplus

@@ -74,6 +74,7 @@ SIGNATURES = {
     "pgd_prefill_plan": (_I, [_I] * 5 + [ctypes.POINTER(_Z)]),
     "paged_kv_slots": (_I, [_P] * 10 + [_I] * 6 + [_P]),
     "paged_kv_write": (_I, [_P] * 5 + [_I] * 5 + [_L] * 5 + [_P]),
+    "paged_kv_write_strided": (_I, [_P] * 5 + [_I] * 5 + [_L] * 7 + [_P]),
     "pgd_plan": (_I, [_I] * 7 + [ctypes.POINTER(_I), ctypes.POINTER(_Z)]),
     "pgd_workspace_size": (_Z, [_I] * 6),
     "pgd_release": (_I, []),
@@ -718,15 +719,13 @@ def paged_kv_slots(slots, cu_seqlens_q, seq_lens, free_end, block_tables, contex
 
 def paged_kv_write(k_cache, v_cache, k_new, v_new, slots, layout=None, stream=None) -> None:
     """Writes the fp16 rows k_new, v_new [N, num_kv_heads, head_dim] (contiguous
-    rows of head_dim; any token and head strides, so slices of a fused
-    projection need no copy) into the cache at rows slots[n] = page *
+    rows of head_dim; any token and head strides, each its own, so slices of a
+    fused projection need no copy) into the cache at rows slots[n] = page *
     block_size + row (int32 [N], distinct; negative: skipped).  Caches
     head-major [NB, Hkv, BS, D], or any tensors with ``layout =
     (num_kv_heads, block_size, num_blocks, strides)``."""
     lib = _lib or load_library()
-    src = _packed_strides(k_new, "k_new")
-    if _packed_strides(v_new, "v_new") != src:
-        raise ValueError("k_new and v_new must have the same strides")
+    ks, vs = _packed_strides(k_new, "k_new"), _packed_strides(v_new, "v_new")
     dev = _index(slots)
     if not _fits(dev, _I32, 1, slots):
         _check(slots, "slots", _I32, 1)
@@ -750,9 +749,9 @@ def paged_kv_write(k_cache, v_cache, k_new, v_new, slots, layout=None, stream=No
         _one_device(dev, k_cache, v_cache)
         sp, sh, st = (int(x) for x in strides)
     _one_device(dev, k_new, v_new)
-    _on(dev, lib.paged_kv_write, k_cache.data_ptr(), v_cache.data_ptr(), k_new.data_ptr(),
-        v_new.data_ptr(), slots.data_ptr(), N, Hkv, D, int(BS), int(NB), sp, sh, st, *src,
-        stream=stream)
+    fn, src = (lib.paged_kv_write, ks) if ks == vs else (lib.paged_kv_write_strided, ks + vs)
+    _on(dev, fn, k_cache.data_ptr(), v_cache.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+        slots.data_ptr(), N, Hkv, D, int(BS), int(NB), sp, sh, st, *src, stream=stream)
 
 
 NOALLOC_SCRATCH_BYTES = 64 << 20  # PGD_NOALLOC_SCRATCH_BYTES of include/pgd.h

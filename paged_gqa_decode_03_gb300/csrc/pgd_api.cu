@@ -1639,8 +1639,8 @@ pgd_status run_slots(int32_t *slots, int32_t *positions, int32_t *cu_seqlens_q, 
 
 pgd_status run_write(uint16_t *k_cache, uint16_t *v_cache, const uint16_t *k_new,
                      const uint16_t *v_new, const int32_t *slots, int rows, int Hkv, int D, int BS,
-                     int NB, const Strides &kv, long long src_token, long long src_head,
-                     void *stream)
+                     int NB, const Strides &kv, long long k_token, long long k_head,
+                     long long v_token, long long v_head, void *stream)
 {
     if (rows < 0 || Hkv <= 0 || NB <= 0)
         return fail(PGD_ERR_INVALID_ARG, "num_rows %d, num_kv_heads %d, num_blocks %d", rows, Hkv,
@@ -1654,12 +1654,12 @@ pgd_status run_write(uint16_t *k_cache, uint16_t *v_cache, const uint16_t *k_new
     pgd_status st;
     if ((st = check_strides(kv, D)))
         return st;
-    for (long long x : {src_token, src_head})
+    for (long long x : {k_token, k_head, v_token, v_head})
         if (x <= 0 || x % 8 != 0 || x >= (1ll << 39))
             return fail(PGD_ERR_INVALID_ARG,
-                        "source strides (%lld, %lld) must be positive multiples of 8 halves "
-                        "below 2^39",
-                        src_token, src_head);
+                        "source strides (%lld, %lld; %lld, %lld) must be positive multiples of 8 "
+                        "halves below 2^39",
+                        k_token, k_head, v_token, v_head);
     if (rows == 0) {
         t_last_error.clear();
         return PGD_OK;
@@ -1688,8 +1688,10 @@ pgd_status run_write(uint16_t *k_cache, uint16_t *v_cache, const uint16_t *k_new
     p.page_stride = kv.page;
     p.head_stride = kv.head;
     p.token_stride = kv.token;
-    p.src_token_stride = src_token;
-    p.src_head_stride = src_head;
+    p.k_token_stride = k_token;
+    p.k_head_stride = k_head;
+    p.v_token_stride = v_token;
+    p.v_head_stride = v_head;
     const cudaError_t e = launch_kv_write(p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return cuda_fail(e, "kernel launch");
@@ -2243,10 +2245,23 @@ pgd_status paged_kv_write(uint16_t *k_cache, uint16_t *v_cache, const uint16_t *
                           int64_t page_stride, int64_t head_stride, int64_t token_stride,
                           int64_t src_token_stride, int64_t src_head_stride, void *stream)
 {
+    return paged_kv_write_strided(k_cache, v_cache, k_new, v_new, slots, num_rows, num_kv_heads,
+                                  head_dim, block_size, num_blocks, page_stride, head_stride,
+                                  token_stride, src_token_stride, src_head_stride,
+                                  src_token_stride, src_head_stride, stream);
+}
+
+pgd_status paged_kv_write_strided(uint16_t *k_cache, uint16_t *v_cache, const uint16_t *k_new,
+                                  const uint16_t *v_new, const int32_t *slots, int num_rows,
+                                  int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                  int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                                  int64_t k_token_stride, int64_t k_head_stride,
+                                  int64_t v_token_stride, int64_t v_head_stride, void *stream)
+{
     return guarded([&]() -> pgd_status {
         return run_write(k_cache, v_cache, k_new, v_new, slots, num_rows, num_kv_heads, head_dim,
                          block_size, num_blocks, Strides{page_stride, head_stride, token_stride},
-                         src_token_stride, src_head_stride, stream);
+                         k_token_stride, k_head_stride, v_token_stride, v_head_stride, stream);
     });
 }
 

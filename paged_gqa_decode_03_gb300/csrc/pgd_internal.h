@@ -375,7 +375,7 @@ struct WriteParams {
     int rows, Hkv, vec, log2BS, NB;       // vec: 16-byte pieces of a row (head_dim / 8)
     int rows_per_cta;                     // set by the launcher
     long long page_stride, head_stride, token_stride;   // halves
-    long long src_token_stride, src_head_stride;
+    long long k_token_stride, k_head_stride, v_token_stride, v_head_stride;
 };
 cudaError_t launch_kv_write(WriteParams p, cudaStream_t stream);
 
