@@ -602,8 +602,8 @@ pgd_status pgd_prefill_plan(int num_seqs, int total, int num_q_heads, int num_kv
  *                   read (those of the rows' pages), the new ones written, no
  *                   other touched
  * context_lens, query_lens  [num_seqs]; free_pages [num_free]; free_start [1] or
- *                   NULL (0): read.  free_end must not be free_start, nor
- *                   seq_lens one of the counts.
+ *                   NULL (0): read.
+ * No array that is written may overlap another one (PGD_ERR_INVALID_ARG).
  * The result depends on the arguments alone (the same pages every time), so a
  * call may be repeated or replayed before its counts are advanced.
  *

@@ -1602,10 +1602,29 @@ pgd_status run_slots(int32_t *slots, int32_t *positions, int32_t *cu_seqlens_q, 
                           (const void *)free_start})
         if (!aligned(a, 4))
             return fail(PGD_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
-    // every thread block reads the counts while one writes the results
-    if (free_end == free_start || (S > 0 && (seq_lens == context_lens || seq_lens == query_lens)))
-        return fail(PGD_ERR_INVALID_ARG, "free_end and seq_lens are written while free_start and "
-                                         "the counts are read: give other arrays");
+    // every thread block reads its inputs while others write: no array that is
+    // written (the first six) shares memory with another
+    const struct {
+        const void *at;
+        long long values;
+        const char *name;
+    } arrays[] = {{slots, N, "slots"},
+                  {positions, positions ? N : 0, "positions"},
+                  {cu_seqlens_q, S + 1ll, "cu_seqlens_q"},
+                  {seq_lens, S, "seq_lens"},
+                  {free_end, 1, "free_end"},
+                  {block_tables, (long long)S * MB, "block_tables"},
+                  {context_lens, S, "context_lens"},
+                  {query_lens, S, "query_lens"},
+                  {free_pages, num_free, "free_pages"},
+                  {free_start, free_start ? 1 : 0, "free_start"}};
+    for (int i = 0; i < 6; ++i)
+        for (int j = i + 1; j < 10; ++j) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(arrays[i].at),
+                            b = reinterpret_cast<uintptr_t>(arrays[j].at);
+            if (a < b + 4 * arrays[j].values && b < a + 4 * arrays[i].values)
+                return fail(PGD_ERR_INVALID_ARG, "%s overlaps %s", arrays[i].name, arrays[j].name);
+        }
     DeviceState *ds;
     pgd_status st;
     if ((st = device_state(&ds)))
