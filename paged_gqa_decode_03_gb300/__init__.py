@@ -518,10 +518,13 @@ def _index(t):
 
 def _fits(index, dtype, ndim, *tensors):
     """All contiguous, of ``dtype`` and ``ndim``, on CUDA device ``index``."""
-    for t in tensors:
-        if (t.dtype is not dtype or t.get_device() != index or t.dim() != ndim
-                or not t.is_contiguous()):
-            return False
+    try:
+        for t in tensors:
+            if (t.dtype is not dtype or t.get_device() != index or t.dim() != ndim
+                    or not t.is_contiguous()):
+                return False
+    except AttributeError:     # no tensor
+        return False
     return index >= 0
 
 
@@ -559,6 +562,8 @@ def _workspace(workspace):
     """(pointer, bytes) of an optional workspace."""
     if workspace is None:
         return None, 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
