@@ -25,6 +25,25 @@ def _built():
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("first", [1, 77, 300])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_rows_before_the_first_prompt_stay(D, first, dtype):
+    """cu_seqlens that begins above 0: the rows in front hold NaN, are not
+    written and reach no prompt; nor are those behind the last."""
+    lens = [first, 50, 200, 31]
+    c = case(lens, 8, 2, D, seed=51)
+    for t in (c["q"], c["k"], c["v"]):
+        t[:first] = float("nan")
+        t[first + 250:] = float("nan")
+    cu = torch.tensor([first, first + 50, first + 250], dtype=torch.int32, device=DEV)
+    out = torch.full((sum(lens), 8, D), 7.0, dtype=dtype, device=DEV)
+    pgd.packed_gqa_prefill(out, c["q"], c["k"], c["v"], cu, c["scale"], 200)
+    torch.cuda.synchronize()
+    assert (out[:first] == 7.0).all() and (out[first + 250:] == 7.0).all()
+    check(out, c, f"D{D} behind {first} rows", prompts=(1, 2))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_weights_far_below_the_largest(D):
     """The first token takes nearly all of the weight and its V is 0; the others' weights
     are 2^-24.4 of it.  Weights may be off by 2^-11 of themselves or 2^-32 of

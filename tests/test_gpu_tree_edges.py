@@ -160,3 +160,32 @@ def test_weights_far_below_the_largest(D, nodes):
     lim = (2.0 ** -11 + 2 * (2.0 ** -18 + L * 2.0 ** -24)) * A + L * 2.0 ** -32
     err = np.abs(out.double().cpu().numpy() - ref)
     assert (err <= lim).all(), (err / lim).max()
+
+
+# ------------------------------------------------------------------ the division of the work
+@pytest.mark.parametrize("S", [383, 384, 385, 768, 769, 1300])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 8, 2), (128, 4, 1)])
+def test_division_over_many_sequences(S, D, Hq, Hkv):
+    """The scan over the sequences takes 384 at a time: one, two, three and four
+    rounds; empty sequences lie between the others, at the rounds' borders too."""
+    rng = random.Random(S)
+    ctx = [rng.choice([0, 3, 128, 129, 500]) for _ in range(S)]
+    n = [rng.choice([0, 1, 2, 5, 40]) for _ in range(S)]
+    n[0], n[-1] = 2, 3
+    if S > 385:
+        n[383] = n[384] = 0
+    w, trees, parents = case(ctx, n, Hq, Hkv, D, 8, seed=S)
+    out = run(w, parents)
+    assert torch.isfinite(out).all()
+    check(out, w, trees, ctx, f"S {S}",
+          seqs=sorted({0, 1, 382, 383 % S, 384 % S, 385 % S, 767 % S, 768 % S, S - 2, S - 1}
+                      | set(range(5, S, 97))))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_loose_bound_on_the_nodes(D):
+    """max_q_len 256 for trees of at most 8: at head_dim 128 and 256 pairs of CTAs whose
+    second tile is empty."""
+    ctx, n = [3000, 40, 0, 500], [8, 1, 3, 5]
+    w, trees, parents = case(ctx, n, 16, 4, D, 16, seed=46)
+    check(run(w, parents, max_q=256), w, trees, ctx, "loose")
