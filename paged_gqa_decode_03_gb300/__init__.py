@@ -32,8 +32,8 @@ __all__ = ["paged_gqa_decode", "paged_gqa_decode_ex", "paged_gqa_decode_noalloc"
            "paged_gqa_varlen", "pgd_varlen_plan", "paged_gqa_decode_q8",
            "paged_gqa_decode_q8_append", "paged_gqa_decode_q8_strided", "q8_strides",
            "paged_kv_quantize", "paged_gqa_tree", "pgd_tree_plan",
-           "packed_gqa_prefill", "pgd_prefill_plan", "paged_kv_slots", "paged_kv_write", "pgd_plan", "pgd_workspace_size", "pgd_release",
-           "pgd_last_partition_size",
+           "packed_gqa_prefill", "pgd_prefill_plan", "paged_kv_slots", "paged_kv_write",
+           "pgd_plan", "pgd_workspace_size", "pgd_release", "pgd_last_partition_size",
            "pgd_last_error", "pgd_check_device_error", "pgd_set_timing_events",
            "pgd_test_stall_next_decode", "pgd_test_fail_next_reduce", "pgd_test_fail_next_set_up",
            "pgd_device_info", "pgd_version", "PGDError", "library_path", "load_library"]

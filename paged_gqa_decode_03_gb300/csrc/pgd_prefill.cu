@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             int4 next = unit_at(p, 0, units);
             if (warp == 1) {
                 const uint32_t idesc_s = IDESC_S | (p.scale_log2 < 0.f ? kNegateA : 0u);
-            const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
+                const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
                 const uint64_t k_desc = tc_sdesc(k_s, 16, 1024);
                 int nk = 0, nq = 0, ns = 0;
                 for (int k = 0; k < turns && ok; ++k) {
