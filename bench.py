@@ -54,20 +54,20 @@ FALLBACK_HBM_GBS = 6800.0
 # partition size).
 TRAFFIC = {
     # decode kernels (hash without pgd_varlen.cu and the step's operators)
-    "ca5c1dac27761114": {("long_context", 512): 1_293_067_264 + 6_864_896,
-                         ("long_context", 256): 1_293_185_024 + 7_358_208,
-                         ("ragged_tails", 256): 888_200_704 + 6_841_344,
-                         ("serving_mix", 512): 1_212_336_640 + 6_846_208,
-                         ("batch_decode", 512): 633_309_952 + 5_264_896,
-                         ("batch_decode_q8", 512): 336_819_456 + 4_822_272,
-                         ("long_context_q8", 512): 687_138_048 + 6_886_656,
-                         ("ragged_tails_q8", 256): 472_705_536 + 6_773_760,
-                         ("serving_mix_q8", 512): 644_734_976 + 7_085_824},
+    "27a795e22b2567dd": {("long_context", 512): 1_293_081_344 + 7_224_576,
+                         ("long_context", 256): 1_293_123_072 + 7_288_320,
+                         ("ragged_tails", 256): 888_195_840 + 6_817_536,
+                         ("serving_mix", 512): 1_212_328_704 + 6_879_232,
+                         ("batch_decode", 512): 633_370_624 + 4_934_144,
+                         ("batch_decode_q8", 512): 336_772_864 + 4_451_072,
+                         ("long_context_q8", 512): 687_137_024 + 6_614_016,
+                         ("ragged_tails_q8", 256): 472_703_488 + 6_818_304,
+                         ("serving_mix_q8", 512): 644_733_440 + 6_870_016},
     # the several-query-token kernels (hash without the decode kernels' files
     # and the step's operators)
-    "581bd824679a3af2": {("chunked_prefill", 8320): 265_761_280 + 41_800_960,
-                         ("prefill", 2048): 103_046_656 + 82_970_368,
-                         ("spec_verify", 4096): 605_144_320 + 4_453_376},
+    "dda3238b57b948a1": {("chunked_prefill", 8320): 269_380_096 + 41_804_544,
+                         ("prefill", 2048): 102_834_688 + 82_900_480,
+                         ("spec_verify", 4096): 605_202_944 + 4_104_448},
 }
 
 
