@@ -495,15 +495,21 @@ pgd_status pgd_varlen_plan(int num_seqs, int total_q, int max_q_len, int num_q_h
  *            In both, the weights are rounded to fp16 before they multiply V:
  *            by 2^-11 of themselves at most, or, below 2^-21 of the row's
  *            largest, by 2^-32 of that; sums are fp32.
- * max_q_len  bound on every n_s, at most PGD_TREE_MAX_NODES.
+ * max_q_len  bound on every n_s, at most PGD_TREE_MAX_NODES.  It sizes the launch:
+ *            at head_dim 128 and 256 a bound above 128 / (num_q_heads /
+ *            num_kv_heads) nodes has two SMs work on each unit, of which one
+ *            has nothing to do where all trees are smaller (64 trees of 8
+ *            nodes over 512 to 4096 tokens, 32 / 8 heads x 128: 101 us with 8,
+ *            193 us with 256).
  * workspace  NULL: library scratch; else at least pgd_tree_plan's bytes, 256-byte
  *            aligned, not used by anything else until the call's work is done.
  *
  * parents[i] = i - 1 is paged_gqa_varlen's causal form.  A sequence whose length
  * is negative or past its table (PGD_DEVERR_SEQ_LEN) or whose query rows are
  * inconsistent (PGD_DEVERR_QUERY_LEN, also where they do not lie inside
- * total_q) is skipped, its rows are not written; rows behind the last sequence (total_q above
- * cu_seqlens_q[num_seqs], a padded batch) are left as they were.  K and V rows
+ * total_q) is skipped, its rows are not written; rows behind the last sequence
+ * (total_q above cu_seqlens_q[num_seqs], a padded batch) are left as they were.
+ * A query row of NaN gives NaN.  K and V rows
  * of one sequence's tree must be finite: a weight of 0 does not hide an
  * infinity or NaN in a sibling's V.  out must not overlap an input.  Library
  * scratch, where there is any, is per call (also in a captured graph), and
@@ -560,7 +566,7 @@ pgd_status pgd_tree_plan(int num_seqs, int total_q, int max_q_len, int num_q_hea
  * max_len, has a negative length or does not lie inside total is skipped and
  * sets PGD_DEVERR_QUERY_LEN.  Other prompts' rows may hold anything; within
  * one prompt an infinity or NaN in V is not hidden from earlier rows of the same
- * 128 keys by their weight of 0.
+ * 128 keys by their weight of 0.  A query row of NaN gives NaN.
  */
 pgd_status packed_gqa_prefill(void *out, int out_type, const uint16_t *q, const uint16_t *k,
                               const uint16_t *v, const int32_t *cu_seqlens, float scale,
@@ -591,7 +597,9 @@ pgd_status pgd_prefill_plan(int num_seqs, int total, int num_q_heads, int num_kv
  *     seq_lens[s]      = context_lens[s] + query_lens[s]
  *     *free_end        = *free_start + the pages taken
  * and for row r = cu_seqlens_q[s] + i, which is token t = context_lens[s] + i:
- *     positions[r]     = t
+ *     positions[r]     = t   (the row's place in the cache: a prompt's rows are
+ *                        rotated by it, the nodes of a drafted tree are not, whose
+ *                        rotary position is context_lens[s] + the node's depth)
  *     slots[r]         = block_tables[s][t / block_size] * block_size + t % block_size
  * Rows behind the last request, up to num_rows (a launch padded to a fixed row
  * count), get slot and position -1, which the writing calls skip.

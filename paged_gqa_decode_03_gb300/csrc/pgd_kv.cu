@@ -1,6 +1,7 @@
 // The bookkeeping and the writes of a serving step over the paged cache: the
 // step's page tables, slots, positions and lengths from the requests' token
-// counts, and the step's K and V rows into their pages.
+// counts, and the step's K and V rows into their pages.  Times are of a call in
+// a captured graph of such calls, unless "a call" is said.
 #include <algorithm>
 #include <climits>
 
@@ -18,16 +19,16 @@ namespace pgd {
 // opens the page (t % BS == 0) also enters into the table.  So every output is
 // a function of the counts: no claim, no atomic, the same pages every time.
 //
-// A launch moves little (20 bytes a row and request: 0.1 us of HBM time for a
-// thousand rows) and is bound by latency: one launch, in which every CTA scans
-// the counts itself (two loads, one block scan, one barrier: cheaper than a second
-// launch or a wait across CTAs) and then takes four consecutive rows per
+// A launch moves little (8 bytes a row and some 20 a request: a thousand of both
+// are 4 ns of HBM time) and is bound by latency: one launch, in which every CTA
+// scans the counts itself (two loads, one block scan, one barrier: cheaper than a
+// second launch or a wait across CTAs) and then takes four consecutive rows per
 // thread, which share one search of the request in shared memory.  On the
-// device 4.8 us for 64 requests of one token, 5.6 for 257 with 17 prompt
-// chunks, 8.1 for 2048 with 2000 prompts of up to 511 tokens (the 4 counts a
-// thread scans twice, then 3.4 rows a thread); a call from Python takes the
-// host 8.6 us.  Sums saturate (min(a + b, cap) is associative on
-// non-negative numbers), so no count can overflow them.
+// device 4.9 us for 64 requests of one token, 5.6 for 257 with 17 prompt
+// chunks, 8.1 for 2048 with 2000 prompts of up to 511 tokens (the 4 requests that
+// a thread scans twice, one load at a time, then 6.5 rows a thread); a call from
+// Python takes the host 8.2 to 9 us.  Sums saturate (min(a + b, cap) is
+// associative on non-negative numbers), so no count can overflow them.
 constexpr int kSlotThreads = 512;
 constexpr int kSlotRows = 4;  // rows per thread and turn
 
@@ -238,13 +239,16 @@ cudaError_t launch_kv_slots(const SlotParams &p, int num_sms, cudaStream_t strea
 // tokens; a thread moves 16-byte pieces, of K and of V, consecutive threads
 // consecutive pieces of a token's heads (runs of head_dim halves on both
 // sides).  131072 rows of 8 heads x 128: 162 us, 6.6 TB/s of reads and writes
-// (a plain copy: 6.8); 10007 rows of 4 x 256 into 8-row pages, token-major:
-// 9.1 us, less than HBM's 11.5, since the L2 takes in the writes; 64 rows: 2.0.
+// (a plain copy: 6.8); 64 rows: 2.0.  10007 rows of 4 x 256 into 8-row pages,
+// token-major: 16.4 us a call in turn with other work, 4.8 TB/s (a copy's rate
+// would give 11.5): 5004 short CTAs, each with a slot to read before its one
+// load of K and of V.  (The same call over and over takes 9.0 us, with its 39 MB
+// of rows and most of its writes in the L2: no measure of HBM.)
 constexpr int kWriteThreads = 256;
 
 // SAME: K's and V's rows lie at the same strides, so one address calculation
-// serves both (two take 64 rows 2.15 us, 10007 rows 9.35 and 131072 rows 163.8,
-// one 2.07, 9.1 and 163.1).
+// serves both (with two, 64 rows take 2.15 us instead of 2.07, 10007 rows 9.35
+// instead of 9.1, 131072 rows 163.8 instead of 163.1).
 template <bool SAME>
 __global__ void __launch_bounds__(kWriteThreads) paged_kv_write_kernel(const WriteParams p)
 {

@@ -8,7 +8,8 @@
 // and sum.  A tile is 128 rows: TQ = 128 / G tokens x the G heads of one KV
 // head, so that every K and V byte serves the group.  Work is 4 D operations
 // per row and key on operands that come from L2 almost always: the tensor
-// cores are what bounds a long prompt.
+// cores are what bounds a long prompt.  Times are of calls in a captured graph,
+// unless "a call" is said: called from Python in turn with other work.
 #include <algorithm>
 
 #include "pgd_device.cuh"
@@ -156,8 +157,9 @@ __device__ __forceinline__ float max128(const float (&v)[4][32])
 // 330 cycles of reading, 250 until the next product is issued and the 512 of
 // it behind what the pipe still holds.  A tile's softmax takes 2400 of the
 // period (reading 330, maximum 400, exponentials 900, P 200, barriers).
-// One prompt of 16381 tokens, 32 / 8 heads x 128: 1450 to 1500 us by the GPU's
-// clock at the time, 1450 to 1520 TFLOP/s; 4 x 2048 tokens: 111 us.  Tried
+// One prompt of 16381 tokens, 32 / 8 heads x 128: 1450 to 1530 us by the GPU's
+// clock at the time, a call 1504, 1460 TFLOP/s; 4 x 2048 tokens: 111 us, a call
+// 122.  Tried
 // and slower: part of the exponentials as polynomials on the FMA pipes (a
 // quarter of them: 1450 -> 1690 us: the issue slots, not the special-function
 // unit, are short); two threads per row (16 softmax warps: 1630); the rows'
@@ -659,13 +661,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // all of head_dim, so that beside the 64 KB of Q nine of them fit and each is
 // free again after its own products: a stage's copies are never waited for as
 // a whole.  Eight softmax warps: rows r by halves of a stage's keys.
-// A prompt of 8192 tokens, 16 / 2 heads: 396 us, 1390 TFLOP/s.  37 prompts of 1
-// to 512 tokens, 24 / 4 heads: 31 us, of which a unit's start and end are the
-// larger part: a unit of one token costs 3.8 us of its CTA's time.  The output's
-// product of a unit's last stage ends at the tile's last key, rounded up to 16,
-// so that of the rows behind a prompt 15 at most have to be zeroed (the whole
-// stage: 34.5 us).  Ending its copies and scores there as well added 5 % to the
-// long prompt: not taken.
+// A prompt of 8192 tokens, 16 / 2 heads: 396 to 405 us, 1360 to 1390 TFLOP/s.  37
+// prompts of 1 to 512 tokens, 24 / 4 heads: 29 to 32 us, a call 32, of which a
+// unit's start and end are the larger part: a unit of one token costs 3.8 us of
+// its CTA's time.  The output's product of a unit's last stage ends at the tile's
+// last key, rounded up to 16, so that of the rows behind a prompt 15 at most have
+// to be zeroed (the whole stage: 34.5 us).  Ending its copies and scores there as
+// well added 5 % to the long prompt: not taken.
 constexpr int kWideThreads = 384;
 constexpr int kWideNK = 5, kWideNV = 4;  // pieces
 constexpr int kWideD = 256;

@@ -11,7 +11,8 @@
 //
 // Every K and V byte serves at most a few hundred rows, so the call is bound by
 // the K and V bytes from HBM; everything below is about keeping all SMs reading
-// until the end:
+// until the end.  (Times are of calls in a captured graph, unless "a call" is
+// said: called from Python in turn with other work.)
 //   * A unit is one (sequence, KV head, one or two tiles); a tile is 128 rows (TQ =
 //     128 / G nodes x the G heads of the KV head).  An SM takes in some 55 GB/s
 //     whatever the copies, 152 of them 8.3 TB/s: little more than HBM gives, so a
@@ -19,10 +20,11 @@
 //     two CTAs work on two tiles as a pair (tcgen05 cta_group::2): one product of
 //     256 rows, whose B operand is split over the two, so that each copies half of
 //     every stage (half of K's tokens, half of V's head_dim) and both use all of it.
-//     32 sequences of 8 k to 32 k tokens, 16 / 2 heads x 256: 270 us, 5.1 TB/s
-//     (two CTAs of a cluster that each hold all of a stage, copied by multicast:
-//     338 us); 64 of 512 to 4096 tokens, 32 / 8 heads x 128, single CTAs:
-//     107 us, 6.1 TB/s; one of 1000: 12.5 us, latency.
+//     32 sequences of 8 k to 32 k tokens, 16 / 2 heads x 256: 268 to 290 us by the
+//     machine, a call 297 us, 4.6 TB/s (two CTAs of a cluster that each hold all
+//     of a stage, copied by multicast: 338 us); 64 of 512 to 4096 tokens, 32 / 8
+//     heads x 128, single CTAs: 107 us, a call 115 us, 5.6 TB/s; one of 1000:
+//     12.5 us, a call 15.7, latency.
 //   * The stages of all units, one after the other, are cut into equal runs, one
 //     per resident CTA or pair: no run has more than another, whatever the
 //     lengths.  A unit that is cut leaves pieces (reference maximum, exp-sum,
@@ -363,8 +365,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
     if (warp < 4) {
       // to the softmax warps (128 x 152 + 256 x 176 of the launch's 384 x 168): at
-      // head_dim 64 and 128 no role spills.  (With 104 and 200 the copying warps
-      // did: 64 requests 111.5 us instead of 107.9.)
+      // head_dim 64 and 128 nothing spills but 8 bytes in the pairs.  (With 104
+      // and 200 the copying warps did: 64 requests 111.5 us instead of 107.9.)
       regs_give<152>();
       if (warp == 0 || warp == kTreeVWarp) {
         // ============================================================ copies
