@@ -669,6 +669,187 @@ pgd_status paged_kv_write_strided(uint16_t *k_cache, uint16_t *v_cache, const ui
                                   int64_t k_token_stride, int64_t k_head_stride,
                                   int64_t v_token_stride, int64_t v_head_stride, void *stream);
 
+/*
+ * paged_rope_write — the rotary positions of a step's queries and keys, with the
+ * write of its K and V rows into their pages (paged_kv_write), in one launch.
+ *
+ * For row n at position t = positions[n], the first rotary_dim values of every
+ * query and key head are turned pair by pair, pair i by the angle t * inv_freq[i]:
+ *     (a, b) -> magnitude * (a cos - b sin, b cos + a sin)
+ * where a, b are values i and i + rotary_dim / 2 of the head (interleaved 0) or 2i
+ * and 2i + 1 (interleaved non-zero); its other values are copied as they are.  The
+ * turned keys and the values go to cache row slots[n], the turned queries to q_out.
+ * The angle is exact but for 2^-53 of itself: the position of a token far out in
+ * a long context costs no accuracy.  Arithmetic is fp32, rounded once to fp16.
+ *
+ * q, q_out      [num_rows][num_q_heads][head_dim] fp16 at token and head strides of
+ *               their own; q_out may be q itself, with the same strides (the values
+ *               behind rotary_dim are then not touched), else it shares no memory
+ *               with an input.  Both NULL with num_q_heads 0: keys alone.
+ * k_new, v_new  [num_rows][num_kv_heads][head_dim], strides of their own (all four
+ *               in halves, positive multiples of 8), 16-byte aligned, read
+ * slots         [num_rows] int32 as for paged_kv_write; negative: the row is not
+ *               written to the cache (its queries are turned all the same)
+ * positions     [num_rows] int32, 0 .. 2^31 - 1, independent of the slot (a node of a
+ *               drafted tree is turned by its depth in it); negative: a row of
+ *               padding, of which nothing is read or written
+ * inv_freq      [rotary_dim / 2] fp32, device, finite: radians a position of each
+ *               pair (pgd_rope_frequencies makes the usual tables, long contexts'
+ *               among them)
+ * rotary_dim    a multiple of 16 up to head_dim
+ * k_cache, v_cache, strides, device checks: as for paged_kv_write.
+ */
+pgd_status paged_rope_write(uint16_t *k_cache, uint16_t *v_cache, uint16_t *q_out,
+                            const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new,
+                            const int32_t *slots, const int32_t *positions,
+                            const float *inv_freq, float magnitude, int interleaved, int num_rows,
+                            int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                            int block_size, int num_blocks, int64_t page_stride,
+                            int64_t head_stride, int64_t token_stride, int64_t q_out_token_stride,
+                            int64_t q_out_head_stride, int64_t q_token_stride,
+                            int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                            int64_t v_token_stride, int64_t v_head_stride, void *stream);
+
+/*
+ * pgd_rope_frequencies — a table of inverse frequencies (host memory, rotary_dim / 2
+ * values) for paged_rope_write and paged_latent_write, and the magnitude that goes
+ * with it.  base^(-2i / rotary_dim), and for contexts longer than the trained one
+ * by `factor` (>= 1):
+ *   PGD_ROPE_PLAIN     as it is
+ *   PGD_ROPE_LINEAR    positions shrunk: every frequency divided by factor
+ *   PGD_ROPE_BASE      the base raised to base * factor^(rotary_dim / (rotary_dim - 2)):
+ *                      the highest frequency stays, the lowest shrinks by factor
+ *   PGD_ROPE_BY_PARTS  pairs that turn more than beta_fast times in original_len tokens
+ *                      stay, those that turn less than beta_slow times shrink by factor,
+ *                      those between in proportion to their index; magnitude 0.1 ln(factor) + 1
+ *                      ("YaRN", Peng et al. 2023, section 3)
+ * original_len, beta_fast > beta_slow > 0 matter to BY_PARTS alone.  Arithmetic in
+ * 64 bits, rounded once.  *magnitude (if not NULL) is 1 but for BY_PARTS.  Needs no GPU.
+ */
+#define PGD_ROPE_PLAIN 0
+#define PGD_ROPE_LINEAR 1
+#define PGD_ROPE_BASE 2
+#define PGD_ROPE_BY_PARTS 3
+
+pgd_status pgd_rope_frequencies(float *inv_freq, float *magnitude, int rotary_dim, double base,
+                                int scaling, double factor, double original_len, double beta_fast,
+                                double beta_slow);
+
+/*
+ * A latent cache holds one row a token for all heads: latent_dim values, from which
+ * every head's key and value follow by a projection, and behind them rope_dim values
+ * of one rotated key that all heads share.
+ *   cache   [num_blocks][block_size][latent_dim + rope_dim] fp16, page and token
+ *           strides in halves (positive multiples of 8 below 2^39, token_stride >=
+ *           latent_dim + rope_dim), 16-byte aligned
+ * Page tables, slots and lengths are those of the other caches (paged_kv_slots).
+ * latent_dim 128, 256 or 512, rope_dim 32 or 64, block sizes 8 to 128.
+ *
+ * paged_latent_write — a step's rows into a latent cache: row n's latent vector as
+ * it is and its key turned by its position, to cache row slots[n]; the queries'
+ * rotary parts turned into q_out.  The rotation, slots, positions, inv_freq (rope_dim
+ * / 2 values) and q_out's rules are those of paged_rope_write, with all of rope_dim
+ * turned.
+ *
+ * latent        [num_rows][latent_dim], k_rope [num_rows][rope_dim] fp16, each with
+ *               its own token stride: slices of one projection's output need no copy
+ * q_rope, q_out [num_rows][num_heads][rope_dim] fp16 at strides of their own, or both
+ *               NULL with num_heads 0
+ */
+pgd_status paged_latent_write(uint16_t *cache, uint16_t *q_out, const uint16_t *q_rope,
+                              const uint16_t *latent, const uint16_t *k_rope,
+                              const int32_t *slots, const int32_t *positions,
+                              const float *inv_freq, float magnitude, int interleaved,
+                              int num_rows, int num_heads, int latent_dim, int rope_dim,
+                              int block_size, int num_blocks, int64_t page_stride,
+                              int64_t token_stride, int64_t q_out_token_stride,
+                              int64_t q_out_head_stride, int64_t q_token_stride,
+                              int64_t q_head_stride, int64_t latent_token_stride,
+                              int64_t k_rope_token_stride, void *stream);
+
+/*
+ * paged_latent_attention — attention over a latent cache with the queries taken
+ * through the keys' projection beforehand (the absorbed form): every head reads the
+ * same rows, and a row's latent part is its key and its value.  With c_t the latent
+ * part and k_t the rotated key of cached token t, for query row r and head h:
+ *     out[r][h][:] = sum_t w_t c_t,
+ *     w = softmax( (q[r][h] . c_t + q_rope[r][h] . k_t) * scale )
+ * The caller takes out through the values' projection.
+ *
+ * Sequence s has the query rows cu_seqlens_q[s] .. cu_seqlens_q[s+1]-1, its newest
+ * tokens, already in the cache, causal among themselves (as in paged_gqa_varlen).
+ * cu_seqlens_q NULL: a decode step, one row a sequence (total_q == num_seqs), which
+ * sees all of seq_lens[s] tokens; a sequence of length 0 gets zeros.
+ *
+ * out        [total_q][num_heads][latent_dim], contiguous, 16-byte aligned;
+ *            out_type PGD_OUT_F32 or PGD_OUT_F16 (rounded to nearest).  The weights
+ *            are rounded to fp16 before they multiply the rows, in both, as in
+ *            paged_gqa_tree; sums are fp32.
+ * q          [total_q][num_heads][latent_dim], q_rope [total_q][num_heads][rope_dim]
+ *            fp16, 16-byte aligned, each with its own token and head strides (halves,
+ *            positive multiples of 8 below 2^39): parts of one tensor, or a batched
+ *            product's output [num_heads][total_q][latent_dim], need no copy
+ * max_q_len  bound on every sequence's query rows (1 with cu_seqlens_q NULL)
+ * workspace  NULL: library scratch (per call, also in a captured graph); else at
+ *            least pgd_latent_plan's bytes, 256-byte aligned, not used by anything
+ *            else until the call's work is done
+ *
+ * A sequence whose length is negative or past its table (PGD_DEVERR_SEQ_LEN) or
+ * whose query rows are inconsistent (PGD_DEVERR_QUERY_LEN) is skipped, its rows are
+ * not written; rows behind the last sequence are left as they were.  A page id
+ * outside [0, num_blocks) reads as zeros (PGD_DEVERR_PAGE_RANGE).  A query row of NaN
+ * gives NaN.  The cached rows of one sequence's own query tokens must be finite: a
+ * weight of 0 does not hide an infinity or NaN in a later one.  out must not overlap
+ * an input.
+ */
+pgd_status paged_latent_attention(void *out, int out_type, const uint16_t *q,
+                                  const uint16_t *q_rope, const int32_t *cu_seqlens_q,
+                                  const uint16_t *cache, const int32_t *block_tables,
+                                  const int32_t *seq_lens, float scale, int num_seqs, int total_q,
+                                  int max_q_len, int num_heads, int latent_dim, int rope_dim,
+                                  int block_size, int max_blocks_per_seq, int num_blocks,
+                                  int64_t page_stride, int64_t token_stride,
+                                  int64_t q_token_stride, int64_t q_head_stride,
+                                  int64_t q_rope_token_stride, int64_t q_rope_head_stride,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Scratch bytes a paged_latent_attention call with these sizes needs on the current
+ * device: the pieces of the units that its even division of the work cuts. */
+pgd_status pgd_latent_plan(int num_seqs, int total_q, int max_q_len, int num_heads,
+                           int latent_dim, int rope_dim, int block_size, int max_blocks_per_seq,
+                           size_t *workspace_bytes);
+
+/*
+ * packed_latent_prefill — causal attention over whole packed prompts whose keys and
+ * values have been expanded from their latent vectors (the expanded form), before or
+ * beside the latent cache's write: each head has keys of its own and, behind them,
+ * the one rotated key of the token that all heads share.
+ *     out[row][h][:] = softmax( (q[row][h] . [k[t][h] | k_rope[t]]) * scale
+ *                               over positions t up to the row's ) . v[t][h]
+ *
+ * q        [total][num_heads][head_dim + rope_dim], k, v [total][num_heads][head_dim],
+ *          k_rope [total][rope_dim] fp16, 16-byte aligned, strides of their own
+ *          (halves, positive multiples of 8 below 2^39): halves of the up projection's
+ *          output and a slice of the down projection's need no copy
+ * out      [total][num_heads][head_dim] contiguous, 16-byte aligned
+ * head_dim 64 or 128, rope_dim 32 or 64.  cu_seqlens, max_len, out_type, workspace
+ * (pgd_latent_prefill_plan) and the rules on other rows, lengths, NaN and overlaps are
+ * those of packed_gqa_prefill.
+ */
+pgd_status packed_latent_prefill(void *out, int out_type, const uint16_t *q, const uint16_t *k,
+                                 const uint16_t *k_rope, const uint16_t *v,
+                                 const int32_t *cu_seqlens, float scale, int num_seqs, int total,
+                                 int max_len, int num_heads, int head_dim, int rope_dim,
+                                 int64_t q_token_stride, int64_t q_head_stride,
+                                 int64_t k_token_stride, int64_t k_head_stride,
+                                 int64_t k_rope_token_stride, int64_t v_token_stride,
+                                 int64_t v_head_stride, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* Scratch bytes a packed_latent_prefill call with these sizes needs.  Pure arithmetic. */
+pgd_status pgd_latent_prefill_plan(int num_seqs, int total, int num_heads, int head_dim,
+                                   int rope_dim, size_t *workspace_bytes);
+
 /* Partition size used by this thread's last successful call (0 if none);
  * the diagnostic of the pages' "Hands-on" section. */
 int pgd_last_partition_size(void);
@@ -739,7 +920,8 @@ pgd_status pgd_device_info(int head_dim, int block_size, int *num_sms, int *ctas
  * sequence; 1.3.0: quantised pages; 1.4.0: pgd_workspace_size, pgd_release,
  * paged_gqa_decode_host; 1.5.0: paged_gqa_tree, packed_gqa_prefill,
  * paged_kv_slots, paged_kv_write; 1.5.1: paged_kv_write_strided,
- * pgd_test_fail_next_set_up). */
+ * pgd_test_fail_next_set_up; 1.6.0: paged_rope_write, pgd_rope_frequencies,
+ * paged_latent_write, paged_latent_attention, packed_latent_prefill). */
 int pgd_version(void);
 
 #ifdef __cplusplus

@@ -33,6 +33,8 @@ __all__ = ["paged_gqa_decode", "paged_gqa_decode_ex", "paged_gqa_decode_noalloc"
            "paged_gqa_decode_q8_append", "paged_gqa_decode_q8_strided", "q8_strides",
            "paged_kv_quantize", "paged_gqa_tree", "pgd_tree_plan",
            "packed_gqa_prefill", "pgd_prefill_plan", "paged_kv_slots", "paged_kv_write",
+           "paged_rope_write", "rope_frequencies", "paged_latent_write", "paged_latent_attention",
+           "pgd_latent_plan", "packed_latent_prefill", "pgd_latent_prefill_plan",
            "pgd_plan", "pgd_workspace_size", "pgd_release", "pgd_last_partition_size",
            "pgd_last_error", "pgd_check_device_error", "pgd_set_timing_events",
            "pgd_test_stall_next_decode", "pgd_test_fail_next_reduce", "pgd_test_fail_next_set_up",
@@ -50,10 +52,11 @@ DEVERR_NO_PAGE, DEVERR_TREE = 16, 32
 OUT_F32, OUT_F16 = 0, 1
 TREE_MAX_NODES = 256        # PGD_TREE_MAX_NODES of include/pgd.h
 SLOTS_MAX_SEQS = 16384      # PGD_SLOTS_MAX_SEQS
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}   # PGD_ROPE_*
 
 # Every exported symbol of include/pgd.h with its ctypes signature.
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-_L = ctypes.c_int64
+_L, _D = ctypes.c_int64, ctypes.c_double
 SIGNATURES = {
     "paged_gqa_decode": (_I, [_P] * 6 + [_F] + [_I] * 8 + [_P]),
     "paged_gqa_decode_ex": (_I, [_P] * 6 + [_F] + [_I] * 8 + [_P, _Z, _P, _P]),
@@ -75,6 +78,13 @@ SIGNATURES = {
     "paged_kv_slots": (_I, [_P] * 10 + [_I] * 6 + [_P]),
     "paged_kv_write": (_I, [_P] * 5 + [_I] * 5 + [_L] * 5 + [_P]),
     "paged_kv_write_strided": (_I, [_P] * 5 + [_I] * 5 + [_L] * 7 + [_P]),
+    "paged_rope_write": (_I, [_P] * 9 + [_F] + [_I] * 8 + [_L] * 11 + [_P]),
+    "pgd_rope_frequencies": (_I, [_P, _P, _I, _D, _I] + [_D] * 4),
+    "paged_latent_write": (_I, [_P] * 8 + [_F] + [_I] * 7 + [_L] * 8 + [_P]),
+    "paged_latent_attention": (_I, [_P, _I] + [_P] * 6 + [_F] + [_I] * 9 + [_L] * 6 + [_P, _Z, _P]),
+    "pgd_latent_plan": (_I, [_I] * 8 + [ctypes.POINTER(_Z)]),
+    "packed_latent_prefill": (_I, [_P, _I] + [_P] * 5 + [_F] + [_I] * 6 + [_L] * 7 + [_P, _Z, _P]),
+    "pgd_latent_prefill_plan": (_I, [_I] * 5 + [ctypes.POINTER(_Z)]),
     "pgd_plan": (_I, [_I] * 7 + [ctypes.POINTER(_I), ctypes.POINTER(_Z)]),
     "pgd_workspace_size": (_Z, [_I] * 6),
     "pgd_release": (_I, []),
@@ -757,6 +767,236 @@ def paged_kv_write(k_cache, v_cache, k_new, v_new, slots, layout=None, stream=No
     fn, src = (lib.paged_kv_write, ks) if ks == vs else (lib.paged_kv_write_strided, ks + vs)
     _on(dev, fn, k_cache.data_ptr(), v_cache.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
         slots.data_ptr(), N, Hkv, D, int(BS), int(NB), sp, sh, st, *src, stream=stream)
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "plain",
+                     factor: float = 1.0, original_len: float = 0.0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq float32 [rotary_dim / 2] on ``device``, magnitude) for
+    ``paged_rope_write`` and ``paged_latent_write``: base^(-2i / rotary_dim), for
+    contexts longer than the trained one by ``factor`` "linear" (every frequency
+    divided by it), "base" (the base raised) or "by_parts" (frequencies that turn
+    less than beta_slow times in original_len tokens divided, those that turn
+    more than beta_fast times kept)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling {scaling!r}: one of {', '.join(ROPE_SCALINGS)}")
+    rot = int(rotary_dim)
+    table = (ctypes.c_float * max(1, rot // 2))()
+    magnitude = ctypes.c_float(1.0)
+    _raise(load_library().pgd_rope_frequencies(
+        ctypes.cast(table, _P), ctypes.cast(ctypes.byref(magnitude), _P), rot, float(base),
+        ROPE_SCALINGS[scaling], float(factor), float(original_len), float(beta_fast),
+        float(beta_slow)))
+    return torch.tensor(list(table), dtype=torch.float32, device=device), magnitude.value
+
+
+def _rope_table(dev, slots, positions, inv_freq, rows):
+    """The checks that paged_rope_write and paged_latent_write share."""
+    if not (_fits(dev, _I32, 1, slots, positions) and _fits(dev, torch.float32, 1, inv_freq)):
+        _check_all((slots, "slots", _I32, 1), (positions, "positions", _I32, 1),
+                   (inv_freq, "inv_freq", torch.float32, 1))
+        _one_device(dev, positions, inv_freq)
+    if slots.numel() != rows or positions.numel() != rows:
+        raise ValueError("a slot and a position per row")
+
+
+def paged_rope_write(k_cache, v_cache, q_out, q, k_new, v_new, slots, positions, inv_freq,
+                     magnitude: float = 1.0, interleaved: bool = False, layout=None,
+                     stream=None) -> None:
+    """Turns the first 2 * len(inv_freq) values of every head of q [N, Hq, D] and
+    k_new [N, Hkv, D] by the rows' ``positions`` (int32 [N]; negative: a row of
+    padding) and ``inv_freq`` (float32, radians a position of each pair, on the
+    device), into ``q_out`` (q itself, or another tensor of its shape) and, with
+    v_new [N, Hkv, D], into the cache at rows ``slots`` (int32 [N]; negative: not
+    written), as ``paged_kv_write`` does.  Pairs are values i and i +
+    len(inv_freq), or 2i and 2i + 1 (``interleaved``).  Row tensors are fp16 with
+    contiguous rows of head_dim and any token and head strides; q and q_out may
+    both be None.  Caches and ``layout`` as for ``paged_kv_write``."""
+    lib = _lib or load_library()
+    ks, vs = _packed_strides(k_new, "k_new"), _packed_strides(v_new, "v_new")
+    dev = _index(k_new)
+    N, Hkv, D = k_new.shape
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have the same shape")
+    _rope_table(dev, slots, positions, inv_freq, N)
+    if (q is None) != (q_out is None):
+        raise ValueError("give both q and q_out or neither")
+    Hq, qs, os_ = 0, (D, D), (D, D)
+    if q is not None:
+        qs, os_ = _packed_strides(q, "q"), _packed_strides(q_out, "q_out")
+        Hq = q.shape[1]
+        if q.shape[0] != N or q.shape[2] != D or q_out.shape != q.shape:
+            raise ValueError("inconsistent shapes of q, q_out, k_new")
+    if layout is None:
+        if not _fits(dev, _F16, 4, k_cache, v_cache):
+            _check_all((k_cache, "k_cache", _F16, 4), (v_cache, "v_cache", _F16, 4))
+            _one_device(dev, k_cache, v_cache)
+        NB, H2, BS, D2 = k_cache.shape
+        if v_cache.shape != k_cache.shape or D2 != D or H2 != Hkv:
+            raise ValueError("inconsistent shapes of k_cache, v_cache, k_new")
+        sp, sh, st = Hkv * BS * D, BS * D, D
+    else:
+        H2, BS, NB, strides = layout
+        if H2 != Hkv:
+            raise ValueError(f"layout of {H2} KV heads for rows of {Hkv}")
+        _check_rows_inside(k_cache, "k_cache", NB, Hkv, BS, D, strides)
+        _check_rows_inside(v_cache, "v_cache", NB, Hkv, BS, D, strides)
+        _one_device(dev, k_cache, v_cache)
+        sp, sh, st = (int(x) for x in strides)
+    _one_device(dev, v_new, q, q_out)
+    _on(dev, lib.paged_rope_write, k_cache.data_ptr(), v_cache.data_ptr(),
+        None if q is None else q_out.data_ptr(), None if q is None else q.data_ptr(),
+        k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+        inv_freq.data_ptr(), float(magnitude), 1 if interleaved else 0, N, Hq, Hkv, D,
+        2 * inv_freq.numel(), int(BS), int(NB), sp, sh, st, *os_, *qs, *ks, *vs, stream=stream)
+
+
+def _latent_cache(cache, R, P):
+    """(num_blocks, block_size, page stride, token stride) of a latent cache
+    [num_blocks, block_size, R + P] with contiguous rows and any page and token
+    strides."""
+    if not isinstance(cache, torch.Tensor) or cache.dtype is not _F16 or not cache.is_cuda:
+        raise TypeError("cache must be a float16 CUDA tensor")
+    if cache.dim() != 3 or cache.shape[2] != R + P or cache.stride(2) != 1:
+        raise ValueError(f"cache must be [num_blocks, block_size, {R + P}] with contiguous rows")
+    NB, BS, W = cache.shape
+    token = cache.stride(1) if BS > 1 else W
+    return NB, BS, cache.stride(0) if NB > 1 else BS * token, token
+
+
+def _row_stride(t, name):
+    """Token stride of rows [tokens, values] with contiguous values."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _F16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a float16 CUDA tensor")
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name} must have 2 dimensions and contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def paged_latent_write(cache, q_out, q_rope, latent, k_rope, slots, positions, inv_freq,
+                       magnitude: float = 1.0, interleaved: bool = False, stream=None) -> None:
+    """Writes a step's rows into a latent cache [num_blocks, block_size, R + P]
+    (fp16, contiguous rows, any page and token strides): latent [N, R] as it is and
+    behind it k_rope [N, P] turned by the rows' ``positions``, at cache rows
+    ``slots``; turns the queries' rotary parts q_rope [N, H, P] into ``q_out`` (q_rope
+    itself or another tensor; both may be None).  Rotation, slots and positions as
+    for ``paged_rope_write``, with len(inv_freq) == P / 2."""
+    lib = _lib or load_library()
+    ls, krs = _row_stride(latent, "latent"), _row_stride(k_rope, "k_rope")
+    dev = _index(latent)
+    N, R = latent.shape
+    P = k_rope.shape[1]
+    if k_rope.shape[0] != N:
+        raise ValueError("latent and k_rope must have the same rows")
+    _rope_table(dev, slots, positions, inv_freq, N)
+    if 2 * inv_freq.numel() != P:
+        raise ValueError(f"inv_freq must hold {P // 2} values")
+    NB, BS, page, token = _latent_cache(cache, R, P)
+    if (q_rope is None) != (q_out is None):
+        raise ValueError("give both q_rope and q_out or neither")
+    H, qs, os_ = 0, (P, P), (P, P)
+    if q_rope is not None:
+        qs, os_ = _packed_strides(q_rope, "q_rope"), _packed_strides(q_out, "q_out")
+        H = q_rope.shape[1]
+        if q_rope.shape[0] != N or q_rope.shape[2] != P or q_out.shape != q_rope.shape:
+            raise ValueError("inconsistent shapes of q_rope, q_out, k_rope")
+    _one_device(dev, cache, k_rope, q_rope, q_out)
+    _on(dev, lib.paged_latent_write, cache.data_ptr(),
+        None if q_rope is None else q_out.data_ptr(),
+        None if q_rope is None else q_rope.data_ptr(), latent.data_ptr(), k_rope.data_ptr(),
+        slots.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), float(magnitude),
+        1 if interleaved else 0, N, H, R, P, BS, NB, page, token, *os_, *qs, ls, krs,
+        stream=stream)
+
+
+def paged_latent_attention(out, q, q_rope, cache, block_tables, seq_lens, scale,
+                           cu_seqlens_q=None, max_q_len: int = 1, workspace=None,
+                           stream=None) -> None:
+    """Attention over a latent cache [num_blocks, block_size, R + P] (fp16, contiguous
+    rows, any page and token strides) with absorbed queries: q [total_q, H, R] against
+    a row's latent part, q_rope [total_q, H, P] against its rotated key (fp16, any
+    token and head strides); the latent part is the value.  Into ``out`` (contiguous
+    [total_q, H, R], float16 or float32).  ``cu_seqlens_q`` None: one query row a
+    sequence; else sequence s owns rows cu_seqlens_q[s]..cu_seqlens_q[s+1]-1, its newest
+    tokens, at most ``max_q_len``, causal."""
+    lib = _lib or load_library()
+    kind = _out_type(out)
+    dev = _index(q)
+    if not (_fits(dev, out.dtype, 3, out) and _fits(dev, _I32, 1, seq_lens)
+            and _fits(dev, _I32, 2, block_tables)
+            and (cu_seqlens_q is None or _fits(dev, _I32, 1, cu_seqlens_q))):
+        _packed_strides(q, "q")
+        _check_all((out, "out", out.dtype, 3), (seq_lens, "seq_lens", _I32, 1),
+                   (block_tables, "block_tables", _I32, 2), (cu_seqlens_q, "cu_seqlens_q?", _I32, 1))
+        _one_device(dev, out, seq_lens, block_tables, cu_seqlens_q)
+    qs, rs = _packed_strides(q, "q"), _packed_strides(q_rope, "q_rope")
+    T, H, R = q.shape
+    P = q_rope.shape[2]
+    S, MB = block_tables.shape
+    if (out.shape != q.shape or q_rope.shape[0] != T or q_rope.shape[1] != H
+            or seq_lens.numel() != S):
+        raise ValueError("inconsistent shapes of out, q, q_rope, block_tables, seq_lens")
+    if cu_seqlens_q is None:
+        if T != S:
+            raise ValueError("without cu_seqlens_q there is one query row a sequence")
+    elif cu_seqlens_q.numel() != S + 1:
+        raise ValueError("cu_seqlens_q holds num_seqs + 1 values")
+    NB, BS, page, token = _latent_cache(cache, R, P)
+    ws, ws_bytes = _workspace(workspace)
+    _one_device(dev, q_rope, cache, workspace)
+    _on(dev, lib.paged_latent_attention, out.data_ptr(), kind, q.data_ptr(), q_rope.data_ptr(),
+        None if cu_seqlens_q is None else cu_seqlens_q.data_ptr(), cache.data_ptr(),
+        block_tables.data_ptr(), seq_lens.data_ptr(), float(scale), S, T, int(max_q_len), H, R, P,
+        BS, MB, NB, page, token, *qs, *rs, ws, ws_bytes, stream=stream)
+
+
+def pgd_latent_plan(num_seqs, total_q, max_q_len, num_heads, latent_dim, rope_dim, block_size,
+                    max_blocks_per_seq) -> int:
+    """Scratch bytes of a paged_latent_attention call on the current device."""
+    b = ctypes.c_size_t(0)
+    _raise(load_library().pgd_latent_plan(num_seqs, total_q, max_q_len, num_heads, latent_dim,
+                                          rope_dim, block_size, max_blocks_per_seq,
+                                          ctypes.byref(b)))
+    return b.value
+
+
+def packed_latent_prefill(out, q, k, k_rope, v, cu_seqlens, scale, max_len: int, workspace=None,
+                          stream=None) -> None:
+    """Causal attention over whole packed prompts (rows cu_seqlens[s] ..
+    cu_seqlens[s+1]-1) with keys and values expanded from latent vectors: q [total, H,
+    D + P] against [k | k_rope], k and v [total, H, D] a head's own, k_rope [total, P]
+    shared by all heads (fp16, contiguous rows, any token and head strides), into
+    ``out`` (contiguous [total, H, D], float16 or float32)."""
+    lib = _lib or load_library()
+    kind = _out_type(out)
+    dev = _index(q)
+    if not (_fits(dev, out.dtype, 3, out) and _fits(dev, _I32, 1, cu_seqlens)):
+        _packed_strides(q, "q")
+        _check_all((out, "out", out.dtype, 3), (cu_seqlens, "cu_seqlens", _I32, 1))
+        _one_device(dev, out, cu_seqlens)
+    qs, ks, vs = _packed_strides(q, "q"), _packed_strides(k, "k"), _packed_strides(v, "v")
+    krs = _row_stride(k_rope, "k_rope")
+    T, H, D = v.shape
+    P = k_rope.shape[1]
+    if (out.shape != v.shape or k.shape != v.shape or k_rope.shape[0] != T
+            or tuple(q.shape) != (T, H, D + P)):
+        raise ValueError("inconsistent shapes of out, q, k, k_rope, v")
+    S = cu_seqlens.numel() - 1
+    if S < 0:
+        raise ValueError("cu_seqlens holds num_seqs + 1 values")
+    ws, ws_bytes = _workspace(workspace)
+    _one_device(dev, k, k_rope, v, workspace)
+    _on(dev, lib.packed_latent_prefill, out.data_ptr(), kind, q.data_ptr(), k.data_ptr(),
+        k_rope.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), float(scale), S, T, int(max_len),
+        H, D, P, *qs, *ks, krs, *vs, ws, ws_bytes, stream=stream)
+
+
+def pgd_latent_prefill_plan(num_seqs, total, num_heads, head_dim, rope_dim) -> int:
+    """Scratch bytes of a packed_latent_prefill call (needs no GPU)."""
+    b = ctypes.c_size_t(0)
+    _raise(load_library().pgd_latent_prefill_plan(num_seqs, total, num_heads, head_dim, rope_dim,
+                                                  ctypes.byref(b)))
+    return b.value
 
 
 NOALLOC_SCRATCH_BYTES = 64 << 20  # PGD_NOALLOC_SCRATCH_BYTES of include/pgd.h

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <unordered_map>
@@ -1870,6 +1871,324 @@ pgd_status run_prefill(float *out, uint16_t *out_half, const uint16_t *q, const 
     return PGD_OK;
 }
 
+// ------------------------------------------------------------------ rotary positions, latent caches
+bool stride_ok(long long x) { return x > 0 && x % 8 == 0 && x < (1ll << 39); }
+
+pgd_status check_row_strides(std::initializer_list<long long> strides)
+{
+    for (long long x : strides)
+        if (!stride_ok(x))
+            return fail(PGD_ERR_INVALID_ARG,
+                        "stride %lld: positive multiples of 8 halves below 2^39", x);
+    return PGD_OK;
+}
+
+pgd_status check_latent_dims(int R, int P)
+{
+    if (R != 128 && R != 256 && R != 512)
+        return fail(PGD_ERR_UNSUPPORTED, "latent_dim %d not in {128, 256, 512}", R);
+    if (P != 32 && P != 64)
+        return fail(PGD_ERR_UNSUPPORTED, "rope_dim %d not in {32, 64}", P);
+    return PGD_OK;
+}
+
+pgd_status check_latent_cache(int R, int P, int BS, int NB, long long page, long long token)
+{
+    pgd_status st;
+    if ((st = check_latent_dims(R, P)))
+        return st;
+    if (!supported_block_size(BS))
+        return fail(PGD_ERR_UNSUPPORTED, "block_size %d not in {8, 16, 32, 64, 128}", BS);
+    if (NB <= 0)
+        return fail(PGD_ERR_INVALID_ARG, "num_blocks %d <= 0", NB);
+    if (!stride_ok(page) || !stride_ok(token))
+        return fail(PGD_ERR_INVALID_ARG,
+                    "cache strides (%lld, %lld) must be positive multiples of 8 halves below 2^39",
+                    page, token);
+    if (token < R + P)
+        return fail(PGD_ERR_INVALID_ARG, "token stride %lld below latent_dim + rope_dim %d", token,
+                    R + P);
+    return PGD_OK;
+}
+
+// What paged_rope_write and paged_latent_write share: `p` is filled but for the
+// error word.
+pgd_status run_rope(RopeParams &p, void *stream)
+{
+    if (!std::isfinite(p.magnitude))
+        return fail(PGD_ERR_INVALID_ARG, "magnitude is not finite");
+    if (p.rows == 0) {
+        t_last_error.clear();
+        return PGD_OK;
+    }
+    if (!p.k_cache || !p.v_cache || !p.k_new || !p.v_new || !p.slots || !p.positions ||
+        !p.inv_freq || (p.Hq > 0 && (!p.q || !p.q_out)))
+        return fail(PGD_ERR_INVALID_ARG, "null array argument");
+    for (const void *a : {(const void *)p.k_cache, (const void *)p.v_cache, (const void *)p.k_new,
+                          (const void *)p.v_new, (const void *)p.q, (const void *)p.q_out})
+        if (!aligned(a, 16))
+            return fail(PGD_ERR_INVALID_ARG, "fp16 arrays must be 16-byte aligned");
+    if (!aligned(p.slots, 4) || !aligned(p.positions, 4) || !aligned(p.inv_freq, 4))
+        return fail(PGD_ERR_INVALID_ARG, "slots, positions and inv_freq must be 4-byte aligned");
+    p.in_place = p.Hq > 0 && p.q == p.q_out;
+    if (p.in_place && ((p.rows > 1 && p.q_token != p.qo_token) || (p.Hq > 1 && p.q_head != p.qo_head)))
+        return fail(PGD_ERR_INVALID_ARG, "q_out is q with other strides");
+    DeviceState *ds;
+    pgd_status st;
+    if ((st = device_state(&ds)))
+        return st;
+    p.err = ds->err_word;
+    const cudaError_t e = launch_rope_write(p, ds->num_sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "kernel launch");
+    t_last_error.clear();
+    return PGD_OK;
+}
+
+int log2_of(int x)
+{
+    int n = 0;
+    while ((1 << n) < x)
+        ++n;
+    return n;
+}
+
+pgd_status run_rope_frequencies(float *inv_freq, float *magnitude, int rot, double base, int scaling,
+                                double factor, double original_len, double beta_fast,
+                                double beta_slow)
+{
+    if (!inv_freq)
+        return fail(PGD_ERR_INVALID_ARG, "null array argument");
+    if (rot < 4 || rot % 2 != 0 || rot > 65536)
+        return fail(PGD_ERR_INVALID_ARG, "rotary_dim %d: an even number from 4 on", rot);
+    if (!(base > 1.0) || !std::isfinite(base))
+        return fail(PGD_ERR_INVALID_ARG, "base %g", base);
+    if (scaling < PGD_ROPE_PLAIN || scaling > PGD_ROPE_BY_PARTS)
+        return fail(PGD_ERR_INVALID_ARG, "scaling %d", scaling);
+    if (scaling != PGD_ROPE_PLAIN && !(factor >= 1.0 && std::isfinite(factor)))
+        return fail(PGD_ERR_INVALID_ARG, "factor %g: 1 or more", factor);
+    const int pairs = rot / 2;
+    double low = 0.0, high = 0.0;
+    if (scaling == PGD_ROPE_BY_PARTS) {
+        if (!(original_len > 0.0) || !(beta_slow > 0.0) || !(beta_fast > beta_slow) ||
+            !std::isfinite(original_len) || !std::isfinite(beta_fast))
+            return fail(PGD_ERR_INVALID_ARG, "original_len %g, beta_fast %g, beta_slow %g",
+                        original_len, beta_fast, beta_slow);
+        // the pair that turns `beta` times in original_len tokens
+        auto index = [&](double beta) {
+            return rot * std::log(original_len / (beta * 6.283185307179586)) / (2.0 * std::log(base));
+        };
+        low = std::max(std::floor(index(beta_fast)), 0.0);
+        high = std::min(std::ceil(index(beta_slow)), rot - 1.0);
+        if (high <= low)
+            high = low + 0.001;  // a step
+    }
+    if (scaling == PGD_ROPE_BASE)
+        base *= std::pow(factor, rot / (rot - 2.0));
+    for (int i = 0; i < pairs; ++i) {
+        double f = std::pow(base, -2.0 * i / rot);
+        if (scaling == PGD_ROPE_LINEAR)
+            f /= factor;
+        if (scaling == PGD_ROPE_BY_PARTS) {
+            const double shrunk = std::min(std::max((i - low) / (high - low), 0.0), 1.0);
+            f = f / factor * shrunk + f * (1.0 - shrunk);
+        }
+        inv_freq[i] = (float)f;
+    }
+    if (magnitude)
+        *magnitude = scaling == PGD_ROPE_BY_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+    t_last_error.clear();
+    return PGD_OK;
+}
+
+struct LatentPlan {
+    size_t ws_bytes;
+};
+
+pgd_status make_latent_plan(int S, int total_q, int max_q, int H, int R, int P, int BS, int MB,
+                            LatentPlan *lp)
+{
+    if (S < 0 || total_q < 0 || max_q < 0 || (total_q > 0 && max_q < 1))
+        return fail(PGD_ERR_INVALID_ARG, "num_seqs %d, total_q %d, max_q_len %d", S, total_q, max_q);
+    if (H <= 0)
+        return fail(PGD_ERR_INVALID_ARG, "num_heads %d", H);
+    if (H > 65536)
+        return fail(PGD_ERR_UNSUPPORTED, "num_heads %d above 65536", H);
+    pgd_status st;
+    if ((st = check_latent_dims(R, P)))
+        return st;
+    if (!supported_block_size(BS))
+        return fail(PGD_ERR_UNSUPPORTED, "block_size %d not in {8, 16, 32, 64, 128}", BS);
+    if (MB <= 0)
+        return fail(PGD_ERR_INVALID_ARG, "max_blocks_per_seq %d <= 0", MB);
+    if ((long long)MB * BS > (1ll << 30))
+        return fail(PGD_ERR_UNSUPPORTED, "length bound %lld above 2^30", (long long)MB * BS);
+    lp->ws_bytes = 0;
+    return PGD_OK;
+}
+
+struct LatentStrides {
+    long long page, token, q_token, q_head, qr_token, qr_head;
+};
+
+pgd_status run_latent(void *out, bool half, const uint16_t *q, const uint16_t *q_rope,
+                      const int32_t *cu_q, const uint16_t *cache, const int32_t *block_tables,
+                      const int32_t *seq_lens, float scale, int S, int total_q, int max_q, int H,
+                      int R, int P, int BS, int MB, int NB, const LatentStrides &x, void *workspace,
+                      size_t ws_bytes, void *stream_v)
+{
+    pgd_status st;
+    if ((st = check_latent_cache(R, P, BS, NB, x.page, x.token)) ||
+        (st = check_row_strides({x.q_token, x.q_head, x.qr_token, x.qr_head})))
+        return st;
+    if (!std::isfinite(scale))
+        return fail(PGD_ERR_INVALID_ARG, "scale is not finite");
+    if (!cu_q && total_q != S)
+        return fail(PGD_ERR_INVALID_ARG, "total_q %d for %d sequences of one row", total_q, S);
+    if (!cu_q)
+        max_q = 1;
+    LatentPlan lp;
+    if ((st = make_latent_plan(S, total_q, max_q, H, R, P, BS, MB, &lp)))
+        return st;
+    if (S == 0 || total_q == 0) {
+        t_last_error.clear();
+        return PGD_OK;
+    }
+    if (!out || !q || !q_rope || !cache || !block_tables || !seq_lens)
+        return fail(PGD_ERR_INVALID_ARG, "null array argument");
+    if (!aligned(q, 16) || !aligned(q_rope, 16) || !aligned(cache, 16) || !aligned(out, 16))
+        return fail(PGD_ERR_INVALID_ARG, "q, q_rope, cache and out must be 16-byte aligned");
+    if (!aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4))
+        return fail(PGD_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+    if (workspace && (ws_bytes < lp.ws_bytes || !aligned(workspace, 256)))
+        return fail(PGD_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) given, %zu needed",
+                    ws_bytes, lp.ws_bytes);
+    DeviceState *ds;
+    if ((st = device_state(&ds)))
+        return st;
+    LatentParams p = {};
+    p.out = out;
+    p.out_half = half;
+    p.q = reinterpret_cast<const __half *>(q);
+    p.q_rope = reinterpret_cast<const __half *>(q_rope);
+    p.cache = reinterpret_cast<const __half *>(cache);
+    p.q_token = x.q_token;
+    p.q_head = x.q_head;
+    p.qr_token = x.qr_token;
+    p.qr_head = x.qr_head;
+    p.page_stride = x.page;
+    p.token_stride = x.token;
+    p.cu_q = cu_q;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.err = ds->err_word;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.S = S;
+    p.total_q = total_q;
+    p.max_q = max_q;
+    p.H = H;
+    p.R = R;
+    p.P = P;
+    p.MB = MB;
+    p.NB = NB;
+    p.BS = BS;
+    p.log2BS = 3 + bs_index(BS);
+    const cudaError_t e = launch_latent(p, static_cast<cudaStream_t>(stream_v));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "kernel launch");
+    t_last_error.clear();
+    return PGD_OK;
+}
+
+struct LatentPrefillPlan {
+    size_t ws_bytes;
+};
+
+pgd_status make_latent_prefill_plan(int S, int total, int H, int D, int P, LatentPrefillPlan *pp)
+{
+    if (S < 0 || total < 0)
+        return fail(PGD_ERR_INVALID_ARG, "num_seqs %d, total %d", S, total);
+    if (H <= 0)
+        return fail(PGD_ERR_INVALID_ARG, "num_heads %d", H);
+    if (H > 65536)
+        return fail(PGD_ERR_UNSUPPORTED, "num_heads %d above 65536", H);
+    if (D != 64 && D != 128)
+        return fail(PGD_ERR_UNSUPPORTED, "head_dim %d not in {64, 128}", D);
+    if (P != 32 && P != 64)
+        return fail(PGD_ERR_UNSUPPORTED, "rope_dim %d not in {32, 64}", P);
+    pp->ws_bytes = 0;
+    return PGD_OK;
+}
+
+struct ExpandedStrides {
+    long long q_token, q_head, k_token, k_head, kr_token, v_token, v_head;
+};
+
+pgd_status run_latent_prefill(float *out, uint16_t *out_half, const uint16_t *q, const uint16_t *k,
+                              const uint16_t *k_rope, const uint16_t *v, const int32_t *cu_seqlens,
+                              float scale, int S, int total, int max_len, int H, int D, int P,
+                              const ExpandedStrides &x, void *workspace, size_t ws_bytes,
+                              void *stream_v)
+{
+    LatentPrefillPlan pp;
+    pgd_status st = make_latent_prefill_plan(S, total, H, D, P, &pp);
+    if (st)
+        return st;
+    if (max_len < 0)
+        return fail(PGD_ERR_INVALID_ARG, "max_len %d < 0", max_len);
+    if ((st = check_row_strides({x.q_token, x.q_head, x.k_token, x.k_head, x.kr_token, x.v_token,
+                                 x.v_head})))
+        return st;
+    if (!std::isfinite(scale))
+        return fail(PGD_ERR_INVALID_ARG, "scale is not finite");
+    if (S == 0 || total == 0) {
+        t_last_error.clear();
+        return PGD_OK;
+    }
+    const void *dst = out_half ? static_cast<const void *>(out_half) : out;
+    if (!dst || !q || !k || !k_rope || !v || !cu_seqlens)
+        return fail(PGD_ERR_INVALID_ARG, "null array argument");
+    for (const void *a : {dst, (const void *)q, (const void *)k, (const void *)k_rope, (const void *)v})
+        if (!aligned(a, 16))
+            return fail(PGD_ERR_INVALID_ARG, "out, q, k, k_rope and v must be 16-byte aligned");
+    if (!aligned(cu_seqlens, 4))
+        return fail(PGD_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
+    if (workspace && (ws_bytes < pp.ws_bytes || !aligned(workspace, 256)))
+        return fail(PGD_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) given, %zu needed",
+                    ws_bytes, pp.ws_bytes);
+    DeviceState *ds;
+    if ((st = device_state(&ds)))
+        return st;
+    LatentPrefillParams p = {};
+    p.out = out;
+    p.out_half = reinterpret_cast<__half *>(out_half);
+    p.q = reinterpret_cast<const __half *>(q);
+    p.k = reinterpret_cast<const __half *>(k);
+    p.k_rope = reinterpret_cast<const __half *>(k_rope);
+    p.v = reinterpret_cast<const __half *>(v);
+    p.q_token = x.q_token;
+    p.q_head = x.q_head;
+    p.k_token = x.k_token;
+    p.k_head = x.k_head;
+    p.kr_token = x.kr_token;
+    p.v_token = x.v_token;
+    p.v_head = x.v_head;
+    p.cu_seqlens = cu_seqlens;
+    p.err = ds->err_word;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.S = S;
+    p.total = total;
+    p.max_len = max_len;
+    p.H = H;
+    p.D = D;
+    p.P = P;
+    const cudaError_t e = launch_latent_prefill(p, static_cast<cudaStream_t>(stream_v));
+    if (e != cudaSuccess)
+        return cuda_fail(e, "kernel launch");
+    t_last_error.clear();
+    return PGD_OK;
+}
+
 // Runs a C entry's body: nothing it throws (an allocation of the host's that
 // failed) leaves the library.
 template <class F> pgd_status guarded(F &&body) noexcept
@@ -2284,6 +2603,218 @@ pgd_status paged_kv_write_strided(uint16_t *k_cache, uint16_t *v_cache, const ui
     });
 }
 
+pgd_status paged_rope_write(uint16_t *k_cache, uint16_t *v_cache, uint16_t *q_out,
+                            const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new,
+                            const int32_t *slots, const int32_t *positions,
+                            const float *inv_freq, float magnitude, int interleaved, int num_rows,
+                            int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                            int block_size, int num_blocks, int64_t page_stride,
+                            int64_t head_stride, int64_t token_stride, int64_t q_out_token_stride,
+                            int64_t q_out_head_stride, int64_t q_token_stride,
+                            int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                            int64_t v_token_stride, int64_t v_head_stride, void *stream)
+{
+    return guarded([&]() -> pgd_status {
+        if (num_rows < 0 || num_q_heads < 0 || num_kv_heads <= 0 || num_blocks <= 0)
+            return fail(PGD_ERR_INVALID_ARG,
+                        "num_rows %d, num_q_heads %d, num_kv_heads %d, num_blocks %d", num_rows,
+                        num_q_heads, num_kv_heads, num_blocks);
+        if (!supported_head_dim(head_dim))
+            return fail(PGD_ERR_UNSUPPORTED, "head_dim %d not in {64, 128, 256}", head_dim);
+        if (!supported_block_size(block_size))
+            return fail(PGD_ERR_UNSUPPORTED, "block_size %d not in {8, 16, 32, 64, 128}",
+                        block_size);
+        if (num_q_heads > 65536 || num_kv_heads > 65536)
+            return fail(PGD_ERR_UNSUPPORTED, "head counts %d / %d above 65536", num_q_heads,
+                        num_kv_heads);
+        if (rotary_dim <= 0 || rotary_dim % 16 != 0 || rotary_dim > head_dim)
+            return fail(PGD_ERR_INVALID_ARG, "rotary_dim %d: a multiple of 16 up to head_dim %d",
+                        rotary_dim, head_dim);
+        pgd_status st;
+        if ((st = check_strides(Strides{page_stride, head_stride, token_stride}, head_dim)) ||
+            (st = check_row_strides({k_token_stride, k_head_stride, v_token_stride,
+                                     v_head_stride})) ||
+            (num_q_heads && (st = check_row_strides({q_out_token_stride, q_out_head_stride,
+                                                     q_token_stride, q_head_stride}))))
+            return st;
+        RopeParams p = {};
+        p.k_cache = k_cache;
+        p.v_cache = v_cache;
+        p.q_out = q_out;
+        p.q = q;
+        p.k_new = k_new;
+        p.v_new = v_new;
+        p.slots = slots;
+        p.positions = positions;
+        p.inv_freq = inv_freq;
+        p.magnitude = magnitude;
+        p.interleaved = interleaved != 0;
+        p.rows = num_rows;
+        p.Hq = num_q_heads;
+        p.Hkv = num_kv_heads;
+        p.rot = rotary_dim;
+        p.log2BS = 3 + bs_index(block_size);
+        p.NB = num_blocks;
+        p.log2q = p.log2k = p.log2v = log2_of(head_dim / 16);
+        p.page_stride = page_stride;
+        p.head_stride = head_stride;
+        p.token_stride = token_stride;
+        p.qo_token = q_out_token_stride;
+        p.qo_head = q_out_head_stride;
+        p.q_token = q_token_stride;
+        p.q_head = q_head_stride;
+        p.k_token = k_token_stride;
+        p.k_head = k_head_stride;
+        p.v_token = v_token_stride;
+        p.v_head = v_head_stride;
+        return run_rope(p, stream);
+    });
+}
+
+pgd_status pgd_rope_frequencies(float *inv_freq, float *magnitude, int rotary_dim, double base,
+                                int scaling, double factor, double original_len, double beta_fast,
+                                double beta_slow)
+{
+    return guarded([&]() -> pgd_status {
+        return run_rope_frequencies(inv_freq, magnitude, rotary_dim, base, scaling, factor,
+                                    original_len, beta_fast, beta_slow);
+    });
+}
+
+pgd_status paged_latent_write(uint16_t *cache, uint16_t *q_out, const uint16_t *q_rope,
+                              const uint16_t *latent, const uint16_t *k_rope,
+                              const int32_t *slots, const int32_t *positions,
+                              const float *inv_freq, float magnitude, int interleaved,
+                              int num_rows, int num_heads, int latent_dim, int rope_dim,
+                              int block_size, int num_blocks, int64_t page_stride,
+                              int64_t token_stride, int64_t q_out_token_stride,
+                              int64_t q_out_head_stride, int64_t q_token_stride,
+                              int64_t q_head_stride, int64_t latent_token_stride,
+                              int64_t k_rope_token_stride, void *stream)
+{
+    return guarded([&]() -> pgd_status {
+        if (num_rows < 0 || num_heads < 0)
+            return fail(PGD_ERR_INVALID_ARG, "num_rows %d, num_heads %d", num_rows, num_heads);
+        if (num_heads > 65536)
+            return fail(PGD_ERR_UNSUPPORTED, "num_heads %d above 65536", num_heads);
+        pgd_status st;
+        if ((st = check_latent_cache(latent_dim, rope_dim, block_size, num_blocks, page_stride,
+                                     token_stride)) ||
+            (st = check_row_strides({latent_token_stride, k_rope_token_stride})) ||
+            (num_heads && (st = check_row_strides({q_out_token_stride, q_out_head_stride,
+                                                   q_token_stride, q_head_stride}))))
+            return st;
+        // one head of keys, rope_dim wide, and one of "values", latent_dim wide
+        RopeParams p = {};
+        p.k_cache = cache ? cache + latent_dim : nullptr;
+        p.v_cache = cache;
+        p.q_out = q_out;
+        p.q = q_rope;
+        p.k_new = k_rope;
+        p.v_new = latent;
+        p.slots = slots;
+        p.positions = positions;
+        p.inv_freq = inv_freq;
+        p.magnitude = magnitude;
+        p.interleaved = interleaved != 0;
+        p.rows = num_rows;
+        p.Hq = num_heads;
+        p.Hkv = 1;
+        p.rot = rope_dim;
+        p.log2BS = 3 + bs_index(block_size);
+        p.NB = num_blocks;
+        p.log2q = p.log2k = log2_of(rope_dim / 16);
+        p.log2v = log2_of(latent_dim / 16);
+        p.page_stride = page_stride;
+        p.token_stride = token_stride;
+        p.qo_token = q_out_token_stride;
+        p.qo_head = q_out_head_stride;
+        p.q_token = q_token_stride;
+        p.q_head = q_head_stride;
+        p.k_token = k_rope_token_stride;
+        p.v_token = latent_token_stride;
+        return run_rope(p, stream);
+    });
+}
+
+pgd_status paged_latent_attention(void *out, int out_type, const uint16_t *q,
+                                  const uint16_t *q_rope, const int32_t *cu_seqlens_q,
+                                  const uint16_t *cache, const int32_t *block_tables,
+                                  const int32_t *seq_lens, float scale, int num_seqs, int total_q,
+                                  int max_q_len, int num_heads, int latent_dim, int rope_dim,
+                                  int block_size, int max_blocks_per_seq, int num_blocks,
+                                  int64_t page_stride, int64_t token_stride,
+                                  int64_t q_token_stride, int64_t q_head_stride,
+                                  int64_t q_rope_token_stride, int64_t q_rope_head_stride,
+                                  void *workspace, size_t workspace_bytes, void *stream)
+{
+    return guarded([&]() -> pgd_status {
+        if (out_type != PGD_OUT_F32 && out_type != PGD_OUT_F16)
+            return fail(PGD_ERR_INVALID_ARG, "out_type %d: PGD_OUT_F32 or PGD_OUT_F16", out_type);
+        return run_latent(out, out_type == PGD_OUT_F16, q, q_rope, cu_seqlens_q, cache,
+                          block_tables, seq_lens, scale, num_seqs, total_q, max_q_len, num_heads,
+                          latent_dim, rope_dim, block_size, max_blocks_per_seq, num_blocks,
+                          {page_stride, token_stride, q_token_stride, q_head_stride,
+                           q_rope_token_stride, q_rope_head_stride},
+                          workspace, workspace_bytes, stream);
+    });
+}
+
+pgd_status pgd_latent_plan(int num_seqs, int total_q, int max_q_len, int num_heads,
+                           int latent_dim, int rope_dim, int block_size, int max_blocks_per_seq,
+                           size_t *workspace_bytes)
+{
+    return guarded([&]() -> pgd_status {
+        LatentPlan lp;
+        const pgd_status st = make_latent_plan(num_seqs, total_q, max_q_len, num_heads, latent_dim,
+                                               rope_dim, block_size, max_blocks_per_seq, &lp);
+        if (st)
+            return st;
+        if (workspace_bytes)
+            *workspace_bytes = lp.ws_bytes;
+        return PGD_OK;
+    });
+}
+
+pgd_status packed_latent_prefill(void *out, int out_type, const uint16_t *q, const uint16_t *k,
+                                 const uint16_t *k_rope, const uint16_t *v,
+                                 const int32_t *cu_seqlens, float scale, int num_seqs, int total,
+                                 int max_len, int num_heads, int head_dim, int rope_dim,
+                                 int64_t q_token_stride, int64_t q_head_stride,
+                                 int64_t k_token_stride, int64_t k_head_stride,
+                                 int64_t k_rope_token_stride, int64_t v_token_stride,
+                                 int64_t v_head_stride, void *workspace, size_t workspace_bytes,
+                                 void *stream)
+{
+    return guarded([&]() -> pgd_status {
+        if (out_type != PGD_OUT_F32 && out_type != PGD_OUT_F16)
+            return fail(PGD_ERR_INVALID_ARG, "out_type %d: PGD_OUT_F32 or PGD_OUT_F16", out_type);
+        const bool half = out_type == PGD_OUT_F16;
+        return run_latent_prefill(half ? nullptr : static_cast<float *>(out),
+                                  half ? static_cast<uint16_t *>(out) : nullptr, q, k, k_rope, v,
+                                  cu_seqlens, scale, num_seqs, total, max_len, num_heads, head_dim,
+                                  rope_dim,
+                                  {q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+                                   k_rope_token_stride, v_token_stride, v_head_stride},
+                                  workspace, workspace_bytes, stream);
+    });
+}
+
+pgd_status pgd_latent_prefill_plan(int num_seqs, int total, int num_heads, int head_dim,
+                                   int rope_dim, size_t *workspace_bytes)
+{
+    return guarded([&]() -> pgd_status {
+        LatentPrefillPlan pp;
+        const pgd_status st =
+            make_latent_prefill_plan(num_seqs, total, num_heads, head_dim, rope_dim, &pp);
+        if (st)
+            return st;
+        if (workspace_bytes)
+            *workspace_bytes = pp.ws_bytes;
+        return PGD_OK;
+    });
+}
+
 pgd_status pgd_plan(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                     int block_size, int partition_size, int max_blocks_per_seq,
                     int *chosen_partition_size, size_t *workspace_bytes)
@@ -2443,6 +2974,6 @@ pgd_status pgd_device_info(int head_dim, int block_size, int *num_sms, int *ctas
     return PGD_OK;
 }
 
-int pgd_version(void) { return 10501; }
+int pgd_version(void) { return 10600; }
 
 }  // extern "C"

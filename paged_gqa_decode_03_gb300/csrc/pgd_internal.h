@@ -379,6 +379,53 @@ struct WriteParams {
 };
 cudaError_t launch_kv_write(WriteParams p, cudaStream_t stream);
 
+// ---------------------------------------------------------------- rotary positions
+// The step's rows rotated and written (pgd_rope.cu): queries into q_out, keys and
+// values into their pages.  A latent cache's rows are keys and "values" of one head.
+struct RopeParams {
+    uint16_t *k_cache, *v_cache, *q_out;
+    const uint16_t *q, *k_new, *v_new;
+    const int32_t *slots, *positions;     // [rows]
+    const float *inv_freq;                // [rot / 2]
+    unsigned *err;
+    float magnitude;
+    bool interleaved, in_place;           // in_place: q_out is q
+    int rows, Hq, Hkv, rot, log2BS, NB;
+    int log2q, log2k, log2v;              // of a head's 32-byte items (values / 16)
+    int rows_per_cta;                     // set by the launcher
+    long long page_stride, head_stride, token_stride;   // halves
+    long long qo_token, qo_head, q_token, q_head, k_token, k_head, v_token, v_head;
+};
+cudaError_t launch_rope_write(RopeParams p, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- latent caches
+// Attention over one latent vector a token (pgd_latent.cu).
+struct LatentParams {
+    void *out;                    // [total_q][H][R], fp16 (out_half) or fp32
+    bool out_half;
+    const __half *q, *q_rope, *cache;
+    long long q_token, q_head, qr_token, qr_head, page_stride, token_stride;
+    const int32_t *cu_q;          // [S + 1], or null: one row a sequence
+    const int32_t *block_tables;  // [S][MB]
+    const int32_t *seq_lens;      // [S]
+    unsigned *err;
+    float scale_log2;
+    int S, total_q, max_q, H, R, P, MB, NB, BS, log2BS;
+};
+cudaError_t launch_latent(const LatentParams &p, cudaStream_t stream);
+
+struct LatentPrefillParams {
+    float *out;                   // [total][H][D], or null with
+    __half *out_half;             //   out_half, the output as fp16
+    const __half *q, *k, *k_rope, *v;
+    long long q_token, q_head, k_token, k_head, kr_token, v_token, v_head;
+    const int32_t *cu_seqlens;    // [S + 1]
+    unsigned *err;
+    float scale_log2;
+    int S, total, max_len, H, D, P;
+};
+cudaError_t launch_latent_prefill(const LatentPrefillParams &p, cudaStream_t stream);
+
 // Quantiser of rows into quantised pages (pgd_quantize.cu).
 cudaError_t launch_quantize(int head_dim, uint8_t *codes, uint16_t *meta, const uint16_t *src,
                             const int32_t *slots, int rows, int Hkv, int BS, int NB,
