@@ -65,6 +65,7 @@ struct DeviceState {
     // them or fails with them
     std::atomic<int> tree_runs[3][2] = {};       // [head_dim][pairs]: resident runs, 0: not set up
     std::atomic<bool> prefill_ready[3] = {};     // [head_dim]
+    std::atomic<int> latent_runs[3] = {};        // [latent_dim 128/256/512]: resident pairs
     unsigned *err_word = nullptr;   // address of g_device_error on this device
     std::mutex pool_mu;             // the pool is made on first library-owned scratch
     cudaMemPool_t pool = nullptr;   //   (and again after pgd_release): stream-ordered scratch
@@ -186,6 +187,18 @@ pgd_status prefill_ready(DeviceState &st, int D)
     const pgd_status s = set_up("set-up of the prompt kernel", [&] { return prefill_set_up(D); });
     if (!s)
         known.store(true, std::memory_order_release);
+    return s;
+}
+
+pgd_status latent_runs(DeviceState &st, int R, int *runs)
+{
+    std::atomic<int> &known = st.latent_runs[R == 128 ? 0 : R == 256 ? 1 : 2];
+    if ((*runs = known.load(std::memory_order_acquire)) > 0)
+        return PGD_OK;
+    const pgd_status s =
+        set_up("set-up of the latent kernel", [&] { return latent_resident(R, runs); });
+    if (!s)
+        known.store(*runs, std::memory_order_release);
     return s;
 }
 
@@ -2002,7 +2015,8 @@ pgd_status run_rope_frequencies(float *inv_freq, float *magnitude, int rot, doub
 }
 
 struct LatentPlan {
-    size_t ws_bytes;
+    int hb, TQ, HB, runs;
+    size_t ws_bytes, off_ml, off_cut;  // pieces' outputs, (maximum, exp-sum)s, cuts
 };
 
 pgd_status make_latent_plan(int S, int total_q, int max_q, int H, int R, int P, int BS, int MB,
@@ -2023,7 +2037,84 @@ pgd_status make_latent_plan(int S, int total_q, int max_q, int H, int R, int P, 
         return fail(PGD_ERR_INVALID_ARG, "max_blocks_per_seq %d <= 0", MB);
     if ((long long)MB * BS > (1ll << 30))
         return fail(PGD_ERR_UNSUPPORTED, "length bound %lld above 2^30", (long long)MB * BS);
-    lp->ws_bytes = 0;
+    DeviceState *ds;
+    if ((st = device_state(&ds)))
+        return st;
+    int resident;
+    if ((st = latent_runs(*ds, R, &resident)))
+        return st;
+    if (resident < 1)
+        return fail(PGD_ERR_UNSUPPORTED, "the latent kernel does not fit on this device");
+    lp->hb = std::min(H, kLatentRows);
+    lp->HB = (H + kLatentRows - 1) / kLatentRows;
+    lp->TQ = H <= kLatentRows ? kLatentRows / H : 1;
+    const int most_q = std::min(max_q, total_q);
+    const long long halves = lp->HB == 1 ? (most_q + lp->TQ - 1) / lp->TQ : (long long)most_q * lp->HB;
+    const long long stages = (long long)S * ((halves + 1) / 2) *
+                             (((long long)MB * BS + kLatentNT - 1) / kLatentNT);
+    // (the kernel counts stages, and two more per unit, in 32-bit integers)
+    if (3 * stages >= (1ll << 31))
+        return fail(PGD_ERR_UNSUPPORTED, "batch of %d rows x %d heads x %lld tokens too large", total_q,
+                    H, (long long)MB * BS);
+    lp->runs = (int)std::max(1ll, std::min<long long>(resident, stages));
+    const size_t rows = (size_t)2 * lp->runs * 2 * kLatentRows;
+    lp->off_ml = align256(rows * R * 4);
+    lp->off_cut = lp->off_ml + align256(rows * 8);
+    lp->ws_bytes = S && total_q ? lp->off_cut + align256((size_t)lp->runs * 16) : 0;
+    return PGD_OK;
+}
+
+// The five views of a call: the queries' two parts [tokens][heads][64-wide slabs], a
+// box being one slab of a half tile's rows; the cache's pages by groups of 8 rows
+// (as encode_cache_map_groups), its latent part for K and V in copies of their own,
+// its rotary keys.  Where rope_dim is 32 the slab's other half reads as zeros.
+struct LatentViews {
+    const void *q, *q_rope, *cache;
+    long long q_token, q_head, qr_token, qr_head, page, token;
+    int total_q, H, R, P, NB, BS, hb, TQ, k_slabs, k_rows, v_slabs, v_rows;
+};
+
+pgd_status encode_view(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+                       const cuuint64_t *strides, const cuuint32_t *box)
+{
+    EncodeTiledFn fn;
+    pgd_status st = encode_fn(&fn);
+    if (st)
+        return st;
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void *>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(PGD_ERR_CUDA, "cuTensorMapEncodeTiled (latent rows) failed (CUresult %d)", (int)r);
+    return PGD_OK;
+}
+
+pgd_status encode_latent_maps(const LatentViews &v, LatentMaps *m)
+{
+    using u64 = cuuint64_t;
+    using u32 = cuuint32_t;
+    const u64 T = (u64)v.total_q, H = (u64)v.H, slabs = (u64)v.R / 64, groups = (u64)v.BS / 8,
+              NB = (u64)v.NB;
+    const u64 tok = (u64)v.token * 2, page = (u64)v.page * 2;
+    const u64 q_dims[4] = {64, H, T, slabs}, q_str[3] = {(u64)v.q_head * 2, (u64)v.q_token * 2, 128};
+    const u64 r_dims[4] = {(u64)v.P, H, T, 1},
+              r_str[3] = {(u64)v.qr_head * 2, (u64)v.qr_token * 2, 128};
+    const u32 q_box[4] = {64, (u32)v.hb, (u32)v.TQ, 1};
+    const u64 c_dims[5] = {64, 8, slabs, groups, NB}, c_str[4] = {tok, 128, tok * 8, page};
+    const u32 k_box[5] = {64, 8, (u32)v.k_slabs, (u32)v.k_rows / 8, 1};
+    const u32 v_box[5] = {64, 8, (u32)v.v_slabs, (u32)v.v_rows / 8, 1};
+    const u64 kr_dims[4] = {(u64)v.P, 8, groups, NB}, kr_str[3] = {tok, tok * 8, page};
+    const u32 kr_box[4] = {64, 8, (u32)v.k_rows / 8, 1};
+    pgd_status st;
+    if ((st = encode_view(&m->q, v.q, 4, q_dims, q_str, q_box)) ||
+        (st = encode_view(&m->qr, v.q_rope, 4, r_dims, r_str, q_box)) ||
+        (st = encode_view(&m->k, v.cache, 5, c_dims, c_str, k_box)) ||
+        (st = encode_view(&m->v, v.cache, 5, c_dims, c_str, v_box)) ||
+        (st = encode_view(&m->kr, static_cast<const uint16_t *>(v.cache) + v.R, 4, kr_dims, kr_str,
+                          kr_box)))
+        return st;
     return PGD_OK;
 }
 
@@ -2060,27 +2151,42 @@ pgd_status run_latent(void *out, bool half, const uint16_t *q, const uint16_t *q
         return fail(PGD_ERR_INVALID_ARG, "q, q_rope, cache and out must be 16-byte aligned");
     if (!aligned(cu_q, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4))
         return fail(PGD_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
-    if (workspace && (ws_bytes < lp.ws_bytes || !aligned(workspace, 256)))
+    char *ws = static_cast<char *>(workspace);
+    const bool own = workspace == nullptr;
+    if (!own && (ws_bytes < lp.ws_bytes || !aligned(ws, 256)))
         return fail(PGD_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) given, %zu needed",
                     ws_bytes, lp.ws_bytes);
     DeviceState *ds;
     if ((st = device_state(&ds)))
         return st;
+    const int v_keys = 128 / (R / 128);  // of a piece (LatentShape)
+    const LatentViews views = {q,        q_rope,     cache,      x.q_token, x.q_head, x.qr_token,
+                               x.qr_head, x.page,    x.token,    total_q,   H,        R,
+                               P,        NB,         BS,         lp.hb,     lp.TQ,    2,
+                               std::min(BS, kLatentRows), R / 128, std::min(BS, v_keys)};
+    LatentMaps maps;
+    if ((st = encode_latent_maps(views, &maps)))
+        return st;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    cudaError_t e;
+    if (own) {
+        cudaMemPool_t pool;
+        if ((st = device_pool(*ds, &pool)))
+            return st;
+        if ((e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), lp.ws_bytes, pool,
+                                         stream)) != cudaSuccess)
+            return cuda_fail(e, "scratch allocation");
+    }
     LatentParams p = {};
     p.out = out;
     p.out_half = half;
-    p.q = reinterpret_cast<const __half *>(q);
-    p.q_rope = reinterpret_cast<const __half *>(q_rope);
-    p.cache = reinterpret_cast<const __half *>(cache);
-    p.q_token = x.q_token;
-    p.q_head = x.q_head;
-    p.qr_token = x.qr_token;
-    p.qr_head = x.qr_head;
-    p.page_stride = x.page;
-    p.token_stride = x.token;
+    p.wide_rows = aligned(out, 32);
     p.cu_q = cu_q;
     p.block_tables = block_tables;
     p.seq_lens = seq_lens;
+    p.part_o = reinterpret_cast<float *>(ws);
+    p.part_ml = reinterpret_cast<float2 *>(ws + lp.off_ml);
+    p.cut = reinterpret_cast<int4 *>(ws + lp.off_cut);
     p.err = ds->err_word;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.S = S;
@@ -2088,12 +2194,23 @@ pgd_status run_latent(void *out, bool half, const uint16_t *q, const uint16_t *q
     p.max_q = max_q;
     p.H = H;
     p.R = R;
-    p.P = P;
     p.MB = MB;
     p.NB = NB;
     p.BS = BS;
     p.log2BS = 3 + bs_index(BS);
-    const cudaError_t e = launch_latent(p, static_cast<cudaStream_t>(stream_v));
+    p.hb = lp.hb;
+    p.TQ = lp.TQ;
+    p.HB = lp.HB;
+    p.k_rows = views.k_rows;
+    p.v_rows = views.v_rows;
+    p.runs = lp.runs;
+    p.wait_budget_ns = kWaitBudgetNs;
+    e = launch_latent(maps, p, stream);
+    if (own) {
+        const cudaError_t e2 = cudaFreeAsync(ws, stream);
+        if (e == cudaSuccess)
+            e = e2;
+    }
     if (e != cudaSuccess)
         return cuda_fail(e, "kernel launch");
     t_last_error.clear();

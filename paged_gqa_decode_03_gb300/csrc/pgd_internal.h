@@ -399,20 +399,51 @@ struct RopeParams {
 cudaError_t launch_rope_write(RopeParams p, int num_sms, cudaStream_t stream);
 
 // ---------------------------------------------------------------- latent caches
-// Attention over one latent vector a token (pgd_latent.cu).
+// Attention over a latent cache by pairs of CTAs (pgd_latent.cu).  A stage is kLatentNT
+// tokens; a CTA has kLatentRows rows of queries, copies half of a stage's tokens as
+// keys in KP pieces of KSLABS 64-wide slabs, and half of the values of all of them in
+// VP pieces of VKEYS tokens.  Every piece is kLatentPiece bytes; NK, NV pieces in the
+// rings, NS score buffers.
+constexpr int kLatentNT = 128, kLatentRows = 64, kLatentPiece = 16384;
+template <int R> struct LatentShape {
+    static constexpr int KSLABS = 2, KP = R / 128;
+    static constexpr int VSLABS = R / 128, VKEYS = 128 / VSLABS, VP = VSLABS;
+    static constexpr int NK = 4, NV = 4, NS = 4;
+};
+// Q with its rotary part, the weights, the rotary keys, the rings (what 227 KB leave
+// beside the static part at R 512)
+template <int R> constexpr size_t latent_smem_bytes()
+{
+    return size_t(R / 64 + 1) * kLatentRows * 128 + 2 * kLatentRows * 128 + kLatentRows * 128 +
+           size_t(LatentShape<R>::NK + LatentShape<R>::NV) * kLatentPiece;
+}
 struct LatentParams {
     void *out;                    // [total_q][H][R], fp16 (out_half) or fp32
-    bool out_half;
-    const __half *q, *q_rope, *cache;
-    long long q_token, q_head, qr_token, qr_head, page_stride, token_stride;
+    bool out_half, wide_rows;     // wide_rows: it starts on a 32-byte border
     const int32_t *cu_q;          // [S + 1], or null: one row a sequence
     const int32_t *block_tables;  // [S][MB]
     const int32_t *seq_lens;      // [S]
+    // scratch: the pieces of the units that are cut, two per run, of 64 rows in each
+    // CTA, and where the cut units begin
+    float *part_o;                // [2 * runs][2][64][R] sums of p c
+    float2 *part_ml;              // [2 * runs][2][64] (reference maximum, exp-sum)
+    int4 *cut;                    // [runs] {sequence or -1, tile, last run, -}
     unsigned *err;
     float scale_log2;
-    int S, total_q, max_q, H, R, P, MB, NB, BS, log2BS;
+    int S, total_q, max_q, H, R, MB, NB, BS, log2BS;
+    int hb, TQ, HB;               // a half tile: TQ tokens x hb heads; HB blocks of heads a token
+    int k_rows, v_rows;           // tokens of one page copy of K and of V
+    int runs;
+    uint64_t wait_budget_ns;
+    // half tiles of n query tokens
+    __host__ __device__ int half_tiles(int n) const { return HB == 1 ? (n + TQ - 1) / TQ : n * HB; }
 };
-cudaError_t launch_latent(const LatentParams &p, cudaStream_t stream);
+struct LatentMaps {
+    CUtensorMap q, qr, k, kr, v;
+};
+// Pairs that are resident at once on the current device; also the kernel's set-up there.
+cudaError_t latent_resident(int latent_dim, int *runs);
+cudaError_t launch_latent(const LatentMaps &m, const LatentParams &p, cudaStream_t stream);
 
 struct LatentPrefillParams {
     float *out;                   // [total][H][D], or null with

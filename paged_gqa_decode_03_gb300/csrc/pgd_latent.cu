@@ -1,161 +1,891 @@
-// Attention over one latent vector a token: the absorbed form over the pages of a
-// latent cache, and the expanded form over packed prompts.  A warp per query row
-// and head, one pass over the tokens with a running maximum and sum.
+// Attention over a latent cache, absorbed queries (paged_latent_attention), on the
+// 5th-generation tensor cores: every head reads the same rows, whose latent part is
+// key and value at once.
+//
+// For row r of the queries and cached token t, s_t = (q_r . c_t + q_rope_r . k_t)
+// scale log2(e); out_r = sum p_t c_t / sum p_t over the tokens that r sees, p_t =
+// exp2(s_t - m), in one pass with a running reference m and sum.
+//
+// A cached row of 2 (R + P) bytes serves all rows of its sequence with 2 (2 R + P)
+// operations each: at R 512, P 64 and 128 rows 242 operations a byte, just below what
+// the GPU has (284), so HBM bounds a decode step with up to 128 heads, if nothing
+// else does.  What decides the shape of the work:
+//   * Output: 128 rows x 512 fp32 would fill an SM's tensor memory and leave no room
+//     for scores, and the 128 x 576 queries take 147 KB of its shared memory.  So two
+//     CTAs (a pair of the tensor cores, cta_group::2, M 128) share a tile of 128 rows:
+//     64 rows of queries, weights and outputs in each.
+//   * A stage is 128 tokens.  Scores: each CTA copies 64 of them (all R + P values):
+//     B, split over the pair by tokens.  Outputs: each CTA copies all 128, of half of
+//     the R values: B, split by values.  That takes the latent part in twice, the
+//     second time from L2: every byte comes from HBM once, and an SM takes in from L2
+//     two to three times what HBM gives it (130 GB/s and more in copies of 32 KB).
+//   * A product takes 48 cycles at least: scores (N 128) 36 x 48, outputs (N 256, 64
+//     each, the full rate) 16 x 64, 2752 cycles a stage at R 512, against 3150 in
+//     which HBM brings its 147 KB.  Fewer rows cost the same; HBM still bounds.
+//   * The stages of all units (sequence, tile of rows) are cut into equal runs, one
+//     per resident pair, whatever the lengths; a unit that is cut leaves pieces
+//     (reference maximum, exp-sum, unscaled output; two per run at most), which a
+//     second kernel joins.  Rings run on from unit to unit.
+//   * Weights go to shared memory as fp16 (an A operand of M 128 over a pair would
+//     have to lie twice in tensor memory).  Four score buffers: the scores run ahead of
+//     the softmax, so the one place for weights, free again when its product is over,
+//     does not hold them up.
 #include "pgd_device.cuh"
 #include "pgd_internal.h"
+#include "pgd_rows.cuh"
 
 namespace pgd {
 
-__device__ __forceinline__ float warp_sum(float x)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        x += __shfl_xor_sync(~0u, x, o);
-    return x;
-}
+namespace {
 
-__global__ void __launch_bounds__(128) paged_latent_kernel(const LatentParams p)
+// warp 0 Q, K and rotary-key copies, 1 V copies, 2 scores, 3 outputs, 4-11 softmax
+constexpr int kLatentThreads = 384;
+constexpr uint32_t kLatentNegateA = 1u << 13;  // of the products' descriptor: -A for A
+
+// What a sequence asks for: its length, first query row, rows (0 where its numbers do
+// not fit together), stages per unit and units (tiles of two half tiles).
+struct LatentSeq {
+    int L, row0, n, T, tiles;
+    unsigned bad;
+};
+
+__device__ __forceinline__ LatentSeq latent_seq(const LatentParams &p, int s)
 {
-    const int lane = threadIdx.x & 31;
-    const int h = blockIdx.y * 4 + (threadIdx.x >> 5), s = blockIdx.x, i = blockIdx.z;
-    if (h >= p.H)
-        return;
+    LatentSeq q;
     const int maxlen = p.MB << p.log2BS;
-    const int L = __ldg(p.seq_lens + s);
-    const int row0 = p.cu_q ? __ldg(p.cu_q + s) : s, n = p.cu_q ? __ldg(p.cu_q + s + 1) - row0 : 1;
-    unsigned bad = 0;
-    if (L < 0 || L > maxlen)
-        bad = kErrSeqLen;
-    else if (n < 0 || n > (p.cu_q ? L : 1) || n > p.max_q || row0 < 0 || row0 > p.total_q - n)
-        bad = kErrQueryLen;
-    if (bad) {
-        if (i == 0 && h == 0 && lane == 0)
-            atomicOr(p.err, bad);
-        return;
+    q.L = __ldg(p.seq_lens + s);
+    q.row0 = p.cu_q ? __ldg(p.cu_q + s) : s;
+    q.n = p.cu_q ? __ldg(p.cu_q + s + 1) - q.row0 : 1;
+    q.bad = 0;
+    if (q.L < 0 || q.L > maxlen)
+        q.bad = kErrSeqLen;
+    else if (q.n < 0 || q.n > (p.cu_q ? q.L : 1) || q.n > p.max_q || q.row0 < 0 ||
+             q.row0 > p.total_q - q.n)
+        q.bad = kErrQueryLen;
+    if (q.bad)
+        q.n = 0;
+    // (a row of a sequence without tokens: one stage, in which it sees nothing)
+    q.T = q.n ? max(1, (q.L + kLatentNT - 1) / kLatentNT) : 0;
+    q.tiles = (p.half_tiles(q.n) + 1) / 2;
+    return q;
+}
+// What a unit counts in the division of the work: its stages and, in stages, its
+// start and end.
+constexpr int kLatentUnitCost = 2;
+__device__ __forceinline__ int latent_cost(const LatentSeq &q)
+{
+    return q.tiles * (q.T + kLatentUnitCost);
+}
+
+// A run [x0, x1) of the cost of all units, a unit (or the part of it that the run
+// holds) at a time: stage t of a unit that begins at cost c lies at c +
+// kLatentUnitCost + t.  Every role walks its own copy.
+struct LatentWalk {
+    LatentSeq q;
+    int s, v, t, t_end;  // sequence, its tile, stages [t, t_end)
+    int at, x1;          // where unit v begins, and the run's end
+
+    __device__ __forceinline__ LatentWalk(const LatentParams &p, int s0, int begin, int x0, int x1_)
+    {
+        s = s0;
+        x1 = at = x1_;
+        v = t = t_end = 0;
+        if (x0 >= x1)
+            return;
+        q = latent_seq(p, s);
+        v = (x0 - begin) / (q.T + kLatentUnitCost);
+        at = begin + v * (q.T + kLatentUnitCost);
+        t = max(0, x0 - at - kLatentUnitCost);
+        set_end();
     }
-    if (i >= n)
-        return;
-    const int row = row0 + i, end = p.cu_q ? L - n + i + 1 : L;
-    float q[16], qr[2], o[16];
-    for (int k = 0; k < 16; ++k) {
-        const int d = lane + 32 * k;
-        q[k] = d < p.R ? __half2float(p.q[(size_t)row * p.q_token + (size_t)h * p.q_head + d]) : 0.f;
-        o[k] = 0.f;
+    __device__ __forceinline__ void set_end()
+    {
+        t_end = min(q.T, x1 - at - kLatentUnitCost);
+        if (t_end <= t)  // the run ends before the unit's first stage
+            at = x1;
     }
-    for (int k = 0; k < 2; ++k) {
-        const int d = lane + 32 * k;
-        qr[k] = d < p.P ? __half2float(p.q_rope[(size_t)row * p.qr_token + (size_t)h * p.qr_head + d]) : 0.f;
+    __device__ __forceinline__ bool more() const { return at < x1; }
+    __device__ __forceinline__ void next(const LatentParams &p)
+    {
+        at += q.T + kLatentUnitCost;
+        if (at >= x1)
+            return;
+        t = 0;
+        if (++v == q.tiles) {
+            v = 0;
+            do
+                q = latent_seq(p, ++s);
+            while (latent_cost(q) == 0);
+        }
+        set_end();
     }
-    float m = -INFINITY, l = 0.f;
-    for (int t = 0; t < end; ++t) {
-        const int id = __ldg(p.block_tables + (size_t)s * p.MB + (t >> p.log2BS));
-        float c[16], dot = 0.f;
-        if ((unsigned)id >= (unsigned)p.NB) {
-            atomicOr(p.err, kErrPageRange);
-            for (int k = 0; k < 16; ++k)
-                c[k] = 0.f;
-        } else {
-            const __half *kv = p.cache + (size_t)id * p.page_stride +
-                               (size_t)(t & (p.BS - 1)) * p.token_stride;
-            for (int k = 0; k < 16; ++k) {
-                const int d = lane + 32 * k;
-                c[k] = d < p.R ? __half2float(kv[d]) : 0.f;
-                dot += c[k] * q[k];
+    // the run that holds the unit's last stage, of `runs` equal ones of `total`
+    __device__ __forceinline__ int last_run(int total, int runs) const
+    {
+        return (int)(((long long)(at + q.T + kLatentUnitCost) * runs - 1) / total);
+    }
+};
+
+// A half tile: the rows of one CTA.  Heads up to 64 go together with as many tokens as
+// fit, more heads in blocks of 64 of one token.
+struct HalfTile {
+    int token, head;  // of its first row, within the sequence
+    __device__ __forceinline__ HalfTile(const LatentParams &p, int index)
+    {
+        token = p.HB == 1 ? index * p.TQ : index / p.HB;
+        head = p.HB == 1 ? 0 : (index - token * p.HB) * 64;
+    }
+};
+
+// Sum over the CTA's threads before this one of `x`, and over all in *total.
+__device__ __forceinline__ int latent_prefix(int x, int *warp_sum, int *total)
+{
+    constexpr int WARPS = kLatentThreads / 32;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int inc = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(~0u, inc, off);
+        if (lane >= off)
+            inc += y;
+    }
+    if (lane == 31)
+        warp_sum[w] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        if (i < w)
+            before += warp_sum[i];
+        all += warp_sum[i];
+    }
+    __syncthreads();
+    *total = all;
+    return before + inc - x;
+}
+
+}  // namespace
+
+template <int R>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
+    paged_latent_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                        const __grid_constant__ CUtensorMap tmap_qr,
+                        const __grid_constant__ CUtensorMap tmap_k,
+                        const __grid_constant__ CUtensorMap tmap_kr,
+                        const __grid_constant__ CUtensorMap tmap_v, const LatentParams p)
+{
+    using X = LatentShape<R>;
+    constexpr int NT = kLatentNT, NK = X::NK, NV = X::NV, KP = X::KP, VP = X::VP, NS = X::NS;
+    constexpr int KSLABS = X::KSLABS, VSLABS = X::VSLABS, VKEYS = X::VKEYS;
+    constexpr int PIECE = kLatentPiece, KGROUP = KSLABS * 1024, VGROUP = VSLABS * 1024;
+    constexpr int SLABS = R / 64, ROWS = kLatentRows, Q_SLAB = ROWS * 128, P_SLAB = ROWS * 128;
+    static_assert(NV >= VP, "a stage's V fits its ring: its last rows are zeroed in front of all of its products");
+    constexpr uint32_t O_COL = 0, S_COL = R / 2;  // a CTA's columns of a pair's product: N / 2
+    static_assert(S_COL + NS * NT / 2 <= 512, "tensor memory");
+    constexpr int ON = R >= 256 ? 256 : R;        // N of an output's product
+    constexpr uint32_t IDESC_S = tc_idesc_f16(128, NT, 0, 0);
+    constexpr uint32_t IDESC_O = tc_idesc_f16(128, ON, 0, 1);
+
+    extern __shared__ __align__(1024) uint8_t dyn_smem[];
+    // (the even CTA's q_full, k_full, r_full, v_full, s_free, p_full and o_free count for both)
+    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], r_full, r_empty,
+        v_full[NV], v_empty[NV], v_here, s_full[NS], s_free[NS], p_full, p_here, o_done, o_free,
+        mma_done;
+    __shared__ uint32_t tmem_base_s;
+    __shared__ int abort_flag;
+    __shared__ float red[2][4][ROWS];  // [parity][quarter of a stage's tokens][row]
+    __shared__ int warp_sum[kLatentThreads / 32], run_begin, run_seq;
+
+    const uint32_t q_s = smem_addr(dyn_smem), p_s = q_s + (SLABS + 1) * Q_SLAB, r_s = p_s + 2 * P_SLAB,
+                   k_s = r_s + ROWS * 128, v_s = k_s + NK * PIECE;
+    uint8_t *const p_ptr = dyn_smem + (p_s - q_s);
+    uint8_t *const v_ptr = dyn_smem + (v_s - q_s);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int run = (int)blockIdx.x / 2;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&q_full), 1);
+        mbar_init(smem_addr(&q_empty), 1);
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(smem_addr(&k_full[i]), 1);
+            mbar_init(smem_addr(&k_empty[i]), 1);
+        }
+        mbar_init(smem_addr(&r_full), 1);
+        mbar_init(smem_addr(&r_empty), 1);
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(smem_addr(&v_full[i]), 1);
+            mbar_init(smem_addr(&v_empty[i]), 1);
+        }
+        mbar_init(smem_addr(&v_here), 1);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(smem_addr(&s_full[i]), 1);
+            mbar_init(smem_addr(&s_free[i]), 16);
+        }
+        mbar_init(smem_addr(&p_full), 9);  // eight warps here, and the other CTA's eight by one thread
+        mbar_init(smem_addr(&p_here), 8);
+        mbar_init(smem_addr(&o_done), 1);
+        mbar_init(smem_addr(&o_free), 16);
+        mbar_init(smem_addr(&mma_done), 2);
+        abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmap_q);
+        prefetch_tensormap(&tmap_qr);
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_kr);
+        prefetch_tensormap(&tmap_v);
+    }
+    if (warp == 0)
+        tc_alloc_pair(smem_addr(&tmem_base_s), 512);
+
+    // ---- the run: [x0, x1) of the cost of all units; the sequence that holds x0
+    int total = 0, mine = 0, before = 0;  // before: this thread's (last) sequence
+    for (int s0 = 0; s0 < p.S; s0 += kLatentThreads) {
+        const int s = s0 + (int)threadIdx.x;
+        int all;
+        mine = 0;
+        if (s < p.S) {
+            const LatentSeq q = latent_seq(p, s);
+            if (q.bad && blockIdx.x == 0)
+                atomicOr(p.err, q.bad);
+            mine = latent_cost(q);
+        }
+        before = total + latent_prefix(mine, warp_sum, &all);
+        total += all;
+    }
+    const int x0 = (int)((long long)total * run / p.runs);
+    const int x1 = (int)((long long)total * (run + 1) / p.runs);
+    if (x1 > x0 && p.S <= kLatentThreads) {
+        if (mine > 0 && before <= x0 && x0 < before + mine) {
+            run_seq = (int)threadIdx.x;
+            run_begin = before;
+        }
+    } else if (x1 > x0) {
+        int past = 0;
+        for (int s0 = 0; s0 < p.S && past <= x0; s0 += kLatentThreads) {
+            const int s = s0 + (int)threadIdx.x;
+            const int here = s < p.S ? latent_cost(latent_seq(p, s)) : 0;
+            int all;
+            const int at = past + latent_prefix(here, warp_sum, &all);
+            if (here > 0 && at <= x0 && x0 < at + here) {
+                run_seq = s;
+                run_begin = at;
             }
-            for (int k = 0; k < 2; ++k)
-                if (lane + 32 * k < p.P)
-                    dot += qr[k] * __half2float(kv[p.R + lane + 32 * k]);
-        }
-        const float x = warp_sum(dot) * p.scale_log2, top = fmaxf(m, x);
-        const float keep = ex2(m - top), w = ex2(x - top);
-        l = l * keep + w;
-        for (int k = 0; k < 16; ++k)
-            o[k] = o[k] * keep + w * c[k];
-        m = top;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int k = 0; k < 16; ++k) {
-        const int d = lane + 32 * k;
-        const size_t at = ((size_t)row * p.H + h) * p.R + d;
-        if (d >= p.R)
-            continue;
-        if (p.out_half)
-            static_cast<__half *>(p.out)[at] = __float2half_rn(o[k] * inv);
-        else
-            static_cast<float *>(p.out)[at] = o[k] * inv;
-    }
-}
-
-cudaError_t launch_latent(const LatentParams &p, cudaStream_t stream)
-{
-    paged_latent_kernel<<<dim3(p.S, (p.H + 3) / 4, p.max_q), 128, 0, stream>>>(p);
-    return cudaGetLastError();
-}
-
-__global__ void __launch_bounds__(128) packed_latent_prefill_kernel(const LatentPrefillParams p)
-{
-    const int lane = threadIdx.x & 31;
-    const int h = blockIdx.y * 4 + (threadIdx.x >> 5), row = blockIdx.x;
-    if (h >= p.H)
-        return;
-    int s = -1, row0 = 0;
-    for (int i = 0; i < p.S; ++i) {
-        const int a = __ldg(p.cu_seqlens + i), n = __ldg(p.cu_seqlens + i + 1) - a;
-        if (n < 0 || n > p.max_len || a < 0 || a > p.total - n) {
-            if (row == 0 && h == 0 && lane == 0)
-                atomicOr(p.err, kErrQueryLen);
-        } else if (row >= a && row < a + n) {
-            s = i;
-            row0 = a;
+            past += all;
         }
     }
-    if (s < 0)
+    tc_fence_before();
+    cluster_sync();  // both CTAs' barriers exist
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    griddep_launch_dependents();
+    LatentWalk walk(p, x1 > x0 ? run_seq : 0, x1 > x0 ? run_begin : 0, x0, x1);
+
+    auto give_up = [&]() {
+        if (!abort_flag)
+            atomicOr(p.err, kErrTimeout);
+        abort_flag = 1;
+    };
+    // a barrier of the CTA that issues the products
+    auto lead = [&](uint64_t *bar) { return cluster_addr(smem_addr(bar), 0); };
+
+    if (warp < 2) {
+        // ============================================================ copies
+        // warp 0: Q, the latent part as K by slabs of this CTA's 64 tokens, the rotary
+        // keys; warp 1: the latent part as V, tokens of this CTA's half of the values.
+        // A piece is a copy per page (or one copy, where pages are longer): lane c
+        // issues copy c.
+        const bool is_v = warp == 1;
+        const uint64_t first_use = l2_evict_last_policy(), last_use = l2_evict_first_policy();
+        const int rows = is_v ? p.v_rows : p.k_rows;
+        const int copies = (is_v ? VKEYS : ROWS) / rows;
+        const int row = lane * rows, from = row + (is_v ? 0 : rank * ROWS);
+        const uint32_t place = (row / 8) * (is_v ? VGROUP : KGROUP);
+        int nst = 0, nq = 0, nr = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, int parity) {
+            bool w = true;
+            if (lane == 0)
+                w = mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns);
+            ok = __shfl_sync(~0u, w, 0);
+            return ok;
+        };
+        for (; walk.more() && ok; walk.next(p)) {
+            const LatentSeq &q = walk.q;
+            const int npages = (q.L + p.BS - 1) >> p.log2BS;
+            const int32_t *bt = p.block_tables + (size_t)walk.s * p.MB;
+            auto page_of = [&](int token) -> int {  // -1: none (reads zeros)
+                const int pg = (token + from) >> p.log2BS;
+                int b = -1;
+                if (lane < copies && pg < npages) {
+                    const int id = __ldg(bt + pg);
+                    if ((unsigned)id < (unsigned)p.NB)
+                        b = id;
+                    else
+                        atomicOr(p.err, kErrPageRange);
+                }
+                return b;
+            };
+            const int step = is_v ? VKEYS : NT, end = walk.t_end * NT;
+            int page_next = page_of(walk.t * NT);
+            for (int token = walk.t * NT; token < end && ok; token += step) {
+                const int page = page_next;
+                if (token + step < end)
+                    page_next = page_of(token + step);  // in flight while this one waits
+                const int grp = ((token + from) & (p.BS - 1)) >> 3;
+                if (is_v) {
+                    const int st = nst % NV;
+                    if (!wait(&v_empty[st], ((nst / NV) & 1) ^ 1))
+                        break;
+                    if (lane == 0 && rank == 0)  // for both CTAs' copies
+                        mbar_arrive_expect_tx(smem_addr(&v_full[st]), 2 * PIECE);
+                    __syncwarp();
+                    if (lane < copies)
+                        tma_load_5d_pair(v_s + st * PIECE + place, &tmap_v, 0, 0, rank * VSLABS, grp,
+                                         page, lead(&v_full[st]), last_use);
+                    ++nst;
+                    continue;
+                }
+                if (!wait(&r_empty, (nr & 1) ^ 1))
+                    break;
+                ++nr;
+                if (lane == 0 && rank == 0)
+                    mbar_arrive_expect_tx(smem_addr(&r_full), 2 * ROWS * 128);
+                __syncwarp();
+                if (lane < copies)
+                    tma_load_4d_pair(r_s + (row / 8) * 1024, &tmap_kr, 0, 0, grp, page,
+                                     lead(&r_full));
+                for (int kp = 0; kp < KP; ++kp, ++nst) {
+                    const int st = nst % NK;
+                    if (!wait(&k_empty[st], ((nst / NK) & 1) ^ 1))
+                        break;
+                    if (lane == 0 && rank == 0)
+                        mbar_arrive_expect_tx(smem_addr(&k_full[st]), 2 * PIECE);
+                    __syncwarp();
+                    if (lane < copies)
+                        tma_load_5d_pair(k_s + st * PIECE + place, &tmap_k, 0, 0, kp * KSLABS, grp,
+                                         page, lead(&k_full[st]), first_use);
+                }
+                if (ok && token == walk.t * NT) {
+                    // Q after the unit's first K: its place is free only after the last
+                    // unit's last scores
+                    if (!wait(&q_empty, (nq & 1) ^ 1))
+                        break;
+                    ++nq;
+                    const int bytes = p.TQ * p.hb * 128;
+                    if (lane == 0 && rank == 0)
+                        mbar_arrive_expect_tx(smem_addr(&q_full), 2 * (SLABS + 1) * bytes);
+                    __syncwarp();
+                    const HalfTile h(p, walk.v * 2 + rank);
+                    const int first = q.row0 + h.token;
+                    if (lane < SLABS)
+                        tma_load_4d_pair(q_s + lane * Q_SLAB, &tmap_q, 0, h.head, first, lane,
+                                         lead(&q_full));
+                    else if (lane == SLABS)
+                        tma_load_4d_pair(q_s + lane * Q_SLAB, &tmap_qr, 0, h.head, first, 0,
+                                         lead(&q_full));
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            give_up();
+            // let the copies in flight land before the CTA exits (the even CTA's
+            // barriers count both CTAs' copies, and neither leaves alone)
+            if (rank == 0) {
+                if (nq)
+                    mbar_wait_bounded(smem_addr(&q_full), (nq - 1) & 1, nullptr, p.wait_budget_ns);
+                if (nr)
+                    mbar_wait_bounded(smem_addr(&r_full), (nr - 1) & 1, nullptr, p.wait_budget_ns);
+                uint64_t *full = is_v ? v_full : k_full;
+                const int slots = is_v ? NV : NK;
+                for (int i = max(0, nst - slots); i < nst; ++i)
+                    mbar_wait_bounded(smem_addr(&full[i % slots]), (i / slots) & 1, nullptr,
+                                      p.wait_budget_ns);
+            }
+        }
+    } else if (warp < 4) {
+        if (lane == 0 && rank == 0) {
+            // ======================================================== products
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, int parity) {
+                if (ok && !mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns))
+                    ok = false;
+                return ok;
+            };
+            if (warp == 2) {
+                // (a negative scale: -q for q)
+                const uint32_t idesc_s = IDESC_S | (p.scale_log2 < 0.f ? kLatentNegateA : 0u);
+                const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
+                const uint64_t k_desc = tc_sdesc(k_s, 16, KGROUP);
+                const uint64_t r_desc = tc_sdesc(r_s, 16, 1024);
+                const uint64_t qr_desc = q_desc + ((SLABS * Q_SLAB) >> 4);
+                int nk = 0, ns = 0, nq = 0;  // K pieces, score products, Q tiles
+                for (; walk.more() && ok; walk.next(p)) {
+                    wait(&q_full, nq & 1);
+                    ++nq;
+                    for (int t = walk.t; t < walk.t_end && ok; ++t, ++ns) {
+                        // the buffer's last scores have been read
+                        const int b = ns % NS;
+                        if (ns >= NS)
+                            wait(&s_free[b], ((ns / NS) & 1) ^ 1);
+                        const uint32_t d = tmem + S_COL + b * (NT / 2);
+                        if (!wait(&r_full, ns & 1))
+                            break;
+                        tc_fence_after();
+                        // (of rope_dim 32 the other half of both rows is zeros)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_pair(d, qr_desc + ((kk * 32) >> 4), r_desc + ((kk * 32) >> 4),
+                                        idesc_s, kk > 0);
+                        tc_commit_pair(smem_addr(&r_empty));
+                        for (int kp = 0; kp < KP; ++kp, ++nk) {
+                            const int st = nk % NK;
+                            if (!wait(&k_full[st], (nk / NK) & 1))
+                                break;
+                            tc_fence_after();
+                            const uint64_t ks = k_desc + ((st * PIECE) >> 4);
+                            const uint64_t qs = q_desc + ((kp * KSLABS * Q_SLAB) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < 4 * KSLABS; ++kk)
+                                tc_mma_pair(d, qs + (((kk / 4) * Q_SLAB + (kk % 4) * 32) >> 4),
+                                            ks + (((kk / 4) * 1024 + (kk % 4) * 32) >> 4), idesc_s,
+                                            true);
+                            tc_commit_pair(smem_addr(&k_empty[st]));
+                        }
+                        tc_commit_pair(smem_addr(&s_full[b]));
+                    }
+                    tc_commit_pair(smem_addr(&q_empty));
+                }
+            } else {
+                const uint64_t v_desc = tc_sdesc(v_s, 1024, VGROUP);
+                const uint64_t p_desc = tc_sdesc(p_s, 16, 1024);
+                int nv = 0, np = 0, no = 0;  // V pieces, output products, units
+                for (; walk.more() && ok; walk.next(p)) {
+                    // the last unit's output has been read
+                    if (no++ && !wait(&o_free, no & 1))
+                        break;
+                    for (int t = walk.t; t < walk.t_end && ok; ++t, ++np) {
+                        if (!wait(&p_full, np & 1))
+                            break;
+                        for (int vp = 0; vp < VP; ++vp, ++nv) {
+                            const int st = nv % NV;
+                            if (!wait(&v_full[st], (nv / NV) & 1))
+                                break;
+                            tc_fence_after();
+                            const uint64_t vs = v_desc + ((st * PIECE) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < VKEYS / 16; ++kk) {
+                                const int ka = vp * (VKEYS / 16) + kk;
+                                const uint64_t a = p_desc + (((ka / 4) * P_SLAB + (ka % 4) * 32) >> 4);
+                                const bool more = t > walk.t || vp > 0 || kk > 0;
+#pragma unroll
+                                for (int n = 0; n < R / ON; ++n)
+                                    tc_mma_pair(tmem + O_COL + n * (ON / 2), a,
+                                                vs + ((kk * 2 * VGROUP + n * 2048) >> 4), IDESC_O,
+                                                more);
+                            }
+                            tc_commit_pair(smem_addr(&v_empty[st]));
+                        }
+                        tc_commit_pair(smem_addr(&o_done));
+                    }
+                }
+            }
+            if (!ok)
+                give_up();
+            // every product issued here has completed before the memory is freed
+            tc_commit_pair(smem_addr(&mma_done));
+            mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
+        } else if (lane == 0 && warp == 3) {
+            // ======================================================== the odd CTA's word
+            // that its weights are written, given to the even one: one release to the
+            // whole cluster a stage (see mbar_arrive_cluster), off the softmax warps
+            int np = 0;
+            bool ok = true;
+            for (; walk.more() && ok; walk.next(p))
+                for (int t = walk.t; t < walk.t_end && ok; ++t, ++np) {
+                    ok = mbar_wait_bounded(smem_addr(&p_here), np & 1, &abort_flag,
+                                           p.wait_budget_ns);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    tc_fence_before();
+                    mbar_arrive_cluster<true>(lead(&p_full));
+                }
+            if (!ok)
+                give_up();
+        }
+        __syncwarp();
+    } else {
+        // ============================================================ softmax
+        // A pair's product leaves in each CTA 64 rows over 128 lanes: lanes 64 h + r
+        // hold row r, of its columns the half h (of the scores: the CTA h's tokens,
+        // of the outputs: the CTA h's half of the values).  Warps 4-7 take the first
+        // half of a lane's columns, warps 8-11 the second: four threads a row.
+        constexpr int SC = NT / 4, OC = R / 4;  // columns of a thread
+        const int quarter = warp & 3, ch = (warp - 4) >> 2;
+        const int h = quarter >> 1, r = 32 * (quarter & 1) + lane;
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
+        const uint32_t row_bar = 1 + (quarter & 1);  // the four warps of 32 rows
+        const int part = 2 * h + ch;                 // which quarter of a stage's tokens
+        const int ti = r / p.hb, hh = r - ti * p.hb;
+        // a scale of 0 runs as 1e-30: exp2 of every score is then 1 in fp32 (the mean,
+        // as for 0) while masked scores, -inf, still give 0
+        const float sc = p.scale_log2 == 0.f ? 1e-30f : fabsf(p.scale_log2);
+        const float2 sc2 = make_float2(sc, sc);
+        const bool scribe = threadIdx.x == 128 && rank == 0;
+        if (scribe)
+            p.cut[run] = make_int4(-1, 0, 0, 0);
+        if (!walk.more() && part == 0)  // a run without a stage, perhaps between a unit's pieces
+            p.part_ml[((size_t)(2 * run) * 2 + rank) * ROWS + r] = make_float2(-INFINITY, 0.f);
+        const size_t row_bytes = (size_t)R * (p.out_half ? 2 : 4);
+        int ns = 0;
+        bool ok = true;
+        // after a failed wait the loops keep running without doing work, so that warps
+        // meet at every named barrier; outcomes are made warp-uniform (tensor-memory
+        // loads and stores are warp-collective)
+        auto wait = [&](uint64_t *bar, int parity) {
+            if (ok && !__all_sync(~0u, mbar_wait_bounded(smem_addr(bar), parity, &abort_flag,
+                                                         p.wait_budget_ns))) {
+                ok = false;
+                give_up();
+            }
+        };
+        // waits for all of a stage's V; the even CTA's barriers count both CTAs'
+        // copies, and it tells the odd one
+        int told = 0;
+        auto wait_v = [&](int a) {
+            if (rank == 1) {
+                mbar_wait_bounded(smem_addr(&v_here), told++ & 1, &abort_flag, p.wait_budget_ns);
+                return;
+            }
+            for (int i = a; i < a + VP; ++i)
+                mbar_wait_bounded(smem_addr(&v_full[i % NV]), (i / NV) & 1, &abort_flag,
+                                  p.wait_budget_ns);
+            if (threadIdx.x == 128)
+                mbar_arrive_cluster<true>(cluster_addr(smem_addr(&v_here), 1));
+        };
+        for (; walk.more(); walk.next(p)) {
+            const LatentSeq &q = walk.q;
+            const HalfTile half(p, walk.v * 2 + rank);
+            const int token = half.token + ti;  // this row's, within the sequence's new ones
+            const bool row_ok = ti < p.TQ && token < q.n && half.head + hh < p.H;
+            const int lim = row_ok ? q.L - q.n + token : -1;  // the last token it sees
+            float m_ref = -INFINITY, l = 0.f;
+            for (int t = walk.t; t < walk.t_end; ++t, ++ns) {
+                const int t0 = t * NT, c0 = t0 + part * SC, b = ns % NS;
+                wait(&s_full[b], (ns / NS) & 1);
+                float v[SC];
+                float e = -INFINITY;
+                if (ok) {
+                    tc_fence_after();
+                    tc_ld32(t_lane + S_COL + b * (NT / 2) + ch * SC, v);
+                    tc_wait_ld();
+                    tc_ld_ready(v);
+                    // the buffer takes other scores
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster<false>(lead(&s_free[b]));
+                    if (c0 + SC - 1 > lim) {
+#pragma unroll
+                        for (int i = 0; i < SC; ++i)
+                            v[i] = c0 + i > lim ? -INFINITY : v[i];
+                    }
+                    float ec[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        ec[c] = fmaxf(v[8 * c], v[8 * c + 1]);
+#pragma unroll
+                        for (int i = 2; i < 8; i += 2)
+                            ec[c] = fmax3(ec[c], v[8 * c + i], v[8 * c + i + 1]);
+                    }
+                    e = fmax3(ec[0], ec[1], fmaxf(ec[2], ec[3]));
+                }
+                red[ns & 1][part][r] = e;
+                named_barrier_sync(row_bar, 128);
+                if (!ok)
+                    continue;
+                const float mt = fmax3(fmaxf(red[ns & 1][0][r], red[ns & 1][1][r]),
+                                       red[ns & 1][2][r], red[ns & 1][3][r]) * sc;
+                // the reference moves only when the maximum has grown by more than 8
+                // (log2 units): O is rescaled rarely
+                bool rescale = false;
+                float alpha = 1.f;
+                if (mt > m_ref + kRefRoom) {
+                    const float ref = mt - kRefBelow;
+                    rescale = row_ok && m_ref != -INFINITY;
+                    alpha = rescale ? ex2(m_ref - ref) : 1.f;
+                    m_ref = ref;
+                }
+                const float off = m_ref == -INFINITY ? 0.f : -m_ref;
+                const float2 off2 = make_float2(off, off);
+                float2 sum2 = make_float2(0.f, 0.f);
+                uint32_t pk[SC / 2];
+#pragma unroll
+                for (int i = 0; i < SC; i += 2) {
+                    float2 a = ffma2(make_float2(v[i], v[i + 1]), sc2, off2);
+                    a.x = ex2(a.x);
+                    a.y = ex2(a.y);
+                    pk[i / 2] = pack_half2(a.x, a.y);
+                    sum2 = fadd2(sum2, a);
+                }
+                l = l * alpha + (sum2.x + sum2.y);
+                if (ns > 0) {  // the last product has read its weights, and O may be rescaled
+                    wait(&o_done, (ns - 1) & 1);
+                    if (!ok)
+                        continue;
+                    tc_fence_after();
+                }
+                uint8_t *const row_p = p_ptr + h * P_SLAB + r * 128;
+#pragma unroll
+                for (int c = 0; c < SC / 8; ++c)
+                    *reinterpret_cast<uint4 *>(row_p + (((SC / 8 * ch + c) ^ (r & 7)) << 4)) =
+                        make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                if (t > walk.t && __any_sync(~0u, rescale)) {
+#pragma unroll 1
+                    for (int c = 0; c < OC; c += 32) {
+                        float o[32];
+                        tc_ld32(t_lane + O_COL + ch * OC + c, o);
+                        tc_wait_ld();
+                        tc_ld_ready(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] *= alpha;
+                        tc_st32(t_lane + O_COL + ch * OC + c, o);
+                    }
+                    tc_wait_st();
+                }
+                // rows of the stage behind the sequence may hold anything: zero them in V
+                // (their weights are 0, which does not hide a NaN)
+                if (t0 + NT > q.L) {
+                    const int za = q.L - t0;  // first row behind it
+                    wait_v(ns * VP);
+                    for (int i = threadIdx.x - 128; i < (NT - za) * VSLABS * 8; i += 256) {
+                        const int row = za + i / (VSLABS * 8), c = i % (VSLABS * 8);
+                        const int st = (ns * VP + row / VKEYS) % NV, in = row % VKEYS;
+                        *reinterpret_cast<uint4 *>(v_ptr + st * PIECE + (in / 8) * VGROUP +
+                                                   (c >> 3) * 1024 + (in % 8) * 128 + (c & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(rank ? &p_here : &p_full));
+            }
+            // The row's exp-sum from its four threads (through the last stage's slot: its
+            // readers are past it, since o_done came after every warp's weights, and the
+            // next stage takes the other), then each writes its columns.  No warp goes on
+            // to the next unit before that product is over: p_full, v_here and the V ring
+            // count on it.
+            wait(&o_done, (ns - 1) & 1);
+            red[(ns & 1) ^ 1][part][r] = l;
+            named_barrier_sync(row_bar, 128);
+            const float *lr = &red[(ns & 1) ^ 1][0][r];
+            const float lt = (lr[0] + lr[ROWS]) + (lr[2 * ROWS] + lr[3 * ROWS]);
+            // (and all of its readers are past it before the stage after the next)
+            if (!ok)
+                continue;
+            tc_fence_after();
+            const bool whole = walk.t == 0 && walk.t_end == q.T;
+            const size_t piece = (size_t)(2 * run + (walk.t == 0)) * 2 + rank;
+            auto read = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster<false>(lead(&o_free));
+            };
+            // where the rows go that this thread writes together with its neighbours
+            RowOut rows;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 32 * (quarter & 1) + (lane & ~3) + i;
+                const int tok = row / p.hb, head = row - tok * p.hb;
+                const bool there = tok < p.TQ && half.token + tok < q.n && half.head + head < p.H;
+                char *at = whole ? static_cast<char *>(p.out) +
+                                       ((size_t)(q.row0 + half.token + tok) * p.H + half.head + head) *
+                                           row_bytes
+                                 : reinterpret_cast<char *>(p.part_o + (piece * ROWS + row) * R);
+                rows.at[i] = there ? at : nullptr;
+            }
+            // a store takes 64 columns at least: at R 128 the first half's warps write
+            // all of a lane's
+            constexpr int WC = R == 128 ? 64 : OC;
+            const int col = R == 128 ? 0 : ch * OC;
+            if (R == 128 && ch == 1)
+                read();
+            else
+                write_rows<WC>(rows, whole && p.out_half, !whole || p.wide_rows, t_lane + O_COL + col,
+                               h * (R / 2) + col, !whole ? 1.f : lt > 0.f ? 1.f / lt : 0.f, lane, read);
+            if (!whole) {
+                // (-inf says that there is nothing to join; scores that are all NaN leave
+                // it too, with a sum of NaN, which is to reach the output)
+                if (row_ok && part == 0)
+                    p.part_ml[piece * ROWS + r] =
+                        make_float2(m_ref == -INFINITY && lt != 0.f ? 0.f : m_ref, lt);
+                if (scribe && walk.t == 0)
+                    p.cut[run] = make_int4(walk.s, walk.v, walk.last_run(total, p.runs), 0);
+            }
+        }
+    }
+    tc_fence_before();
+    cluster_sync();  // neither CTA leaves while the other may still use its memory
+    if (warp == 0) {
+        tc_fence_after();
+        tc_dealloc_pair(tmem, 512);
+    }
+    cluster_sync();  // the memory is given back by both while both are there
+}
+
+// Joins the pieces of the unit that is cut at the end of run blockIdx.x (if one is):
+// its piece 1 there, then piece 0 of every later run up to the last.  A row's output
+// is sum_i w_i o_i / sum_i w_i l_i with w_i = exp2(m_i - max m).  A warp per row, a
+// row's pieces loaded several at a time.
+constexpr int kLatentJoinThreads = 256;
+constexpr int kLatentJoinRows = kLatentJoinThreads / 32;
+
+template <int R>
+__global__ void __launch_bounds__(kLatentJoinThreads) paged_latent_join_kernel(const LatentParams p)
+{
+    constexpr int VPL = R / 32, V4 = VPL / 4;  // values per lane
+    constexpr int AHEAD = 4;
+    const int run = blockIdx.x, rank = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = kLatentJoinRows * blockIdx.z + warp;
+    const int ti = r / p.hb, hh = r - ti * p.hb;
+    griddep_wait();
+    const int4 cut = p.cut[run];
+    if (cut.x < 0 || ti >= p.TQ)
         return;
-    float q[4], qr[2], o[4];
-    const __half *qp = p.q + (size_t)row * p.q_token + (size_t)h * p.q_head;
-    for (int k = 0; k < 4; ++k) {
-        const int d = lane + 32 * k;
-        q[k] = d < p.D ? __half2float(qp[d]) : 0.f;
-        o[k] = 0.f;
-    }
-    for (int k = 0; k < 2; ++k)
-        qr[k] = lane + 32 * k < p.P ? __half2float(qp[p.D + lane + 32 * k]) : 0.f;
-    float m = -INFINITY, l = 0.f;
-    for (int t = row0; t <= row; ++t) {
-        const __half *kp = p.k + (size_t)t * p.k_token + (size_t)h * p.k_head;
-        const __half *vp = p.v + (size_t)t * p.v_token + (size_t)h * p.v_head;
-        float dot = 0.f;
-        for (int k = 0; k < 4; ++k)
-            if (lane + 32 * k < p.D)
-                dot += q[k] * __half2float(kp[lane + 32 * k]);
-        for (int k = 0; k < 2; ++k)
-            if (lane + 32 * k < p.P)
-                dot += qr[k] * __half2float(p.k_rope[(size_t)t * p.kr_token + lane + 32 * k]);
-        const float x = warp_sum(dot) * p.scale_log2, top = fmaxf(m, x);
-        const float keep = ex2(m - top), w = ex2(x - top);
-        l = l * keep + w;
-        for (int k = 0; k < 4; ++k)
-            if (lane + 32 * k < p.D)
-                o[k] = o[k] * keep + w * __half2float(vp[lane + 32 * k]);
-        m = top;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int k = 0; k < 4; ++k) {
-        const int d = lane + 32 * k;
-        const size_t at = ((size_t)row * p.H + h) * p.D + d;
-        if (d >= p.D)
+    const int row0 = p.cu_q ? __ldg(p.cu_q + cut.x) : cut.x;
+    const int n = p.cu_q ? __ldg(p.cu_q + cut.x + 1) - row0 : 1;
+    const HalfTile half(p, cut.y * 2 + rank);
+    if (half.token + ti >= n || half.head + hh >= p.H)
+        return;
+    auto piece = [&](int i) -> size_t {
+        return ((size_t)(i == run ? 2 * run + 1 : 2 * i) * 2 + rank) * kLatentRows + r;
+    };
+    float4 acc[V4];
+    float den = 0.f, top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < V4; ++k)
+        acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = run; i0 <= cut.z; i0 += AHEAD) {
+        float2 ml[AHEAD];
+        float4 x[AHEAD][V4];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            ml[a] = make_float2(-INFINITY, 0.f);
+            if (i0 + a > cut.z)
+                continue;
+            const size_t at = piece(i0 + a);
+            ml[a] = p.part_ml[at];
+#pragma unroll
+            for (int k = 0; k < V4; ++k)
+                x[a][k] = *reinterpret_cast<const float4 *>(p.part_o + at * R + 128 * k + 4 * lane);
+        }
+        float m = top;
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+            m = fmaxf(m, ml[a].x);
+        if (m == -INFINITY)
             continue;
+        const float keep = ex2(top - m);
+        den *= keep;
+#pragma unroll
+        for (int k = 0; k < V4; ++k) {
+            acc[k].x *= keep;
+            acc[k].y *= keep;
+            acc[k].z *= keep;
+            acc[k].w *= keep;
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            if (ml[a].x == -INFINITY)  // nothing there, or nothing that the row sees
+                continue;
+            const float w = ex2(ml[a].x - m);
+            den += w * ml[a].y;
+#pragma unroll
+            for (int k = 0; k < V4; ++k) {
+                acc[k].x += w * x[a][k].x;
+                acc[k].y += w * x[a][k].y;
+                acc[k].z += w * x[a][k].z;
+                acc[k].w += w * x[a][k].w;
+            }
+        }
+        top = m;
+    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const size_t at = ((size_t)(row0 + half.token + ti) * p.H + half.head + hh) * R + 4 * lane;
+#pragma unroll
+    for (int k = 0; k < V4; ++k) {
+        const float4 o = make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
         if (p.out_half)
-            p.out_half[at] = __float2half_rn(o[k] * inv);
+            *reinterpret_cast<uint2 *>(static_cast<__half *>(p.out) + at + 128 * k) =
+                make_uint2(pack_half2(o.x, o.y), pack_half2(o.z, o.w));
         else
-            p.out[at] = o[k] * inv;
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at + 128 * k) = o;
     }
 }
 
-cudaError_t launch_latent_prefill(const LatentPrefillParams &p, cudaStream_t stream)
+namespace {
+
+template <int R> cudaError_t latent_resident_of(int *runs)
 {
-    packed_latent_prefill_kernel<<<dim3(p.total, (p.H + 3) / 4), 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    const int smem = (int)latent_smem_bytes<R>();
+    cudaError_t e = cudaFuncSetAttribute(paged_latent_kernel<R>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kLatentThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(runs, paged_latent_kernel<R>, &cfg);
+}
+
+template <int R>
+cudaError_t launch_latent_of(const LatentMaps &m, const LatentParams &p, cudaStream_t stream)
+{
+    paged_latent_kernel<R><<<2 * p.runs, kLatentThreads, latent_smem_bytes<R>(), stream>>>(
+        m.q, m.qr, m.k, m.kr, m.v, p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchAttribute overlap;
+    overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    overlap.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t join = {};
+    join.gridDim = dim3((unsigned)p.runs, 2, kLatentRows / kLatentJoinRows);
+    join.blockDim = dim3(kLatentJoinThreads);
+    join.stream = stream;
+    join.attrs = &overlap;
+    join.numAttrs = 1;
+    return cudaLaunchKernelEx(&join, paged_latent_join_kernel<R>, p);
+}
+
+}  // namespace
+
+cudaError_t latent_resident(int latent_dim, int *runs)
+{
+    *runs = 0;
+    return latent_dim == 128   ? latent_resident_of<128>(runs)
+           : latent_dim == 256 ? latent_resident_of<256>(runs)
+                               : latent_resident_of<512>(runs);
+}
+
+cudaError_t launch_latent(const LatentMaps &m, const LatentParams &p, cudaStream_t stream)
+{
+    return p.R == 128   ? launch_latent_of<128>(m, p, stream)
+           : p.R == 256 ? launch_latent_of<256>(m, p, stream)
+                        : launch_latent_of<512>(m, p, stream);
 }
 
 }  // namespace pgd
