@@ -2064,7 +2064,7 @@ pgd_status make_latent_plan(int S, int total_q, int max_q, int H, int R, int P, 
     return PGD_OK;
 }
 
-// The five views of a call: the queries' two parts [tokens][heads][64-wide slabs], a
+// The views of a call: the queries' two parts [tokens][heads][64-wide slabs], a
 // box being one slab of a half tile's rows; the cache's pages by groups of 8 rows
 // (as encode_cache_map_groups), its latent part for K and V in copies of their own,
 // its rotary keys.  Where rope_dim is 32 the slab's other half reads as zeros.

@@ -248,6 +248,18 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// True in one lane of the converged warp.  Behind it the compiler knows that a single
+// thread runs, and keeps the operands of products, commits and tensor copies in uniform
+// registers; behind `lane == 0` it moves them there one by one (M 128 products of a pair
+// of CTAs: 32 cycles each, the pipe's rate, instead of 50 and 300 more a loop's turn).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+                 : "=r"(is));
+    return is != 0;
+}
+
 // ---------------------------------------------------------------- tensor core (tcgen05)
 // Shared-memory matrix descriptor of a 128-byte-swizzled operand (rows of
 // 128 bytes, 8-row atoms of 1024 bytes, 1024-byte aligned): start address,

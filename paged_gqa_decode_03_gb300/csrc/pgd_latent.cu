@@ -178,8 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
     constexpr int NT = kLatentNT, NK = X::NK, NV = X::NV, KP = X::KP, VP = X::VP, NS = X::NS;
     constexpr int KSLABS = X::KSLABS, VSLABS = X::VSLABS, VKEYS = X::VKEYS;
     constexpr int PIECE = kLatentPiece, KGROUP = KSLABS * 1024, VGROUP = VSLABS * 1024;
-    constexpr int SLABS = R / 64, ROWS = kLatentRows, Q_SLAB = ROWS * 128, P_SLAB = ROWS * 128;
-    static_assert(NV >= VP, "a stage's V fits its ring: its last rows are zeroed in front of all of its products");
+    constexpr int SLABS = R / 64, ROWS = kLatentRows, Q_SLAB = ROWS * 128, P_SLAB = ROWS * 128, P_BYTES = 2 * P_SLAB;
     constexpr uint32_t O_COL = 0, S_COL = R / 2;  // a CTA's columns of a pair's product: N / 2
     static_assert(S_COL + NS * NT / 2 <= 512, "tensor memory");
     constexpr int ON = R >= 256 ? 256 : R;        // N of an output's product
@@ -187,21 +186,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
     constexpr uint32_t IDESC_O = tc_idesc_f16(128, ON, 0, 1);
 
     extern __shared__ __align__(1024) uint8_t dyn_smem[];
-    // (the even CTA's q_full, k_full, r_full, v_full, s_free, p_full and o_free count for both)
+    // (the even CTA's q_full, k_full, r_full, v_full, s_free, z_full, p_full and o_free count for both)
     __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], r_full, r_empty,
-        v_full[NV], v_empty[NV], v_here, s_full[NS], s_free[NS], p_full, p_here, o_done, o_free,
+        v_full[NV], v_empty[NV], z_go, z_full, s_full[NS], s_free[NS], p_full[2], p_here[2], o_done[2], o_free,
         mma_done;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag;
     __shared__ float red[2][4][ROWS];  // [parity][quarter of a stage's tokens][row]
     __shared__ int warp_sum[kLatentThreads / 32], run_begin, run_seq;
 
-    const uint32_t q_s = smem_addr(dyn_smem), p_s = q_s + (SLABS + 1) * Q_SLAB, r_s = p_s + 2 * P_SLAB,
+    const uint32_t q_s = smem_addr(dyn_smem), p_s = q_s + (SLABS + 1) * Q_SLAB, r_s = p_s + 2 * P_BYTES,
                    k_s = r_s + ROWS * 128, v_s = k_s + NK * PIECE;
     uint8_t *const p_ptr = dyn_smem + (p_s - q_s);
     uint8_t *const v_ptr = dyn_smem + (v_s - q_s);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
     const int run = (int)blockIdx.x / 2;
     if (threadIdx.x == 0) {
@@ -217,14 +216,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
             mbar_init(smem_addr(&v_full[i]), 1);
             mbar_init(smem_addr(&v_empty[i]), 1);
         }
-        mbar_init(smem_addr(&v_here), 1);
+        mbar_init(smem_addr(&z_go), 1);
+        mbar_init(smem_addr(&z_full), 16);
         for (int i = 0; i < NS; ++i) {
             mbar_init(smem_addr(&s_full[i]), 1);
             mbar_init(smem_addr(&s_free[i]), 16);
         }
-        mbar_init(smem_addr(&p_full), 9);  // eight warps here, and the other CTA's eight by one thread
-        mbar_init(smem_addr(&p_here), 8);
-        mbar_init(smem_addr(&o_done), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&p_full[i]), 9);  // eight warps here, and the other CTA's eight by one thread
+            mbar_init(smem_addr(&p_here[i]), 8);
+            mbar_init(smem_addr(&o_done[i]), 1);
+        }
         mbar_init(smem_addr(&o_free), 16);
         mbar_init(smem_addr(&mma_done), 2);
         abort_flag = 0;
@@ -295,95 +297,116 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
         // keys; warp 1: the latent part as V, tokens of this CTA's half of the values.
         // A piece is a copy per page (or one copy, where pages are longer): lane c
         // issues copy c.
+        // (barriers are tested by all lanes, copies issued by an elected one, their pages
+        // handed round: whatever a single lane does by itself costs it hundreds of cycles)
         const bool is_v = warp == 1;
-        const uint64_t first_use = l2_evict_last_policy(), last_use = l2_evict_first_policy();
         const int rows = is_v ? p.v_rows : p.k_rows;
         const int copies = (is_v ? VKEYS : ROWS) / rows;
-        const int row = lane * rows, from = row + (is_v ? 0 : rank * ROWS);
-        const uint32_t place = (row / 8) * (is_v ? VGROUP : KGROUP);
+        const int from = lane * rows + (is_v ? 0 : rank * ROWS);
+        const uint32_t copy_bytes = (rows / 8) * (is_v ? VGROUP : KGROUP);
         int nst = 0, nq = 0, nr = 0;
         bool ok = true;
         auto wait = [&](uint64_t *bar, int parity) {
-            bool w = true;
-            if (lane == 0)
-                w = mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns);
-            ok = __shfl_sync(~0u, w, 0);
+            ok = __all_sync(~0u, mbar_wait_bounded(smem_addr(bar), parity, &abort_flag,
+                                                   p.wait_budget_ns));
             return ok;
         };
-        for (; walk.more() && ok; walk.next(p)) {
-            const LatentSeq &q = walk.q;
-            const int npages = (q.L + p.BS - 1) >> p.log2BS;
-            const int32_t *bt = p.block_tables + (size_t)walk.s * p.MB;
-            auto page_of = [&](int token) -> int {  // -1: none (reads zeros)
-                const int pg = (token + from) >> p.log2BS;
-                int b = -1;
-                if (lane < copies && pg < npages) {
-                    const int id = __ldg(bt + pg);
-                    if ((unsigned)id < (unsigned)p.NB)
-                        b = id;
-                    else
-                        atomicOr(p.err, kErrPageRange);
-                }
-                return b;
-            };
-            const int step = is_v ? VKEYS : NT, end = walk.t_end * NT;
-            int page_next = page_of(walk.t * NT);
-            for (int token = walk.t * NT; token < end && ok; token += step) {
-                const int page = page_next;
-                if (token + step < end)
-                    page_next = page_of(token + step);  // in flight while this one waits
-                const int grp = ((token + from) & (p.BS - 1)) >> 3;
-                if (is_v) {
+        // The page of this lane's copy of the tokens from `token` on: looked up (page_at),
+        // and a turn later, when the value has come, checked (-1: none, reads zeros).
+        auto page_at = [&](const LatentWalk &w, int token, bool &there) -> int {
+            const int pg = (token + from) >> p.log2BS;
+            there = lane < copies && pg < (w.q.L + p.BS - 1) >> p.log2BS;
+            return ldg_if(there, p.block_tables + (size_t)w.s * p.MB + (there ? pg : 0));
+        };
+        auto checked = [&](int id, bool there) -> int {
+            const bool good = (unsigned)id < (unsigned)p.NB;
+            if (there && !good)
+                atomicOr(p.err, kErrPageRange);
+            return there && good ? id : -1;
+        };
+        if (is_v) {
+            const uint64_t last_use = l2_evict_first_policy();
+            for (; walk.more() && ok; walk.next(p)) {
+                const int end = walk.t_end * NT;
+                bool there;
+                int id = page_at(walk, walk.t * NT, there);
+                for (int token = walk.t * NT; token < end; token += VKEYS, ++nst) {
+                    const int page = checked(id, there);
+                    id = page_at(walk, token + VKEYS, there);
+                    const int grp = (token & (p.BS - 1)) >> 3;     // (0 where there are more copies)
                     const int st = nst % NV;
                     if (!wait(&v_empty[st], ((nst / NV) & 1) ^ 1))
                         break;
-                    if (lane == 0 && rank == 0)  // for both CTAs' copies
+                    if (rank == 0 && elect_one())  // for both CTAs' copies
                         mbar_arrive_expect_tx(smem_addr(&v_full[st]), 2 * PIECE);
-                    __syncwarp();
-                    if (lane < copies)
-                        tma_load_5d_pair(v_s + st * PIECE + place, &tmap_v, 0, 0, rank * VSLABS, grp,
-                                         page, lead(&v_full[st]), last_use);
-                    ++nst;
-                    continue;
+                    const uint32_t bar = lead(&v_full[st]);
+                    for (int c = 0; c < copies; ++c) {
+                        const int pg = __shfl_sync(~0u, page, c);
+                        if (elect_one())
+                            tma_load_5d_pair(v_s + st * PIECE + c * copy_bytes, &tmap_v, 0, 0,
+                                             rank * VSLABS, grp, pg, bar, last_use);
+                    }
                 }
-                if (!wait(&r_empty, (nr & 1) ^ 1))
-                    break;
-                ++nr;
-                if (lane == 0 && rank == 0)
-                    mbar_arrive_expect_tx(smem_addr(&r_full), 2 * ROWS * 128);
-                __syncwarp();
-                if (lane < copies)
-                    tma_load_4d_pair(r_s + (row / 8) * 1024, &tmap_kr, 0, 0, grp, page,
-                                     lead(&r_full));
-                for (int kp = 0; kp < KP; ++kp, ++nst) {
-                    const int st = nst % NK;
-                    if (!wait(&k_empty[st], ((nst / NK) & 1) ^ 1))
+            }
+        } else {
+            const uint64_t pol = l2_evict_last_policy();
+            const int grp = p.BS == 2 * ROWS ? rank * (ROWS / 8) : 0;
+            for (; walk.more() && ok; walk.next(p)) {
+                bool there;
+                int id = page_at(walk, walk.t * NT, there);
+                for (int t = walk.t; t < walk.t_end; ++t) {
+                    const int page = checked(id, there);
+                    id = page_at(walk, (t + 1) * NT, there);
+                    if (!wait(&r_empty, (nr & 1) ^ 1))
                         break;
-                    if (lane == 0 && rank == 0)
-                        mbar_arrive_expect_tx(smem_addr(&k_full[st]), 2 * PIECE);
-                    __syncwarp();
-                    if (lane < copies)
-                        tma_load_5d_pair(k_s + st * PIECE + place, &tmap_k, 0, 0, kp * KSLABS, grp,
-                                         page, lead(&k_full[st]), first_use);
-                }
-                if (ok && token == walk.t * NT) {
-                    // Q after the unit's first K: its place is free only after the last
-                    // unit's last scores
-                    if (!wait(&q_empty, (nq & 1) ^ 1))
+                    ++nr;
+                    if (rank == 0 && elect_one())
+                        mbar_arrive_expect_tx(smem_addr(&r_full), 2 * ROWS * 128);
+                    const uint32_t r_bar = lead(&r_full);
+                    for (int c = 0; c < copies; ++c) {
+                        const int pg = __shfl_sync(~0u, page, c);
+                        if (elect_one())
+                            tma_load_4d_pair(r_s + c * rows * 128, &tmap_kr, 0, 0, grp, pg, r_bar);
+                    }
+#pragma unroll 1
+                    for (int kp = 0; kp < KP; ++kp, ++nst) {
+                        const int st = nst % NK;
+                        if (!wait(&k_empty[st], ((nst / NK) & 1) ^ 1))
+                            break;
+                        if (rank == 0 && elect_one())
+                            mbar_arrive_expect_tx(smem_addr(&k_full[st]), 2 * PIECE);
+                        const uint32_t bar = lead(&k_full[st]);
+                        for (int c = 0; c < copies; ++c) {
+                            const int pg = __shfl_sync(~0u, page, c);
+                            if (elect_one())
+                                tma_load_5d_pair(k_s + st * PIECE + c * copy_bytes, &tmap_k, 0, 0,
+                                                 kp * KSLABS, grp, pg, bar, pol);
+                        }
+                        if (t == walk.t && kp == (KP < NK ? KP : NK) - 1) {
+                            // Q after the unit's first K: its place is free only after the
+                            // last unit's last scores, and no place for K comes free before it
+                            if (!wait(&q_empty, (nq & 1) ^ 1))
+                                break;
+                            ++nq;
+                            const int bytes = p.TQ * p.hb * 128;
+                            const HalfTile half(p, walk.v * 2 + rank);
+                            const int row = walk.q.row0 + half.token;
+                            const uint32_t q_bar = lead(&q_full);
+                            if (elect_one()) {
+                                if (rank == 0)
+                                    mbar_arrive_expect_tx(smem_addr(&q_full),
+                                                          2 * (SLABS + 1) * bytes);
+                                for (int sl = 0; sl < SLABS; ++sl)
+                                    tma_load_4d_pair(q_s + sl * Q_SLAB, &tmap_q, 0, half.head, row,
+                                                     sl, q_bar);
+                                tma_load_4d_pair(q_s + SLABS * Q_SLAB, &tmap_qr, 0, half.head, row,
+                                                 0, q_bar);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (!ok)
                         break;
-                    ++nq;
-                    const int bytes = p.TQ * p.hb * 128;
-                    if (lane == 0 && rank == 0)
-                        mbar_arrive_expect_tx(smem_addr(&q_full), 2 * (SLABS + 1) * bytes);
-                    __syncwarp();
-                    const HalfTile h(p, walk.v * 2 + rank);
-                    const int first = q.row0 + h.token;
-                    if (lane < SLABS)
-                        tma_load_4d_pair(q_s + lane * Q_SLAB, &tmap_q, 0, h.head, first, lane,
-                                         lead(&q_full));
-                    else if (lane == SLABS)
-                        tma_load_4d_pair(q_s + lane * Q_SLAB, &tmap_qr, 0, h.head, first, 0,
-                                         lead(&q_full));
                 }
             }
         }
@@ -404,7 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
             }
         }
     } else if (warp < 4) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && elect_one()) {
             // ======================================================== products
             bool ok = true;
             auto wait = [&](uint64_t *bar, int parity) {
@@ -459,34 +482,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
             } else {
                 const uint64_t v_desc = tc_sdesc(v_s, 1024, VGROUP);
                 const uint64_t p_desc = tc_sdesc(p_s, 16, 1024);
-                int nv = 0, np = 0, no = 0;  // V pieces, output products, units
+                int nv = 0, np = 0, no = 0, nz = 0;  // V pieces, output products, units, zeroed tails
                 for (; walk.more() && ok; walk.next(p)) {
                     // the last unit's output has been read
                     if (no++ && !wait(&o_free, no & 1))
                         break;
                     for (int t = walk.t; t < walk.t_end && ok; ++t, ++np) {
-                        if (!wait(&p_full, np & 1))
+                        if (!wait(&p_full[np & 1], (np >> 1) & 1))
                             break;
+                        const uint64_t ps = p_desc + (((np & 1) * P_BYTES) >> 4);
+                        // steps of 16 tokens: up to the sequence's last (one at least)
+                        const int rows = walk.q.L - t * NT;
+                        const int steps = max(1, (rows + 15) / 16);
                         for (int vp = 0; vp < VP; ++vp, ++nv) {
-                            const int st = nv % NV;
+                            const int st = nv % NV, k0 = vp * (VKEYS / 16);
                             if (!wait(&v_full[st], (nv / NV) & 1))
                                 break;
                             tc_fence_after();
                             const uint64_t vs = v_desc + ((st * PIECE) >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < VKEYS / 16; ++kk) {
-                                const int ka = vp * (VKEYS / 16) + kk;
-                                const uint64_t a = p_desc + (((ka / 4) * P_SLAB + (ka % 4) * 32) >> 4);
-                                const bool more = t > walk.t || vp > 0 || kk > 0;
+                            auto step = [&](int kk, bool more) {
+                                const uint64_t a =
+                                    ps + ((((k0 + kk) / 4) * P_SLAB + ((k0 + kk) % 4) * 32) >> 4);
 #pragma unroll
                                 for (int n = 0; n < R / ON; ++n)
                                     tc_mma_pair(tmem + O_COL + n * (ON / 2), a,
                                                 vs + ((kk * 2 * VGROUP + n * 2048) >> 4), IDESC_O,
                                                 more);
+                            };
+                            if (rows >= NT) {
+#pragma unroll
+                                for (int kk = 0; kk < VKEYS / 16; ++kk)
+                                    step(kk, t > walk.t || vp > 0 || kk > 0);
+                            } else {
+                                const int here = min(VKEYS / 16, steps - k0);
+                                if (here > 0 && steps <= k0 + VKEYS / 16 && rows < 16 * steps) {
+                                    // the last step's rows behind the sequence are zeroed first
+                                    mbar_arrive_cluster<true>(cluster_addr(smem_addr(&z_go), 1));
+                                    mbar_arrive(smem_addr(&z_go));
+                                    if (!wait(&z_full, nz++ & 1))
+                                        break;
+                                    tc_fence_after();
+                                }
+#pragma unroll 1
+                                for (int kk = 0; kk < here; ++kk)
+                                    step(kk, t > walk.t || vp > 0 || kk > 0);
                             }
                             tc_commit_pair(smem_addr(&v_empty[st]));
                         }
-                        tc_commit_pair(smem_addr(&o_done));
+                        tc_commit_pair(smem_addr(&o_done[np & 1]));
                     }
                 }
             }
@@ -495,21 +538,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
             // every product issued here has completed before the memory is freed
             tc_commit_pair(smem_addr(&mma_done));
             mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
-        } else if (lane == 0 && warp == 3) {
+        } else if (rank == 1 && elect_one()) {
             // ======================================================== the odd CTA's word
             // that its weights are written, given to the even one: one release to the
-            // whole cluster a stage (see mbar_arrive_cluster), off the softmax warps
+            // whole cluster a stage (1500 to 3500 cycles), off the softmax warps and by
+            // two warps in turn
             int np = 0;
             bool ok = true;
             for (; walk.more() && ok; walk.next(p))
                 for (int t = walk.t; t < walk.t_end && ok; ++t, ++np) {
-                    ok = mbar_wait_bounded(smem_addr(&p_here), np & 1, &abort_flag,
+                    if ((np ^ warp) & 1)
+                        continue;
+                    ok = mbar_wait_bounded(smem_addr(&p_here[np & 1]), (np >> 1) & 1, &abort_flag,
                                            p.wait_budget_ns);
                     if (!ok)
                         break;
                     tc_fence_after();
                     tc_fence_before();
-                    mbar_arrive_cluster<true>(lead(&p_full));
+                    mbar_arrive_cluster<true>(lead(&p_full[np & 1]));
                 }
             if (!ok)
                 give_up();
@@ -550,20 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                 give_up();
             }
         };
-        // waits for all of a stage's V; the even CTA's barriers count both CTAs'
-        // copies, and it tells the odd one
-        int told = 0;
-        auto wait_v = [&](int a) {
-            if (rank == 1) {
-                mbar_wait_bounded(smem_addr(&v_here), told++ & 1, &abort_flag, p.wait_budget_ns);
-                return;
-            }
-            for (int i = a; i < a + VP; ++i)
-                mbar_wait_bounded(smem_addr(&v_full[i % NV]), (i / NV) & 1, &abort_flag,
-                                  p.wait_budget_ns);
-            if (threadIdx.x == 128)
-                mbar_arrive_cluster<true>(cluster_addr(smem_addr(&v_here), 1));
-        };
+        int nz = 0;  // tails zeroed
         for (; walk.more(); walk.next(p)) {
             const LatentSeq &q = walk.q;
             const HalfTile half(p, walk.v * 2 + rank);
@@ -630,18 +663,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                     sum2 = fadd2(sum2, a);
                 }
                 l = l * alpha + (sum2.x + sum2.y);
-                if (ns > 0) {  // the last product has read its weights, and O may be rescaled
-                    wait(&o_done, (ns - 1) & 1);
+                if (ns > 1) {  // the product before the last has read its weights
+                    wait(&o_done[ns & 1], ((ns >> 1) & 1) ^ 1);
                     if (!ok)
                         continue;
-                    tc_fence_after();
                 }
-                uint8_t *const row_p = p_ptr + h * P_SLAB + r * 128;
+                uint8_t *const row_p = p_ptr + (ns & 1) * P_BYTES + h * P_SLAB + r * 128;
 #pragma unroll
                 for (int c = 0; c < SC / 8; ++c)
                     *reinterpret_cast<uint4 *>(row_p + (((SC / 8 * ch + c) ^ (r & 7)) << 4)) =
                         make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
                 if (t > walk.t && __any_sync(~0u, rescale)) {
+                    wait(&o_done[(ns - 1) & 1], ((ns - 1) >> 1) & 1);  // O is whole
+                    if (!ok)
+                        continue;
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < OC; c += 32) {
                         float o[32];
@@ -655,31 +691,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                     }
                     tc_wait_st();
                 }
-                // rows of the stage behind the sequence may hold anything: zero them in V
-                // (their weights are 0, which does not hide a NaN)
-                if (t0 + NT > q.L) {
-                    const int za = q.L - t0;  // first row behind it
-                    wait_v(ns * VP);
-                    for (int i = threadIdx.x - 128; i < (NT - za) * VSLABS * 8; i += 256) {
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(rank ? &p_here[ns & 1] : &p_full[ns & 1]));
+                // Rows of the last step behind the sequence may hold anything: they are zeroed
+                // in V (their weights are 0, which does not hide a NaN), when the products
+                // have come to their piece.
+                const int za = q.L - t0, ze = max(16, (za + 15) & ~15);
+                if (t0 + NT > q.L && za < ze) {
+                    wait(&z_go, nz++ & 1);
+                    if (!ok)
+                        continue;
+                    for (int i = threadIdx.x - 128; i < (ze - za) * VSLABS * 8; i += 256) {
                         const int row = za + i / (VSLABS * 8), c = i % (VSLABS * 8);
                         const int st = (ns * VP + row / VKEYS) % NV, in = row % VKEYS;
                         *reinterpret_cast<uint4 *>(v_ptr + st * PIECE + (in / 8) * VGROUP +
                                                    (c >> 3) * 1024 + (in % 8) * 128 + (c & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
                     }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank)
+                            mbar_arrive_cluster<true>(lead(&z_full));
+                        else
+                            mbar_arrive(smem_addr(&z_full));
+                    }
                 }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(rank ? &p_here : &p_full));
             }
             // The row's exp-sum from its four threads (through the last stage's slot: its
             // readers are past it, since o_done came after every warp's weights, and the
-            // next stage takes the other), then each writes its columns.  No warp goes on
-            // to the next unit before that product is over: p_full, v_here and the V ring
-            // count on it.
-            wait(&o_done, (ns - 1) & 1);
+            // next stage takes the other), then each writes its columns.
+            wait(&o_done[(ns - 1) & 1], ((ns - 1) >> 1) & 1);
             red[(ns & 1) ^ 1][part][r] = l;
             named_barrier_sync(row_bar, 128);
             const float *lr = &red[(ns & 1) ^ 1][0][r];
