@@ -71,7 +71,7 @@ __device__ __forceinline__ LatentSeq latent_seq(const LatentParams &p, int s)
 }
 // What a unit counts in the division of the work: its stages and, in stages, its
 // start and end.
-constexpr int kLatentUnitCost = 2;
+constexpr int kLatentUnitCost = 3;
 __device__ __forceinline__ int latent_cost(const LatentSeq &q)
 {
     return q.tiles * (q.T + kLatentUnitCost);
@@ -175,7 +175,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                         const __grid_constant__ CUtensorMap tmap_v, const LatentParams p)
 {
     using X = LatentShape<R>;
-    constexpr int NT = kLatentNT, NK = X::NK, NV = X::NV, KP = X::KP, VP = X::VP, NS = X::NS;
+    constexpr int NT = kLatentNT, NK = X::NK, NV = X::NV, KP = X::KP, VP = X::VP, NS = X::NS,
+                  NR = X::NR;
     constexpr int KSLABS = X::KSLABS, VSLABS = X::VSLABS, VKEYS = X::VKEYS;
     constexpr int PIECE = kLatentPiece, KGROUP = KSLABS * 1024, VGROUP = VSLABS * 1024;
     constexpr int SLABS = R / 64, ROWS = kLatentRows, Q_SLAB = ROWS * 128, P_SLAB = ROWS * 128, P_BYTES = 2 * P_SLAB;
@@ -186,9 +187,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
     constexpr uint32_t IDESC_O = tc_idesc_f16(128, ON, 0, 1);
 
     extern __shared__ __align__(1024) uint8_t dyn_smem[];
-    // (the even CTA's q_full, k_full, r_full, v_full, s_free, z_full, p_full and o_free count for both)
-    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], r_full, r_empty,
-        v_full[NV], v_empty[NV], z_go, z_full, s_full[NS], s_free[NS], p_full[2], p_here[2], o_done[2], o_free,
+    // (the even CTA's q_full, k_full, v_full, s_free, z_full, p_full and o_free count for both)
+    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], z_go, z_full, s_full[NS], s_free[NS], p_full[2], p_here[2], o_done[2], o_free,
         mma_done;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag;
@@ -196,7 +196,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
     __shared__ int warp_sum[kLatentThreads / 32], run_begin, run_seq;
 
     const uint32_t q_s = smem_addr(dyn_smem), p_s = q_s + (SLABS + 1) * Q_SLAB, r_s = p_s + 2 * P_BYTES,
-                   k_s = r_s + ROWS * 128, v_s = k_s + NK * PIECE;
+                   k_s = r_s + NR * ROWS * 128, v_s = k_s + NK * PIECE;
     uint8_t *const p_ptr = dyn_smem + (p_s - q_s);
     uint8_t *const v_ptr = dyn_smem + (v_s - q_s);
 
@@ -210,8 +210,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
             mbar_init(smem_addr(&k_full[i]), 1);
             mbar_init(smem_addr(&k_empty[i]), 1);
         }
-        mbar_init(smem_addr(&r_full), 1);
-        mbar_init(smem_addr(&r_empty), 1);
         for (int i = 0; i < NV; ++i) {
             mbar_init(smem_addr(&v_full[i]), 1);
             mbar_init(smem_addr(&v_empty[i]), 1);
@@ -304,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
         const int copies = (is_v ? VKEYS : ROWS) / rows;
         const int from = lane * rows + (is_v ? 0 : rank * ROWS);
         const uint32_t copy_bytes = (rows / 8) * (is_v ? VGROUP : KGROUP);
-        int nst = 0, nq = 0, nr = 0;
+        int nst = 0, nq = 0;
         bool ok = true;
         auto wait = [&](uint64_t *bar, int parity) {
             ok = __all_sync(~0u, mbar_wait_bounded(smem_addr(bar), parity, &abort_flag,
@@ -337,9 +335,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                     const int st = nst % NV;
                     if (!wait(&v_empty[st], ((nst / NV) & 1) ^ 1))
                         break;
+                    const uint32_t bar = lead(&v_full[st]);
                     if (rank == 0 && elect_one())  // for both CTAs' copies
                         mbar_arrive_expect_tx(smem_addr(&v_full[st]), 2 * PIECE);
-                    const uint32_t bar = lead(&v_full[st]);
                     for (int c = 0; c < copies; ++c) {
                         const int pg = __shfl_sync(~0u, page, c);
                         if (elect_one())
@@ -351,59 +349,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
         } else {
             const uint64_t pol = l2_evict_last_policy();
             const int grp = p.BS == 2 * ROWS ? rank * (ROWS / 8) : 0;
+            auto load_q = [&] {
+                if (!wait(&q_empty, (nq & 1) ^ 1))
+                    return false;
+                ++nq;
+                const int bytes = p.TQ * p.hb * 128;
+                const HalfTile half(p, walk.v * 2 + rank);
+                const int row = walk.q.row0 + half.token;
+                const uint32_t q_bar = lead(&q_full);
+                if (elect_one()) {
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(smem_addr(&q_full), 2 * (SLABS + 1) * bytes);
+                    for (int sl = 0; sl < SLABS; ++sl)
+                        tma_load_4d_pair(q_s + sl * Q_SLAB, &tmap_q, 0, half.head, row, sl, q_bar);
+                    tma_load_4d_pair(q_s + SLABS * Q_SLAB, &tmap_qr, 0, half.head, row, 0, q_bar);
+                }
+                __syncwarp();
+                return true;
+            };
+            int nq_from = 0;  // K pieces in front of the unit
             for (; walk.more() && ok; walk.next(p)) {
                 bool there;
                 int id = page_at(walk, walk.t * NT, there);
+                nq_from = nst;
+                if (nst == 0 && !load_q())  // the run's first, while the page comes
+                    break;
                 for (int t = walk.t; t < walk.t_end; ++t) {
                     const int page = checked(id, there);
                     id = page_at(walk, (t + 1) * NT, there);
-                    if (!wait(&r_empty, (nr & 1) ^ 1))
-                        break;
-                    ++nr;
-                    if (rank == 0 && elect_one())
-                        mbar_arrive_expect_tx(smem_addr(&r_full), 2 * ROWS * 128);
-                    const uint32_t r_bar = lead(&r_full);
-                    for (int c = 0; c < copies; ++c) {
-                        const int pg = __shfl_sync(~0u, page, c);
-                        if (elect_one())
-                            tma_load_4d_pair(r_s + c * rows * 128, &tmap_kr, 0, 0, grp, pg, r_bar);
-                    }
 #pragma unroll 1
                     for (int kp = 0; kp < KP; ++kp, ++nst) {
                         const int st = nst % NK;
                         if (!wait(&k_empty[st], ((nst / NK) & 1) ^ 1))
                             break;
-                        if (rank == 0 && elect_one())
-                            mbar_arrive_expect_tx(smem_addr(&k_full[st]), 2 * PIECE);
                         const uint32_t bar = lead(&k_full[st]);
+                        if (rank == 0 && elect_one())
+                            mbar_arrive_expect_tx(smem_addr(&k_full[st]),
+                                                  2 * (PIECE + (kp == 0 ? ROWS * 128 : 0)));
                         for (int c = 0; c < copies; ++c) {
                             const int pg = __shfl_sync(~0u, page, c);
-                            if (elect_one())
+                            if (elect_one()) {
+                                if (kp == 0)  // the rotary keys with the stage's first piece
+                                    tma_load_4d_pair(r_s + (st / KP * ROWS + c * rows) * 128,
+                                                     &tmap_kr, 0, 0, grp, pg, bar);
                                 tma_load_5d_pair(k_s + st * PIECE + c * copy_bytes, &tmap_k, 0, 0,
                                                  kp * KSLABS, grp, pg, bar, pol);
-                        }
-                        if (t == walk.t && kp == (KP < NK ? KP : NK) - 1) {
-                            // Q after the unit's first K: its place is free only after the
-                            // last unit's last scores, and no place for K comes free before it
-                            if (!wait(&q_empty, (nq & 1) ^ 1))
-                                break;
-                            ++nq;
-                            const int bytes = p.TQ * p.hb * 128;
-                            const HalfTile half(p, walk.v * 2 + rank);
-                            const int row = walk.q.row0 + half.token;
-                            const uint32_t q_bar = lead(&q_full);
-                            if (elect_one()) {
-                                if (rank == 0)
-                                    mbar_arrive_expect_tx(smem_addr(&q_full),
-                                                          2 * (SLABS + 1) * bytes);
-                                for (int sl = 0; sl < SLABS; ++sl)
-                                    tma_load_4d_pair(q_s + sl * Q_SLAB, &tmap_q, 0, half.head, row,
-                                                     sl, q_bar);
-                                tma_load_4d_pair(q_s + SLABS * Q_SLAB, &tmap_qr, 0, half.head, row,
-                                                 0, q_bar);
                             }
-                            __syncwarp();
                         }
+                        // Q after the unit's first K: its place is free only after the last
+                        // unit's last scores, and no place for K comes free before it
+                        if (nq_from > 0 && t == walk.t && kp == (KP < NK ? KP : NK) - 1 && !load_q())
+                            break;
                     }
                     if (!ok)
                         break;
@@ -417,8 +413,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
             if (rank == 0) {
                 if (nq)
                     mbar_wait_bounded(smem_addr(&q_full), (nq - 1) & 1, nullptr, p.wait_budget_ns);
-                if (nr)
-                    mbar_wait_bounded(smem_addr(&r_full), (nr - 1) & 1, nullptr, p.wait_budget_ns);
                 uint64_t *full = is_v ? v_full : k_full;
                 const int slots = is_v ? NV : NK;
                 for (int i = max(0, nst - slots); i < nst; ++i)
@@ -452,20 +446,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                         if (ns >= NS)
                             wait(&s_free[b], ((ns / NS) & 1) ^ 1);
                         const uint32_t d = tmem + S_COL + b * (NT / 2);
-                        if (!wait(&r_full, ns & 1))
-                            break;
-                        tc_fence_after();
-                        // (of rope_dim 32 the other half of both rows is zeros)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc_mma_pair(d, qr_desc + ((kk * 32) >> 4), r_desc + ((kk * 32) >> 4),
-                                        idesc_s, kk > 0);
-                        tc_commit_pair(smem_addr(&r_empty));
                         for (int kp = 0; kp < KP; ++kp, ++nk) {
                             const int st = nk % NK;
                             if (!wait(&k_full[st], (nk / NK) & 1))
                                 break;
                             tc_fence_after();
+                            if (kp == 0) {
+                                // (of rope_dim 32 the other half of both rows is zeros)
+                                const uint64_t rs = r_desc + ((st / KP * ROWS * 128) >> 4);
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    tc_mma_pair(d, qr_desc + ((kk * 32) >> 4), rs + ((kk * 32) >> 4),
+                                                idesc_s, kk > 0);
+                            }
                             const uint64_t ks = k_desc + ((st * PIECE) >> 4);
                             const uint64_t qs = q_desc + ((kp * KSLABS * Q_SLAB) >> 4);
 #pragma unroll
