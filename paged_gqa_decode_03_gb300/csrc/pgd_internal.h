@@ -408,14 +408,14 @@ constexpr int kLatentNT = 128, kLatentRows = 64, kLatentPiece = 16384;
 template <int R> struct LatentShape {
     static constexpr int KSLABS = 2, KP = R / 128;
     static constexpr int VSLABS = R / 128, VKEYS = 128 / VSLABS, VP = VSLABS;
-    static constexpr int NK = 4, NV = 3, NS = 4;
+    static constexpr int NK = 4, NV = 4, NS = 2;
     static constexpr int NR = NK / KP;  // the rotary keys' places: one for every stage in K's ring
 };
 // Q with its rotary part, two stages' weights, the rotary keys, the rings (what 227 KB leave
 // beside the static part at R 512)
 template <int R> constexpr size_t latent_smem_bytes()
 {
-    return size_t(R / 64 + 1 + 4 + LatentShape<R>::NR) * kLatentRows * 128 +
+    return size_t(R / 64 + 1 + 2 + LatentShape<R>::NR) * kLatentRows * 128 +
            size_t(LatentShape<R>::NK + LatentShape<R>::NV) * kLatentPiece;
 }
 struct LatentParams {

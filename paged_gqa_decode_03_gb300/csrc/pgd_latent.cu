@@ -179,25 +179,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                   NR = X::NR;
     constexpr int KSLABS = X::KSLABS, VSLABS = X::VSLABS, VKEYS = X::VKEYS;
     constexpr int PIECE = kLatentPiece, KGROUP = KSLABS * 1024, VGROUP = VSLABS * 1024;
-    constexpr int SLABS = R / 64, ROWS = kLatentRows, Q_SLAB = ROWS * 128, P_SLAB = ROWS * 128, P_BYTES = 2 * P_SLAB;
-    constexpr uint32_t O_COL = 0, S_COL = R / 2;  // a CTA's columns of a pair's product: N / 2
-    static_assert(S_COL + NS * NT / 2 <= 512, "tensor memory");
+    constexpr int SLABS = R / 64, ROWS = kLatentRows, Q_SLAB = ROWS * 128, X_BYTES = 8 * 32 * 64;
+    // a CTA's columns: outputs and scores (N / 2 of a pair's product), two stages' weights
+    constexpr uint32_t O_COL = 0, S_COL = R / 2, P_COL = S_COL + NS * NT / 2;
+    static_assert(P_COL + 2 * NT / 2 <= 512, "tensor memory");
     constexpr int ON = R >= 256 ? 256 : R;        // N of an output's product
     constexpr uint32_t IDESC_S = tc_idesc_f16(128, NT, 0, 0);
     constexpr uint32_t IDESC_O = tc_idesc_f16(128, ON, 0, 1);
 
     extern __shared__ __align__(1024) uint8_t dyn_smem[];
     // (the even CTA's q_full, k_full, v_full, s_free, z_full, p_full and o_free count for both)
-    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], z_go, z_full, s_full[NS], s_free[NS], p_full[2], p_here[2], o_done[2], o_free,
+    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], z_go, z_full, s_full[NS], s_free[NS], p_full[2], o_done[2], o_free,
         mma_done;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag;
     __shared__ float red[2][4][ROWS];  // [parity][quarter of a stage's tokens][row]
     __shared__ int warp_sum[kLatentThreads / 32], run_begin, run_seq;
 
-    const uint32_t q_s = smem_addr(dyn_smem), p_s = q_s + (SLABS + 1) * Q_SLAB, r_s = p_s + 2 * P_BYTES,
+    const uint32_t q_s = smem_addr(dyn_smem), x_s = q_s + (SLABS + 1) * Q_SLAB, r_s = x_s + X_BYTES,
                    k_s = r_s + NR * ROWS * 128, v_s = k_s + NK * PIECE;
-    uint8_t *const p_ptr = dyn_smem + (p_s - q_s);
+    uint8_t *const x_ptr = dyn_smem + (x_s - q_s);
     uint8_t *const v_ptr = dyn_smem + (v_s - q_s);
 
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -221,8 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
             mbar_init(smem_addr(&s_free[i]), 16);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&p_full[i]), 9);  // eight warps here, and the other CTA's eight by one thread
-            mbar_init(smem_addr(&p_here[i]), 8);
+            mbar_init(smem_addr(&p_full[i]), 16);
             mbar_init(smem_addr(&o_done[i]), 1);
         }
         mbar_init(smem_addr(&o_free), 16);
@@ -474,7 +474,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                 }
             } else {
                 const uint64_t v_desc = tc_sdesc(v_s, 1024, VGROUP);
-                const uint64_t p_desc = tc_sdesc(p_s, 16, 1024);
                 int nv = 0, np = 0, no = 0, nz = 0;  // V pieces, output products, units, zeroed tails
                 for (; walk.more() && ok; walk.next(p)) {
                     // the last unit's output has been read
@@ -483,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                     for (int t = walk.t; t < walk.t_end && ok; ++t, ++np) {
                         if (!wait(&p_full[np & 1], (np >> 1) & 1))
                             break;
-                        const uint64_t ps = p_desc + (((np & 1) * P_BYTES) >> 4);
+                        const uint32_t ps = tmem + P_COL + (np & 1) * (NT / 2);
                         // steps of 16 tokens: up to the sequence's last (one at least)
                         const int rows = walk.q.L - t * NT;
                         const int steps = max(1, (rows + 15) / 16);
@@ -494,11 +493,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                             tc_fence_after();
                             const uint64_t vs = v_desc + ((st * PIECE) >> 4);
                             auto step = [&](int kk, bool more) {
-                                const uint64_t a =
-                                    ps + ((((k0 + kk) / 4) * P_SLAB + ((k0 + kk) % 4) * 32) >> 4);
 #pragma unroll
                                 for (int n = 0; n < R / ON; ++n)
-                                    tc_mma_pair(tmem + O_COL + n * (ON / 2), a,
+                                    tc_mma_ta_pair(tmem + O_COL + n * (ON / 2), ps + (k0 + kk) * 8,
                                                 vs + ((kk * 2 * VGROUP + n * 2048) >> 4), IDESC_O,
                                                 more);
                             };
@@ -531,27 +528,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
             // every product issued here has completed before the memory is freed
             tc_commit_pair(smem_addr(&mma_done));
             mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
-        } else if (rank == 1 && elect_one()) {
-            // ======================================================== the odd CTA's word
-            // that its weights are written, given to the even one: one release to the
-            // whole cluster a stage (1500 to 3500 cycles), off the softmax warps and by
-            // two warps in turn
-            int np = 0;
-            bool ok = true;
-            for (; walk.more() && ok; walk.next(p))
-                for (int t = walk.t; t < walk.t_end && ok; ++t, ++np) {
-                    if ((np ^ warp) & 1)
-                        continue;
-                    ok = mbar_wait_bounded(smem_addr(&p_here[np & 1]), (np >> 1) & 1, &abort_flag,
-                                           p.wait_budget_ns);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    tc_fence_before();
-                    mbar_arrive_cluster<true>(lead(&p_full[np & 1]));
-                }
-            if (!ok)
-                give_up();
         }
         __syncwarp();
     } else {
@@ -566,6 +542,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
         const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t row_bar = 1 + (quarter & 1);  // the four warps of 32 rows
         const int part = 2 * h + ch;                 // which quarter of a stage's tokens
+        const uint32_t swap_bar = 3 + 2 * (quarter & 1) + ch;  // this warp and the one of quarter ^ 2
+        const int swap = (lane >> 1) & 3;
+        uint8_t *const mine_x = x_ptr + ((warp - 4) * 32 + lane) * 64;
+        const uint8_t *const other_x = x_ptr + (((warp - 4) ^ 2) * 32 + lane) * 64;
         const int ti = r / p.hb, hh = r - ti * p.hb;
         // a scale of 0 runs as 1e-30: exp2 of every score is then 1 in fp32 (the mean,
         // as for 0) while masked scores, -inf, still give 0
@@ -629,8 +609,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                 }
                 red[ns & 1][part][r] = e;
                 named_barrier_sync(row_bar, 128);
-                if (!ok)
+                if (!ok) {
+                    named_barrier_sync(swap_bar, 64);
                     continue;
+                }
                 const float mt = fmax3(fmaxf(red[ns & 1][0][r], red[ns & 1][1][r]),
                                        red[ns & 1][2][r], red[ns & 1][3][r]) * sc;
                 // the reference moves only when the maximum has grown by more than 8
@@ -658,14 +640,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                 l = l * alpha + (sum2.x + sum2.y);
                 if (ns > 1) {  // the product before the last has read its weights
                     wait(&o_done[ns & 1], ((ns >> 1) & 1) ^ 1);
-                    if (!ok)
-                        continue;
+                    tc_fence_after();
                 }
-                uint8_t *const row_p = p_ptr + (ns & 1) * P_BYTES + h * P_SLAB + r * 128;
+                // A (weights) of a pair's product of 128 rows lies twice in tensor memory:
+                // lanes r and 64 + r both hold row r, for their halves of the outputs.  So
+                // the two warps of a row exchange what they have.
 #pragma unroll
                 for (int c = 0; c < SC / 8; ++c)
-                    *reinterpret_cast<uint4 *>(row_p + (((SC / 8 * ch + c) ^ (r & 7)) << 4)) =
+                    *reinterpret_cast<uint4 *>(mine_x + ((c ^ swap) << 4)) =
                         make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                named_barrier_sync(swap_bar, 64);
+                const uint32_t p_col = t_lane + P_COL + (ns & 1) * (NT / 2) + ch * (SC / 2);
+                tc_st16u(p_col + h * (NT / 4), pk);
+#pragma unroll
+                for (int c = 0; c < SC / 8; ++c) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(other_x + ((c ^ swap) << 4));
+                    pk[4 * c] = w.x;
+                    pk[4 * c + 1] = w.y;
+                    pk[4 * c + 2] = w.z;
+                    pk[4 * c + 3] = w.w;
+                }
+                tc_st16u(p_col + (h ^ 1) * (NT / 4), pk);
                 if (t > walk.t && __any_sync(~0u, rescale)) {
                     wait(&o_done[(ns - 1) & 1], ((ns - 1) >> 1) & 1);  // O is whole
                     if (!ok)
@@ -682,13 +677,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                             o[i] *= alpha;
                         tc_st32(t_lane + O_COL + ch * OC + c, o);
                     }
-                    tc_wait_st();
                 }
-                fence_proxy_async_smem();
+                tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(smem_addr(rank ? &p_here[ns & 1] : &p_full[ns & 1]));
+                    mbar_arrive_cluster<false>(lead(&p_full[ns & 1]));
                 // Rows of the last step behind the sequence may hold anything: they are zeroed
                 // in V (their weights are 0, which does not hide a NaN), when the products
                 // have come to their piece.
