@@ -22,7 +22,7 @@ SOURCES = ["pgd_api.cu", "pgd_kernels_d64.cu", "pgd_kernels_d128.cu", "pgd_kerne
            "pgd_varlen.cu", "pgd_kv.cu", "pgd_prefill.cu",
            "pgd_tree.cu", "pgd_rope.cu", "pgd_latent.cu",
            "pgd_latent_prefill.cu"]
-HEADERS = ["pgd_device.cuh", "pgd_internal.h", "pgd_kernels.cuh", "pgd_rows.cuh"]
+HEADERS = ["pgd_device.cuh", "pgd_internal.h", "pgd_kernels.cuh", "pgd_rows.cuh", "pgd_units.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          f"-I{os.path.join(ROOT, 'include')}"]

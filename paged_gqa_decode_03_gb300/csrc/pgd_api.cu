@@ -66,6 +66,7 @@ struct DeviceState {
     std::atomic<int> tree_runs[3][2] = {};       // [head_dim][pairs]: resident runs, 0: not set up
     std::atomic<bool> prefill_ready[3] = {};     // [head_dim]
     std::atomic<int> latent_runs[3] = {};        // [latent_dim 128/256/512]: resident pairs
+    std::atomic<bool> latent_prefill_ready[2] = {};  // [head_dim 64/128]
     unsigned *err_word = nullptr;   // address of g_device_error on this device
     std::mutex pool_mu;             // the pool is made on first library-owned scratch
     cudaMemPool_t pool = nullptr;   //   (and again after pgd_release): stream-ordered scratch
@@ -185,6 +186,18 @@ pgd_status prefill_ready(DeviceState &st, int D)
     if (known.load(std::memory_order_acquire))
         return PGD_OK;
     const pgd_status s = set_up("set-up of the prompt kernel", [&] { return prefill_set_up(D); });
+    if (!s)
+        known.store(true, std::memory_order_release);
+    return s;
+}
+
+pgd_status latent_prefill_ready(DeviceState &st, int D)
+{
+    std::atomic<bool> &known = st.latent_prefill_ready[D == 64 ? 0 : 1];
+    if (known.load(std::memory_order_acquire))
+        return PGD_OK;
+    const pgd_status s =
+        set_up("set-up of the latent prompt kernel", [&] { return latent_prefill_set_up(D); });
     if (!s)
         known.store(true, std::memory_order_release);
     return s;
@@ -2218,7 +2231,8 @@ pgd_status run_latent(void *out, bool half, const uint16_t *q, const uint16_t *q
 }
 
 struct LatentPrefillPlan {
-    size_t ws_bytes;
+    int max_units;
+    size_t ws_bytes;  // [256 B: unit count][units]
 };
 
 pgd_status make_latent_prefill_plan(int S, int total, int H, int D, int P, LatentPrefillPlan *pp)
@@ -2233,7 +2247,15 @@ pgd_status make_latent_prefill_plan(int S, int total, int H, int D, int P, Laten
         return fail(PGD_ERR_UNSUPPORTED, "head_dim %d not in {64, 128}", D);
     if (P != 32 && P != 64)
         return fail(PGD_ERR_UNSUPPORTED, "rope_dim %d not in {32, 64}", P);
-    pp->ws_bytes = 0;
+    // disjoint prompts: whole pairs of tiles of all rows, and one begun per prompt
+    const long long units = ((long long)total / 256 + S) * H;
+    if (units >= (1ll << 30))
+        return fail(PGD_ERR_UNSUPPORTED, "%lld work units", units);
+    pp->max_units = (int)units;
+    pp->ws_bytes = total && S ? 256 + align256((size_t)units * 16) : 0;
+    if (pp->ws_bytes > kMaxWorkspaceBytes)
+        return fail(PGD_ERR_WORKSPACE, "scratch of %zu bytes needed, above the %zu-byte cap",
+                    pp->ws_bytes, kMaxWorkspaceBytes);
     return PGD_OK;
 }
 
@@ -2270,36 +2292,68 @@ pgd_status run_latent_prefill(float *out, uint16_t *out_half, const uint16_t *q,
             return fail(PGD_ERR_INVALID_ARG, "out, q, k, k_rope and v must be 16-byte aligned");
     if (!aligned(cu_seqlens, 4))
         return fail(PGD_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
-    if (workspace && (ws_bytes < pp.ws_bytes || !aligned(workspace, 256)))
+    char *ws = static_cast<char *>(workspace);
+    const bool own = workspace == nullptr;
+    if (!own && (ws_bytes < pp.ws_bytes || !aligned(ws, 256)))
         return fail(PGD_ERR_WORKSPACE, "workspace of %zu bytes (256-byte aligned) given, %zu needed",
                     ws_bytes, pp.ws_bytes);
     DeviceState *ds;
-    if ((st = device_state(&ds)))
+    if ((st = device_state(&ds)) || (st = latent_prefill_ready(*ds, D)))
         return st;
-    LatentPrefillParams p = {};
+    // rows of one head (of all heads: rope) as 64 halves x tokens x slabs x heads, a box
+    // being 128 tokens of Q with all slabs, of K with one, 64 or 128 of V with all
+    using u64 = cuuint64_t;
+    using u32 = cuuint32_t;
+    const u64 T = (u64)total, heads = (u64)H, slabs = (u64)D / 64;
+    const u32 v_keys = D == 64 ? kLatentVKeys64 : kLatentVKeys128;
+    LatentPrefillMaps maps;
+    auto view = [&](CUtensorMap *map, const uint16_t *base, u64 width, u64 n_slabs, u64 n_heads,
+                    long long token, long long head, u32 box_tokens, u32 box_slabs) -> pgd_status {
+        const u64 dims[4] = {width, T, n_slabs, n_heads};
+        const u64 strides[3] = {(u64)token * 2, 128, (u64)head * 2};
+        const u32 box[4] = {64, box_tokens, box_slabs, 1};
+        return encode_view(map, base, 4, dims, strides, box);
+    };
+    if ((st = view(&maps.q, q, 64, slabs, heads, x.q_token, x.q_head, 128, (u32)slabs)) ||
+        (st = view(&maps.qr, q + D, (u64)P, 1, heads, x.q_token, x.q_head, 128, 1)) ||
+        (st = view(&maps.k, k, 64, slabs, heads, x.k_token, x.k_head, 128, 1)) ||
+        (st = view(&maps.kr, k_rope, (u64)P, 1, 1, x.kr_token, 8, 128, 1)) ||
+        (st = view(&maps.v, v, 64, slabs, heads, x.v_token, x.v_head, v_keys, (u32)slabs)))
+        return st;
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    cudaError_t e;
+    if (own) {
+        cudaMemPool_t pool;
+        if ((st = device_pool(*ds, &pool)))
+            return st;
+        if ((e = cudaMallocFromPoolAsync(reinterpret_cast<void **>(&ws), pp.ws_bytes, pool,
+                                         stream)) != cudaSuccess)
+            return cuda_fail(e, "scratch allocation");
+    }
+    PrefillParams p = {};
     p.out = out;
     p.out_half = reinterpret_cast<__half *>(out_half);
-    p.q = reinterpret_cast<const __half *>(q);
-    p.k = reinterpret_cast<const __half *>(k);
-    p.k_rope = reinterpret_cast<const __half *>(k_rope);
-    p.v = reinterpret_cast<const __half *>(v);
-    p.q_token = x.q_token;
-    p.q_head = x.q_head;
-    p.k_token = x.k_token;
-    p.k_head = x.k_head;
-    p.kr_token = x.kr_token;
-    p.v_token = x.v_token;
-    p.v_head = x.v_head;
     p.cu_seqlens = cu_seqlens;
+    p.num_units = reinterpret_cast<int *>(ws);
+    p.units = reinterpret_cast<int4 *>(ws + 256);
     p.err = ds->err_word;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.S = S;
     p.total = total;
     p.max_len = max_len;
-    p.H = H;
-    p.D = D;
-    p.P = P;
-    const cudaError_t e = launch_latent_prefill(p, static_cast<cudaStream_t>(stream_v));
+    p.Hq = p.Hkv = H;
+    p.G = 1;
+    p.TQ = 128;
+    p.span = 256;
+    p.max_units = pp.max_units;
+    p.wide_rows = aligned(dst, 32);
+    p.wait_budget_ns = kWaitBudgetNs;
+    e = launch_latent_prefill(D, maps, p, std::min(ds->num_sms, pp.max_units), stream);
+    if (own) {
+        const cudaError_t e2 = cudaFreeAsync(ws, stream);
+        if (e == cudaSuccess)
+            e = e2;
+    }
     if (e != cudaSuccess)
         return cuda_fail(e, "kernel launch");
     t_last_error.clear();

@@ -339,6 +339,8 @@ struct PrefillParams {
     bool wide_rows;               // the output starts on a 32-byte border
     uint64_t wait_budget_ns;
 };
+// The list of units, longest first (also the kernel in front of pgd_latent_prefill.cu's).
+cudaError_t launch_prefill_order(const PrefillParams &p, cudaStream_t stream);
 // On the current device, once before the launches of this head_dim.
 cudaError_t prefill_set_up(int head_dim);
 cudaError_t launch_prefill(int head_dim, const CUtensorMap &tq, const CUtensorMap &tk,
@@ -446,17 +448,16 @@ struct LatentMaps {
 cudaError_t latent_resident(int latent_dim, int *runs);
 cudaError_t launch_latent(const LatentMaps &m, const LatentParams &p, cudaStream_t stream);
 
-struct LatentPrefillParams {
-    float *out;                   // [total][H][D], or null with
-    __half *out_half;             //   out_half, the output as fp16
-    const __half *q, *k, *k_rope, *v;
-    long long q_token, q_head, k_token, k_head, kr_token, v_token, v_head;
-    const int32_t *cu_seqlens;    // [S + 1]
-    unsigned *err;
-    float scale_log2;
-    int S, total, max_len, H, D, P;
+// Packed prompts with keys and values expanded from latent vectors
+// (pgd_latent_prefill.cu): PrefillParams with a KV head per query head; the queries'
+// and keys' own parts and their rotary parts are views of their own.
+struct LatentPrefillMaps {
+    CUtensorMap q, qr, k, kr, v;
 };
-cudaError_t launch_latent_prefill(const LatentPrefillParams &p, cudaStream_t stream);
+constexpr int kLatentVKeys64 = 128, kLatentVKeys128 = 64;  // keys of a V copy, by head_dim
+cudaError_t latent_prefill_set_up(int head_dim);
+cudaError_t launch_latent_prefill(int head_dim, const LatentPrefillMaps &m, const PrefillParams &p,
+                                  int grid, cudaStream_t stream);
 
 // Quantiser of rows into quantised pages (pgd_quantize.cu).
 cudaError_t launch_quantize(int head_dim, uint8_t *codes, uint16_t *meta, const uint16_t *src,
