@@ -1943,6 +1943,8 @@ pgd_status run_rope(RopeParams &p, void *stream)
 {
     if (!std::isfinite(p.magnitude))
         return fail(PGD_ERR_INVALID_ARG, "magnitude is not finite");
+    if (p.rows >= 1 << 30)
+        return fail(PGD_ERR_UNSUPPORTED, "num_rows %d: below 2^30", p.rows);
     if (p.rows == 0) {
         t_last_error.clear();
         return PGD_OK;

@@ -394,7 +394,8 @@ struct RopeParams {
     bool interleaved, in_place;           // in_place: q_out is q
     int rows, Hq, Hkv, rot, log2BS, NB;
     int log2q, log2k, log2v;              // of a head's 32-byte items (values / 16)
-    int rows_per_cta;                     // set by the launcher
+    int rows_per_cta;                     // set by the launcher, as
+    uint32_t row_inverse, pair_inverse;   //   the reciprocals of a row's items and pairs
     long long page_stride, head_stride, token_stride;   // halves
     long long qo_token, qo_head, q_token, q_head, k_token, k_head, v_token, v_head;
 };

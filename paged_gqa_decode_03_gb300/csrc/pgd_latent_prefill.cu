@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
     // take registers that the copying and issuing warps do not need (128 x 80 +
     // 256 x 208 of the 384 x 168 of the launch)
     if (warp < 4) {
-      regs_give<80>();
+      regs_give<104>();
       if (warp == 0 || warp == 3) {
         if (elect_one()) {
             // ======================================================== copies
@@ -225,22 +225,25 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
             }
         }
         __syncwarp();
-      } else if (warp == 1) {
-        if (elect_one()) {
-            // ======================================================== scores
+      } else {
+        // ============================================================ products
+        // warp 1: scores, warp 2: outputs.  The warp stays together: barriers are tested by
+        // all lanes (34 cycles each; 88 by a lane alone), products issued by an elected one.
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, int parity) {
+            if (ok && !__all_sync(~0u, mbar_wait_bounded(smem_addr(bar), parity, &abort_flag,
+                                                         p.wait_budget_ns)))
+                ok = false;
+            return ok;
+        };
+        int4 next = unit_at(p, 0, units);
+        if (warp == 1) {
             const uint32_t idesc_s = IDESC_S | (p.scale_log2 < 0.f ? kNegateA : 0u);
             const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
             const uint64_t k_desc = tc_sdesc(k_s, 16, 1024);
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, int parity) {
-                if (ok && !mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns))
-                    ok = false;
-                return ok;
-            };
             int nk = 0, nq = 0;        // K pieces, Q pairs used up
             int uses[2] = {0, 0};      // of each score buffer
             int ns[2] = {0, 0};        // S products of each tile
-            int4 next = unit_at(p, 0, units);
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
                 const int4 u = next;
@@ -251,14 +254,15 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
                 wait(&q_full, nq & 1);
                 ++nq;
                 for (int j = 0; j < nmax && ok; ++j, nk += KP) {
-                    for (int x = 0; x < 2 && ok; ++x) {
-                        const bool only = j >= (x ? nt0 : nt1);  // no other tile's product here
-                        if (j >= (x ? nt1 : nt0))
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const bool last_user = x == 1 || j >= nt1;
+                        if (j >= (x ? nt1 : nt0) || !ok)
                             continue;
                         // the buffer's last scores have been read
                         const int b = SBUF == 2 ? x : 0;
                         if (uses[b] && !wait(&s_free[b], (uses[b] - 1) & 1))
-                            break;
+                            continue;
                         ++uses[b];
                         const uint64_t qx = q_desc + ((x * Q_TILE) >> 4);
                         const uint32_t d = tmem + S_COL + b * kNT;
@@ -269,40 +273,30 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
                             tc_fence_after();
                             const uint64_t ks = k_desc + ((st * PIECE) >> 4);
                             const uint64_t qs = qx + ((kp * kSlab) >> 4);
+                            if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc_mma(d, qs + ((kk * 32) >> 4), ks + ((kk * 32) >> 4), idesc_s,
-                                       kp > 0 || kk > 0);
-                            if (x == 1 || only)
-                                tc_commit(smem_addr(&k_empty[st]));
+                                for (int kk = 0; kk < 4; ++kk)
+                                    tc_mma(d, qs + ((kk * 32) >> 4), ks + ((kk * 32) >> 4), idesc_s,
+                                           kp > 0 || kk > 0);
+                                if (kp == KP - 1)
+                                    tc_commit(smem_addr(&s_full[x]));
+                                if (last_user)
+                                    tc_commit(smem_addr(&k_empty[st]));
+                            }
+                            __syncwarp();
                         }
-                        tc_commit(smem_addr(&s_full[x]));
                         s_issued[x] = ++ns[x];
                     }
                 }
-                tc_commit(smem_addr(&q_empty));
+                if (elect_one())
+                    tc_commit(smem_addr(&q_empty));
+                __syncwarp();
             }
-            if (!ok)
-                give_up();
-            // every product issued has completed before the memory is freed
-            tc_commit(smem_addr(&mma_done));
-            mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
-        }
-        __syncwarp();
-      } else if (warp == 2) {
-        if (elect_one()) {
-            // ======================================================== outputs
+        } else {
             const uint64_t v_desc = tc_sdesc(v_s, VKEYS * 128, 1024);
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, int parity) {
-                if (ok && !mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns))
-                    ok = false;
-                return ok;
-            };
             int nv = 0;                           // V pieces used up
             // P V products, units, zeroed tails of each tile
             int np[2] = {0, 0}, no[2] = {0, 0}, nz[2] = {0, 0};
-            int4 next = unit_at(p, 0, units);
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
                 const int4 u = next;
@@ -311,68 +305,95 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
                     continue;
                 const int nt0 = stages(u, 0), nt1 = stages(u, 1), nmax = max(nt0, nt1);
                 for (int j = 0; j < nmax && ok; ++j, nv += VP) {
-                    for (int x = 0; x < 2 && ok; ++x) {
-                        const bool only = j >= (x ? nt0 : nt1);
-                        if (j >= (x ? nt1 : nt0))
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int nt = x ? nt1 : nt0;
+                        const bool last_user = x == 1 || j >= nt1;
+                        if (j >= nt || !ok)
                             continue;
                         // the last unit's output has been read
                         if (j == 0 && no[x]++ && !wait(&o_free[x], no[x] & 1))
-                            break;
+                            continue;
                         if (!wait(&p_full[x], np[x] & 1))
-                            break;
+                            continue;
                         ++np[x];
-                        // let the tile's next scores go first: they are on the
-                        // path that sets the period, this product is not.  Only
-                        // a matter of order, so the look is short and goes on
-                        // either way.
-                        if (j + 1 < (x ? nt1 : nt0))
-                            for (int i = 0; i < 16 && s_issued[x] <= np[x]; ++i)
-                                ;
                         const uint32_t o = tmem + x * D, a = tmem + P_COL + x * 64;
-                        const bool last = j + 1 == (x ? nt1 : nt0);
+                        const bool last = j + 1 == nt;
                         const int steps = last ? last_steps(u, x) : kNT / 16;
                         // keys behind the prompt in the last step: zeroed in V first
                         const bool tail = last && u.y + u.z - j * kNT < 16 * steps;
-                        for (int vp = 0; vp < VP; ++vp) {
+                        if (steps == kNT / 16 && !tail) {
+                            for (int vp = 0; vp < VP; ++vp)
+                                wait(&v_full[(nv + vp) % NV], ((nv + vp) / NV) & 1);
+                            // The tile's next scores go first: they are on the path that
+                            // sets the period, and this product fills the time in which
+                            // the softmax reads them out.  Only a matter of order, so the
+                            // look is short and goes on either way.
+                            if (!last)
+                                for (int i = 0; i < 256 && s_issued[x] <= np[x]; ++i)
+                                    ;
+                            if (!ok)
+                                continue;
+                            tc_fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int vp = 0; vp < VP; ++vp) {
+                                    const int st = (nv + vp) % NV;
+                                    const uint64_t vs = v_desc + ((st * PIECE) >> 4);
+#pragma unroll
+                                    for (int kk = 0; kk < VKEYS / 16; ++kk)
+                                        tc_mma_ta(o, a + (vp * (VKEYS / 16) + kk) * 8,
+                                                  vs + ((kk * 2048) >> 4), IDESC_O,
+                                                  j > 0 || vp > 0 || kk > 0);
+                                    if (last_user)
+                                        tc_commit(smem_addr(&v_empty[st]));
+                                }
+                                tc_commit(smem_addr(&o_done[x]));
+                            }
+                            __syncwarp();
+                            continue;
+                        }
+                        for (int vp = 0; vp < VP && ok; ++vp) {
                             const int st = (nv + vp) % NV, k0 = vp * (VKEYS / 16);
                             if (!wait(&v_full[st], ((nv + vp) / NV) & 1))
                                 break;
                             tc_fence_after();
                             const uint64_t vs = v_desc + ((st * PIECE) >> 4);
-                            if (steps == kNT / 16 && !tail) {
-#pragma unroll
-                                for (int kk = 0; kk < VKEYS / 16; ++kk)
-                                    tc_mma_ta(o, a + (k0 + kk) * 8, vs + ((kk * 2048) >> 4), IDESC_O,
-                                              j > 0 || vp > 0 || kk > 0);
-                            } else {
-                                const int here = min(VKEYS / 16, steps - k0);
-                                if (here > 0 && steps <= k0 + VKEYS / 16 && tail) {
+                            const int here = min(VKEYS / 16, steps - k0);
+                            if (here > 0 && steps <= k0 + VKEYS / 16 && tail) {
+                                if (lane == 0)
                                     mbar_arrive(smem_addr(&z_go[x]));
-                                    if (!wait(&z_full[x], nz[x]++ & 1))
-                                        break;
-                                    tc_fence_after();
-                                }
+                                __syncwarp();
+                                if (!wait(&z_full[x], nz[x]++ & 1))
+                                    break;
+                                tc_fence_after();
+                            }
+                            if (elect_one()) {
 #pragma unroll 1
                                 for (int kk = 0; kk < here; ++kk)
                                     tc_mma_ta(o, a + (k0 + kk) * 8, vs + ((kk * 2048) >> 4), IDESC_O,
                                               j > 0 || vp > 0 || kk > 0);
+                                if (last_user)
+                                    tc_commit(smem_addr(&v_empty[st]));
+                                if (vp == VP - 1)
+                                    tc_commit(smem_addr(&o_done[x]));
                             }
-                            if (x == 1 || only)
-                                tc_commit(smem_addr(&v_empty[st]));
+                            __syncwarp();
                         }
-                        tc_commit(smem_addr(&o_done[x]));
                     }
                 }
             }
-            if (!ok)
-                give_up();
-            tc_commit(smem_addr(&mma_done));
-            mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
         }
+        if (!ok && lane == 0)
+            give_up();
+        // every product issued has completed before the memory is freed
+        if (elect_one())
+            tc_commit(smem_addr(&mma_done));
         __syncwarp();
+        mbar_wait_bounded(smem_addr(&mma_done), 0, nullptr, p.wait_budget_ns);
       }
     } else {
-        regs_take<208>();
+        regs_take<200>();
         // ============================================================ softmax
         const int x = (warp - 4) >> 2;
         const int quarter = warp & 3;
