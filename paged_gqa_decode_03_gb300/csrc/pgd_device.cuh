@@ -191,6 +191,17 @@ __device__ __forceinline__ int ldg_if(bool pred, const int32_t *addr)
                  : "l"(addr), "r"((unsigned)pred));
     return v;
 }
+// The same from memory that an earlier launch may be writing up to griddep_wait.
+__device__ __forceinline__ int ld_if(bool pred, const int32_t *addr)
+{
+    int v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+                 "@p ld.global.b32 %0, [%1];\n\t}"
+                 : "=r"(v)
+                 : "l"(addr), "r"((unsigned)pred)
+                 : "memory");
+    return v;
+}
 
 // Adds one pending arrival to the barrier's current phase now and performs
 // it once this thread's earlier cp.async copies have landed.

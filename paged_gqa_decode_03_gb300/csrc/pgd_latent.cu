@@ -19,17 +19,29 @@
 //     the R values: B, split by values.  That takes the latent part in twice, the
 //     second time from L2: every byte comes from HBM once, and an SM takes in from L2
 //     two to three times what HBM gives it (130 GB/s and more in copies of 32 KB).
-//   * A product takes 48 cycles at least: scores (N 128) 36 x 48, outputs (N 256, 64
-//     each, the full rate) 16 x 64, 2752 cycles a stage at R 512, against 3150 in
-//     which HBM brings its 147 KB.  Fewer rows cost the same; HBM still bounds.
+//   * A product of a pair takes 32 cycles (scores, N 128: 36 a stage) or 64 (outputs,
+//     N 256: 16), 2176 cycles a stage at R 512, against 3150 in which HBM brings its
+//     147 KB.  Fewer rows cost the same; HBM still bounds.  They run at that rate only
+//     when an elected lane of a converged warp issues them: `if (lane == 0)` costs 50
+//     cycles a product and 300 a turn (32 requests of 8 k to 32 k tokens 231 us, so 139).
 //   * The stages of all units (sequence, tile of rows) are cut into equal runs, one
 //     per resident pair, whatever the lengths; a unit that is cut leaves pieces
 //     (reference maximum, exp-sum, unscaled output; two per run at most), which a
 //     second kernel joins.  Rings run on from unit to unit.
-//   * Weights go to shared memory as fp16 (an A operand of M 128 over a pair would
-//     have to lie twice in tensor memory).  Four score buffers: the scores run ahead of
-//     the softmax, so the one place for weights, free again when its product is over,
-//     does not hold them up.
+//   * Weights go to tensor memory as fp16, two stages of them, next to two score
+//     buffers.  A row of A lies there twice (lanes r and 64 + r), and its scores come
+//     split over the same lanes: the two warps of a row exchange their halves through
+//     16 KB of shared memory.  (Weights in shared memory: 48 cycles a score product in
+//     their bandwidth's share, and no room for two stages.)
+//
+// Measured: 32 requests of 8 k to 32 k tokens with 16 heads 128 us (602 MB: 4.7 TB/s;
+// HBM's floor 97), 64 of 512 to 4096 tokens with 128 heads 62, 24 of up to 8 k tokens
+// with up to 5 rows of 32 heads 55, one of 1000 tokens 18 (of it 16 in every call: the
+// runs' division 2, the first pages, copies and Q 5, the last softmax and outputs 4, the
+// joining kernel 4).  What bounds a long run is the chain of a piece (its place free, its
+// copy of 16 KB issued, arrived, used): 64 KB of K in flight an SM.  Other divisions of
+// the same memory: pieces of 32 KB for K, two of them, 143 us, but 51 for the 24 requests;
+// Q's place cut to a tile's rows where they are few and longer rings 132 and 57.
 #include "pgd_device.cuh"
 #include "pgd_internal.h"
 #include "pgd_rows.cuh"
@@ -43,7 +55,9 @@ constexpr int kLatentThreads = 384;
 constexpr uint32_t kLatentNegateA = 1u << 13;  // of the products' descriptor: -A for A
 
 // What a sequence asks for: its length, first query row, rows (0 where its numbers do
-// not fit together), stages per unit and units (tiles of two half tiles).
+// not fit together), stages per unit and units (tiles of two half tiles).  (Plain
+// loads: the kernel starts while the one before it may still be writing, up to
+// griddep_wait, so its inputs are not read-only here.)
 struct LatentSeq {
     int L, row0, n, T, tiles;
     unsigned bad;
@@ -53,9 +67,9 @@ __device__ __forceinline__ LatentSeq latent_seq(const LatentParams &p, int s)
 {
     LatentSeq q;
     const int maxlen = p.MB << p.log2BS;
-    q.L = __ldg(p.seq_lens + s);
-    q.row0 = p.cu_q ? __ldg(p.cu_q + s) : s;
-    q.n = p.cu_q ? __ldg(p.cu_q + s + 1) - q.row0 : 1;
+    q.L = p.seq_lens[s];
+    q.row0 = p.cu_q ? p.cu_q[s] : s;
+    q.n = p.cu_q ? p.cu_q[s + 1] - q.row0 : 1;
     q.bad = 0;
     if (q.L < 0 || q.L > maxlen)
         q.bad = kErrSeqLen;
@@ -70,7 +84,8 @@ __device__ __forceinline__ LatentSeq latent_seq(const LatentParams &p, int s)
     return q;
 }
 // What a unit counts in the division of the work: its stages and, in stages, its
-// start and end.
+// start and end.  (Of 2, 3, 4, 5 about the best: 64 requests of 128 heads 63.6, 63.3, 62.2, 63.9
+// us, 24 of up to 5 rows 54.0, 52.7, 54.6, 54.7, 32 long ones 133, 130, 131, 132.)
 constexpr int kLatentUnitCost = 3;
 __device__ __forceinline__ int latent_cost(const LatentSeq &q)
 {
@@ -238,6 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
     if (warp == 0)
         tc_alloc_pair(smem_addr(&tmem_base_s), 512);
 
+    griddep_wait();  // what the launches before wrote
     // ---- the run: [x0, x1) of the cost of all units; the sequence that holds x0
     int total = 0, mine = 0, before = 0;  // before: this thread's (last) sequence
     for (int s0 = 0; s0 < p.S; s0 += kLatentThreads) {
@@ -314,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
         auto page_at = [&](const LatentWalk &w, int token, bool &there) -> int {
             const int pg = (token + from) >> p.log2BS;
             there = lane < copies && pg < (w.q.L + p.BS - 1) >> p.log2BS;
-            return ldg_if(there, p.block_tables + (size_t)w.s * p.MB + (there ? pg : 0));
+            return ld_if(there, p.block_tables + (size_t)w.s * p.MB + (there ? pg : 0));
         };
         auto checked = [&](int id, bool there) -> int {
             const bool good = (unsigned)id < (unsigned)p.NB;
@@ -786,12 +802,13 @@ __global__ void __launch_bounds__(kLatentJoinThreads) paged_latent_join_kernel(c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = kLatentJoinRows * blockIdx.z + warp;
     const int ti = r / p.hb, hh = r - ti * p.hb;
+    griddep_launch_dependents();  // a next call's kernel may set itself up
     griddep_wait();
     const int4 cut = p.cut[run];
     if (cut.x < 0 || ti >= p.TQ)
         return;
-    const int row0 = p.cu_q ? __ldg(p.cu_q + cut.x) : cut.x;
-    const int n = p.cu_q ? __ldg(p.cu_q + cut.x + 1) - row0 : 1;
+    const int row0 = p.cu_q ? p.cu_q[cut.x] : cut.x;
+    const int n = p.cu_q ? p.cu_q[cut.x + 1] - row0 : 1;
     const HalfTile half(p, cut.y * 2 + rank);
     if (half.token + ti >= n || half.head + hh >= p.H)
         return;
@@ -886,14 +903,21 @@ template <int R> cudaError_t latent_resident_of(int *runs)
 template <int R>
 cudaError_t launch_latent_of(const LatentMaps &m, const LatentParams &p, cudaStream_t stream)
 {
-    paged_latent_kernel<R><<<2 * p.runs, kLatentThreads, latent_smem_bytes<R>(), stream>>>(
-        m.q, m.qr, m.k, m.kr, m.v, p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return e;
+    // (the main kernel too sets itself up under the launch before it: 4 us less a call)
     cudaLaunchAttribute overlap;
     overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     overlap.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * p.runs));  // (pairs by the kernel's cluster size)
+    cfg.blockDim = dim3(kLatentThreads);
+    cfg.dynamicSmemBytes = latent_smem_bytes<R>();
+    cfg.stream = stream;
+    cfg.attrs = &overlap;
+    cfg.numAttrs = 1;
+    const cudaError_t e =
+        cudaLaunchKernelEx(&cfg, paged_latent_kernel<R>, m.q, m.qr, m.k, m.kr, m.v, p);
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t join = {};
     join.gridDim = dim3((unsigned)p.runs, 2, kLatentRows / kLatentJoinRows);
     join.blockDim = dim3(kLatentJoinThreads);
