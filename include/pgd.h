@@ -697,6 +697,7 @@ pgd_status paged_kv_write_strided(uint16_t *k_cache, uint16_t *v_cache, const ui
  *               pair (pgd_rope_frequencies makes the usual tables, long contexts'
  *               among them)
  * rotary_dim    a multiple of 16 up to head_dim
+ * num_rows      below 2^30
  * k_cache, v_cache, strides, device checks: as for paged_kv_write.
  */
 pgd_status paged_rope_write(uint16_t *k_cache, uint16_t *v_cache, uint16_t *q_out,
@@ -724,7 +725,8 @@ pgd_status paged_rope_write(uint16_t *k_cache, uint16_t *v_cache, uint16_t *q_ou
  *                      those between in proportion to their index; magnitude 0.1 ln(factor) + 1
  *                      ("YaRN", Peng et al. 2023, section 3)
  * original_len, beta_fast > beta_slow > 0 matter to BY_PARTS alone.  Arithmetic in
- * 64 bits, rounded once.  *magnitude (if not NULL) is 1 but for BY_PARTS.  Needs no GPU.
+ * 64 bits, rounded once.  rotary_dim is even, 4 to 65536, base above 1.  *magnitude (if
+ * not NULL) is 1 but for BY_PARTS.  Needs no GPU.
  */
 #define PGD_ROPE_PLAIN 0
 #define PGD_ROPE_LINEAR 1
@@ -789,7 +791,9 @@ pgd_status paged_latent_write(uint16_t *cache, uint16_t *q_out, const uint16_t *
  *            fp16, 16-byte aligned, each with its own token and head strides (halves,
  *            positive multiples of 8 below 2^39): parts of one tensor, or a batched
  *            product's output [num_heads][total_q][latent_dim], need no copy
- * max_q_len  bound on every sequence's query rows (1 with cu_seqlens_q NULL)
+ * max_q_len  bound on every sequence's query rows (1 with cu_seqlens_q NULL).  Its tiles
+ *            of 128 rows (of queries x heads), times the table's stages of 128 tokens,
+ *            times num_seqs are to stay below 2^29 (PGD_ERR_UNSUPPORTED)
  * workspace  NULL: library scratch (per call, also in a captured graph); else at
  *            least pgd_latent_plan's bytes, 256-byte aligned, not used by anything
  *            else until the call's work is done
@@ -895,8 +899,8 @@ pgd_status pgd_test_fail_next_reduce(int enable);
 
 /*
  * pgd_test_fail_next_set_up — failure-injection test knob, on the host.  The
- * kernels of paged_gqa_tree and packed_gqa_prefill are set up on a device by the
- * first call that needs them.  When enable is non-zero, the next such set-up on
+ * kernels of paged_gqa_tree, packed_gqa_prefill, paged_latent_attention and
+ * packed_latent_prefill are set up on a device by the first call that needs them.  When enable is non-zero, the next such set-up on
  * this thread fails: its call returns PGD_ERR_CUDA, calls that need none are not
  * affected, and the next call tries again.  enable = 0 cancels a pending
  * request.  Tests only.

@@ -2063,15 +2063,16 @@ pgd_status make_latent_plan(int S, int total_q, int max_q, int H, int R, int P, 
     lp->hb = std::min(H, kLatentRows);
     lp->HB = (H + kLatentRows - 1) / kLatentRows;
     lp->TQ = H <= kLatentRows ? kLatentRows / H : 1;
-    const int most_q = std::min(max_q, total_q);
-    const long long halves = lp->HB == 1 ? (most_q + lp->TQ - 1) / lp->TQ : (long long)most_q * lp->HB;
-    const long long stages = (long long)S * ((halves + 1) / 2) *
-                             (((long long)MB * BS + kLatentNT - 1) / kLatentNT);
-    // (the kernel counts stages, and two more per unit, in 32-bit integers)
-    if (3 * stages >= (1ll << 31))
-        return fail(PGD_ERR_UNSUPPORTED, "batch of %d rows x %d heads x %lld tokens too large", total_q,
-                    H, (long long)MB * BS);
-    lp->runs = (int)std::max(1ll, std::min<long long>(resident, stages));
+    const long long most_q = std::min(max_q, total_q);
+    const long long halves = lp->HB == 1 ? (most_q + lp->TQ - 1) / lp->TQ : most_q * lp->HB;
+    const long long stages = (halves + 1) / 2 * (((long long)MB * BS + kLatentNT - 1) / kLatentNT);
+    // (the kernel counts stages, and a unit's start and end, in 32-bit integers; a unit
+    // has one stage at least)
+    constexpr long long most = (1ll << 31) / (1 + kLatentUnitCost);
+    if (S && (stages >= most || S * stages >= most))
+        return fail(PGD_ERR_UNSUPPORTED, "%d sequences of up to %lld rows x %d heads, %lld tokens: too large",
+                    S, most_q, H, (long long)MB * BS);
+    lp->runs = (int)std::max(1ll, std::min<long long>(resident, S * stages));
     const size_t rows = (size_t)2 * lp->runs * 2 * kLatentRows;
     lp->off_ml = align256(rows * R * 4);
     lp->off_cut = lp->off_ml + align256(rows * 8);

@@ -408,6 +408,11 @@ cudaError_t launch_rope_write(RopeParams p, int num_sms, cudaStream_t stream);
 // VP pieces of VKEYS tokens.  Every piece is kLatentPiece bytes; NK, NV pieces in the
 // rings, NS score buffers.
 constexpr int kLatentNT = 128, kLatentRows = 64, kLatentPiece = 16384;
+// What a unit (a tile of a sequence's rows) counts in the division of the work: its
+// stages and, in stages, its start and end.  (Of 2, 3, 4, 5 about the best: 64 requests of
+// 128 heads 63.6, 63.3, 62.2, 63.9 us, 24 of up to 5 rows 54.0, 52.7, 54.6, 54.7, 32 long
+// ones 133, 130, 131, 132.)
+constexpr int kLatentUnitCost = 3;
 template <int R> struct LatentShape {
     static constexpr int KSLABS = 2, KP = R / 128;
     static constexpr int VSLABS = R / 128, VKEYS = 128 / VSLABS, VP = VSLABS;

@@ -83,10 +83,6 @@ __device__ __forceinline__ LatentSeq latent_seq(const LatentParams &p, int s)
     q.tiles = (p.half_tiles(q.n) + 1) / 2;
     return q;
 }
-// What a unit counts in the division of the work: its stages and, in stages, its
-// start and end.  (Of 2, 3, 4, 5 about the best: 64 requests of 128 heads 63.6, 63.3, 62.2, 63.9
-// us, 24 of up to 5 rows 54.0, 52.7, 54.6, 54.7, 32 long ones 133, 130, 131, 132.)
-constexpr int kLatentUnitCost = 3;
 __device__ __forceinline__ int latent_cost(const LatentSeq &q)
 {
     return q.tiles * (q.T + kLatentUnitCost);
@@ -204,8 +200,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
 
     extern __shared__ __align__(1024) uint8_t dyn_smem[];
     // (the even CTA's q_full, k_full, v_full, s_free, z_full, p_full and o_free count for both)
-    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], z_go, z_full, s_full[NS], s_free[NS], p_full[2], o_done[2], o_free,
-        mma_done;
+    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV],
+        v_empty[NV], z_go, z_full, s_full[NS], s_free[NS], p_full[2], o_done[2], o_free, mma_done;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag;
     __shared__ float red[2][4][ROWS];  // [parity][quarter of a stage's tokens][row]
