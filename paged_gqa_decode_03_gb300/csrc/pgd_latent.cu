@@ -360,6 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
             }
         } else {
             const uint64_t pol = l2_evict_last_policy();
+            const uint32_t lead_k = lead(k_full);
             const int grp = p.BS == 2 * ROWS ? rank * (ROWS / 8) : 0;
             auto load_q = [&] {
                 if (!wait(&q_empty, (nq & 1) ^ 1))
@@ -389,30 +390,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                 for (int t = walk.t; t < walk.t_end; ++t) {
                     const int page = checked(id, there);
                     id = page_at(walk, (t + 1) * NT, there);
-#pragma unroll 1
-                    for (int kp = 0; kp < KP; ++kp, ++nst) {
-                        const int st = nst % NK;
-                        if (!wait(&k_empty[st], ((nst / NK) & 1) ^ 1))
-                            break;
-                        const uint32_t bar = lead(&k_full[st]);
+                    const int page0 = __shfl_sync(~0u, page, 0);
+                    int made = 0;
+#pragma unroll
+                    for (int kp = 0; kp < KP; ++kp) {
+                        // (a stage's pieces lie in the ring's first or second half, or all of it)
+                        const int st = KP == NK ? kp : (nst + kp) % NK;
+                        const uint32_t parity = ((KP == NK ? nst / NK : (nst + kp) / NK) & 1) ^ 1;
+                        if (!ok || !wait(&k_empty[st], parity))
+                            continue;
+                        ++made;
+                        const uint32_t bar = lead_k + 8 * st;
                         if (rank == 0 && elect_one())
-                            mbar_arrive_expect_tx(smem_addr(&k_full[st]),
+                            mbar_arrive_expect_tx(smem_addr(k_full) + 8 * st,
                                                   2 * (PIECE + (kp == 0 ? ROWS * 128 : 0)));
-                        for (int c = 0; c < copies; ++c) {
-                            const int pg = __shfl_sync(~0u, page, c);
+                        if (copies == 1) {
                             if (elect_one()) {
                                 if (kp == 0)  // the rotary keys with the stage's first piece
-                                    tma_load_4d_pair(r_s + (st / KP * ROWS + c * rows) * 128,
-                                                     &tmap_kr, 0, 0, grp, pg, bar);
-                                tma_load_5d_pair(k_s + st * PIECE + c * copy_bytes, &tmap_k, 0, 0,
-                                                 kp * KSLABS, grp, pg, bar, pol);
+                                    tma_load_4d_pair(r_s + st / KP * ROWS * 128, &tmap_kr, 0, 0, grp,
+                                                     page0, bar);
+                                tma_load_5d_pair(k_s + st * PIECE, &tmap_k, 0, 0, kp * KSLABS, grp,
+                                                 page0, bar, pol);
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int c = 0; c < copies; ++c) {
+                                const int pg = __shfl_sync(~0u, page, c);
+                                if (elect_one()) {
+                                    if (kp == 0)
+                                        tma_load_4d_pair(r_s + (st / KP * ROWS + c * rows) * 128,
+                                                         &tmap_kr, 0, 0, grp, pg, bar);
+                                    tma_load_5d_pair(k_s + st * PIECE + c * copy_bytes, &tmap_k, 0, 0,
+                                                     kp * KSLABS, grp, pg, bar, pol);
+                                }
                             }
                         }
                         // Q after the unit's first K: its place is free only after the last
                         // unit's last scores, and no place for K comes free before it
-                        if (nq_from > 0 && t == walk.t && kp == (KP < NK ? KP : NK) - 1 && !load_q())
-                            break;
+                        if (kp == (KP < NK ? KP : NK) - 1 && nq_from > 0 && t == walk.t)
+                            load_q();
                     }
+                    nst += made;
                     if (!ok)
                         break;
                 }
@@ -740,28 +758,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                 if (lane == 0)
                     mbar_arrive_cluster<false>(lead(&o_free));
             };
-            // where the rows go that this thread writes together with its neighbours
-            RowOut rows;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 32 * (quarter & 1) + (lane & ~3) + i;
-                const int tok = row / p.hb, head = row - tok * p.hb;
-                const bool there = tok < p.TQ && half.token + tok < q.n && half.head + head < p.H;
-                char *at = whole ? static_cast<char *>(p.out) +
-                                       ((size_t)(q.row0 + half.token + tok) * p.H + half.head + head) *
-                                           row_bytes
-                                 : reinterpret_cast<char *>(p.part_o + (piece * ROWS + row) * R);
-                rows.at[i] = there ? at : nullptr;
-            }
-            // a store takes 64 columns at least: at R 128 the first half's warps write
-            // all of a lane's
-            constexpr int WC = R == 128 ? 64 : OC;
-            const int col = R == 128 ? 0 : ch * OC;
-            if (R == 128 && ch == 1)
-                read();
-            else
-                write_rows<WC>(rows, whole && p.out_half, !whole || p.wide_rows, t_lane + O_COL + col,
-                               h * (R / 2) + col, !whole ? 1.f : lt > 0.f ? 1.f / lt : 0.f, lane, read);
+            const size_t row =
+                whole ? (size_t)(q.row0 + token) * p.H + half.head + hh : piece * ROWS + r;
+            char *const dst = whole ? static_cast<char *>(p.out) + row * row_bytes
+                                    : reinterpret_cast<char *>(p.part_o) + row * R * 4;
+            const bool half_out = whole && p.out_half;
+            write_own_row<OC>(row_ok ? dst + (h * (R / 2) + ch * OC) * (half_out ? 2 : 4) : nullptr,
+                              half_out, !whole || p.wide_rows, t_lane + O_COL + ch * OC,
+                              !whole ? 1.f : lt > 0.f ? 1.f / lt : 0.f, read);
             if (!whole) {
                 // (-inf says that there is nothing to join; scores that are all NaN leave
                 // it too, with a sum of NaN, which is to reach the output)

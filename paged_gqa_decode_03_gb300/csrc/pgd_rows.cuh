@@ -96,6 +96,58 @@ __device__ __forceinline__ void write_rows(const RowOut &o, bool half, bool wide
     }
 }
 
+// The same without the exchange: each lane writes its own row's columns, 32 at a time
+// (dst: where the first goes, or null).  A store touches 32 lines, but whole sectors of
+// each, and the code is a quarter as long: for kernels in which it runs between long
+// loops, fetched anew each time (latent prompts: 37 short ones 32.5 -> 29.5 us, 4 x 2048
+// 169 -> 162, 16381 tokens 897 -> 867).
+__device__ __forceinline__ void store_8_words(char *dst, const uint32_t *w, bool wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {  // an output that starts on 16 bytes only
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(dst + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+template <int COLS, class F>
+__device__ __forceinline__ void write_own_row(char *dst, bool half, bool wide, uint32_t taddr,
+                                              float inv, F &&last)
+{
+    static_assert(COLS % 32 == 0, "32 columns at a time");
+#pragma unroll 1
+    for (int c = 0; c < COLS; c += 32) {
+        float v[32];
+        uint32_t w[32];
+        tc_ld32(taddr + c, v);
+        tc_wait_ld();
+        tc_ld_ready(v);
+        if (c + 32 == COLS)
+            last();
+        if (half) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i] = pack_half2(v[2 * i] * inv, v[2 * i + 1] * inv);
+            if (dst) {
+                store_8_words(dst + 2 * c, w, wide);
+                store_8_words(dst + 2 * c + 32, w + 8, wide);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                w[i] = __float_as_uint(v[i] * inv);
+            if (dst) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+                    store_8_words(dst + 4 * c + 4 * i, w + i, wide);
+            }
+        }
+    }
+}
+
 // Where the rows of a warp's quarter of a tile (TQ tokens x the G heads of a KV
 // head) lie in out [tokens][Hq][row_bytes], from the tile's first token and head
 // on: the same for every tile, so worked out once.
