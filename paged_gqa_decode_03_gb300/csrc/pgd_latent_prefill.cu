@@ -14,7 +14,20 @@
 //   * The queries of two tiles, head_dim 128 with its rotary part, take 96 KB, so K and
 //     V move in pieces of 16 KB, K by 64-wide slabs (the last of them the rotary keys,
 //     from a tensor without heads), V by 64 keys: eight places, five for K, three for V.
-//   * Products, copies and commits are issued by an elected lane (see elect_one).
+//     Each tile's queries come as soon as its own last scores of the unit before are done.
+//   * Products, copies and commits are issued by an elected lane (see elect_one), all of
+//     a product's together: a wait between them costs more than a piece's products.
+//   * What runs once a unit (the causal border, the zeroed tail, the output) is short
+//     loops outside the loop over stages: long unrolled code is fetched anew each time.
+//     The border written into the loop's 128 scores took a tile's last stage 3900 cycles
+//     where a stage takes 1300, and slowed the loop by its mere presence.
+//
+// Measured, head_dim 128 (rope_dim 64): one prompt of 16381 tokens x 16 heads 815 us (1685
+// TFLOP/s; 88 % of what a large library product reaches here), 4 x 2048 x 32 heads 155,
+// 37 prompts of 1 to 512 tokens x 16 heads 33.  By clock stamps a period of both tiles takes
+// 2600 to 2900 cycles, of which the products take 2560: the tensor cores bound it.  A short
+// unit is bound by its chain instead (queries and first keys, scores, softmax, product,
+// output: 6000 cycles), a call by the order kernel and the first copies in front (5 us).
 #include <algorithm>
 
 #include "pgd_device.cuh"
@@ -67,11 +80,10 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
     constexpr uint32_t IDESC_O = tc_idesc_f16(128, D, 0, 1);
 
     extern __shared__ uint8_t dyn_smem[];
-    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV],
+    __shared__ __align__(8) uint64_t q_full[2], q_empty[2], k_full[NK], k_empty[NK], v_full[NV],
         v_empty[NV], s_full[2], s_free[2], p_full[2], z_go[2], z_full[2], o_done[2], o_free[2], mma_done;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag;
-    __shared__ volatile int s_issued[2];  // S products issued for each tile
 
     const uint32_t dyn_base = smem_addr(dyn_smem);
     const uint32_t base = (dyn_base + 1023u) & ~1023u;
@@ -81,8 +93,6 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
 
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        mbar_init(smem_addr(&q_full), 1);
-        mbar_init(smem_addr(&q_empty), 1);
         for (int i = 0; i < NK; ++i) {
             mbar_init(smem_addr(&k_full[i]), 1);
             mbar_init(smem_addr(&k_empty[i]), 1);
@@ -92,6 +102,8 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
             mbar_init(smem_addr(&v_empty[i]), 1);
         }
         for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_addr(&q_full[x]), 1);
+            mbar_init(smem_addr(&q_empty[x]), 1);
             mbar_init(smem_addr(&s_full[x]), 1);
             mbar_init(smem_addr(&s_free[x]), 4);
             mbar_init(smem_addr(&p_full[x]), 4);
@@ -101,7 +113,6 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
             mbar_init(smem_addr(&o_free[x]), 4);
         }
         mbar_init(smem_addr(&mma_done), 2);
-        s_issued[0] = s_issued[1] = 0;
         abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&tmap_q);
@@ -153,13 +164,13 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
             const uint64_t pol = l2_evict_last_policy();
             uint64_t *full = is_v ? v_full : k_full;
             const int slots = is_v ? NV : NK;
-            int n = 0, nq = 0;   // copies issued so far
+            int n = 0, nq[2] = {0, 0};   // copies issued so far
             bool ok = true;
             auto wait = [&](uint64_t *bar, int parity) {
                 return mbar_wait_bounded(smem_addr(bar), parity, &abort_flag, p.wait_budget_ns);
             };
-            auto load_k = [&](int row, int head) {
-                for (int kp = 0; kp < KP; ++kp, ++n) {
+            auto load_k = [&](int row, int head, int from, int to) {
+                for (int kp = from; kp < to; ++kp, ++n) {
                     const int st = n % NK;
                     if (!wait(&k_empty[st], ((n / NK) & 1) ^ 1))
                         return false;
@@ -197,28 +208,31 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
                         ok = load_v(row0 + j * kNT, head);
                     continue;
                 }
-                // the unit's first K goes out before its Q, whose place is
-                // free only after the last unit's last S
-                ok = load_k(row0, head) && wait(&q_empty, (nq & 1) ^ 1);
-                if (!ok)
-                    break;
-                const int ntq = u.z > kTile ? 2 : 1;
-                const uint32_t bar = smem_addr(&q_full);
-                mbar_arrive_expect_tx(bar, ntq * Q_TILE);
-                for (int x = 0; x < ntq; ++x) {
+                // A tile's place for Q is free after the last unit's last scores of that
+                // tile: tile A's comes before the last of the first K, tile B's behind it
+                auto load_q = [&](int x) {
+                    if (!wait(&q_empty[x], (nq[x] & 1) ^ 1))
+                        return false;
+                    const uint32_t bar = smem_addr(&q_full[x]);
+                    mbar_arrive_expect_tx(bar, Q_TILE);
                     tma_load_4d(q_s + x * Q_TILE, &tmap_q, 0, u.x + x * kTile, 0, head, bar);
                     tma_load_4d(q_s + x * Q_TILE + SLABS * kSlab, &tmap_qr, 0, u.x + x * kTile, 0, head,
                                 bar);
-                }
-                ++nq;
+                    ++nq[x];
+                    return true;
+                };
+                ok = load_k(row0, head, 0, KP - 1) && load_q(0) && load_k(row0, head, KP - 1, KP) &&
+                     (u.z <= kTile || load_q(1));
                 for (int j = 1; j < nt && ok; ++j)
-                    ok = load_k(row0 + j * kNT, head);
+                    ok = load_k(row0 + j * kNT, head, 0, KP);
             }
             if (!ok) {
                 give_up();
                 // let the copies in flight land before the CTA exits
-                if (nq)
-                    mbar_wait_bounded(smem_addr(&q_full), (nq - 1) & 1, nullptr, p.wait_budget_ns);
+                for (int x = 0; x < 2; ++x)
+                    if (nq[x])
+                        mbar_wait_bounded(smem_addr(&q_full[x]), (nq[x] - 1) & 1, nullptr,
+                                          p.wait_budget_ns);
                 for (int i = max(0, n - slots); i < n; ++i)
                     mbar_wait_bounded(smem_addr(&full[i % slots]), (i / slots) & 1, nullptr,
                                       p.wait_budget_ns);
@@ -241,9 +255,8 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
             const uint32_t idesc_s = IDESC_S | (p.scale_log2 < 0.f ? kNegateA : 0u);
             const uint64_t q_desc = tc_sdesc(q_s, 16, 1024);
             const uint64_t k_desc = tc_sdesc(k_s, 16, 1024);
-            int nk = 0, nq = 0;        // K pieces, Q pairs used up
+            int nk = 0, nq[2] = {0, 0};  // K pieces, Q tiles used up
             int uses[2] = {0, 0};      // of each score buffer
-            int ns[2] = {0, 0};        // S products of each tile
             for (int k = 0; k < turns && ok; ++k) {
                 const int ui = unit_of(k);
                 const int4 u = next;
@@ -251,29 +264,35 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
                 if (ui >= units)
                     continue;
                 const int nt0 = stages(u, 0), nt1 = stages(u, 1), nmax = max(nt0, nt1);
-                wait(&q_full, nq & 1);
-                ++nq;
                 for (int j = 0; j < nmax && ok; ++j, nk += KP) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const bool last_user = x == 1 || j >= nt1;
                         if (j >= (x ? nt1 : nt0) || !ok)
                             continue;
+                        // (all waits come first: groups of products with a wait between them
+                        // reach the pipe 300 cycles apart, more than a group's 256)
+                        if (j == 0 && !wait(&q_full[x], nq[x]++ & 1))
+                            continue;
+                        if (x == 0 || j >= nt0)
+                            for (int kp = 0; kp < KP; ++kp)
+                                wait(&k_full[(nk + kp) % NK], ((nk + kp) / NK) & 1);
                         // the buffer's last scores have been read
                         const int b = SBUF == 2 ? x : 0;
                         if (uses[b] && !wait(&s_free[b], (uses[b] - 1) & 1))
                             continue;
                         ++uses[b];
+                        if (!ok)
+                            continue;
                         const uint64_t qx = q_desc + ((x * Q_TILE) >> 4);
                         const uint32_t d = tmem + S_COL + b * kNT;
-                        for (int kp = 0; kp < KP; ++kp) {
-                            const int st = (nk + kp) % NK;
-                            if (!wait(&k_full[st], ((nk + kp) / NK) & 1))
-                                break;
-                            tc_fence_after();
-                            const uint64_t ks = k_desc + ((st * PIECE) >> 4);
-                            const uint64_t qs = qx + ((kp * kSlab) >> 4);
-                            if (elect_one()) {
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kp = 0; kp < KP; ++kp) {
+                                const int st = (nk + kp) % NK;
+                                const uint64_t ks = k_desc + ((st * PIECE) >> 4);
+                                const uint64_t qs = qx + ((kp * kSlab) >> 4);
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
                                     tc_mma(d, qs + ((kk * 32) >> 4), ks + ((kk * 32) >> 4), idesc_s,
@@ -283,14 +302,12 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
                                 if (last_user)
                                     tc_commit(smem_addr(&k_empty[st]));
                             }
-                            __syncwarp();
+                            if (j == (x ? nt1 : nt0) - 1)
+                                tc_commit(smem_addr(&q_empty[x]));
                         }
-                        s_issued[x] = ++ns[x];
+                        __syncwarp();
                     }
                 }
-                if (elect_one())
-                    tc_commit(smem_addr(&q_empty));
-                __syncwarp();
             }
         } else {
             const uint64_t v_desc = tc_sdesc(v_s, VKEYS * 128, 1024);
@@ -325,13 +342,6 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
                         if (steps == kNT / 16 && !tail) {
                             for (int vp = 0; vp < VP; ++vp)
                                 wait(&v_full[(nv + vp) % NV], ((nv + vp) / NV) & 1);
-                            // The tile's next scores go first: they are on the path that
-                            // sets the period, and this product fills the time in which
-                            // the softmax reads them out.  Only a matter of order, so the
-                            // look is short and goes on either way.
-                            if (!last)
-                                for (int i = 0; i < 256 && s_issued[x] <= np[x]; ++i)
-                                    ;
                             if (!ok)
                                 continue;
                             tc_fence_after();
@@ -406,7 +416,6 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
         // give 0
         const float sc = p.scale_log2 == 0.f ? 1e-30f : fabsf(p.scale_log2);
         const float2 sc2 = make_float2(sc, sc);
-        const RowPlaces places(row_bytes, p.Hq, 1, kTile, quarter, lane);
         int ns = 0, nv = 0, nz = 0;  // S tiles of this tile, V pieces of the CTA, zeroed tails so far
         bool ok = true;
         int4 next = unit_at(p, 0, units);
@@ -422,116 +431,133 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
             const int n = u.y + u.z;                     // tokens of the prompt
             const bool row_ok = r < left;
             const int lo = u.y + x * kTile;          // position of the tile's first token
-            const int lim = row_ok ? lo + r : -1;  // and of this row's
             float m_ref = -INFINITY, l = 0.f;
-            for (int j = 0; j < ntx; ++j, ++ns) {
-                const int t0 = j * kNT;
-                // wait outcomes are warp-uniform: tensor-memory loads and
-                // stores are warp-collective
-                if (!__all_sync(~0u, mbar_wait_bounded(smem_addr(&s_full[x]), ns & 1, &abort_flag,
-                                                       p.wait_budget_ns))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                float v[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tc_ld32(t_lane + s_col + 32 * c, v[c]);
-                tc_wait_ld();
-                // the scores are in registers: the buffer takes the next ones
-                tc_fence_before();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&s_free[SBUF == 2 ? x : 0]));
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tc_ld_ready(v[c]);
-                // where the causal border crosses this stage: 32 keys at a time
-                if (t0 + kNT - 1 > lo) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (t0 + 32 * c + 31 > lo) {
-                            const uint32_t seen = first_bits(lim + 1 - (t0 + 32 * c));
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[c][i] = (seen >> i) & 1u ? v[c][i] : -INFINITY;
-                        }
-                }
-                // has this tile's last P V ended?  (asked here, used below)
-                const bool pv_over =
-                    j == 0 || mbar_try_wait(smem_addr(&o_done[x]), (ns - 1) & 1);
-                const float mt = max128(v) * sc;
-                // the reference moves only when the maximum has grown by more
-                // than 8 (log2 units): O is rescaled rarely
-                bool rescale = false;
-                float alpha = 1.f;
-                if (mt > m_ref + kRefRoom) {
-                    const float ref = mt - kRefBelow;
-                    rescale = row_ok && m_ref != -INFINITY;
-                    alpha = rescale ? ex2(m_ref - ref) : 1.f;
-                    m_ref = ref;
-                }
-                const float off = m_ref == -INFINITY ? 0.f : -m_ref;
-                const float2 off2 = make_float2(off, off);
-                float2 sum2 = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float2 a = ffma2(make_float2(v[2 * h + c][i], v[2 * h + c][i + 1]), sc2,
-                                             off2);
-                            a.x = ex2(a.x);
-                            a.y = ex2(a.y);
-                            pk[16 * c + i / 2] = pack_half2(a.x, a.y);
-                            sum2 = fadd2(sum2, a);
-                        }
-                    }
-                    if (h == 0 && j > 0) {
-                        // this tile's last P V is done with P (and O may be rescaled)
-                        if (!__all_sync(~0u, pv_over) &&
-                            !__all_sync(~0u, mbar_wait_bounded(smem_addr(&o_done[x]), (ns - 1) & 1,
-                                                               &abort_flag, p.wait_budget_ns))) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                    }
-                    tc_st32u(t_lane + p_col + 32 * h, pk);
-                }
-                if (!ok)
-                    break;
-                if (j > 0 && __any_sync(~0u, rescale)) {
+            int j = 0;
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        tc_ld32(t_lane + o_col + 32 * c, o);
-                        tc_wait_ld();
-                        tc_ld_ready(o);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] *= alpha;
-                        tc_st32(t_lane + o_col + 32 * c, o);
-                    }
-                }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&p_full[x]));
-                // Rows behind the prompt belong to the next one and may hold anything: those
-                // that the tile's last step takes in are zeroed in V (their weights are 0,
-                // which does not hide a NaN), when the products have come to their piece.
-                const int za = n - t0, ze = j + 1 < ntx ? 0 : 16 * last_steps(u, x);
-                if (za < ze) {
-                    if (!__all_sync(~0u, mbar_wait_bounded(smem_addr(&z_go[x]), nz++ & 1, &abort_flag,
+            for (int part = 0; part < 2 && ok && ntx > 0; ++part) {
+                if (part == 1) {
+                    // The causal border crosses a tile's last stage alone (tiles and stages begin at
+                    // multiples of 128): of a warp's 32 rows it cuts the warp's own 32 keys, the rows
+                    // see all keys before and none behind.  The scores behind it are replaced where
+                    // they lie, in a loop of few instructions: they run once a unit, cold.
+                    if (!__all_sync(~0u, mbar_wait_bounded(smem_addr(&s_full[x]), ns & 1, &abort_flag,
                                                            p.wait_budget_ns))) {
                         ok = false;
                         break;
                     }
-                    const int vp = za / VKEYS, st = (nv + j * VP + vp) % NV;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = quarter; c < 4; ++c) {
+                        const int seen = 32 * (quarter - c) + lane;
+                        float w[32];
+                        tc_ld32(t_lane + s_col + 32 * c, w);
+                        tc_wait_ld();
+                        tc_ld_ready(w);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            w[i] = i <= seen ? w[i] : -INFINITY;
+                        tc_st32(t_lane + s_col + 32 * c, w);
+                    }
+                    tc_wait_st();
+                }
+                for (const int end = ntx - 1 + part; j < end; ++j, ++ns) {
+                    // wait outcomes are warp-uniform: tensor-memory loads and
+                    // stores are warp-collective
+                    if (!__all_sync(~0u, mbar_wait_bounded(smem_addr(&s_full[x]), ns & 1, &abort_flag,
+                                                           p.wait_budget_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    float v[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tc_ld32(t_lane + s_col + 32 * c, v[c]);
+                    tc_wait_ld();
+                    // the scores are in registers: the buffer takes the next ones
+                    tc_fence_before();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&s_free[SBUF == 2 ? x : 0]));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tc_ld_ready(v[c]);
+                    // has this tile's last P V ended?  (asked here, used below)
+                    const bool pv_over =
+                        j == 0 || mbar_try_wait(smem_addr(&o_done[x]), (ns - 1) & 1);
+                    const float mt = max128(v) * sc;
+                    // the reference moves only when the maximum has grown by more
+                    // than 8 (log2 units): O is rescaled rarely
+                    bool rescale = false;
+                    float alpha = 1.f;
+                    if (mt > m_ref + kRefRoom) {
+                        const float ref = mt - kRefBelow;
+                        rescale = row_ok && m_ref != -INFINITY;
+                        alpha = rescale ? ex2(m_ref - ref) : 1.f;
+                        m_ref = ref;
+                    }
+                    const float off = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const float2 off2 = make_float2(off, off);
+                    float2 sum2 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                float2 a = ffma2(make_float2(v[2 * h + c][i], v[2 * h + c][i + 1]), sc2,
+                                                 off2);
+                                a.x = ex2(a.x);
+                                a.y = ex2(a.y);
+                                pk[16 * c + i / 2] = pack_half2(a.x, a.y);
+                                sum2 = fadd2(sum2, a);
+                            }
+                        }
+                        if (h == 0 && j > 0) {
+                            // this tile's last P V is done with P (and O may be rescaled)
+                            if (!__all_sync(~0u, pv_over) &&
+                                !__all_sync(~0u, mbar_wait_bounded(smem_addr(&o_done[x]), (ns - 1) & 1,
+                                                                   &abort_flag, p.wait_budget_ns))) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                        }
+                        tc_st32u(t_lane + p_col + 32 * h, pk);
+                    }
+                    if (!ok)
+                        break;
+                    if (j > 0 && __any_sync(~0u, rescale)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+                            tc_ld32(t_lane + o_col + 32 * c, o);
+                            tc_wait_ld();
+                            tc_ld_ready(o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] *= alpha;
+                            tc_st32(t_lane + o_col + 32 * c, o);
+                        }
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&p_full[x]));
+                    l = l * alpha + (sum2.x + sum2.y);
+                }
+            }
+            // Rows behind the prompt belong to the next one and may hold anything: those
+            // that the tile's last step takes in are zeroed in V (their weights are 0,
+            // which does not hide a NaN), when the products have come to their piece.
+            const int za = n - lo, ze = 16 * last_steps(u, x);
+            if (ok && ntx > 0 && za < ze) {
+                if (!__all_sync(~0u, mbar_wait_bounded(smem_addr(&z_go[x]), nz++ & 1, &abort_flag,
+                                                       p.wait_budget_ns))) {
+                    ok = false;
+                } else {
+                    const int vp = za / VKEYS, st = (nv + (ntx - 1) * VP + vp) % NV;
                     uint8_t *vs = v_ptr + st * PIECE;
                     for (int idx = r; idx < (ze - za) * SLABS * 8; idx += 128) {
                         const int row = za - vp * VKEYS + idx / (SLABS * 8), c = idx % (SLABS * 8);
@@ -543,7 +569,6 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
                     if (lane == 0)
                         mbar_arrive(smem_addr(&z_full[x]));
                 }
-                l = l * alpha + (sum2.x + sum2.y);
             }
             // ---- out = O / l
             if (ok && ntx > 0) {
@@ -552,14 +577,16 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
                 if (ok) {
                     tc_fence_after();
                     const float inv = l > 0.f ? 1.f / l : 0.f;
-                    const RowOut rows =
-                        places.at(out + ((size_t)(u.x + x * kTile) * p.Hq + head) * row_bytes, left);
-                    write_rows<D>(rows, half_out, p.wide_rows, t_lane + o_col, 0, inv, lane, [&] {
+                    auto read = [&] {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
                             mbar_arrive(smem_addr(&o_free[x]));
-                    });
+                    };
+                    char *const dst =
+                        out + ((size_t)(u.x + x * kTile + r) * p.Hq + head) * row_bytes;
+                    write_own_row<D>(row_ok ? dst : nullptr, half_out, p.wide_rows, t_lane + o_col,
+                                     inv, read);
                 }
             }
             nv += VP * max(nt0, nt1);

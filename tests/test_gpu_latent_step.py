@@ -395,3 +395,49 @@ def test_set_up_in_a_process_of_its_own(R, D, code):
     r = subprocess.run([sys.executable, "-c", text, str(R), str(D)], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "as it should" in r.stdout, r.stdout + r.stderr[-3000:]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_outputs_that_start_on_16_bytes(dtype):
+    """16 bytes past a 32-byte boundary, where rows go out in stores of 16 bytes; what lies
+    in front and behind is left alone."""
+    step = 16 // torch.empty(0, dtype=dtype).element_size()
+
+    def room(shape):
+        n = int(np.prod(shape))
+        flat = torch.full((n + 4 * step,), 3.0, dtype=dtype, device=DEV)
+        assert flat.data_ptr() % 32 == 0
+        return flat, flat[step:step + n].view(shape)
+    for lens, new, R in (([700, 3], [2, 3], 512), ([129, 5000], [1, 1], 128)):
+        w = LatentCase(lens, new, 20, R, 64, 16, seed=50)
+        flat, out = room((w.T, w.H, R))
+        pgd.paged_latent_attention(out, w.q, w.q_rope, w.cache, w.tables, w.seq_lens, w.scale,
+                                   cu_seqlens_q=w.cu, max_q_len=max(new))
+        torch.cuda.synchronize()
+        w.check(out, "absorbed")
+        assert (flat[:step] == 3.0).all() and (flat[step + out.numel():] == 3.0).all()
+    for D in (64, 128):
+        c = Prompts([130, 300, 1], 3, D, seed=51)
+        flat, out = room((c.T, c.H, D))
+        pgd.packed_latent_prefill(out, c.q, c.k, c.k_rope, c.v, c.cu, c.scale, 300)
+        torch.cuda.synchronize()
+        c.check(out, "expanded")
+        assert (flat[:step] == 3.0).all() and (flat[step + out.numel():] == 3.0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("seed", range(6))
+def test_drawn_prompts(D, seed):
+    rng = random.Random(100 + seed)
+    hi = rng.choice([1, 130, 260, 700, 2500])
+    lens = [rng.randint(0 if rng.random() < 0.3 else 1, hi) for _ in range(rng.choice([1, 5, 40]))]
+    if not sum(lens):
+        lens[0] = 1
+    H = rng.choice([1, 3, 8, 20])
+    c = Prompts(lens, H, D, rng.choice([32, 64]), seed=seed, between=rng.choice([0, 5]),
+                behind=rng.choice([0, 3]))
+    dtype = rng.choice([torch.float16, torch.float32])
+    first = c.run(dtype=dtype)
+    c.check(first, "drawn", heads=sorted({0, H - 1}))
+    again = c.run(dtype=dtype, max_len=max(lens) + 7)
+    assert torch.equal(torch.nan_to_num(again, nan=9.0), torch.nan_to_num(first, nan=9.0))
