@@ -34,14 +34,16 @@
 //     16 KB of shared memory.  (Weights in shared memory: 48 cycles a score product in
 //     their bandwidth's share, and no room for two stages.)
 //
-// Measured: 32 requests of 8 k to 32 k tokens with 16 heads 128 us (602 MB: 4.7 TB/s;
-// HBM's floor 97), 64 of 512 to 4096 tokens with 128 heads 62, 24 of up to 8 k tokens
-// with up to 5 rows of 32 heads 55, one of 1000 tokens 18 (of it 16 in every call: the
-// runs' division 2, the first pages, copies and Q 5, the last softmax and outputs 4, the
+// Measured in a graph: 32 requests of 8 k to 32 k tokens with 16 heads 124.5 us (655 MB: 5.3
+// TB/s; HBM's floor 97), 64 of 512 to 4096 tokens with 128 heads 61.5, 24 of up to 8 k tokens
+// with up to 5 rows of 32 heads 47, one of 1000 tokens 15 (nearly all of it in every call:
+// the runs' division 2, the first pages, copies and Q 4, the last softmax and outputs 3, the
 // joining kernel 4).  What bounds a long run is the chain of a piece (its place free, its
 // copy of 16 KB issued, arrived, used): 64 KB of K in flight an SM.  Other divisions of
-// the same memory: pieces of 32 KB for K, two of them, 143 us, but 51 for the 24 requests;
-// Q's place cut to a tile's rows where they are few and longer rings 132 and 57.
+// the same memory, against 126: pieces of 32 KB for K, two of them, 143; Q's place cut to a
+// tile's rows where they are few and longer rings 132.
+#include <type_traits>
+
 #include "pgd_device.cuh"
 #include "pgd_internal.h"
 #include "pgd_rows.cuh"
@@ -305,10 +307,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
         // ============================================================ copies
         // warp 0: Q, the latent part as K by slabs of this CTA's 64 tokens, the rotary
         // keys; warp 1: the latent part as V, tokens of this CTA's half of the values.
-        // A piece is a copy per page (or one copy, where pages are longer): lane c
-        // issues copy c.
-        // (barriers are tested by all lanes, copies issued by an elected one, their pages
-        // handed round: whatever a single lane does by itself costs it hundreds of cycles)
+        // A piece is a copy per page (or one copy, where pages are longer).
+        // (barriers are tested by all lanes, copies issued by an elected one, a piece's all
+        // together, their pages handed round: whatever a single lane does by itself costs
+        // it hundreds of cycles, and each choice of one some tens)
         const bool is_v = warp == 1;
         const int rows = is_v ? p.v_rows : p.k_rows;
         const int copies = (is_v ? VKEYS : ROWS) / rows;
@@ -348,14 +350,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                     if (!wait(&v_empty[st], ((nst / NV) & 1) ^ 1))
                         break;
                     const uint32_t bar = lead(&v_full[st]);
-                    if (rank == 0 && elect_one())  // for both CTAs' copies
-                        mbar_arrive_expect_tx(smem_addr(&v_full[st]), 2 * PIECE);
-                    for (int c = 0; c < copies; ++c) {
-                        const int pg = __shfl_sync(~0u, page, c);
-                        if (elect_one())
-                            tma_load_5d_pair(v_s + st * PIECE + c * copy_bytes, &tmap_v, 0, 0,
-                                             rank * VSLABS, grp, pg, bar, last_use);
+                    int pages[VKEYS / 8];
+#pragma unroll
+                    for (int c = 0; c < VKEYS / 8; ++c)
+                        pages[c] = __shfl_sync(~0u, page, c);
+                    if (elect_one()) {
+                        if (rank == 0)  // for both CTAs' copies
+                            mbar_arrive_expect_tx(smem_addr(&v_full[st]), 2 * PIECE);
+#pragma unroll
+                        for (int c = 0; c < VKEYS / 8; ++c)
+                            if (c < copies)
+                                tma_load_5d_pair(v_s + st * PIECE + c * copy_bytes, &tmap_v, 0, 0,
+                                                 rank * VSLABS, grp, pages[c], bar, last_use);
                     }
+                    __syncwarp();
                 }
             }
         } else {
@@ -390,46 +398,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                 for (int t = walk.t; t < walk.t_end; ++t) {
                     const int page = checked(id, there);
                     id = page_at(walk, (t + 1) * NT, there);
-                    const int page0 = __shfl_sync(~0u, page, 0);
                     int made = 0;
+                    // (copies of a piece as a constant, so that their code has no tests: pages of
+                    // 16 rows 54.7 -> 48.1 us for 24 requests of up to 5 rows)
+                    auto stage = [&](auto n) {
+                        constexpr int C = decltype(n)::value;
+                        int pages[C];
 #pragma unroll
-                    for (int kp = 0; kp < KP; ++kp) {
-                        // (a stage's pieces lie in the ring's first or second half, or all of it)
-                        const int st = KP == NK ? kp : (nst + kp) % NK;
-                        const uint32_t parity = ((KP == NK ? nst / NK : (nst + kp) / NK) & 1) ^ 1;
-                        if (!ok || !wait(&k_empty[st], parity))
-                            continue;
-                        ++made;
-                        const uint32_t bar = lead_k + 8 * st;
-                        if (rank == 0 && elect_one())
-                            mbar_arrive_expect_tx(smem_addr(k_full) + 8 * st,
-                                                  2 * (PIECE + (kp == 0 ? ROWS * 128 : 0)));
-                        if (copies == 1) {
+                        for (int c = 0; c < C; ++c)
+                            pages[c] = __shfl_sync(~0u, page, c);
+#pragma unroll
+                        for (int kp = 0; kp < KP; ++kp) {
+                            // (a stage's pieces lie in the ring's first or second half, or all of it)
+                            const int st = KP == NK ? kp : (nst + kp) % NK;
+                            const uint32_t parity = ((KP == NK ? nst / NK : (nst + kp) / NK) & 1) ^ 1;
+                            if (!ok || !wait(&k_empty[st], parity))
+                                continue;
+                            ++made;
+                            const uint32_t bar = lead_k + 8 * st;
+                            if (rank == 0 && elect_one())
+                                mbar_arrive_expect_tx(smem_addr(k_full) + 8 * st,
+                                                      2 * (PIECE + (kp == 0 ? ROWS * 128 : 0)));
                             if (elect_one()) {
-                                if (kp == 0)  // the rotary keys with the stage's first piece
-                                    tma_load_4d_pair(r_s + st / KP * ROWS * 128, &tmap_kr, 0, 0, grp,
-                                                     page0, bar);
-                                tma_load_5d_pair(k_s + st * PIECE, &tmap_k, 0, 0, kp * KSLABS, grp,
-                                                 page0, bar, pol);
-                            }
-                        } else {
-#pragma unroll 1
-                            for (int c = 0; c < copies; ++c) {
-                                const int pg = __shfl_sync(~0u, page, c);
-                                if (elect_one()) {
+                                // (the rotary keys with the stage's first piece)
+#pragma unroll
+                                for (int c = 0; c < C; ++c) {
                                     if (kp == 0)
-                                        tma_load_4d_pair(r_s + (st / KP * ROWS + c * rows) * 128,
-                                                         &tmap_kr, 0, 0, grp, pg, bar);
-                                    tma_load_5d_pair(k_s + st * PIECE + c * copy_bytes, &tmap_k, 0, 0,
-                                                     kp * KSLABS, grp, pg, bar, pol);
+                                        tma_load_4d_pair(r_s + (st / KP * ROWS + c * (ROWS / C)) * 128,
+                                                         &tmap_kr, 0, 0, grp, pages[c], bar);
+                                    tma_load_5d_pair(k_s + st * PIECE + c * (PIECE / C), &tmap_k, 0, 0,
+                                                     kp * KSLABS, grp, pages[c], bar, pol);
                                 }
                             }
+                            __syncwarp();
+                            // Q after the unit's first K: its place is free only after the last
+                            // unit's last scores, and no place for K comes free before it
+                            if (kp == (KP < NK ? KP : NK) - 1 && nq_from > 0 && t == walk.t)
+                                load_q();
                         }
-                        // Q after the unit's first K: its place is free only after the last
-                        // unit's last scores, and no place for K comes free before it
-                        if (kp == (KP < NK ? KP : NK) - 1 && nq_from > 0 && t == walk.t)
-                            load_q();
-                    }
+                    };
+                    if (copies == 1)
+                        stage(std::integral_constant<int, 1>{});
+                    else if (copies == 2)
+                        stage(std::integral_constant<int, 2>{});
+                    else if (copies == 4)
+                        stage(std::integral_constant<int, 4>{});
+                    else
+                        stage(std::integral_constant<int, 8>{});
                     nst += made;
                     if (!ok)
                         break;

@@ -25,9 +25,12 @@
 // Measured, head_dim 128 (rope_dim 64): one prompt of 16381 tokens x 16 heads 815 us (1685
 // TFLOP/s; 88 % of what a large library product reaches here), 4 x 2048 x 32 heads 155,
 // 37 prompts of 1 to 512 tokens x 16 heads 33.  By clock stamps a period of both tiles takes
-// 2600 to 2900 cycles, of which the products take 2560: the tensor cores bound it.  A short
-// unit is bound by its chain instead (queries and first keys, scores, softmax, product,
-// output: 6000 cycles), a call by the order kernel and the first copies in front (5 us).
+// 3200 to 3450 cycles, of which the products take 2560.  They are there in time (a tile's
+// weights 400 cycles before the other's scores are whole), so what is lost lies between the
+// four groups of a period, 150 to 200 cycles each; shared memory is read at a quarter of
+// its rate.  A short unit is bound by its chain instead (queries and first keys, scores,
+// softmax, product, output: 6000 cycles), a call by the order kernel and the first copies
+// in front (5 us).
 #include <algorithm>
 
 #include "pgd_device.cuh"
