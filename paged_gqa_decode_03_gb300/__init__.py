@@ -790,6 +790,22 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "pla
     return torch.tensor(list(table), dtype=torch.float32, device=device), magnitude.value
 
 
+def _rows_on(index, t, name):
+    """(tokens, heads, head_dim, token stride, head stride) of rows as _packed_strides
+    takes them, on CUDA device ``index``."""
+    try:
+        if t.dtype is _F16 and t.get_device() == index >= 0:
+            (T, H, D), (token, head, one) = t.shape, t.stride()
+            if one == 1:
+                if H <= 1:
+                    head = D
+                return T, H, D, token if T > 1 else H * head, head
+    except (AttributeError, ValueError):       # no tensor, or not of three dimensions
+        pass
+    _packed_strides(t, name)
+    raise ValueError(f"{name} must be on CUDA device {index}")
+
+
 def _rope_table(dev, slots, positions, inv_freq, rows):
     """The checks that paged_rope_write and paged_latent_write share."""
     if not (_fits(dev, _I32, 1, slots, positions) and _fits(dev, torch.float32, 1, inv_freq)):
@@ -813,20 +829,21 @@ def paged_rope_write(k_cache, v_cache, q_out, q, k_new, v_new, slots, positions,
     contiguous rows of head_dim and any token and head strides; q and q_out may
     both be None.  Caches and ``layout`` as for ``paged_kv_write``."""
     lib = _lib or load_library()
-    ks, vs = _packed_strides(k_new, "k_new"), _packed_strides(v_new, "v_new")
     dev = _index(k_new)
-    N, Hkv, D = k_new.shape
-    if v_new.shape != k_new.shape:
+    N, Hkv, D, *ks = _rows_on(dev, k_new, "k_new")
+    T, H, W, *vs = _rows_on(dev, v_new, "v_new")
+    if T != N or H != Hkv or W != D:
         raise ValueError("k_new and v_new must have the same shape")
     _rope_table(dev, slots, positions, inv_freq, N)
-    if (q is None) != (q_out is None):
-        raise ValueError("give both q and q_out or neither")
-    Hq, qs, os_ = 0, (D, D), (D, D)
-    if q is not None:
-        qs, os_ = _packed_strides(q, "q"), _packed_strides(q_out, "q_out")
-        Hq = q.shape[1]
-        if q.shape[0] != N or q.shape[2] != D or q_out.shape != q.shape:
+    Hq, qs, os_, q_at, out_at = 0, (D, D), (D, D), None, None
+    if q is not None and q_out is not None:
+        T, Hq, W, *qs = _rows_on(dev, q, "q")
+        T2, H2, W2, *os_ = _rows_on(dev, q_out, "q_out")
+        if T != N or W != D or T2 != N or H2 != Hq or W2 != D:
             raise ValueError("inconsistent shapes of q, q_out, k_new")
+        q_at, out_at = q.data_ptr(), q_out.data_ptr()
+    elif q is not None or q_out is not None:
+        raise ValueError("give both q and q_out or neither")
     if layout is None:
         if not _fits(dev, _F16, 4, k_cache, v_cache):
             _check_all((k_cache, "k_cache", _F16, 4), (v_cache, "v_cache", _F16, 4))
@@ -843,9 +860,7 @@ def paged_rope_write(k_cache, v_cache, q_out, q, k_new, v_new, slots, positions,
         _check_rows_inside(v_cache, "v_cache", NB, Hkv, BS, D, strides)
         _one_device(dev, k_cache, v_cache)
         sp, sh, st = (int(x) for x in strides)
-    _one_device(dev, v_new, q, q_out)
-    _on(dev, lib.paged_rope_write, k_cache.data_ptr(), v_cache.data_ptr(),
-        None if q is None else q_out.data_ptr(), None if q is None else q.data_ptr(),
+    _on(dev, lib.paged_rope_write, k_cache.data_ptr(), v_cache.data_ptr(), out_at, q_at,
         k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr(), positions.data_ptr(),
         inv_freq.data_ptr(), float(magnitude), 1 if interleaved else 0, N, Hq, Hkv, D,
         2 * inv_freq.numel(), int(BS), int(NB), sp, sh, st, *os_, *qs, *ks, *vs, stream=stream)
@@ -892,18 +907,18 @@ def paged_latent_write(cache, q_out, q_rope, latent, k_rope, slots, positions, i
     if 2 * inv_freq.numel() != P:
         raise ValueError(f"inv_freq must hold {P // 2} values")
     NB, BS, page, token = _latent_cache(cache, R, P)
-    if (q_rope is None) != (q_out is None):
-        raise ValueError("give both q_rope and q_out or neither")
-    H, qs, os_ = 0, (P, P), (P, P)
-    if q_rope is not None:
-        qs, os_ = _packed_strides(q_rope, "q_rope"), _packed_strides(q_out, "q_out")
-        H = q_rope.shape[1]
-        if q_rope.shape[0] != N or q_rope.shape[2] != P or q_out.shape != q_rope.shape:
+    H, qs, os_, q_at, out_at = 0, (P, P), (P, P), None, None
+    if q_rope is not None and q_out is not None:
+        T, H, W, *qs = _rows_on(dev, q_rope, "q_rope")
+        T2, H2, W2, *os_ = _rows_on(dev, q_out, "q_out")
+        if T != N or W != P or T2 != N or H2 != H or W2 != P:
             raise ValueError("inconsistent shapes of q_rope, q_out, k_rope")
-    _one_device(dev, cache, k_rope, q_rope, q_out)
-    _on(dev, lib.paged_latent_write, cache.data_ptr(),
-        None if q_rope is None else q_out.data_ptr(),
-        None if q_rope is None else q_rope.data_ptr(), latent.data_ptr(), k_rope.data_ptr(),
+        q_at, out_at = q_rope.data_ptr(), q_out.data_ptr()
+    elif q_rope is not None or q_out is not None:
+        raise ValueError("give both q_rope and q_out or neither")
+    _one_device(dev, cache, k_rope)
+    _on(dev, lib.paged_latent_write, cache.data_ptr(), out_at, q_at, latent.data_ptr(),
+        k_rope.data_ptr(),
         slots.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), float(magnitude),
         1 if interleaved else 0, N, H, R, P, BS, NB, page, token, *os_, *qs, ls, krs,
         stream=stream)
