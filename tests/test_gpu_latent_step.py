@@ -316,6 +316,39 @@ def test_calls_at_once():
             assert torch.equal(outs[i], base), (turn, i)
 
 
+@pytest.mark.parametrize("D", [64, 256])
+def test_beside_the_calls_over_k_and_v_pages(D):
+    """Calls over latent caches and over K and V pages on three streams: each gives what it
+    gives alone."""
+    import test_gpu_step_concurrency as other
+    w = LatentCase([3000, 700, 64], [2, 1, 3], 16, 512, 64, 16, seed=60)
+    c = Prompts([300, 700], 8, 128, seed=61)
+    calls = [other.tree_call([3000, 40, 700], [30, 9, 64], 16, 4, D, 62),
+             (w.run(), lambda out: pgd.paged_latent_attention(
+                 out, w.q, w.q_rope, w.cache, w.tables, w.seq_lens, w.scale, cu_seqlens_q=w.cu,
+                 max_q_len=3)),
+             other.prefill_call([900, 40, 300], 16, 4, D, 63),
+             (c.run(), lambda out: pgd.packed_latent_prefill(
+                 out, c.q, c.k, c.k_rope, c.v, c.cu, c.scale, 700))]
+    w.check(calls[1][0], "alone")
+    c.check(calls[3][0], "alone")
+    outs = [torch.zeros_like(base) for base, _ in calls]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for turn in range(6):
+        for out in outs:
+            out.fill_(7.0)
+        torch.cuda.synchronize()
+        for i in range(8):
+            with torch.cuda.stream(streams[(i + turn) % 3]):
+                if i < 4:
+                    calls[i][1](outs[i])
+                else:                       # the same again, on another stream: its own output
+                    calls[i - 4][1](torch.empty_like(outs[i - 4]))
+        torch.cuda.synchronize()
+        for i, (base, _) in enumerate(calls):
+            assert torch.equal(outs[i], base), (turn, i)
+
+
 def test_prompts_longer_than_any_run():
     """A whole prompt through the absorbed form: many tiles of one request, cut anywhere."""
     w = LatentCase([700], [700], 16, 256, 32, 32, seed=40)
