@@ -24,11 +24,12 @@ namespace pgd {
 namespace {
 
 constexpr int kRopeThreads = 256;
-// Items of a thread in flight and CTAs a SM: with 3 and 4 65536 rows of 32 / 8 heads x 128
-// take 255 us, with 4 and 4 270, 4 and 3 281, 2 and 5 284, 2 and 8 372.
-constexpr int kRopeAhead = 3;
-constexpr int kRopeCtas = 4;
-constexpr int kRopeItems = kRopeAhead * kRopeThreads;  // of a block of rows at most, or one row
+// Items of a thread in flight, and CTAs an SM with them: two and six where blocks of rows
+// fill two items a thread at least as well as three, else three and four.  65536 rows of 32
+// / 8 heads x 128 (384 items a row) take 249 us with three, 270 with two; 10007 of 24 / 4 x
+// 256 (512) 52.6 and 51.0; 30011 of a latent cache with 16 heads (100) 36.6 and 34.7.  Others:
+// three and five 257, 60.4, 37.0; four and three 269, 53.5, 38.1.
+constexpr int rope_ctas(int ahead) { return ahead == 2 ? 6 : 4; }
 
 __device__ __forceinline__ void rotate2(uint32_t &a, uint32_t &b, const float2 &c0, const float2 &c1)
 {
@@ -50,7 +51,9 @@ __device__ __forceinline__ uint32_t rotate1(uint32_t w, const float2 &c)
 // interleaved pairs: 8 pairs in either case), of the others two adjacent pieces.  A
 // CTA goes from block of rows to block of rows: a block's loads go out first, and come
 // while its sines and cosines are worked out.
-__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_rope_write_kernel(const RopeParams p)
+template <int AHEAD>
+__global__ void __launch_bounds__(kRopeThreads, rope_ctas(AHEAD))
+    paged_rope_write_kernel(const RopeParams p)
 {
     extern __shared__ uint8_t rope_smem[];
     const int pairs = p.rot / 2;
@@ -71,12 +74,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_rope_write_kern
         const int rows = min(p.rows_per_cta, p.rows - n0);
         const int count = rows * per_row;
         float2 *const table = cs + (turns & 1) * p.rows_per_cta * pairs;
-        for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < count; i0 += kRopeAhead * kRopeThreads) {
-            uint4 a[kRopeAhead], b[kRopeAhead];
-            uint16_t *dst[kRopeAhead];
-            int second[kRopeAhead], turned[kRopeAhead];  // the second piece's place; first of its pairs or -1
+        for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < count; i0 += AHEAD * kRopeThreads) {
+            uint4 a[AHEAD], b[AHEAD];
+            uint16_t *dst[AHEAD];
+            int second[AHEAD], turned[AHEAD];  // the second piece's place; first of its pairs or -1
 #pragma unroll
-            for (int u = 0; u < kRopeAhead; ++u) {
+            for (int u = 0; u < AHEAD; ++u) {
                 const int i = i0 + u * kRopeThreads;
                 dst[u] = nullptr;
                 if (i >= count)
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_rope_write_kern
                 __syncthreads();
             }
 #pragma unroll
-            for (int u = 0; u < kRopeAhead; ++u) {
+            for (int u = 0; u < AHEAD; ++u) {
                 if (!dst[u])
                     continue;
                 if (turned[u] >= 0) {
@@ -166,16 +169,25 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) paged_rope_write_kern
 cudaError_t launch_rope_write(RopeParams p, int num_sms, cudaStream_t stream)
 {
     const int per_row = (p.Hq << p.log2q) + (p.Hkv << p.log2k) + (p.Hkv << p.log2v);
+    // the rows that a block's items hold, and the share of them that these fill
+    auto rows_of = [&](int ahead) { return std::max(1, std::min(ahead * kRopeThreads / per_row, 16)); };
+    auto fill = [&](int ahead) {
+        const int items = rows_of(ahead) * per_row, at_once = ahead * kRopeThreads;
+        return (double)items / ((items + at_once - 1) / at_once * at_once);
+    };
+    const int ahead = fill(2) >= fill(3) ? 2 : 3;
     // rows enough for a CTA's threads, but CTAs enough for every SM first
-    const int most = std::max(1, std::min(kRopeItems / per_row, 16));
-    p.rows_per_cta = std::max(1, std::min(most, p.rows / (2 * num_sms)));
+    p.rows_per_cta = std::max(1, std::min(rows_of(ahead), p.rows / (2 * num_sms)));
     const long long blocks = (p.rows + (long long)p.rows_per_cta - 1) / p.rows_per_cta;
-    const unsigned grid = (unsigned)std::min<long long>(blocks, (long long)kRopeCtas * num_sms);
+    const unsigned grid = (unsigned)std::min<long long>(blocks, (long long)rope_ctas(ahead) * num_sms);
     // i / d = umulhi(i, 2^32 / d rounded up) while i d < 2^32
     p.row_inverse = (uint32_t)((0xFFFFFFFFull + per_row) / per_row);
     p.pair_inverse = (uint32_t)((0xFFFFFFFFull + p.rot / 2) / (p.rot / 2));
     const size_t smem = (size_t)(p.rot / 2) * 8 * (1 + 2 * p.rows_per_cta);  // 34 KB at most
-    paged_rope_write_kernel<<<grid, kRopeThreads, smem, stream>>>(p);
+    if (ahead == 2)
+        paged_rope_write_kernel<2><<<grid, kRopeThreads, smem, stream>>>(p);
+    else
+        paged_rope_write_kernel<3><<<grid, kRopeThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
