@@ -23,7 +23,8 @@
 //     N 256: 16), 2176 cycles a stage at R 512, against 3150 in which HBM brings its
 //     147 KB.  Fewer rows cost the same; HBM still bounds.  They run at that rate only
 //     when an elected lane of a converged warp issues them: `if (lane == 0)` costs 50
-//     cycles a product and 300 a turn (32 requests of 8 k to 32 k tokens 231 us, so 139).
+//     cycles a product and 300 a turn (32 requests of 8 k to 32 k tokens took 231 us that
+//     way, 139 this way).
 //   * The stages of all units (sequence, tile of rows) are cut into equal runs, one
 //     per resident pair, whatever the lengths; a unit that is cut leaves pieces
 //     (reference maximum, exp-sum, unscaled output; two per run at most), which a
@@ -31,8 +32,8 @@
 //   * Weights go to tensor memory as fp16, two stages of them, next to two score
 //     buffers.  A row of A lies there twice (lanes r and 64 + r), and its scores come
 //     split over the same lanes: the two warps of a row exchange their halves through
-//     16 KB of shared memory.  (Weights in shared memory: 48 cycles a score product in
-//     their bandwidth's share, and no room for two stages.)
+//     16 KB of shared memory.  (In shared memory, as the products would take them too,
+//     they need a release of plain writes to the pair each stage: 1500 cycles or more.)
 //
 // Measured in a graph: 32 requests of 8 k to 32 k tokens with 16 heads 124.5 us (655 MB: 5.3
 // TB/s; HBM's floor 97), 64 of 512 to 4096 tokens with 128 heads 61.5, 24 of up to 8 k tokens

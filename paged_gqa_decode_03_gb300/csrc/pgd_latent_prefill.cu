@@ -8,7 +8,7 @@
 // and key, a head's keys read by its rows alone: the tensor cores bound a long prompt.
 //
 // The shape is that of packed_gqa_prefill's pair kernel: a unit is two tiles of 128
-// tokens of one head that share every stage of 128 keys, a thread each for copies (K,
+// tokens of one head that share every stage of 128 keys, a warp each for copies (K,
 // V), scores and outputs, a softmax thread a row; the units are the order kernel's,
 // longest first.  What differs:
 //   * The queries of two tiles, head_dim 128 with its rotary part, take 96 KB, so K and
@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(kExpandedThreads, 1)
     };
 
     // the softmax warps hold a row's 128 scores and half of its weights: they
-    // take registers that the copying and issuing warps do not need (128 x 80 +
-    // 256 x 208 of the 384 x 168 of the launch)
+    // take registers that the copying and issuing warps do not need (128 x 104
+    // + 256 x 200 of the 384 x 168 of the launch)
     if (warp < 4) {
       regs_give<104>();
       if (warp == 0 || warp == 3) {
