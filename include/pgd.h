@@ -791,9 +791,12 @@ pgd_status paged_latent_write(uint16_t *cache, uint16_t *q_out, const uint16_t *
  *            fp16, 16-byte aligned, each with its own token and head strides (halves,
  *            positive multiples of 8 below 2^39): parts of one tensor, or a batched
  *            product's output [num_heads][total_q][latent_dim], need no copy
- * max_q_len  bound on every sequence's query rows (1 with cu_seqlens_q NULL).  Its tiles
- *            of 128 rows (of queries x heads), times the table's stages of 128 tokens,
- *            times num_seqs are to stay below 2^29 (PGD_ERR_UNSUPPORTED)
+ * max_q_len  bound on every sequence's query rows (1 with cu_seqlens_q NULL)
+ * total_q    the sequences' rows do not overlap.  What they come to in tiles of 128 rows
+ *            (of queries x heads; one begun in each sequence), times the table's stages
+ *            of 128 tokens, is to stay below 2^29 (PGD_ERR_UNSUPPORTED).  Where offsets
+ *            that decrease ask for more all the same, nothing is written
+ *            (PGD_DEVERR_QUERY_LEN)
  * workspace  NULL: library scratch (per call, also in a captured graph); else at
  *            least pgd_latent_plan's bytes, 256-byte aligned, not used by anything
  *            else until the call's work is done

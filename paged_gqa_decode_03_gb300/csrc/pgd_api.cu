@@ -2064,15 +2064,27 @@ pgd_status make_latent_plan(int S, int total_q, int max_q, int H, int R, int P, 
     lp->HB = (H + kLatentRows - 1) / kLatentRows;
     lp->TQ = H <= kLatentRows ? kLatentRows / H : 1;
     const long long most_q = std::min(max_q, total_q);
-    const long long halves = lp->HB == 1 ? (most_q + lp->TQ - 1) / lp->TQ : most_q * lp->HB;
-    const long long stages = (halves + 1) / 2 * (((long long)MB * BS + kLatentNT - 1) / kLatentNT);
+    const long long stages = ((long long)MB * BS + kLatentNT - 1) / kLatentNT;
+    // tiles of one sequence, and of all: a sequence has no more than that, and all of them
+    // together whole tiles of their rows and one begun in each that has any
+    auto tiles_of = [&](long long q, long long begun) {
+        return lp->HB == 1 ? (q + begun * (2 * lp->TQ - 1)) / (2 * lp->TQ)
+                           : (q * lp->HB + begun * (lp->HB & 1)) / 2;
+    };
+    const long long one = tiles_of(most_q, 1);
     // (the kernel counts stages, and a unit's start and end, in 32-bit integers; a unit
-    // has one stage at least)
+    // has one stage at least.  What rows that overlap could ask for beyond it, it refuses.)
     constexpr long long most = (1ll << 31) / (1 + kLatentUnitCost);
-    if (S && (stages >= most || S * stages >= most))
-        return fail(PGD_ERR_UNSUPPORTED, "%d sequences of up to %lld rows x %d heads, %lld tokens: too large",
-                    S, most_q, H, (long long)MB * BS);
-    lp->runs = (int)std::max(1ll, std::min<long long>(resident, S * stages));
+    const long long all =
+        one >= most ? one : std::min(S * one, tiles_of(total_q, std::min(S, total_q)));
+    if (all >= most || all * stages >= most)
+        return fail(PGD_ERR_UNSUPPORTED,
+                    "%d sequences of %d rows (up to %lld each) x %d heads, %lld tokens: too large", S,
+                    total_q, most_q, H, (long long)MB * BS);
+    // (the table's bound, however few rows the call has: the division of a batch's work does
+    // not change with its padding)
+    const long long units = std::min<long long>(resident, S * one);
+    lp->runs = (int)std::max(1ll, std::min<long long>(resident, units * stages));
     const size_t rows = (size_t)2 * lp->runs * 2 * kLatentRows;
     lp->off_ml = align256(rows * R * 4);
     lp->off_cut = lp->off_ml + align256(rows * 8);

@@ -151,6 +151,15 @@ struct HalfTile {
     }
 };
 
+// Sums of costs end at kLatentCostCap (min(a + b, cap) is associative).  The host bounds what
+// rows that do not overlap can cost below it; rows that do overlap (offsets that decrease,
+// of which some sequences are flagged) may ask for more, and nothing is run then.
+constexpr uint32_t kLatentCostCap = 0x7fffffffu;
+__device__ __forceinline__ int sat_cost(int a, int b)
+{
+    return (int)min((uint32_t)a + (uint32_t)b, kLatentCostCap);
+}
+
 // Sum over the CTA's threads before this one of `x`, and over all in *total.
 __device__ __forceinline__ int latent_prefix(int x, int *warp_sum, int *total)
 {
@@ -161,21 +170,22 @@ __device__ __forceinline__ int latent_prefix(int x, int *warp_sum, int *total)
     for (int off = 1; off < 32; off <<= 1) {
         const int y = __shfl_up_sync(~0u, inc, off);
         if (lane >= off)
-            inc += y;
+            inc = sat_cost(inc, y);
     }
     if (lane == 31)
         warp_sum[w] = inc;
+    const int up = __shfl_up_sync(~0u, inc, 1);
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
     for (int i = 0; i < WARPS; ++i) {
-        if (i < w)
-            before += warp_sum[i];
-        all += warp_sum[i];
+        if (i == w)
+            before = all;
+        all = sat_cost(all, warp_sum[i]);
     }
     __syncthreads();
     *total = all;
-    return before + inc - x;
+    return lane ? sat_cost(before, up) : before;
 }
 
 }  // namespace
@@ -265,8 +275,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
                 atomicOr(p.err, q.bad);
             mine = latent_cost(q);
         }
-        before = total + latent_prefix(mine, warp_sum, &all);
-        total += all;
+        before = sat_cost(total, latent_prefix(mine, warp_sum, &all));
+        total = sat_cost(total, all);
+    }
+    if (total == (int)kLatentCostCap) {
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            atomicOr(p.err, kErrQueryLen);
+        total = 0;
     }
     const int x0 = (int)((long long)total * run / p.runs);
     const int x1 = (int)((long long)total * (run + 1) / p.runs);
