@@ -684,8 +684,10 @@ pgd_status paged_kv_write_strided(uint16_t *k_cache, uint16_t *v_cache, const ui
  *
  * q, q_out      [num_rows][num_q_heads][head_dim] fp16 at token and head strides of
  *               their own; q_out may be q itself, with the same strides (the values
- *               behind rotary_dim are then not touched), else it shares no memory
- *               with an input.  Both NULL with num_q_heads 0: keys alone.
+ *               behind rotary_dim are then not touched).  It shares no memory with any
+ *               other array of the call, keys that q reaches over among them, and its rows
+ *               none with one another (PGD_ERR_INVALID_ARG).  Both NULL with num_q_heads
+ *               0: keys alone.
  * k_new, v_new  [num_rows][num_kv_heads][head_dim], strides of their own (all four
  *               in halves, positive multiples of 8), 16-byte aligned, read
  * slots         [num_rows] int32 as for paged_kv_write; negative: the row is not

@@ -827,7 +827,9 @@ def paged_rope_write(k_cache, v_cache, q_out, q, k_new, v_new, slots, positions,
     written), as ``paged_kv_write`` does.  Pairs are values i and i +
     len(inv_freq), or 2i and 2i + 1 (``interleaved``).  Row tensors are fp16 with
     contiguous rows of head_dim and any token and head strides; q and q_out may
-    both be None.  Caches and ``layout`` as for ``paged_kv_write``."""
+    both be None.  But for q itself, q_out shares no memory with another array of
+    the call (slices of one tensor that lie between one another are in order).
+    Caches and ``layout`` as for ``paged_kv_write``."""
     lib = _lib or load_library()
     dev = _index(k_new)
     N, Hkv, D, *ks = _rows_on(dev, k_new, "k_new")

@@ -1937,6 +1937,138 @@ pgd_status check_latent_cache(int R, int P, int BS, int NB, long long page, long
     return PGD_OK;
 }
 
+// Runs of `width` bytes from `at` on, `rows` x `heads` of them at two strides: an array as a
+// call reads or writes it.  (128 bits: strides and counts may come to more than 64.)
+using wide_int = __int128;
+struct ByteRuns {
+    long long at, width, row, head, rows, heads;
+
+    ByteRuns(const void *base, long long halves, long long n = 1, long long row_halves = 0,
+             long long h = 1, long long head_halves = 0)
+        : at((long long)reinterpret_cast<uintptr_t>(base)), width(2 * halves), row(2 * row_halves),
+          head(2 * head_halves), rows(n), heads(h)
+    {
+    }
+    // heads (then rows) that follow one another as one run
+    ByteRuns joined() const
+    {
+        ByteRuns r = *this;
+        if (r.heads > 1 && r.head == r.width) {
+            r.width *= r.heads;
+            r.heads = 1;
+        }
+        if (r.heads == 1 && r.rows > 1 && r.row == r.width) {
+            r.width *= r.rows;
+            r.rows = 1;
+        }
+        return r;
+    }
+    wide_int end() const { return at + (wide_int)(rows - 1) * row + (wide_int)(heads - 1) * head + width; }
+};
+
+wide_int floor_div(wide_int a, wide_int b)  // b > 0
+{
+    return a / b - (a % b < 0);
+}
+
+// Is low < x + k step < high for a whole k in [first, last]?  (low < 0 < high; first <= 0 <=
+// last; step > 0, or first = last)
+bool steps_into(wide_int x, wide_int step, long long first, long long last, wide_int low, wide_int high)
+{
+    auto in = [&](wide_int y) { return low < y && y < high; };
+    if (first == last)
+        return in(x);
+    // (rows that lie within a step of one another, as slices of a row do: no division)
+    if (-step <= low && high <= step && -step < x && x < step)
+        return in(x) || (first < 0 && in(x - step)) || (last > 0 && in(x + step));
+    const wide_int from = floor_div(low - x, step) + 1, to = floor_div(high - x - 1, step);
+    return std::max<wide_int>(from, first) <= std::min<wide_int>(to, last);
+}
+
+// Do two arrays share a byte?  Exactly, so that slices of one projection's output, whose
+// address ranges interleave, are told from arrays that overlap: run (n, h) of a meets run
+// (m, g) of b where -b.width < b's place - a's place < a.width.  Equal strides count by their
+// differences alone.
+bool share_memory(const ByteRuns &one, const ByteRuns &other)
+{
+    if (one.end() <= other.at || other.end() <= one.at)
+        return false;
+    const ByteRuns a = one.joined(), b = other.joined();
+    const bool by_head = a.heads == 1 || b.heads == 1 || a.head == b.head;
+    const bool by_row = a.rows == 1 || b.rows == 1 || a.row == b.row;
+    const long long row = b.rows > 1 ? b.row : a.row, head = b.heads > 1 ? b.head : a.head;
+    auto heads_apart = [&](wide_int x) {  // x: b's head 0 from a's head 0
+        if (by_row)
+            return steps_into(x, row, 1 - a.rows, b.rows - 1, -b.width, a.width);
+        for (long long n = 0; n < a.rows; ++n)
+            if (steps_into(x - (wide_int)n * a.row, b.row, 0, b.rows - 1, -b.width, a.width))
+                return true;
+        return false;
+    };
+    if (by_head) {
+        for (long long h = 1 - a.heads; h < b.heads; ++h)
+            if (heads_apart(b.at - a.at + (wide_int)h * head))
+                return true;
+        return false;
+    }
+    for (long long h = 0; h < a.heads; ++h)
+        for (long long g = 0; g < b.heads; ++g)
+            if (heads_apart(b.at - a.at + (wide_int)g * b.head - (wide_int)h * a.head))
+                return true;
+    return false;
+}
+
+// Do two runs of one array share a byte?
+bool overlaps_itself(const ByteRuns &a)
+{
+    if (a.rows > 1 && a.row < a.width)
+        return true;
+    if (a.head >= a.width && (a.rows == 1 || a.row >= (wide_int)(a.heads - 1) * a.head + a.width))
+        return false;
+    for (long long h = 1; h < a.heads; ++h)
+        if (steps_into((wide_int)h * a.head, a.row, 1 - a.rows, a.rows - 1, -a.width, a.width))
+            return true;
+    return false;
+}
+
+// The turned queries are written while other threads read the call's arrays and write the
+// cache: they share no memory with one of them, but for q itself, which the thread that
+// turns a pair has read, nor with one another.
+pgd_status check_turned_queries(const RopeParams &p)
+{
+    const long long N = p.rows;
+    const int qw = 16 << p.log2q, kw = 16 << p.log2k, vw = 16 << p.log2v;
+    const ByteRuns out(p.q_out, qw, N, p.qo_token, p.Hq, p.qo_head);
+    if (overlaps_itself(out))
+        return fail(PGD_ERR_INVALID_ARG, "rows of q_out overlap one another");
+    const struct {
+        ByteRuns at;
+        const char *name;
+    } reads[] = {{{p.k_new, kw, N, p.k_token, p.Hkv, p.k_head}, "the new keys"},
+                 {{p.v_new, vw, N, p.v_token, p.Hkv, p.v_head}, "the new values"},
+                 {{p.slots, 2 * N}, "slots"},
+                 {{p.positions, 2 * N}, "positions"},
+                 {{p.inv_freq, p.rot}, "inv_freq"}};
+    for (const auto &x : reads)
+        if (share_memory(out, x.at))
+            return fail(PGD_ERR_INVALID_ARG, "q_out overlaps %s", x.name);
+    if (!p.in_place && share_memory(out, ByteRuns(p.q, qw, N, p.q_token, p.Hq, p.q_head)))
+        return fail(PGD_ERR_INVALID_ARG, "q_out overlaps q without being q");
+    for (const bool v : {false, true}) {
+        const uint16_t *const cache = v ? p.v_cache : p.k_cache;
+        const int width = v ? vw : kw, BS = 1 << p.log2BS;
+        const ByteRuns all(cache, (p.Hkv - 1) * p.head_stride + (BS - 1) * p.token_stride + width, p.NB,
+                           p.page_stride);
+        if (out.end() <= all.at || all.end() <= out.at)
+            continue;
+        for (int h = 0; h < p.Hkv; ++h)
+            if (share_memory(out, ByteRuns(cache + h * p.head_stride, width, p.NB, p.page_stride, BS,
+                                           p.token_stride)))
+                return fail(PGD_ERR_INVALID_ARG, "q_out overlaps the cache");
+    }
+    return PGD_OK;
+}
+
 // What paged_rope_write and paged_latent_write share: `p` is filled but for the
 // error word.
 pgd_status run_rope(RopeParams &p, void *stream)
@@ -1963,7 +2095,7 @@ pgd_status run_rope(RopeParams &p, void *stream)
         return fail(PGD_ERR_INVALID_ARG, "q_out is q with other strides");
     DeviceState *ds;
     pgd_status st;
-    if ((st = device_state(&ds)))
+    if ((p.Hq > 0 && (st = check_turned_queries(p))) || (st = device_state(&ds)))
         return st;
     p.err = ds->err_word;
     const cudaError_t e = launch_rope_write(p, ds->num_sms, static_cast<cudaStream_t>(stream));
