@@ -2163,7 +2163,8 @@ pgd_status run_rope_frequencies(float *inv_freq, float *magnitude, int rot, doub
 
 struct LatentPlan {
     int hb, TQ, HB, runs;
-    size_t ws_bytes, off_ml, off_cut;  // pieces' outputs, (maximum, exp-sum)s, cuts
+    bool check_cost;
+    size_t ws_bytes, off_ml, off_cut, off_allowed;  // pieces' outputs, (maximum, exp-sum)s, cuts
 };
 
 pgd_status make_latent_plan(int S, int total_q, int max_q, int H, int R, int P, int BS, int MB,
@@ -2205,7 +2206,8 @@ pgd_status make_latent_plan(int S, int total_q, int max_q, int H, int R, int P, 
     };
     const long long one = tiles_of(most_q, 1);
     // (the kernel counts stages, and a unit's start and end, in 32-bit integers; a unit
-    // has one stage at least.  What rows that overlap could ask for beyond it, it refuses.)
+    // has one stage at least.  Where rows that overlap could ask for more, a kernel in front
+    // adds it up.)
     constexpr long long most = (1ll << 31) / (1 + kLatentUnitCost);
     const long long all =
         one >= most ? one : std::min(S * one, tiles_of(total_q, std::min(S, total_q)));
@@ -2214,13 +2216,15 @@ pgd_status make_latent_plan(int S, int total_q, int max_q, int H, int R, int P, 
                     "%d sequences of %d rows (up to %lld each) x %d heads, %lld tokens: too large", S,
                     total_q, most_q, H, (long long)MB * BS);
     // (the table's bound, however few rows the call has: the division of a batch's work does
-    // not change with its padding)
+    // not change with total_q)
+    lp->check_cost = S * one >= most || S * one * stages >= most;
     const long long units = std::min<long long>(resident, S * one);
     lp->runs = (int)std::max(1ll, std::min<long long>(resident, units * stages));
     const size_t rows = (size_t)2 * lp->runs * 2 * kLatentRows;
     lp->off_ml = align256(rows * R * 4);
     lp->off_cut = lp->off_ml + align256(rows * 8);
-    lp->ws_bytes = S && total_q ? lp->off_cut + align256((size_t)lp->runs * 16) : 0;
+    lp->off_allowed = lp->off_cut + align256((size_t)lp->runs * 16);
+    lp->ws_bytes = S && total_q ? lp->off_allowed + (lp->check_cost ? 256 : 0) : 0;
     return PGD_OK;
 }
 
@@ -2347,6 +2351,7 @@ pgd_status run_latent(void *out, bool half, const uint16_t *q, const uint16_t *q
     p.part_o = reinterpret_cast<float *>(ws);
     p.part_ml = reinterpret_cast<float2 *>(ws + lp.off_ml);
     p.cut = reinterpret_cast<int4 *>(ws + lp.off_cut);
+    p.allowed = lp.check_cost ? reinterpret_cast<int *>(ws + lp.off_allowed) : nullptr;
     p.err = ds->err_word;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.S = S;

@@ -437,6 +437,7 @@ struct LatentParams {
     float *part_o;                // [2 * runs][2][64][R] sums of p c
     float2 *part_ml;              // [2 * runs][2][64] (reference maximum, exp-sum)
     int4 *cut;                    // [runs] {sequence or -1, tile, last run, -}
+    int *allowed;                 // the sequences to run, of the check in front, or null: all
     unsigned *err;
     float scale_log2;
     int S, total_q, max_q, H, R, MB, NB, BS, log2BS;

@@ -35,14 +35,19 @@
 //     16 KB of shared memory.  (In shared memory, as the products would take them too,
 //     they need a release of plain writes to the pair each stage: 1500 cycles or more.)
 //
-// Measured in a graph: 32 requests of 8 k to 32 k tokens with 16 heads 124.5 us (655 MB: 5.3
-// TB/s; HBM's floor 97), 64 of 512 to 4096 tokens with 128 heads 61.5, 24 of up to 8 k tokens
-// with up to 5 rows of 32 heads 47, one of 1000 tokens 15 (nearly all of it in every call:
-// the runs' division 2, the first pages, copies and Q 4, the last softmax and outputs 3, the
-// joining kernel 4).  What bounds a long run is the chain of a piece (its place free, its
-// copy of 16 KB issued, arrived, used): 64 KB of K in flight an SM.  Other divisions of
-// the same memory, against 126: pieces of 32 KB for K, two of them, 143; Q's place cut to a
-// tile's rows where they are few and longer rings 132.
+// Measured in a graph (a call: 0.5 to 4 us more): 32 requests of 8 k to 32 k tokens with 16
+// heads 122 to 125 us (655 MB: 5.3 TB/s; HBM's floor 97), 64 of 512 to 4096 tokens with 128
+// heads 61.5, 24 of up to 8 k tokens with up to 5 rows of 32 heads 47, one of 1000 tokens 15
+// (nearly all of it in every call: the runs' division 2, the first pages, copies and Q 4, the
+// last softmax and outputs 3, the joining kernel 4).  What bounds a long run is not settled.
+// It is not the bytes in flight alone: other divisions of the same memory, against 126, gave
+// 133 with five places for K and three for V, 132 with Q's place cut to a tile's rows where
+// they are few and longer rings, 143 with two pieces of 32 KB for K.  The latent part comes
+// into shared memory twice, 139 KB a stage and SM, which is the likelier cause.
+//
+// A unit's stages are its sequence's, also for tiles of earlier rows that see none of the
+// last: a chunk of 4096 rows takes 375 us with 16 heads, 3046 with 128 (1540 TFLOP/s of
+// which half are of use), behind 8192 cached tokens 1130 and 9267 (1530, 1/1.2 of use).
 #include <type_traits>
 
 #include "pgd_device.cuh"
@@ -151,15 +156,6 @@ struct HalfTile {
     }
 };
 
-// Sums of costs end at kLatentCostCap (min(a + b, cap) is associative).  The host bounds what
-// rows that do not overlap can cost below it; rows that do overlap (offsets that decrease,
-// of which some sequences are flagged) may ask for more, and nothing is run then.
-constexpr uint32_t kLatentCostCap = 0x7fffffffu;
-__device__ __forceinline__ int sat_cost(int a, int b)
-{
-    return (int)min((uint32_t)a + (uint32_t)b, kLatentCostCap);
-}
-
 // Sum over the CTA's threads before this one of `x`, and over all in *total.
 __device__ __forceinline__ int latent_prefix(int x, int *warp_sum, int *total)
 {
@@ -170,25 +166,51 @@ __device__ __forceinline__ int latent_prefix(int x, int *warp_sum, int *total)
     for (int off = 1; off < 32; off <<= 1) {
         const int y = __shfl_up_sync(~0u, inc, off);
         if (lane >= off)
-            inc = sat_cost(inc, y);
+            inc += y;
     }
     if (lane == 31)
         warp_sum[w] = inc;
-    const int up = __shfl_up_sync(~0u, inc, 1);
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
     for (int i = 0; i < WARPS; ++i) {
-        if (i == w)
-            before = all;
-        all = sat_cost(all, warp_sum[i]);
+        if (i < w)
+            before += warp_sum[i];
+        all += warp_sum[i];
     }
     __syncthreads();
     *total = all;
-    return lane ? sat_cost(before, up) : before;
+    return before + inc - x;
 }
 
 }  // namespace
+
+// In front of calls whose rows, if they overlap (offsets that decrease, of which some sequences
+// are flagged), may cost more than 32 bits count: *allowed is then 0 instead of S, and nothing
+// is run.  (A look in the main kernel instead took every call 0.3 to 0.5 us.)
+constexpr int kLatentCheckThreads = 1024;
+__global__ void __launch_bounds__(kLatentCheckThreads) paged_latent_check_kernel(const LatentParams p)
+{
+    __shared__ unsigned long long all;
+    if (threadIdx.x == 0)
+        all = 0;
+    __syncthreads();
+    unsigned long long cost = 0;
+    for (int s = threadIdx.x; s < p.S; s += kLatentCheckThreads) {
+        const LatentSeq q = latent_seq(p, s);
+        if (q.bad)
+            atomicOr(p.err, q.bad);
+        cost += (unsigned)latent_cost(q);
+    }
+    atomicAdd(&all, cost);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const bool fits = all < 1ull << 31;
+        if (!fits)
+            atomicOr(p.err, kErrQueryLen);
+        *p.allowed = fits ? p.S : 0;
+    }
+}
 
 template <int R>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
@@ -264,37 +286,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
 
     griddep_wait();  // what the launches before wrote
     // ---- the run: [x0, x1) of the cost of all units; the sequence that holds x0
+    const int S = p.allowed ? *p.allowed : p.S;
     int total = 0, mine = 0, before = 0;  // before: this thread's (last) sequence
-    for (int s0 = 0; s0 < p.S; s0 += kLatentThreads) {
+    for (int s0 = 0; s0 < S; s0 += kLatentThreads) {
         const int s = s0 + (int)threadIdx.x;
         int all;
         mine = 0;
-        if (s < p.S) {
+        if (s < S) {
             const LatentSeq q = latent_seq(p, s);
             if (q.bad && blockIdx.x == 0)
                 atomicOr(p.err, q.bad);
             mine = latent_cost(q);
         }
-        before = sat_cost(total, latent_prefix(mine, warp_sum, &all));
-        total = sat_cost(total, all);
-    }
-    if (total == (int)kLatentCostCap) {
-        if (blockIdx.x == 0 && threadIdx.x == 0)
-            atomicOr(p.err, kErrQueryLen);
-        total = 0;
+        before = total + latent_prefix(mine, warp_sum, &all);
+        total += all;
     }
     const int x0 = (int)((long long)total * run / p.runs);
     const int x1 = (int)((long long)total * (run + 1) / p.runs);
-    if (x1 > x0 && p.S <= kLatentThreads) {
+    if (x1 > x0 && S <= kLatentThreads) {
         if (mine > 0 && before <= x0 && x0 < before + mine) {
             run_seq = (int)threadIdx.x;
             run_begin = before;
         }
     } else if (x1 > x0) {
         int past = 0;
-        for (int s0 = 0; s0 < p.S && past <= x0; s0 += kLatentThreads) {
+        for (int s0 = 0; s0 < S && past <= x0; s0 += kLatentThreads) {
             const int s = s0 + (int)threadIdx.x;
-            const int here = s < p.S ? latent_cost(latent_seq(p, s)) : 0;
+            const int here = s < S ? latent_cost(latent_seq(p, s)) : 0;
             int all;
             const int at = past + latent_prefix(here, warp_sum, &all);
             if (here > 0 && at <= x0 && x0 < at + here) {
@@ -970,6 +988,12 @@ cudaError_t latent_resident(int latent_dim, int *runs)
 
 cudaError_t launch_latent(const LatentMaps &m, const LatentParams &p, cudaStream_t stream)
 {
+    if (p.allowed) {
+        paged_latent_check_kernel<<<1, kLatentCheckThreads, 0, stream>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess)
+            return e;
+    }
     return p.R == 128   ? launch_latent_of<128>(m, p, stream)
            : p.R == 256 ? launch_latent_of<256>(m, p, stream)
                         : launch_latent_of<512>(m, p, stream);

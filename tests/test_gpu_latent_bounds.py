@@ -57,6 +57,19 @@ def test_a_long_chunk_among_many_decode_rows():
     out = w.run(max_q=2048)
     assert torch.isfinite(out).all()
     w.check(out, "chunk", [0, 1, 2, 100, 254, 255])
+    need = pgd.pgd_latent_plan(256, 2303, 2048, 65, 128, 32, 16, 8192)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    assert torch.equal(w.run(max_q=2048, workspace=ws), out)
+    again = torch.zeros_like(out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pgd.paged_latent_attention(again, w.q, w.q_rope, w.cache, w.tables, w.seq_lens, w.scale,
+                                   cu_seqlens_q=w.cu, max_q_len=2048)
+    for _ in range(2):
+        again.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again, out)
 
 
 def test_rows_that_overlap_past_the_count_are_not_run():
