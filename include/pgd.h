@@ -679,8 +679,14 @@ pgd_status paged_kv_write_strided(uint16_t *k_cache, uint16_t *v_cache, const ui
  * where a, b are values i and i + rotary_dim / 2 of the head (interleaved 0) or 2i
  * and 2i + 1 (interleaved non-zero); its other values are copied as they are.  The
  * turned keys and the values go to cache row slots[n], the turned queries to q_out.
- * The angle is exact but for 2^-53 of itself: the position of a token far out in
- * a long context costs no accuracy.  Arithmetic is fp32, rounded once to fp16.
+ * The angle's place on the circle is off by 1.1e-7 radians at most, whatever the
+ * position, and by position * (|f| 2^-52 + 2 pi 2^-64) more (f below 0: 2^-54 in
+ * 2^-64's place), which for |f| up to 1 reaches as much from positions of 3 x 10^8 on:
+ * a token far out in a long context costs no accuracy.  Arithmetic is fp32, rounded once to fp16.
+ *
+ * Turned keys as rows, as the prompt operators and paged_kv_quantize take them: give
+ * the key heads as further query heads (q over the query and key heads of one
+ * projection, k_new its key heads, q_out a tensor of its own).
  *
  * q, q_out      [num_rows][num_q_heads][head_dim] fp16 at token and head strides of
  *               their own; q_out may be q itself, with the same strides (the values
@@ -753,7 +759,8 @@ pgd_status pgd_rope_frequencies(float *inv_freq, float *magnitude, int rotary_di
  * it is and its key turned by its position, to cache row slots[n]; the queries'
  * rotary parts turned into q_out.  The rotation, slots, positions, inv_freq (rope_dim
  * / 2 values) and q_out's rules are those of paged_rope_write, with all of rope_dim
- * turned.
+ * turned.  The turned key as rows (packed_latent_prefill): a second call with k_rope
+ * as the one query head and negative slots, which writes nothing else.
  *
  * latent        [num_rows][latent_dim], k_rope [num_rows][rope_dim] fp16, each with
  *               its own token stride: slices of one projection's output need no copy
@@ -783,7 +790,10 @@ pgd_status paged_latent_write(uint16_t *cache, uint16_t *q_out, const uint16_t *
  * Sequence s has the query rows cu_seqlens_q[s] .. cu_seqlens_q[s+1]-1, its newest
  * tokens, already in the cache, causal among themselves (as in paged_gqa_varlen).
  * cu_seqlens_q NULL: a decode step, one row a sequence (total_q == num_seqs), which
- * sees all of seq_lens[s] tokens; a sequence of length 0 gets zeros.
+ * sees all of seq_lens[s] tokens; a sequence of length 0 gets zeros.  Every tile of a
+ * sequence's rows runs over all of its tokens, also those that its rows do not see: a
+ * chunk of n rows behind c tokens takes (c + n) / (c + n / 2) times the work it needs
+ * (4096 rows: twice with nothing before them, 1.2 times behind 8192).
  *
  * out        [total_q][num_heads][latent_dim], contiguous, 16-byte aligned;
  *            out_type PGD_OUT_F32 or PGD_OUT_F16 (rounded to nearest).  The weights
@@ -807,7 +817,8 @@ pgd_status paged_latent_write(uint16_t *cache, uint16_t *q_out, const uint16_t *
  * whose query rows are inconsistent (PGD_DEVERR_QUERY_LEN) is skipped, its rows are
  * not written; rows behind the last sequence are left as they were.  A page id
  * outside [0, num_blocks) reads as zeros (PGD_DEVERR_PAGE_RANGE).  A query row of NaN
- * gives NaN.  The cached rows of one sequence's own query tokens must be finite: a
+ * gives NaN, and so does a score of +infinity; scores that are all -infinity give
+ * zeros.  The cached rows of one sequence's own query tokens must be finite: a
  * weight of 0 does not hide an infinity or NaN in a later one.  out must not overlap
  * an input.
  */

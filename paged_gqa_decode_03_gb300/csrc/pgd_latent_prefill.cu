@@ -22,9 +22,10 @@
 //     The border written into the loop's 128 scores took a tile's last stage 3900 cycles
 //     where a stage takes 1300, and slowed the loop by its mere presence.
 //
-// Measured, head_dim 128 (rope_dim 64): one prompt of 16381 tokens x 16 heads 815 us (1685
-// TFLOP/s; 88 % of what a large library product reaches here), 4 x 2048 x 32 heads 155,
-// 37 prompts of 1 to 512 tokens x 16 heads 33.  By clock stamps a period of both tiles takes
+// Measured, head_dim 128 (rope_dim 64): one prompt of 16381 tokens x 16 heads 815 to 935 us
+// (1685 to 1470 TFLOP/s: few calls to sustained ones, by the power limit), 4 x 2048 x 32 heads
+// 159 to 169 a call and 155 in a graph, 37 prompts of 1 to 512 tokens x 16 heads 31 to 33 and
+// 28.5.  By clock stamps a period of both tiles takes
 // 3200 to 3450 cycles, of which the products take 2560.  They are there in time (a tile's
 // weights 400 cycles before the other's scores are whole), so what is lost lies between the
 // four groups of a period, 150 to 200 cycles each; shared memory is read at a quarter of

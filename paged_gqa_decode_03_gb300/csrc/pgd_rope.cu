@@ -8,8 +8,10 @@
 // exactly: a position is a whole number, so whole turns of f_i / 2 pi drop out of
 // it and what is left is a 64-bit fraction of a turn, F_i = frac(f_i / 2 pi) 2^64;
 // position * F_i mod 2^64 is the place on the circle, whatever the position (an
-// fp32 product at position 10^6 is off by up to 0.03 radians).  f_i / 2 pi is
-// rounded to 53 bits, an error of position * f_i * 2^-53 radians at most.
+// fp32 product at position 10^6 is off by up to 0.03 radians).  f_i / 2 pi is the
+// product with a rounded 1 / 2 pi in 53 bits and F_i whole: position * (f_i 2^-52 +
+// 2 pi 2^-64) radians at most (f_i below 0: 2^-54, one rounding next to 1).  The place goes
+// on as 32 bits and an fp32 number of half turns: 1.1e-7 radians more, at any position.
 //
 // Every value moves once, so the call is a copy, bound by HBM, with a few
 // operations a value: the sines and cosines of a row are worked out once, in shared

@@ -99,8 +99,8 @@ __device__ __forceinline__ void write_rows(const RowOut &o, bool half, bool wide
 // The same without the exchange: each lane writes its own row's columns, 32 at a time
 // (dst: where the first goes, or null).  A store touches 32 lines, but whole sectors of
 // each, and the code is a quarter as long: for kernels in which it runs between long
-// loops, fetched anew each time (latent prompts: 37 short ones 32.5 -> 29.5 us, 4 x 2048
-// 169 -> 162, 16381 tokens 897 -> 867).
+// loops, fetched anew each time (latent prompts: 37 short ones 37 -> 34 us, 4 x 2048
+// 174 -> 167, 16381 tokens 900 -> 867).
 __device__ __forceinline__ void store_8_words(char *dst, const uint32_t *w, bool wide)
 {
     if (wide) {

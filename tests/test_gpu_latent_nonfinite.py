@@ -79,6 +79,22 @@ def test_scores_of_infinity(lens, new, R, P, H, scale):
     assert w.T * H // 8 < count < w.T * H * 7 // 8
 
 
+def test_scores_that_are_all_of_minus_infinity_give_zeros():
+    """Of the one token there is, of every token of a cut request, and of some pieces of one."""
+    H, R, P = 16, 512, 64
+    w = LatentCase([1, 5000, 5000], [1, 1, 1], H, R, P, 16, seed=21)
+    for s, tokens in ((0, range(1)), (1, range(5000)), (2, range(2000, 4500))):
+        w.rows[s][list(tokens), R] = float("-inf")
+        for j in range(w.tables.shape[1]):
+            part = w.rows[s][j * 16:(j + 1) * 16]
+            w.cache[int(w.tables[s, j]), :part.shape[0]] = part
+    w.q_rope[:, :, 0] = 0.5 + w.q_rope[:, :, 0].abs()
+    out = w.run(dtype=torch.float32)
+    assert (out[:2] == 0).all()
+    rows, ref, A = w.expected(2)
+    assert_attention(out[rows], ref, A, 5000, R + P, float(w.rows[2][:, :R].abs().max()), w.scale, "in part")
+
+
 def test_a_token_of_nan_reaches_its_readers_alone():
     w = LatentCase([3000, 3000, 200], [1, 2, 1], 16, 512, 64, 32, seed=9)
     w.rows[1][1234, 7] = float("nan")
